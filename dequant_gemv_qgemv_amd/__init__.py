@@ -19,6 +19,9 @@ import os
 
 import torch
 
+from . import _attention
+from ._attention import new_cache, qattn_cache, qattn_prompt, qcache_read, qcache_write
+
 __all__ = [
     "qpack_uint3",
     "qrepack_w4c_uint3",
@@ -27,6 +30,11 @@ __all__ = [
     "qgemv_w3g128_multi",
     "qgemm_w3g128_smallM",
     "qgemm_w3g128_smallM_noalloc",
+    "new_cache",
+    "qcache_write",
+    "qcache_read",
+    "qattn_cache",
+    "qattn_prompt",
     "qstatus_str",
     "check_quantization_config",
     "library_path",
@@ -55,7 +63,8 @@ GROUP = 128
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libqw3.so")
 _EXPORTS = ("qpack_uint3", "qrepack_w4c_uint3", "qdequant_bf16", "qgemv_w3g128", "qgemv_w3g128_multi",
-            "qgemm_w3g128_smallM", "qgemm_w3g128_smallM_noalloc", "qgemm_w3g128_batch_invariant", "qstatus_str",
+            "qgemm_w3g128_smallM", "qgemm_w3g128_smallM_noalloc", "qgemm_w3g128_batch_invariant",
+            "qcache_write", "qcache_read", "qattn_cache", "qattn_prompt", "qstatus_str",
             "qw3_last_hip_error",
             "qw3_abi_version")
 
@@ -115,6 +124,13 @@ def qstatus_str(status: int) -> str:
 def _check(status: int, where: str):
     if status != QW3_OK:
         raise Qw3Error(status, where)
+
+
+def _raise(status: int, where: str):
+    raise Qw3Error(status, where)
+
+
+_attention._bind(_lib, _raise)
 
 
 def _stream():

@@ -1,4 +1,4 @@
-"""Compile the HIP library in-tree: csrc/qw3_gemv.hip + csrc/qw3.hip -> libqw3.so (gfx950 only)."""
+"""Compile the HIP library in-tree: csrc/*.hip -> libqw3.so (gfx950 only)."""
 from __future__ import annotations
 
 import os
@@ -28,6 +28,8 @@ HIP_FLAGS = [
 UNITS = [
     ("qw3_gemv.hip", ["-mllvm", "--amdgpu-sched-strategy=max-ilp"]),
     ("qw3.hip", []),
+    ("qw3_cache.hip", []),
+    ("qw3_attn.hip", []),
 ]
 
 

@@ -1419,7 +1419,9 @@ bool stream_capturing(hipStream_t stream) {
     return cs != hipStreamCaptureStatusNone;
 }
 
-qw3_status workspace(hipStream_t stream, size_t bytes, void **out) {
+}  // namespace
+
+qw3_status qw3_shared::workspace(hipStream_t stream, size_t bytes, void **out) {
     int dev = 0;
     hipError_t err = hipGetDevice(&dev);
     if (err != hipSuccess) return hip_fail(err);
@@ -1447,6 +1449,8 @@ qw3_status workspace(hipStream_t stream, size_t bytes, void **out) {
     *out = p;
     return QW3_OK;
 }
+
+namespace {
 
 // Static source, for callers that cannot allocate (qgemm_w3g128_smallM_noalloc):
 // the file-scope array `scratch`, one copy per device for the life of the
@@ -1893,8 +1897,8 @@ const char *qstatus_str(qw3_status status) {
     switch (status) {
         case QW3_OK: return "ok";
         case QW3_ERR_NULL: return "a required pointer is NULL";
-        case QW3_ERR_SHAPE: return "invalid shape (negative size, K % 128 != 0, or K > QW3_MAX_K)";
-        case QW3_ERR_ALIGN: return "misaligned pointer (x/packed/codes/w_out need 16 bytes)";
+        case QW3_ERR_SHAPE: return "invalid shape or argument (a size, K, heads, page size, stride or scale out of range)";
+        case QW3_ERR_ALIGN: return "misaligned pointer or stride (see the call's alignment in qw3.h)";
         case QW3_ERR_HIP: return "HIP runtime error (see qw3_last_hip_error)";
         case QW3_ERR_CAPTURE: return "the stream's workspace would have to grow during graph capture";
         case QW3_ERR_SCRATCH: return "the call needs more than the static scratch (QW3_NOALLOC_SCRATCH_BYTES)";

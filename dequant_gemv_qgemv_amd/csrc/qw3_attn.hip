@@ -1,0 +1,851 @@
+// Attention between the products: qattn_prompt (whole prompts) and qattn_cache
+// (new or drafted tokens over the quantised cache).  C ABI in include/qw3.h.
+//
+// Both compute, for a query row with the visible keys V,
+//   o = sum_{j in V} p_j v_j / sum_{j in V} p_j,   p_j = 2^(c q.k_j - m),
+// c = sm_scale log2(e), m a running maximum over the keys read so far: one
+// pass over the keys, the sums rescaled by 2^(m - m') when m grows to m'.
+// Scores, m, the sum of p and the weighted sum of v stay in fp32; only p is
+// rounded, to bf16 for the matrix unit (at most 2^-8 of a term, the rounding
+// of the output itself).
+//
+// Orientation.  The matrix unit computes S^T = K Q^T, so a query row is a
+// column of the result: one lane holds many keys of one row, the row's maximum
+// and sum are mostly in-lane, and S^T's registers are, as they lie, the B
+// operand of O^T = V^T P^T once V's rows are taken in the same order.  The
+// rescale factor of a row is then one value per lane.  V^T comes from row-major
+// tiles in LDS through the transposing LDS reads.
+#include "qw3_common.h"
+
+using namespace qw3_shared;
+
+namespace {
+
+typedef float f2_t __attribute__((ext_vector_type(2)));
+typedef float f16_t __attribute__((ext_vector_type(16)));
+typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
+typedef short s4_t __attribute__((ext_vector_type(4)));
+typedef int i2_t __attribute__((ext_vector_type(2)));
+typedef int i4_t __attribute__((ext_vector_type(4)));
+#define LDS_AS __attribute__((address_space(3)))
+
+constexpr float kNegInf = -__builtin_huge_valf();
+// m may stay this far (in log2) below the true maximum before the sums are
+// rescaled: p then reaches at most 2^8, harmless in fp32 and bf16.
+constexpr float kSlack = 8.0f;
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const f2_t f = {lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf2_t));
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)x);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// A buffer descriptor over `bytes` bytes at p (both the same in every lane);
+// reads past the end give zeros.
+typedef __amdgpu_buffer_rsrc_t desc_t;
+__device__ __forceinline__ desc_t descriptor(const void *p, uint32_t bytes) {
+    void *at = reinterpret_cast<void *>(uniform(reinterpret_cast<int64_t>(p)));
+    return __builtin_amdgcn_make_buffer_rsrc(at, 0, uniform((int)bytes), 0x00020000);
+}
+
+// 64 lanes x 16 bytes from memory straight into LDS: lane i's bytes land at
+// lds + 16 i.  The caller waits for vmcnt before it reads them.
+__device__ __forceinline__ void load_to_lds(const char *lds, uint32_t voffset, desc_t desc) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(desc, (LDS_AS void *)lds, 16, voffset, 0, 0, 0);
+}
+
+__device__ __forceinline__ void wait_vm0() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void wait_vm0_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+__device__ __forceinline__ float max_halves(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float max_quarters(float x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return max_halves(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float sum_halves(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float sum_quarters(float x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return sum_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
+// cu[i] as a row number, whatever the array holds.
+__device__ __forceinline__ int clamp_row(int x, int total) { return min(max(x, 0), total); }
+
+// ================================================================= prompt ==
+struct PromptArgs {
+    const uint16_t *q, *k, *v;
+    uint16_t *o;
+    const int32_t *cu_q, *cu_k;
+    int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;  // strides in elements
+    int B, Tq, Tk, Hq, H, tiles;
+    float scale;  // sm_scale log2(e)
+};
+
+// Query rows of a workgroup (4 waves x 32) and keys of a tile.
+constexpr int kRows = 128, kKeys = 64;
+
+// One query row recomputed by a wave from the visible keys alone (keys 0..last).
+// The tiles multiply hidden keys by p = 0, which is not 0 where a hidden value
+// row holds an infinity or NaN; rows that come out non-finite are redone here,
+// so such a value reaches only the rows that see its key.
+template <int D>
+__device__ __forceinline__ void exact_row(const PromptArgs &a, const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                                       uint16_t *o, int last) {
+    const int lane = threadIdx.x & 63;
+    constexpr int kPer = D / 64;
+    auto score = [&](int j) {
+        float s = 0.0f;
+        const uint16_t *kr = k + (int64_t)j * a.k_ts;
+        for (int d = 0; d < D; ++d) s += bf16_to_f32(q[d]) * bf16_to_f32(kr[d]);
+        return s * a.scale;
+    };
+    float m = kNegInf;
+    bool nan = false;
+    for (int j = lane; j <= last; j += 64) {
+        const float s = score(j);
+        nan |= s != s;
+        m = fmaxf(m, s);
+    }
+    for (int x = 32; x >= 1; x /= 2) m = fmaxf(m, __shfl_xor(m, x, 64));
+    if (__any(nan)) m = __uint_as_float(0x7fc00000u);
+    if (m == kNegInf) m = 0.0f;  // every visible score is -inf
+    float l = 0.0f, acc[kPer] = {};
+    for (int j0 = 0; j0 <= last; j0 += 64) {
+        const int j = j0 + lane;
+        const float p = j <= last ? exp2_fast(score(j) - m) : 0.0f;
+        l += p;
+        for (int i = 0; i < 64 && j0 + i <= last; ++i) {
+            const float pi = __shfl(p, i, 64);
+            for (int x = 0; x < kPer; ++x)
+                acc[x] += pi * bf16_to_f32(v[(int64_t)(j0 + i) * a.v_ts + lane * kPer + x]);
+        }
+    }
+    for (int x = 32; x >= 1; x /= 2) l += __shfl_xor(l, x, 64);
+    for (int x = 0; x < kPer; ++x) {
+        const float r = l != 0.0f ? acc[x] / l : 0.0f;
+        o[lane * kPer + x] = (uint16_t)(pack_bf16(r, 0.0f) & 0xffffu);
+    }
+}
+
+template <int D, bool CAUSAL>
+__global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
+    constexpr int kTileBytes = kKeys * D * 2;
+    constexpr int kRowBytes = D * 2;
+    constexpr int kRowsPerLoad = 1024 / kRowBytes;       // rows that one wave-wide load covers
+    constexpr int kLoads = kTileBytes / 1024 / 4;        // loads of one tile per wave
+    __shared__ __attribute__((aligned(1024))) char lds[4 * kTileBytes];  // K, V of the two tiles in flight
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5, col = lane & 31;
+
+    // Workgroups go round the 8 XCDs; give each XCD a contiguous range of
+    // (kv head, tile, head of the group), so its L2 holds few heads' keys.
+    // Tiles run from the end: with a causal mask the last have the most keys.
+    const uint32_t n = gridDim.x, xcd = blockIdx.x & 7, q8 = n >> 3, r8 = n & 7;
+    const uint32_t idx = xcd * q8 + min(xcd, r8) + (blockIdx.x >> 3);
+    const int G = a.Hq / a.H;
+    const int kvh = idx / (uint32_t)(a.tiles * G);
+    const uint32_t rest = idx - (uint32_t)kvh * (a.tiles * G);
+    const int tile = a.tiles - 1 - (int)(rest / (uint32_t)G);
+    const int head = kvh * G + (int)(rest % (uint32_t)G);
+
+    // Sequence b owns the tiles from cu_q[b] / kRows + b on: room for all of
+    // its rows whatever its length, with no lengths known on the host.
+    int b = -1;
+    for (int base = 0; base < a.B; base += 64) {
+        const unsigned long long in = __ballot(
+            base + lane < a.B && clamp_row(a.cu_q[min(base + lane, a.B - 1)], a.Tq) / kRows + base + lane <= tile);
+        b += __popcll(in);
+        if (in != ~0ull) break;
+    }
+    b = uniform(b);
+    if (b < 0) return;
+    const int q0 = clamp_row(a.cu_q[b], a.Tq), nq = clamp_row(a.cu_q[b + 1], a.Tq) - q0;
+    const int k0 = clamp_row(a.cu_k[b], a.Tk), nk = max(clamp_row(a.cu_k[b + 1], a.Tk) - k0, 0);
+    const int row0 = (tile - q0 / kRows - b) * kRows;
+    if (row0 >= nq) return;
+
+    const int off = nk - nq;
+    const int kend = CAUSAL ? min(nk, min(row0 + kRows, nq) + off) : nk;  // keys past every row of the workgroup
+    const int ntiles = kend > 0 ? (kend + kKeys - 1) / kKeys : 0;
+    const int w0 = row0 + 32 * wave, row = w0 + col;
+    const int last = CAUSAL ? min(nk - 1, row + off) : nk - 1;  // the row's last visible key
+    const int wlo = CAUSAL ? min(nk - 1, w0 + off) : nk - 1;    // the same of the wave's first and last row
+    const int whi = CAUSAL ? min(nk - 1, min(w0 + 31, nq - 1) + off) : nk - 1;
+    const bool live = w0 < nq;
+
+    const uint16_t *qp = a.q + (int64_t)(q0 + min(row, nq - 1)) * a.q_ts + head * a.q_hs;
+    const char *kp = reinterpret_cast<const char *>(a.k + (int64_t)k0 * a.k_ts + kvh * a.k_hs);
+    const char *vp = reinterpret_cast<const char *>(a.v + (int64_t)k0 * a.v_ts + kvh * a.v_hs);
+
+    bf8_t qf[D / 16];
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) qf[t] = *reinterpret_cast<const bf8_t *>(qp + 16 * t + 8 * half);
+
+    // LDS tiles: row r, 16-byte piece c of it at place c ^ f(r), so that reads
+    // down a column of pieces spread over the banks.  A load fills its 1 KB in
+    // lane order; the lane picks the piece that belongs there.  Load i of the
+    // wave covers rows (4 i + wave) kRowsPerLoad ..., whose f does not depend on i.
+    const int lrow = wave * kRowsPerLoad + lane / (kRowBytes / 16), lpiece = lane % (kRowBytes / 16);
+    const int fk = D == 128 ? (lrow & 15) : ((lrow >> 1) & 7);
+    const int fv = D == 128 ? ((lrow & 7) << 1) : (((lrow >> 1) & 3) << 1);
+    uint32_t kvo[kLoads], vvo[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        kvo[i] = (uint32_t)((lrow + 4 * kRowsPerLoad * i) * a.k_ts * 2 + (lpiece ^ fk) * 16);
+        vvo[i] = (uint32_t)((lrow + 4 * kRowsPerLoad * i) * a.v_ts * 2 + (lpiece ^ fv) * 16);
+    }
+    char *lds0 = lds + uniform(wave) * 1024;
+    auto fetch = [&](int t, int buf) {
+        const int64_t j0 = (int64_t)t * kKeys;
+        const int64_t kleft = (nk - 1 - j0) * a.k_ts * 2 + kRowBytes, vleft = (nk - 1 - j0) * a.v_ts * 2 + kRowBytes;
+        const desc_t dk = descriptor(kp + j0 * a.k_ts * 2, (uint32_t)min(kleft, (int64_t)0x7fffffff));
+        const desc_t dv = descriptor(vp + j0 * a.v_ts * 2, (uint32_t)min(vleft, (int64_t)0x7fffffff));
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) load_to_lds(lds0 + (2 * buf) * kTileBytes + i * 4096, kvo[i], dk);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) load_to_lds(lds0 + (2 * buf + 1) * kTileBytes + i * 4096, vvo[i], dv);
+    };
+
+    // reads: K piece 2 t + half of row 32 kb + col; V^T through 4-row blocks
+    const int xk = D == 128 ? (col & 15) : ((col >> 1) & 7);
+    const uint32_t kbase = col * kRowBytes + ((half ^ (xk & 1)) << 4);
+    const int vr = 4 * half + ((lane & 15) >> 2);
+    const int xv = D == 128 ? ((vr & 7) << 1) : (((vr >> 1) & 3) << 1);
+    const int vsub = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    const uint32_t vbase = vr * kRowBytes + ((vsub ^ (xv & 3)) << 4) + (lane & 1) * 8;
+
+    f16_t acc[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) acc[i] = f16_t{};
+    float m = kNegInf, l = 0.0f;
+
+    auto compute = [&](int t, int buf, auto masked_c) {
+        constexpr bool kMasked = decltype(masked_c)::value;
+        const char *kt = lds + (2 * buf) * kTileBytes, *vt = lds + (2 * buf + 1) * kTileBytes;
+        f16_t s[2];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            s[kb] = f16_t{};
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const bf8_t kf =
+                    *reinterpret_cast<const bf8_t *>(kt + kb * 32 * kRowBytes + kbase + (((2 * i) ^ (xk & ~1)) << 4));
+                s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[i], s[kb], 0, 0, 0);
+            }
+        }
+        if (kMasked) {
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int key = t * kKeys + 32 * kb + 8 * (r / 4) + 4 * half + (r & 3);
+                    s[kb][r] = key > last ? kNegInf : s[kb][r];
+                }
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int r = 1; r < 16; ++r) top = fmaxf(top, s[0][r]);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[1][r]);
+        top *= a.scale;
+        if (__any(top > m + kSlack)) {
+            const float m1 = fmaxf(m, max_halves(top));
+            const float f = m1 == kNegInf ? 1.0f : exp2_fast(m - m1);
+            m = m1;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) acc[i] *= f;
+        }
+        const float ms = m == kNegInf ? 0.0f : m;
+        uint32_t p[2][8];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const float p0 = exp2_fast(fmaf(s[kb][2 * r], a.scale, -ms));
+                const float p1 = exp2_fast(fmaf(s[kb][2 * r + 1], a.scale, -ms));
+                l += p0 + p1;
+                p[kb][r] = pack_bf16(p0, p1);
+            }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const i4_t pu = {(int)p[u / 2][4 * (u & 1)], (int)p[u / 2][4 * (u & 1) + 1], (int)p[u / 2][4 * (u & 1) + 2],
+                             (int)p[u / 2][4 * (u & 1) + 3]};
+            const bf8_t pf = __builtin_bit_cast(bf8_t, pu);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const char *at = vt + 16 * u * kRowBytes + vbase + (((4 * i) ^ (xv & ~3)) << 4);
+                const s4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS s4_t *)at);
+                const s4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS s4_t *)(at + 8 * kRowBytes));
+                typedef short s8_t __attribute__((ext_vector_type(8)));
+                const s8_t vv = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8_t, vv), pf, acc[i], 0, 0, 0);
+            }
+        }
+    };
+
+    if (ntiles > 0) fetch(0, 0);
+    for (int t = 0; t < ntiles; ++t) {
+        wait_vm0_barrier();  // tile t is here, and nobody reads the other buffer any more
+        if (t + 1 < ntiles) fetch(t + 1, (t + 1) & 1);
+        if (live && t * kKeys <= whi) {
+            if (t * kKeys + kKeys - 1 > wlo)
+                compute(t, t & 1, std::true_type{});
+            else
+                compute(t, t & 1, std::false_type{});
+        }
+    }
+    if (!live) return;
+
+    l = sum_halves(l);
+    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // l NaN stays NaN
+    uint16_t *op = a.o + ((int64_t)(q0 + row) * a.Hq + head) * D;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[e] = acc[i][r + e] * inv;
+                bad |= !(fabsf(x[e]) < __builtin_huge_valf());
+            }
+            if (row < nq)
+                *reinterpret_cast<uint2 *>(op + 32 * i + 2 * r + 4 * half) =
+                    make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+        }
+    unsigned long long redo = __ballot(bad && row < nq);
+    redo |= redo >> 32;
+    for (uint32_t todo = (uint32_t)redo; todo != 0; todo &= todo - 1) {
+        const int r = w0 + __builtin_ctz(todo);
+        exact_row<D>(a, a.q + (int64_t)(q0 + r) * a.q_ts + head * a.q_hs, reinterpret_cast<const uint16_t *>(kp),
+                     reinterpret_cast<const uint16_t *>(vp), a.o + ((int64_t)(q0 + r) * a.Hq + head) * D,
+                     CAUSAL ? min(nk - 1, r + off) : nk - 1);
+    }
+}
+
+// ================================================================== cache ==
+struct CacheArgs {
+    const uint16_t *q;
+    const uint8_t *codes;
+    const float *scales;
+    const int32_t *table, *lens, *cu_q;  // cu_q null: one row per sequence
+    const uint64_t *tree;                // null: causal
+    uint16_t *o;
+    float *part;
+    int64_t q_ts, q_hs, max_pages, pages;
+    int B, Tq, Hq, H, G, page_shift, groups;
+    float scale;
+};
+
+constexpr int kUnit = 128;  // keys of a workgroup's step: 32 for each of its 4 waves
+
+// What a sequence asks for.  An item is (sequence, kv head, block of R query
+// rows); its work is counted in units of kUnit keys, at least one, so that an
+// empty cache still writes its zeros.  All items of the call, laid end to end,
+// are cut into equal runs of units, one per workgroup: a long sequence is split
+// over many workgroups and short ones share one, with no lengths known on the
+// host.
+template <int R>
+struct Seq {
+    int q0, nq, len, blocks;
+    int64_t per_item, units;
+    __device__ Seq() {}
+    __device__ Seq(const CacheArgs &a, int b) {
+        q0 = a.cu_q ? clamp_row(a.cu_q[b], a.Tq) : min(b, a.Tq);
+        nq = (a.cu_q ? clamp_row(a.cu_q[b + 1], a.Tq) : min(b + 1, a.Tq)) - q0;
+        nq = max(nq, 0);
+        len = (int)max((int64_t)0, min((int64_t)a.lens[b], a.max_pages << a.page_shift));
+        blocks = (int)(((int64_t)nq * a.G + R - 1) / R);
+        per_item = max((len + (int64_t)kUnit - 1) / kUnit, (int64_t)1);
+        units = per_item * blocks * a.H;
+    }
+};
+
+__device__ __forceinline__ int64_t wave_scan(int64_t x) {  // inclusive prefix sum over the wave
+    const int lane = threadIdx.x & 63;
+    for (int d = 1; d < 64; d *= 2) {
+        const int64_t y = __shfl_up(x, d, 64);
+        if (lane >= d) x += y;
+    }
+    return x;
+}
+
+template <int R>
+__device__ __forceinline__ int64_t total_units(const CacheArgs &a) {
+    int64_t total = 0;
+    for (int base = 0; base < a.B; base += 64) {
+        const int b = base + (threadIdx.x & 63);
+        total += __shfl(wave_scan(b < a.B ? Seq<R>(a, b).units : 0), 63, 64);
+    }
+    return uniform(total);
+}
+
+// The sequence that holds unit u, and the units before it.
+template <int R>
+__device__ __forceinline__ int find_unit(const CacheArgs &a, int64_t u, int64_t *before) {
+    int64_t done = 0;
+    for (int base = 0; base < a.B; base += 64) {
+        const int b = base + (threadIdx.x & 63);
+        const int64_t mine = b < a.B ? Seq<R>(a, b).units : 0;
+        const int64_t upto = done + wave_scan(mine);
+        const unsigned long long past = __ballot(upto > u);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            *before = uniform((int64_t)__shfl(upto - mine, at, 64));
+            return base + at;
+        }
+        done = __shfl(upto, 63, 64);
+    }
+    return -1;
+}
+
+__device__ __forceinline__ int64_t units_per_group(int64_t total, int groups) {
+    return max((total + groups - 1) / groups, (int64_t)1);
+}
+
+// Partial results: two slots for each workgroup (its first and its last item
+// may be shared with others); a slot is R maxima, R sums, R x D weighted sums.
+template <int R, int D>
+__device__ __forceinline__ float *partial(const CacheArgs &a, int64_t group, int which) {
+    return a.part + (group * 2 + which) * (int64_t)(R * (D + 2));
+}
+
+// Eight codes to eight bf16, exact in both types.
+template <bool E4M3>
+__device__ __forceinline__ bf8_t decode8(uint32_t lo, uint32_t hi) {
+    bf8_t r;
+    const uint32_t w[2] = {lo, hi};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (E4M3) {
+            const bf2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], 1.0f, false);
+            const bf2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], 1.0f, true);
+            r[4 * i] = a[0], r[4 * i + 1] = a[1], r[4 * i + 2] = b[0], r[4 * i + 3] = b[1];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[4 * i + j] = (__bf16)(float)(int8_t)(w[i] >> (8 * j));
+        }
+    }
+    return r;
+}
+
+// R: query rows of an item (16, 32 or 64).  Every wave takes all R rows and 32
+// of the unit's keys, with a ring of two such steps of its own in LDS, so the
+// waves meet only at the end of an item.
+template <int D, bool E4M3, int R>
+__global__ __launch_bounds__(256, R == 64 ? 1 : 2) void attn_cache_kernel(CacheArgs a) {
+    constexpr int kN = R / 16;              // blocks of 16 rows
+    constexpr int kStage = 2 * 32 * D;      // bytes of a step: 32 rows of K, 32 of V
+    constexpr int kCols = R == 16 ? D : R == 32 ? 64 : 32;  // channels joined at a time
+    constexpr int kPad = kCols + 4;
+    constexpr int kRing = 4 * 2 * kStage, kJoin = 4 * R * kPad * 4;
+    __shared__ __attribute__((aligned(1024))) char lds[kRing > kJoin ? kRing : kJoin];
+    __shared__ float stat[2][4][R];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), quarter = lane >> 4, col = lane & 15;
+
+    const int64_t total = total_units<R>(a), per = units_per_group(total, a.groups);
+    int64_t u = blockIdx.x * per;
+    const int64_t uend = min(u + per, total);
+    if (u >= uend) return;
+    int64_t before = 0;
+    int b = uniform(find_unit<R>(a, u, &before));
+    Seq<R> seq(a, b);
+
+    // lane's place in the LDS rows (see attn_prompt_kernel): D-byte rows, piece c of row r at c ^ f(r)
+    constexpr int kPieces = D / 16;
+    const int frow = lane / kPieces;  // row within a load of 1 KB
+    uint32_t vo[D / 64];
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+        const int r = frow + i * (64 / kPieces);
+        const int f = D == 128 ? ((r >> 1) & 7) : ((r >> 2) & 3);
+        vo[i] = (uint32_t)(r * D + ((lane % kPieces) ^ f) * 16);
+    }
+    char *ring = lds + wave * 2 * kStage;
+    const int xk = D == 128 ? ((col >> 1) & 7) : ((col >> 2) & 3);
+
+    while (u < uend) {
+        while (u - before >= seq.units) {  // next sequence (some have no rows)
+            before += seq.units;
+            ++b;
+            seq = Seq<R>(a, b);
+        }
+        const int64_t local = u - before, item = local / seq.per_item;
+        const int64_t t0 = local - item * seq.per_item, t1 = min(seq.per_item, t0 + (uend - u));
+        const int h = (int)(item / seq.blocks), block = (int)(item - (int64_t)h * seq.blocks);
+        const int rows = seq.nq * a.G, r0 = block * R, len = seq.len, ctx = len - seq.nq;
+
+        // the rows' queries, as B operands with the channels in the order of K's pieces
+        bf8_t qf[kN][D / 32];
+        int seen[kN];       // causal: the row's last visible key
+        uint64_t tree[kN];  // otherwise the drafts it sees
+#pragma unroll
+        for (int x = 0; x < kN; ++x) {
+            const int r = min(r0 + 16 * x + col, rows - 1), i = r / a.G, g = r - i * a.G;
+            const uint16_t *qp = a.q + (int64_t)(seq.q0 + i) * a.q_ts + (h * a.G + g) * a.q_hs;
+#pragma unroll
+            for (int t = 0; t < D / 32; ++t)
+                qf[x][t] = *reinterpret_cast<const bf8_t *>(qp + 16 * (quarter + 4 * (t / 2)) + 8 * (t & 1));
+            seen[x] = a.tree ? ctx - 1 : ctx + i;
+            tree[x] = a.tree ? a.tree[seq.q0 + i] : 0;
+        }
+
+        f4_t acc[kN][D / 16];
+        float m[kN], l[kN];
+#pragma unroll
+        for (int x = 0; x < kN; ++x) {
+            m[x] = kNegInf, l[x] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) acc[x][i] = f4_t{};
+        }
+
+        const int key0 = (int)t0 * kUnit + 32 * wave;
+        // steps of this wave: keys key0 + 128 s
+        const int64_t room = (int64_t)len - key0;
+        const int steps = room <= 0 ? 0 : (int)min((int64_t)(t1 - t0), (room + kUnit - 1) / kUnit);
+        // of the step to come: the scales of keys 4 quarter + r of its two 16-key
+        // groups, and whether a group's page does not exist (its keys are hidden)
+        float4 ks[2], vs[2];
+        bool none[2];
+        auto fetch = [&](int s, int buf) {
+            const int key = key0 + s * kUnit;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int pos = key + 16 * g;
+                const int idx = pos >> a.page_shift, in = pos & ((1 << a.page_shift) - 1);
+                const int page = pos < len ? uniform(a.table[(int64_t)b * a.max_pages + idx]) : -1;
+                const bool there = page >= 0 && page < a.pages;
+                const int64_t row = ((((int64_t)(there ? page : 0) * 2) * a.H + h) << a.page_shift) + in;
+                const int64_t vrow = row + ((int64_t)a.H << a.page_shift);
+                const uint32_t bytes = there ? (uint32_t)(min(16, len - pos) * D) : 0;
+                const desc_t dk = descriptor(a.codes + row * D, bytes), dv = descriptor(a.codes + vrow * D, bytes);
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    load_to_lds(ring + buf * kStage + g * 16 * D + i * 1024, vo[i], dk);
+                    load_to_lds(ring + buf * kStage + (32 + g * 16) * D + i * 1024, vo[i], dv);
+                }
+                ks[g] = vs[g] = make_float4(0, 0, 0, 0);
+                none[g] = !there;
+                if (there) {
+                    ks[g] = *reinterpret_cast<const float4 *>(a.scales + row + 4 * quarter);
+                    vs[g] = *reinterpret_cast<const float4 *>(a.scales + vrow + 4 * quarter);
+                }
+            }
+        };
+
+        if (steps > 0) fetch(0, 0);
+        for (int s = 0; s < steps; ++s) {
+            wait_vm0();
+            float kc[2][4], vc[2][4];
+            bool gone[2];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                asm volatile("" : "+v"(ks[g].x), "+v"(ks[g].y), "+v"(ks[g].z), "+v"(ks[g].w));
+                asm volatile("" : "+v"(vs[g].x), "+v"(vs[g].y), "+v"(vs[g].z), "+v"(vs[g].w));
+                gone[g] = none[g];
+                kc[g][0] = ks[g].x * a.scale, kc[g][1] = ks[g].y * a.scale;
+                kc[g][2] = ks[g].z * a.scale, kc[g][3] = ks[g].w * a.scale;
+                vc[g][0] = vs[g].x, vc[g][1] = vs[g].y, vc[g][2] = vs[g].z, vc[g][3] = vs[g].w;
+            }
+            if (s + 1 < steps) fetch(s + 1, (s + 1) & 1);
+            const char *kt = ring + (s & 1) * kStage, *vt = kt + 32 * D;
+            const int key = key0 + s * kUnit;
+
+            f4_t sc[kN][2];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+#pragma unroll
+                for (int x = 0; x < kN; ++x) sc[x][g] = f4_t{};
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(kt + (16 * g + col) * D +
+                                                                     (((quarter + 4 * c) ^ xk) << 4));
+                    const bf8_t k0 = decode8<E4M3>(w.x, w.y), k1 = decode8<E4M3>(w.z, w.w);
+#pragma unroll
+                    for (int x = 0; x < kN; ++x) {
+                        sc[x][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, qf[x][2 * c], sc[x][g], 0, 0, 0);
+                        sc[x][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, qf[x][2 * c + 1], sc[x][g], 0, 0, 0);
+                    }
+                }
+            }
+            const bool masked = key + 31 >= min(ctx, len) || gone[0] || gone[1];
+            bf8_t pf[kN];
+#pragma unroll
+            for (int x = 0; x < kN; ++x) {
+                bool hid[2][4];
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        sc[x][g][r] *= kc[g][r];
+                        hid[g][r] = false;
+                    }
+                if (masked) {
+#pragma unroll
+                    for (int g = 0; g < 2; ++g)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int pos = key + 16 * g + 4 * quarter + r, j = pos - ctx;
+                            const bool draft = j >= 0 && j < 64 && ((tree[x] >> (j & 63)) & 1);
+                            hid[g][r] = gone[g] || pos >= len || (pos > seen[x] && !draft);
+                            sc[x][g][r] = hid[g][r] ? kNegInf : sc[x][g][r];
+                        }
+                }
+                float top = sc[x][0][0];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) top = fmaxf(top, sc[x][i / 4][i % 4]);
+                if (__any(top > m[x] + kSlack)) {
+                    const float m1 = fmaxf(m[x], max_quarters(top));
+                    const float f = m1 == kNegInf ? 1.0f : exp2_fast(m[x] - m1);
+                    m[x] = m1;
+                    l[x] *= f;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) acc[x][i] *= f;
+                }
+                const float ms = m[x] == kNegInf ? 0.0f : m[x];
+                uint32_t p[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float w[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int g = i / 2, r = 2 * (i & 1) + e;
+                        const float pe = exp2_fast(sc[x][g][r] - ms);
+                        l[x] += pe;
+                        // a hidden key's scale may be anything
+                        w[e] = masked && hid[g][r] ? 0.0f : pe * vc[g][r];
+                    }
+                    p[i] = pack_bf16(w[0], w[1]);
+                }
+                pf[x] = __builtin_bit_cast(bf8_t, i4_t{(int)p[0], (int)p[1], (int)p[2], (int)p[3]});
+            }
+            // V^T: keys 4 quarter + 0..3 and 16 + 4 quarter + 0..3 of 16 channels
+            const int vkey = 4 * quarter + ((col >> 1) & 3) + 16 * (col >> 3);
+            const int xv = D == 128 ? ((vkey >> 1) & 7) : ((vkey >> 2) & 3);
+            const char *vrow = vt + vkey * D + (col & 1) * 8;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const i2_t w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS_AS i2_t *)(vrow + ((i ^ xv) << 4)));
+                const bf8_t vf = decode8<E4M3>((uint32_t)w[0], (uint32_t)w[1]);
+#pragma unroll
+                for (int x = 0; x < kN; ++x)
+                    acc[x][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[x], acc[x][i], 0, 0, 0);
+            }
+        }
+
+        // join the four waves
+#pragma unroll
+        for (int x = 0; x < kN; ++x) {
+            l[x] = sum_quarters(l[x]);
+            if (quarter == 0) stat[0][wave][16 * x + col] = m[x], stat[1][wave][16 * x + col] = l[x];
+        }
+        const bool whole = t1 - t0 == seq.per_item;
+        float *out = whole ? nullptr : partial<R, D>(a, blockIdx.x, u == blockIdx.x * per ? 0 : 1);
+        float *join = reinterpret_cast<float *>(lds);
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += kCols) {
+            __syncthreads();  // the ring, or the channels before, are read
+#pragma unroll
+            for (int x = 0; x < kN; ++x)
+#pragma unroll
+                for (int i = 0; i < kCols / 16; ++i)
+                    *reinterpret_cast<f4_t *>(join + (wave * R + 16 * x + col) * kPad + 16 * i + 4 * quarter) =
+                        acc[x][c0 / 16 + i];
+            __syncthreads();
+            for (int e = tid; e < R * kCols / 4; e += 256) {
+                const int r = e / (kCols / 4), c = 4 * (e % (kCols / 4));
+                float mm = kNegInf;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) mm = fmaxf(mm, stat[0][w][r]);
+                float ll = 0.0f;
+                f4_t sum = {};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const float f = stat[0][w][r] == kNegInf ? 0.0f : exp2_fast(stat[0][w][r] - mm);
+                    ll += f * stat[1][w][r];
+                    sum += f * *reinterpret_cast<const f4_t *>(join + (w * R + r) * kPad + c);
+                }
+                if (r0 + r >= rows) continue;
+                if (whole) {
+                    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+                    const int i = (r0 + r) / a.G, g = r0 + r - i * a.G;
+                    *reinterpret_cast<uint2 *>(a.o + ((int64_t)(seq.q0 + i) * a.Hq + h * a.G + g) * D + c0 + c) =
+                        make_uint2(pack_bf16(sum[0] * inv, sum[1] * inv), pack_bf16(sum[2] * inv, sum[3] * inv));
+                } else {
+                    *reinterpret_cast<f4_t *>(out + 2 * R + r * D + c0 + c) = sum;
+                    if (c0 == 0 && c == 0) out[r] = mm, out[R + r] = ll;
+                }
+            }
+        }
+        __syncthreads();
+        u += t1 - t0;
+    }
+}
+
+// Joins the partial results of the items that more than one workgroup worked
+// on, in the workgroups' order: one wave per query row and head.
+template <int D, int R>
+__global__ __launch_bounds__(256) void attn_cache_join_kernel(CacheArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);  // (token, head)
+    const int tok = uniform((int)(at / a.Hq)), head = uniform((int)(at % a.Hq));
+    if (tok >= a.Tq) return;
+    const int64_t total = total_units<R>(a), per = units_per_group(total, a.groups);
+    // the token's sequence, and the units before it
+    int b = -1;
+    int64_t before = 0;
+    for (int base = 0; base < a.B; base += 64) {
+        const int c = base + lane;
+        Seq<R> s;
+        s.q0 = 0, s.nq = 0, s.units = 0;
+        if (c < a.B) s = Seq<R>(a, c);
+        const int64_t upto = before + wave_scan(s.units);
+        const unsigned long long in = __ballot(tok >= s.q0 && tok < s.q0 + s.nq);
+        if (in) {
+            const int w = __builtin_ctzll(in);
+            b = uniform(base + w);
+            before = uniform((int64_t)__shfl(upto - s.units, w, 64));
+            break;
+        }
+        before = uniform((int64_t)__shfl(upto, 63, 64));
+    }
+    if (b < 0) return;
+    const Seq<R> seq(a, b);
+    const int h = head / a.G, r = (tok - seq.q0) * a.G + head - h * a.G;
+    const int64_t ustart = before + ((int64_t)h * seq.blocks + r / R) * seq.per_item, uend = ustart + seq.per_item;
+    const int64_t first = ustart / per, last = (uend - 1) / per;
+    if (first == last) return;  // its workgroup wrote the output
+    constexpr int kPer = D / 64;
+    float m = kNegInf, l = 0.0f, acc[kPer] = {};
+    for (int64_t w = first; w <= last; ++w) {
+        const float *p = partial<R, D>(a, w, w * per >= ustart ? 0 : 1);
+        const float pm = p[r % R], pl = p[R + r % R];
+        if (pm == kNegInf) continue;
+        const float m1 = fmaxf(m, pm), f = exp2_fast(m - m1), g = exp2_fast(pm - m1);
+        m = m1;
+        l = l * f + pl * g;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) acc[i] = acc[i] * f + p[2 * R + (r % R) * D + lane * kPer + i] * g;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t *o = a.o + (int64_t)at * D + lane * kPer;
+    if (kPer == 2)
+        *reinterpret_cast<uint32_t *>(o) = pack_bf16(acc[0] * inv, acc[kPer - 1] * inv);
+    else
+        *o = (uint16_t)(pack_bf16(acc[0] * inv, 0.0f) & 0xffffu);
+}
+
+template <int D, bool E4M3, int R>
+qw3_status launch_cache(CacheArgs a, hipStream_t stream) {
+    int cus = 0;
+    qw3_status st = cu_count(&cus);
+    if (st != QW3_OK) return st;
+    a.groups = cus * (R == 64 ? 1 : 2);
+    void *ws = nullptr;
+    st = workspace(stream, (size_t)a.groups * 2 * R * (D + 2) * sizeof(float), &ws);
+    if (st != QW3_OK) return st;
+    a.part = static_cast<float *>(ws);
+    hipLaunchKernelGGL((attn_cache_kernel<D, E4M3, R>), dim3(a.groups), dim3(256), 0, stream, a);
+    st = check_launch();
+    if (st != QW3_OK) return st;
+    hipLaunchKernelGGL((attn_cache_join_kernel<D, R>), dim3((unsigned)ceil_div((int64_t)a.Tq * a.Hq, 4)), dim3(256), 0,
+                       stream, a);
+    return check_launch();
+}
+
+template <int D, bool E4M3>
+qw3_status launch_cache_rows(const CacheArgs &a, hipStream_t stream) {
+    const int64_t rows = ceil_div(a.Tq, a.B) * a.G;  // of a sequence, on average
+    if (rows <= 16) return launch_cache<D, E4M3, 16>(a, stream);
+    if (rows <= 32) return launch_cache<D, E4M3, 32>(a, stream);
+    return launch_cache<D, E4M3, 64>(a, stream);
+}
+
+bool strides_ok(int64_t ts, int64_t hs) { return ts >= 0 && hs >= 0 && ts < (1 << 23) && hs < (int64_t(1) << 40); }
+
+qw3_status check_heads(int64_t Hq, int64_t H) {
+    return H < 1 || Hq < 1 || Hq % H != 0 || Hq > QW3_MAX_HEADS ? QW3_ERR_SHAPE : QW3_OK;
+}
+
+bool scale_ok(float s) { return s > 0.0f && s < __builtin_huge_valf(); }
+
+}  // namespace
+
+extern "C" {
+
+qw3_status qattn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *cu_q,
+                        const int32_t *cu_k, uint16_t *out, int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t H,
+                        int64_t D, int64_t q_ts, int64_t q_hs, int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs,
+                        int32_t causal, float sm_scale, void *hip_stream) {
+    if (check_heads(Hq, H) != QW3_OK || (D != 64 && D != 128)) return QW3_ERR_SHAPE;
+    if (B < 0 || B > QW3_MAX_SEQS || Tq < 0 || Tk < 0 || Tq > QW3_MAX_TOKENS || Tk > QW3_MAX_TOKENS)
+        return QW3_ERR_SHAPE;
+    if (!scale_ok(sm_scale) || !strides_ok(q_ts, q_hs) || !strides_ok(k_ts, k_hs) || !strides_ok(v_ts, v_hs))
+        return QW3_ERR_SHAPE;
+    if (B == 0 || Tq == 0) return QW3_OK;
+    if (!q || !cu_q || !cu_k || !out || (Tk > 0 && (!k || !v))) return QW3_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_q, 4) ||
+        !aligned(cu_k, 4) || q_ts % 8 || q_hs % 8 || k_ts % 8 || k_hs % 8 || v_ts % 8 || v_hs % 8)
+        return QW3_ERR_ALIGN;
+    const int64_t tiles = Tq / kRows + B;
+    if (tiles * Hq > 0x7fffffff) return QW3_ERR_SHAPE;
+    const PromptArgs a{q,    k,    v,    out,  cu_q,   cu_k,    q_ts,    q_hs,   k_ts,       k_hs,
+                       v_ts, v_hs, (int)B, (int)Tq, (int)Tk, (int)Hq, (int)H, (int)tiles, sm_scale * 1.44269504088896341f};
+    const dim3 grid((unsigned)(tiles * Hq));
+    auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, (hipStream_t)hip_stream, a); };
+    if (D == 128)
+        causal ? run(attn_prompt_kernel<128, true>) : run(attn_prompt_kernel<128, false>);
+    else
+        causal ? run(attn_prompt_kernel<64, true>) : run(attn_prompt_kernel<64, false>);
+    return check_launch();
+}
+
+qw3_status qattn_cache(const uint16_t *q, const void *codes, const float *scales, int32_t code_type,
+                       const int32_t *block_table, const int32_t *lens, const int32_t *cu_q, const int64_t *tree,
+                       uint16_t *out, int64_t B, int64_t max_pages, int64_t Tq, int64_t Hq, int64_t H, int64_t D,
+                       int64_t pages, int64_t page_size, int64_t q_ts, int64_t q_hs, float sm_scale,
+                       void *hip_stream) {
+    int shift = 0;
+    qw3_status st = check_cache(code_type, H, D, pages, page_size, &shift);
+    if (st != QW3_OK) return st;
+    if (check_heads(Hq, H) != QW3_OK) return QW3_ERR_SHAPE;
+    if (B < 0 || B > QW3_MAX_SEQS || Tq < 0 || Tq > QW3_MAX_TOKENS || max_pages < 0 || (!cu_q && Tq != B))
+        return QW3_ERR_SHAPE;
+    if (max_pages * page_size > (int64_t(1) << 30) || Tq * Hq > (int64_t(1) << 31)) return QW3_ERR_SHAPE;
+    if (!scale_ok(sm_scale) || !strides_ok(q_ts, q_hs)) return QW3_ERR_SHAPE;
+    if (B == 0 || Tq == 0) return QW3_OK;
+    if (!q || !lens || !out || (max_pages > 0 && !block_table) || (pages > 0 && (!codes || !scales)))
+        return QW3_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(out, 16) ||
+        !aligned(block_table, 4) || !aligned(lens, 4) || !aligned(cu_q, 4) || !aligned(tree, 8) || q_ts % 8 || q_hs % 8)
+        return QW3_ERR_ALIGN;
+    CacheArgs a{};
+    a.q = q, a.codes = static_cast<const uint8_t *>(codes), a.scales = scales, a.table = block_table, a.lens = lens;
+    a.cu_q = cu_q, a.tree = reinterpret_cast<const uint64_t *>(tree), a.o = out, a.q_ts = q_ts, a.q_hs = q_hs;
+    a.max_pages = max_pages, a.pages = pages, a.B = (int)B, a.Tq = (int)Tq, a.Hq = (int)Hq, a.H = (int)H;
+    a.G = (int)(Hq / H), a.page_shift = shift, a.scale = sm_scale * 1.44269504088896341f;
+    const hipStream_t stream = (hipStream_t)hip_stream;
+    if (D == 128)
+        return code_type == QW3_CODES_E4M3 ? launch_cache_rows<128, true>(a, stream)
+                                           : launch_cache_rows<128, false>(a, stream);
+    return code_type == QW3_CODES_E4M3 ? launch_cache_rows<64, true>(a, stream)
+                                       : launch_cache_rows<64, false>(a, stream);
+}
+
+}  // extern "C"

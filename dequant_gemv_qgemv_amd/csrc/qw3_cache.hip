@@ -1,0 +1,213 @@
+// The quantised key/value cache: rows are quantised as they are written
+// (qcache_write) and read back dense (qcache_read).  C ABI in include/qw3.h.
+//
+// One row is what one token stores for one kv head: D channels x_d with one
+// fp32 scale s.  a = max |x_d|, s = a / L, c_d = rne(x_d / s), L = 127 for
+// int8 codes and 448 for e4m3; the row stands for c_d s.  Both divisions are
+// IEEE divisions in fp32, so the codes do not depend on how the work is laid
+// out.  Both operations do a few operations per byte and are bound by memory.
+#include "qw3_common.h"
+
+using namespace qw3_shared;
+
+namespace {
+
+typedef float f2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bfx2_t __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const f2_t f = {lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bfx2_t));
+}
+
+// ------------------------------------------------------------------ write --
+// A row is quantised by D / 8 lanes of one wave, 8 channels each; a wave holds
+// 64 / (D / 8) rows.  Rows run over (token, key or value, head), head fastest,
+// so a wave's loads are contiguous wherever the heads of a token are.
+template <int D, bool F32, bool E4M3>
+__global__ __launch_bounds__(256) void cache_write_kernel(const void *__restrict__ k, const void *__restrict__ v,
+                                                          const int64_t *__restrict__ slots,
+                                                          uint8_t *__restrict__ codes, float *__restrict__ scales,
+                                                          uint32_t rows, uint32_t H, int page_shift, int64_t n_slots,
+                                                          int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs) {
+    constexpr uint32_t kLanes = D / 8;
+    const uint32_t row = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
+    const uint32_t c = threadIdx.x % kLanes;
+    // every lane of a row takes the same branch, so the row's exchanges below stay whole
+    if (row >= rows) return;
+    const uint32_t t = row / (2 * H), wh = row - t * (2 * H), which = wh / H, h = wh - which * H;
+    const int64_t slot = slots[t];
+    if (slot < 0 || slot >= n_slots) return;
+    const int64_t at = which ? t * v_ts + h * v_hs : t * k_ts + h * k_hs;
+    float x[8];
+    if (F32) {
+        const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(which ? v : k) + at) + 2 * c;
+        const float4 a = src[0], b = src[1];
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+        const uint4 a = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(which ? v : k) + at)[c];
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    // |x| as bits orders like the value, with infinities and NaN on top
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+#pragma unroll
+    for (int m = kLanes / 2; m >= 1; m /= 2) top = max(top, (uint32_t)__shfl_xor((int)top, m, 64));
+    const bool finite = top < 0x7f800000u;
+    const float s = finite ? __uint_as_float(top) / (E4M3 ? 448.0f : 127.0f) : __uint_as_float(0x7fc00000u);
+    uint32_t out[2] = {0, 0};
+    if (s > 0.0f) {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // the quotient can pass L only where s is a denormal and a / L was rounded down
+            const float lim = E4M3 ? 448.0f : 127.0f;
+            y[i] = fminf(fmaxf(x[i] / s, -lim), lim);
+        }
+        if (E4M3) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i], y[4 * i + 1], 0, false);
+                out[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2], y[4 * i + 3], w, true);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) out[i / 4] |= ((uint32_t)(int)rintf(y[i]) & 0xffu) << (8 * (i % 4));
+        }
+    }
+    const int64_t page = slot >> page_shift;
+    const int64_t at_row = (((page * 2 + which) * H + h) << page_shift) + (slot - (page << page_shift));
+    reinterpret_cast<uint2 *>(codes + at_row * D)[c] = make_uint2(out[0], out[1]);
+    if (c == 0) scales[at_row] = s;
+}
+
+// ------------------------------------------------------------------- read --
+// A workgroup reads 16 consecutive rows of the packed output for every head,
+// of the keys or of the values; lanes run over a row's 16-byte pieces, then
+// over the tokens, so loads follow a page's tokens.
+template <int D, bool E4M3>
+__global__ __launch_bounds__(256) void cache_read_kernel(const uint8_t *__restrict__ codes,
+                                                         const float *__restrict__ scales,
+                                                         const int32_t *__restrict__ table,
+                                                         const int32_t *__restrict__ cu, uint16_t *__restrict__ k_out,
+                                                         uint16_t *__restrict__ v_out, int B, int64_t max_pages,
+                                                         int64_t pages, int64_t total, int H, int page_shift) {
+    constexpr int kPieces = D / 16;
+    const int lane = threadIdx.x & 63, which = blockIdx.y;
+    const int64_t t0 = (int64_t)blockIdx.x * 16;
+    // sequences that end at or before t0
+    int b = 0;
+    for (int base = 0; base < B; base += 64) {
+        const unsigned long long in = __ballot(base + lane < B && cu[base + lane + 1] <= t0);
+        b += __popcll(in);
+        if (in != ~0ull) break;
+    }
+    const int tok = (threadIdx.x / kPieces) & 15, piece = threadIdx.x % kPieces;
+    const int64_t t = t0 + tok;
+    while (b < B && cu[b + 1] <= t) ++b;
+    if (b >= B || t >= total) return;
+    const int64_t pos = t - cu[b], idx = pos >> page_shift;
+    if (pos < 0) return;
+    int64_t page = idx < max_pages ? table[b * max_pages + idx] : -1;
+    const bool there = page >= 0 && page < pages;
+    if (!there) page = 0;
+    const int64_t row0 = ((page * 2 + which) * H << page_shift) + (pos & ((int64_t(1) << page_shift) - 1));
+    uint16_t *out = (which ? v_out : k_out) + t * H * D + piece * 16;
+    for (int h = threadIdx.x / (16 * kPieces); h < H; h += 256 / (16 * kPieces)) {
+        const int64_t row = row0 + ((int64_t)h << page_shift);
+        uint4 c = make_uint4(0, 0, 0, 0);
+        float s = 0.0f;
+        if (there) {
+            c = *reinterpret_cast<const uint4 *>(codes + row * D + piece * 16);
+            s = scales[row];
+        }
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float f[4];
+            if (E4M3) {
+                f[0] = __builtin_amdgcn_cvt_f32_fp8(w[i], 0), f[1] = __builtin_amdgcn_cvt_f32_fp8(w[i], 1);
+                f[2] = __builtin_amdgcn_cvt_f32_fp8(w[i], 2), f[3] = __builtin_amdgcn_cvt_f32_fp8(w[i], 3);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = (float)(int8_t)(w[i] >> (8 * j));
+            }
+            o[2 * i] = pack_bf16(f[0] * s, f[1] * s);
+            o[2 * i + 1] = pack_bf16(f[2] * s, f[3] * s);
+        }
+        uint4 *dst = reinterpret_cast<uint4 *>(out + (int64_t)h * D);
+        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+qw3_status qcache_write(const void *k, const void *v, int32_t src_type, const int64_t *slots, void *codes,
+                        float *scales, int32_t code_type, int64_t T, int64_t H, int64_t D, int64_t pages,
+                        int64_t page_size, int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs, void *hip_stream) {
+    int shift = 0;
+    const qw3_status st = check_cache(code_type, H, D, pages, page_size, &shift);
+    if (st != QW3_OK) return st;
+    if (src_type != QW3_SRC_BF16 && src_type != QW3_SRC_F32) return QW3_ERR_SHAPE;
+    if (T < 0 || T * H > (int64_t(1) << 28)) return QW3_ERR_SHAPE;
+    if (T == 0 || pages == 0) return QW3_OK;
+    if (!k || !v || !slots || !codes || !scales) return QW3_ERR_NULL;
+    const int per = src_type == QW3_SRC_F32 ? 4 : 8;  // elements of 16 bytes
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(slots, 8) ||
+        k_ts % per || k_hs % per || v_ts % per || v_hs % per)
+        return QW3_ERR_ALIGN;
+    const uint32_t rows = (uint32_t)(T * 2 * H);
+    const dim3 grid((unsigned)ceil_div(rows, 256 / (D / 8)));
+    auto run = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, (hipStream_t)hip_stream, k, v, slots, (uint8_t *)codes, scales,
+                           rows, (uint32_t)H, shift, pages * page_size, k_ts, k_hs, v_ts, v_hs);
+    };
+    auto by_type = [&](auto d) {
+        constexpr int kD = decltype(d)::value;
+        if (src_type == QW3_SRC_F32)
+            code_type == QW3_CODES_E4M3 ? run(cache_write_kernel<kD, true, true>)
+                                        : run(cache_write_kernel<kD, true, false>);
+        else
+            code_type == QW3_CODES_E4M3 ? run(cache_write_kernel<kD, false, true>)
+                                        : run(cache_write_kernel<kD, false, false>);
+    };
+    D == 128 ? by_type(std::integral_constant<int, 128>{}) : by_type(std::integral_constant<int, 64>{});
+    return check_launch();
+}
+
+qw3_status qcache_read(const void *codes, const float *scales, int32_t code_type, const int32_t *block_table,
+                       const int32_t *cu, uint16_t *k_out, uint16_t *v_out, int64_t B, int64_t max_pages,
+                       int64_t total, int64_t H, int64_t D, int64_t pages, int64_t page_size, void *hip_stream) {
+    int shift = 0;
+    const qw3_status st = check_cache(code_type, H, D, pages, page_size, &shift);
+    if (st != QW3_OK) return st;
+    if (B < 0 || B > QW3_MAX_SEQS || max_pages < 0 || total < 0 || total >= (int64_t(1) << 31)) return QW3_ERR_SHAPE;
+    if (B == 0 || total == 0) return QW3_OK;
+    if (!cu || !k_out || !v_out || (max_pages > 0 && !block_table) || (pages > 0 && (!codes || !scales)))
+        return QW3_ERR_NULL;
+    if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(block_table, 4) || !aligned(cu, 4) ||
+        !aligned(k_out, 16) || !aligned(v_out, 16))
+        return QW3_ERR_ALIGN;
+    const dim3 grid((unsigned)ceil_div(total, 16), 2);
+    auto run = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, (hipStream_t)hip_stream, (const uint8_t *)codes, scales,
+                           block_table, cu, k_out, v_out, (int)B, max_pages, pages, total, (int)H, shift);
+    };
+    if (D == 128)
+        code_type == QW3_CODES_E4M3 ? run(cache_read_kernel<128, true>) : run(cache_read_kernel<128, false>);
+    else
+        code_type == QW3_CODES_E4M3 ? run(cache_read_kernel<64, true>) : run(cache_read_kernel<64, false>);
+    return check_launch();
+}
+
+}  // extern "C"

@@ -2,8 +2,10 @@
 // W3G128 fused dequantize-and-multiply for gfx950 (CDNA4): what every kernel
 // of the library (C ABI in include/qw3.h) shares -- the format, the decode,
 // the activation conversion and the exactness guard -- and the host helpers
-// its two translation units share (qw3_gemv.hip: the batch-1 kernels;
-// qw3.hip: everything else and the C ABI).
+// its translation units share (qw3_gemv.hip: the batch-1 kernels; qw3.hip:
+// the other products, the workspace and their C ABI; qw3_cache.hip and
+// qw3_attn.hip: the key/value cache and attention, which use only the host
+// helpers).
 //
 // Format (GSQ model card "Llama-3.1-70B-Instruct-3Bit-GSQ", "Storage layout"):
 // a row of K weights is a little-endian bitstream of 3K bits packed into 3K/32
@@ -559,6 +561,16 @@ inline qw3_status check_shape(int64_t N, int64_t K) {
     return QW3_OK;
 }
 
+// What every call on the quantised cache checks; *shift = log2(page_size).
+inline qw3_status check_cache(int32_t code_type, int64_t H, int64_t D, int64_t pages, int64_t page_size, int *shift) {
+    if (code_type != QW3_CODES_INT8 && code_type != QW3_CODES_E4M3) return QW3_ERR_SHAPE;
+    if (H < 1 || H > QW3_MAX_HEADS || (D != 64 && D != 128)) return QW3_ERR_SHAPE;
+    if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1)) != 0) return QW3_ERR_SHAPE;
+    if (pages < 0 || pages > 0x7fffffff) return QW3_ERR_SHAPE;
+    *shift = __builtin_ctzll((unsigned long long)page_size);
+    return QW3_OK;
+}
+
 inline std::mutex g_dev_mutex;  // guards the per-device tables
 inline int g_cu_count[64];
 
@@ -588,6 +600,9 @@ inline qw3_status blocks_per_cu(const void *kernel, int wgs, size_t lds, int *ou
     *out = nb > 0 ? nb : 1;
     return QW3_OK;
 }
+
+// Scratch of `stream` on the current device, at least `bytes` (qw3.hip).
+qw3_status workspace(hipStream_t stream, size_t bytes, void **out);
 
 // The batch-1 launches (qw3_gemv.hip).  launch_gemv: y = dequant(W) x for M
 // tokens, token m reading x + m K and writing y + m N (M > 1 only for the

@@ -236,6 +236,114 @@ qw3_status qgemm_w3g128_smallM_noalloc(const uint16_t *x, const int32_t *packed,
                                        const uint16_t *scales, float *y, int64_t M, int64_t N,
                                        int64_t K, void *hip_stream);
 
+/* ---------------------------------------------------------------------------
+ * The key/value cache and attention: what stands between the k/v/q projections
+ * and the o projection of a decoder layer.
+ *
+ * Cache.  Pages of `page_size` tokens (a power of two, 16..65536), shared by
+ * all sequences of a layer:
+ *   codes  [pages, 2, H, page_size, D]  one byte each, int8 or OCP e4m3
+ *   scales [pages, 2, H, page_size]     float32
+ * with index 0 of the second dimension the keys and 1 the values, H the number
+ * of kv heads and D = 64 or 128 channels.  A row (one token, one head) of D
+ * codes c_d and its scale s stand for the values c_d s.  Token n of a sequence
+ * lives at place n % page_size of page block_table[b][n / page_size]; slot =
+ * page * page_size + place names a place directly.
+ *
+ * Shared by the four calls:
+ *   - Strides (_ts: from token to token, _hs: from head to head) are in
+ *     elements; channels are contiguous.  So q, k and v may be views of one
+ *     fused projection output.  Strides are >= 0, and token strides of bf16
+ *     operands below 2^23.
+ *   - Alignment: 16 bytes for every array, except block tables, lengths and
+ *     starts (4) and slots and trees (8); strides are multiples of 16 bytes.
+ *     Otherwise QW3_ERR_ALIGN.
+ *   - Starts: cu[B + 1] with sequence b owning rows cu[b] .. cu[b + 1] - 1 of a
+ *     packed array.  Arrays of starts, lengths, tables, slots and trees are
+ *     read on the device: a call never waits for them.  Entries out of range
+ *     are clipped and never read or write out of bounds: a token whose page is
+ *     not in 0..pages-1 is not attended to and reads back as zeros.
+ *   - 1 <= B <= QW3_MAX_SEQS, at most QW3_MAX_TOKENS rows, QW3_MAX_HEADS heads,
+ *     Hq a multiple of H, sm_scale > 0 and finite, else QW3_ERR_SHAPE.  B or
+ *     the number of rows may be 0: no work.
+ *   - Rows of a packed output that belong to no sequence are not written.
+ *   - Deterministic and safe to capture, like the calls above.
+ * ------------------------------------------------------------------------ */
+enum { QW3_CODES_INT8 = 0, QW3_CODES_E4M3 = 1 }; /* code_type */
+enum { QW3_SRC_BF16 = 0, QW3_SRC_F32 = 1 };      /* src_type */
+#define QW3_MAX_SEQS 65536
+#define QW3_MAX_TOKENS (1 << 26)
+#define QW3_MAX_HEADS 1024
+
+/*
+ * qcache_write -- quantise the keys and values of T tokens and store them.
+ *   k, v  [T, H, D] bf16 or float32 (src_type), strided
+ *   slots [T] int64: where each token goes; an entry outside 0 ..
+ *         pages * page_size - 1 stores nothing (-1 for padding rows).  Slots
+ *         named twice hold one of the rows for each head, unspecified which.
+ * For each row, with a = max |x_d| and L = 127 (int8) or 448 (e4m3):
+ *   s = a / L (float32), c_d = x_d / s rounded to the nearest code, ties to even;
+ *   a = 0 gives s = 0 and c = 0.  A row that holds an infinity or NaN gets
+ *   s = NaN and c = 0, so that it stays visible as NaN to whoever attends to it.
+ * Float32 sources are the outputs of the products above as they are.
+ */
+qw3_status qcache_write(const void *k, const void *v, int32_t src_type, const int64_t *slots, void *codes,
+                        float *scales, int32_t code_type, int64_t T, int64_t H, int64_t D, int64_t pages,
+                        int64_t page_size, int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs,
+                        void *hip_stream);
+
+/*
+ * qcache_read -- read the first tokens of B sequences back dense.
+ *   block_table [B, max_pages] int32, cu [B + 1] int32: row cu[b] + n of the
+ *   outputs is token n of sequence b
+ *   k_out, v_out [total, H, D] bf16, written: RNE_bf16(c_d s)
+ * For a prompt that continues in chunks: the cached prefix comes back as the
+ * dense keys and values that qattn_prompt takes.
+ */
+qw3_status qcache_read(const void *codes, const float *scales, int32_t code_type, const int32_t *block_table,
+                       const int32_t *cu, uint16_t *k_out, uint16_t *v_out, int64_t B, int64_t max_pages,
+                       int64_t total, int64_t H, int64_t D, int64_t pages, int64_t page_size, void *hip_stream);
+
+/*
+ * qattn_cache -- attention of new tokens over the quantised cache.
+ *   q    [Tq, Hq, D] bf16, strided; query head h reads kv head h / (Hq / H)
+ *   lens [B] int32: tokens of each sequence in the cache, the new ones included
+ *   cu_q [B + 1] int32: the new tokens of each sequence; NULL: one each (Tq == B)
+ *   tree [Tq] int64 or NULL
+ *   out  [Tq, Hq, D] bf16, contiguous, written
+ * A sequence with n new tokens has them in the cache as its last n tokens
+ * (qcache_write comes first); the others are its context.  Row i of the n sees
+ * the whole context and
+ *   without tree: the new tokens 0..i;
+ *   with tree:    the new tokens j < 64 whose bit j is set in the row's word,
+ *                 for a tree of drafted tokens each row's ancestors and itself.
+ *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(sm_scale q.k_j - max_j)
+ * over what the row sees; a row that sees nothing gets zeros.  fp32 scores and
+ * sums; the weights p_j s_j are rounded to bf16 for the matrix unit.
+ * Workspace: up to 2 x 2 x CUs x 64 (D + 2) floats per stream (68 MB at most),
+ * by the rules of qgemm_w3g128_smallM.  max_pages * page_size <= 2^30.
+ */
+qw3_status qattn_cache(const uint16_t *q, const void *codes, const float *scales, int32_t code_type,
+                       const int32_t *block_table, const int32_t *lens, const int32_t *cu_q, const int64_t *tree,
+                       uint16_t *out, int64_t B, int64_t max_pages, int64_t Tq, int64_t Hq, int64_t H, int64_t D,
+                       int64_t pages, int64_t page_size, int64_t q_ts, int64_t q_hs, float sm_scale,
+                       void *hip_stream);
+
+/*
+ * qattn_prompt -- attention of whole prompts, packed sequences of any lengths.
+ *   q [Tq, Hq, D], k, v [Tk, H, D] bf16, strided; cu_q, cu_k [B + 1] int32
+ *   out [Tq, Hq, D] bf16, contiguous, written
+ * Row i of a sequence with nq queries and nk keys sees, with `causal`, the keys
+ * j <= i + nk - nq (the last query sees the last key, so that a chunk of a
+ * prompt attends to the whole prefix), else all nk keys.  Formula and empty
+ * rows as for qattn_cache.  A key that a row does not see has no influence on
+ * it, also where it holds an infinity or NaN.  No workspace.
+ */
+qw3_status qattn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *cu_q,
+                        const int32_t *cu_k, uint16_t *out, int64_t B, int64_t Tq, int64_t Tk, int64_t Hq,
+                        int64_t H, int64_t D, int64_t q_ts, int64_t q_hs, int64_t k_ts, int64_t k_hs, int64_t v_ts,
+                        int64_t v_hs, int32_t causal, float sm_scale, void *hip_stream);
+
 /* Text for a status code (static storage, never NULL). */
 const char *qstatus_str(qw3_status status);
 
