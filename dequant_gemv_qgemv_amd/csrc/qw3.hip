@@ -1410,7 +1410,9 @@ std::mutex g_ws_mutex;
 std::vector<Workspace> g_ws;
 std::vector<void *> g_ws_retired;  // superseded buffers, held until the process ends
 
-bool stream_capturing(hipStream_t stream) {
+}  // namespace
+
+bool qw3_shared::stream_capturing(hipStream_t stream) {
     hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
     if (hipStreamIsCapturing(stream, &cs) != hipSuccess) {
         (void)hipGetLastError();
@@ -1418,8 +1420,6 @@ bool stream_capturing(hipStream_t stream) {
     }
     return cs != hipStreamCaptureStatusNone;
 }
-
-}  // namespace
 
 qw3_status qw3_shared::workspace(hipStream_t stream, size_t bytes, void **out) {
     int dev = 0;

@@ -17,6 +17,8 @@
 // tiles in LDS through the transposing LDS reads.
 #include "qw3_common.h"
 
+#include <vector>
+
 using namespace qw3_shared;
 
 namespace {
@@ -26,6 +28,7 @@ typedef float f16_t __attribute__((ext_vector_type(16)));
 typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
 typedef short s4_t __attribute__((ext_vector_type(4)));
+typedef short s8_t __attribute__((ext_vector_type(8)));
 typedef int i2_t __attribute__((ext_vector_type(2)));
 typedef int i4_t __attribute__((ext_vector_type(4)));
 #define LDS_AS __attribute__((address_space(3)))
@@ -51,21 +54,36 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
 
 // A buffer descriptor over `bytes` bytes at p (both the same in every lane);
 // reads past the end give zeros.
-typedef __amdgpu_buffer_rsrc_t desc_t;
-__device__ __forceinline__ desc_t descriptor(const void *p, uint32_t bytes) {
-    void *at = reinterpret_cast<void *>(uniform(reinterpret_cast<int64_t>(p)));
-    return __builtin_amdgcn_make_buffer_rsrc(at, 0, uniform((int)bytes), 0x00020000);
+__device__ __forceinline__ i4_t descriptor(const void *p, uint32_t bytes) {
+    const int64_t a = uniform(reinterpret_cast<int64_t>(p));
+    return i4_t{(int)(uint32_t)a, (int)((uint32_t)((uint64_t)a >> 32) & 0xffffu), uniform((int)bytes), 0x00020000};
 }
 
 // 64 lanes x 16 bytes from memory straight into LDS: lane i's bytes land at
-// lds + 16 i.  The caller waits for vmcnt before it reads them.
-__device__ __forceinline__ void load_to_lds(const char *lds, uint32_t voffset, desc_t desc) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(desc, (LDS_AS void *)lds, 16, voffset, 0, 0, 0);
+// byte address lds + 16 i.  The caller waits for vmcnt before it reads them.  In
+// asm because the compiler, which cannot tell the buffers of a ring apart, would
+// wait for the newest load before every LDS read.  M0 carries the address;
+// nothing else in these kernels uses it.
+__device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t voffset, i4_t desc) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(voffset), "s"(desc)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+    return (uint32_t)uniform((int)reinterpret_cast<uintptr_t>((LDS_AS const char *)p));
 }
 
 __device__ __forceinline__ void wait_vm0() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ void wait_vm0_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// x plus the two bf16 of p.
+__device__ __forceinline__ float add_pair(uint32_t p, float x) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf2_t, p), __builtin_bit_cast(bf2_t, 0x3f803f80u), x, false);
+}
+
+// Over the lanes l and l ^ 32 (halves), or l, l ^ 16, l ^ 32, l ^ 48 (quarters).
 __device__ __forceinline__ float max_halves(float x) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
@@ -142,6 +160,14 @@ __device__ __forceinline__ void exact_row(const PromptArgs &a, const uint16_t *q
     }
 }
 
+// What row r of a V tile is exchanged by.  A transposing read takes 4 rows x 64
+// bytes for lanes 0..31 and the 4 rows behind for the others: the rows' 64-byte
+// pieces go to different banks, and the two halves to different 32 bytes.
+template <int D>
+__device__ __forceinline__ int value_place(int r) {
+    return (D == 128 ? (r & 3) << 2 : ((r >> 1) & 1) << 2) | (((r >> 2) & 1) << 1);
+}
+
 template <int D, bool CAUSAL>
 __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
     constexpr int kTileBytes = kKeys * D * 2;
@@ -201,30 +227,32 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
     // wave covers rows (4 i + wave) kRowsPerLoad ..., whose f does not depend on i.
     const int lrow = wave * kRowsPerLoad + lane / (kRowBytes / 16), lpiece = lane % (kRowBytes / 16);
     const int fk = D == 128 ? (lrow & 15) : ((lrow >> 1) & 7);
-    const int fv = D == 128 ? ((lrow & 7) << 1) : (((lrow >> 1) & 3) << 1);
+    const int fv = value_place<D>(lrow);
     uint32_t kvo[kLoads], vvo[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
         kvo[i] = (uint32_t)((lrow + 4 * kRowsPerLoad * i) * a.k_ts * 2 + (lpiece ^ fk) * 16);
         vvo[i] = (uint32_t)((lrow + 4 * kRowsPerLoad * i) * a.v_ts * 2 + (lpiece ^ fv) * 16);
     }
-    char *lds0 = lds + uniform(wave) * 1024;
-    auto fetch = [&](int t, int buf) {
-        const int64_t j0 = (int64_t)t * kKeys;
-        const int64_t kleft = (nk - 1 - j0) * a.k_ts * 2 + kRowBytes, vleft = (nk - 1 - j0) * a.v_ts * 2 + kRowBytes;
-        const desc_t dk = descriptor(kp + j0 * a.k_ts * 2, (uint32_t)min(kleft, (int64_t)0x7fffffff));
-        const desc_t dv = descriptor(vp + j0 * a.v_ts * 2, (uint32_t)min(vleft, (int64_t)0x7fffffff));
+    const uint32_t lds0 = lds_address(lds + wave * 1024);
+    auto fetch = [&](const char *base, const uint32_t (&vo)[kLoads], int64_t ts, int t, int which) {
+        const int64_t j0 = (int64_t)t * kKeys, left = (nk - 1 - j0) * ts * 2 + kRowBytes;
+        const i4_t d = descriptor(base + j0 * ts * 2, (uint32_t)min(left, (int64_t)0x7fffffff));
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) load_to_lds(lds0 + (2 * buf) * kTileBytes + i * 4096, kvo[i], dk);
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) load_to_lds(lds0 + (2 * buf + 1) * kTileBytes + i * 4096, vvo[i], dv);
+        for (int i = 0; i < kLoads; ++i) load_to_lds(lds0 + (2 * (t & 1) + which) * kTileBytes + i * 4096, vo[i], d);
+    };
+    auto fetch_k = [&](int t) {
+        if (t < ntiles) fetch(kp, kvo, a.k_ts, t, 0);
+    };
+    auto fetch_v = [&](int t) {
+        if (t < ntiles) fetch(vp, vvo, a.v_ts, t, 1);
     };
 
     // reads: K piece 2 t + half of row 32 kb + col; V^T through 4-row blocks
     const int xk = D == 128 ? (col & 15) : ((col >> 1) & 7);
     const uint32_t kbase = col * kRowBytes + ((half ^ (xk & 1)) << 4);
     const int vr = 4 * half + ((lane & 15) >> 2);
-    const int xv = D == 128 ? ((vr & 7) << 1) : (((vr >> 1) & 3) << 1);
+    const int xv = value_place<D>(vr);
     const int vsub = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
     const uint32_t vbase = vr * kRowBytes + ((vsub ^ (xv & 3)) << 4) + (lane & 1) * 8;
 
@@ -233,20 +261,34 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
     for (int i = 0; i < D / 32; ++i) acc[i] = f16_t{};
     float m = kNegInf, l = 0.0f;
 
-    auto compute = [&](int t, int buf, auto masked_c) {
-        constexpr bool kMasked = decltype(masked_c)::value;
-        const char *kt = lds + (2 * buf) * kTileBytes, *vt = lds + (2 * buf + 1) * kTileBytes;
-        f16_t s[2];
+    // scores of 4 of the D / 16 channel steps of a 32-key block
+    auto score_step = [&](f16_t &s, const char *kt, int kb, int i) {
+        const bf8_t kf = *reinterpret_cast<const bf8_t *>(kt + kb * 32 * kRowBytes + kbase + (((2 * i) ^ (xk & ~1)) << 4));
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[i], s, 0, 0, 0);
+    };
+    auto scores = [&](f16_t (&s)[2], int t) {
+        const char *kt = lds + (2 * (t & 1)) * kTileBytes;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             s[kb] = f16_t{};
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const bf8_t kf =
-                    *reinterpret_cast<const bf8_t *>(kt + kb * 32 * kRowBytes + kbase + (((2 * i) ^ (xk & ~1)) << 4));
-                s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[i], s[kb], 0, 0, 0);
-            }
+            for (int i = 0; i < D / 16; ++i) score_step(s[kb], kt, kb, i);
         }
+    };
+    auto value_step = [&](const char *vt, int u, int i, bf8_t pf) {
+        const char *at = vt + 16 * u * kRowBytes + vbase + (((4 * i) ^ (xv & ~3)) << 4);
+        const s4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS s4_t *)at);
+        const s4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS s4_t *)(at + 8 * kRowBytes));
+        const s8_t vv = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8_t, vv), pf, acc[i], 0, 0, 0);
+    };
+
+    // Softmax and values of tile t, whose scores are in s, and beside it the
+    // scores of tile t + 1 into s: the matrix unit works on one while the
+    // vector unit works on the other.
+    auto step = [&](f16_t (&s)[2], int t, auto masked_c, auto next_c) {
+        constexpr bool kMasked = decltype(masked_c)::value, kNext = decltype(next_c)::value;
+        const char *vt = lds + (2 * (t & 1) + 1) * kTileBytes, *kt = lds + (2 * ((t + 1) & 1)) * kTileBytes;
         if (kMasked) {
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
@@ -271,42 +313,58 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
             for (int i = 0; i < D / 32; ++i) acc[i] *= f;
         }
         const float ms = m == kNegInf ? 0.0f : m;
-        uint32_t p[2][8];
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const float p0 = exp2_fast(fmaf(s[kb][2 * r], a.scale, -ms));
-                const float p1 = exp2_fast(fmaf(s[kb][2 * r + 1], a.scale, -ms));
-                l += p0 + p1;
-                p[kb][r] = pack_bf16(p0, p1);
-            }
+        bf8_t pf[4];
+        f16_t n[2] = {f16_t{}, f16_t{}};
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const i4_t pu = {(int)p[u / 2][4 * (u & 1)], (int)p[u / 2][4 * (u & 1) + 1], (int)p[u / 2][4 * (u & 1) + 2],
-                             (int)p[u / 2][4 * (u & 1) + 3]};
-            const bf8_t pf = __builtin_bit_cast(bf8_t, pu);
+            uint32_t p[4];
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const char *at = vt + 16 * u * kRowBytes + vbase + (((4 * i) ^ (xv & ~3)) << 4);
-                const s4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS s4_t *)at);
-                const s4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS s4_t *)(at + 8 * kRowBytes));
-                typedef short s8_t __attribute__((ext_vector_type(8)));
-                const s8_t vv = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8_t, vv), pf, acc[i], 0, 0, 0);
+            for (int e = 0; e < 4; ++e) {
+                const float p0 = exp2_fast(fmaf(s[u / 2][8 * (u & 1) + 2 * e], a.scale, -ms));
+                const float p1 = exp2_fast(fmaf(s[u / 2][8 * (u & 1) + 2 * e + 1], a.scale, -ms));
+                p[e] = pack_bf16(p0, p1);
+                l = add_pair(p[e], l);
+            }
+            pf[u] = __builtin_bit_cast(bf8_t, i4_t{(int)p[0], (int)p[1], (int)p[2], (int)p[3]});
+            if (kNext && u < 2) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) score_step(n[u], kt, u, i);
+            } else if (u >= 2) {
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) value_step(vt, u - 2, i, pf[u - 2]);
             }
         }
+#pragma unroll
+        for (int u = 2; u < 4; ++u)
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) value_step(vt, u, i, pf[u]);
+        if (kNext) s[0] = n[0], s[1] = n[1];
     };
 
-    if (ntiles > 0) fetch(0, 0);
+    // The keys run one tile ahead of the values: iteration t reads V of tile t
+    // and K of t + 1 while V of t + 1 and K of t + 2 are on their way.
+    const int mine = live && whi >= 0 ? whi / kKeys + 1 : 0;  // tiles that a row of the wave sees
+    f16_t s[2];
+    fetch_k(0);
+    fetch_v(0);
+    wait_vm0_barrier();
+    // the compiler sees the queries arrive here: it does not know of the loads
+    // into LDS, and its waits for the queries inside the loop would wait for those
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) asm volatile("" : "+v"(qf[i]));
+    fetch_k(1);
+    if (mine > 0) scores(s, 0);
     for (int t = 0; t < ntiles; ++t) {
-        wait_vm0_barrier();  // tile t is here, and nobody reads the other buffer any more
-        if (t + 1 < ntiles) fetch(t + 1, (t + 1) & 1);
-        if (live && t * kKeys <= whi) {
+        wait_vm0_barrier();  // K of t + 1 and V of t are here; nobody reads what the next loads replace
+        fetch_k(t + 2);
+        fetch_v(t + 1);
+        if (t + 1 < mine) {
             if (t * kKeys + kKeys - 1 > wlo)
-                compute(t, t & 1, std::true_type{});
+                step(s, t, std::true_type{}, std::true_type{});
             else
-                compute(t, t & 1, std::false_type{});
+                step(s, t, std::false_type{}, std::true_type{});
+        } else if (t < mine) {
+            step(s, t, std::true_type{}, std::false_type{});
         }
     }
     if (!live) return;
@@ -347,7 +405,8 @@ struct CacheArgs {
     const int32_t *table, *lens, *cu_q;  // cu_q null: one row per sequence
     const uint64_t *tree;                // null: causal
     uint16_t *o;
-    float *part;
+    float *part;   // partial results
+    int *counts;   // workgroups that have finished with an item, by the first of them
     int64_t q_ts, q_hs, max_pages, pages;
     int B, Tq, Hq, H, G, page_shift, groups;
     float scale;
@@ -370,7 +429,7 @@ struct Seq {
         q0 = a.cu_q ? clamp_row(a.cu_q[b], a.Tq) : min(b, a.Tq);
         nq = (a.cu_q ? clamp_row(a.cu_q[b + 1], a.Tq) : min(b + 1, a.Tq)) - q0;
         nq = max(nq, 0);
-        len = (int)max((int64_t)0, min((int64_t)a.lens[b], a.max_pages << a.page_shift));
+        len = a.pages == 0 ? 0 : (int)max((int64_t)0, min((int64_t)a.lens[b], a.max_pages << a.page_shift));
         blocks = (int)(((int64_t)nq * a.G + R - 1) / R);
         per_item = max((len + (int64_t)kUnit - 1) / kUnit, (int64_t)1);
         units = per_item * blocks * a.H;
@@ -386,110 +445,226 @@ __device__ __forceinline__ int64_t wave_scan(int64_t x) {  // inclusive prefix s
     return x;
 }
 
-template <int R>
-__device__ __forceinline__ int64_t total_units(const CacheArgs &a) {
-    int64_t total = 0;
-    for (int base = 0; base < a.B; base += 64) {
-        const int b = base + (threadIdx.x & 63);
-        total += __shfl(wave_scan(b < a.B ? Seq<R>(a, b).units : 0), 63, 64);
-    }
-    return uniform(total);
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {  // of values >= 0, mostly below 2^32
+    return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
 }
 
-// The sequence that holds unit u, and the units before it.
+// A workgroup's run of units: [u, end) of the call's total, beginning in
+// sequence b, before which there are `before` units.
+struct Run {
+    int64_t per, u, end, before;
+    int b;
+};
 template <int R>
-__device__ __forceinline__ int find_unit(const CacheArgs &a, int64_t u, int64_t *before) {
+__device__ __forceinline__ Run find_run(const CacheArgs &a) {
+    const int lane = threadIdx.x & 63;
+    Run run;
+    int64_t total = 0, mine = 0, upto = 0;
+    for (int base = 0; base < a.B; base += 64) {
+        mine = base + lane < a.B ? Seq<R>(a, base + lane).units : 0;
+        upto = total + (a.B > 1 ? wave_scan(mine) : mine);
+        total = uniform((int64_t)__shfl(upto, min(63, a.B - 1 - base), 64));
+    }
+    run.per = max((total + a.groups - 1) / a.groups, (int64_t)1);
+    run.u = blockIdx.x * run.per;
+    run.end = min(run.u + run.per, total);
+    run.b = 0, run.before = 0;
+    if (run.u >= run.end || a.B == 1) return run;
     int64_t done = 0;
     for (int base = 0; base < a.B; base += 64) {
-        const int b = base + (threadIdx.x & 63);
-        const int64_t mine = b < a.B ? Seq<R>(a, b).units : 0;
-        const int64_t upto = done + wave_scan(mine);
-        const unsigned long long past = __ballot(upto > u);
+        if (a.B > 64) {
+            mine = base + lane < a.B ? Seq<R>(a, base + lane).units : 0;
+            upto = done + wave_scan(mine);
+        }
+        const unsigned long long past = __ballot(upto > run.u);
         if (past) {
             const int at = __builtin_ctzll(past);
-            *before = uniform((int64_t)__shfl(upto - mine, at, 64));
-            return base + at;
+            run.b = uniform(base + at);
+            run.before = uniform((int64_t)__shfl(upto - mine, at, 64));
+            break;
         }
-        done = __shfl(upto, 63, 64);
+        done = uniform((int64_t)__shfl(upto, 63, 64));
     }
-    return -1;
+    return run;
 }
 
-__device__ __forceinline__ int64_t units_per_group(int64_t total, int groups) {
-    return max((total + groups - 1) / groups, (int64_t)1);
-}
-
-// Partial results: two slots for each workgroup (its first and its last item
-// may be shared with others); a slot is R maxima, R sums, R x D weighted sums.
+// Partial results.  An item that several workgroups worked on is joined by the
+// one that finishes last.  A slot holds R maxima, R sums and R x D weighted
+// sums; a workgroup has two, for its first and its last item (those between are
+// its own).  Slots are written and read by atomic 8-byte accesses of agent
+// scope, which go past the per-XCD L2s, so no cache has to be flushed; every
+// thread's stores are complete (vmcnt 0) before its workgroup counts itself.
+// The count belongs to the first workgroup of the item, and the joining
+// workgroup sets it back to zero for the next call.
 template <int R, int D>
 __device__ __forceinline__ float *partial(const CacheArgs &a, int64_t group, int which) {
     return a.part + (group * 2 + which) * (int64_t)(R * (D + 2));
 }
-
-// Eight codes to eight bf16, exact in both types.
-template <bool E4M3>
-__device__ __forceinline__ bf8_t decode8(uint32_t lo, uint32_t hi) {
-    bf8_t r;
-    const uint32_t w[2] = {lo, hi};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (E4M3) {
-            const bf2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], 1.0f, false);
-            const bf2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], 1.0f, true);
-            r[4 * i] = a[0], r[4 * i + 1] = a[1], r[4 * i + 2] = b[0], r[4 * i + 3] = b[1];
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) r[4 * i + j] = (__bf16)(float)(int8_t)(w[i] >> (8 * j));
-        }
-    }
-    return r;
+__device__ __forceinline__ void store_agent(float *p, float x, float y) {
+    const uint64_t v = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
+    __hip_atomic_store(reinterpret_cast<uint64_t *>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 load_agent(const float *p) {
+    const uint64_t v =
+        __hip_atomic_load(reinterpret_cast<const uint64_t *>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
 }
 
-// R: query rows of an item (16, 32 or 64).  Every wave takes all R rows and 32
-// of the unit's keys, with a ring of two such steps of its own in LDS, so the
-// waves meet only at the end of an item.
+// Row r of an item, from the partial results of workgroups first..last in that
+// order; one wave.  `from` is the first one's slot, the others' are their first.
+// Maxima and sums are stored as pairs (m, l).
+template <int R, int D>
+__device__ __forceinline__ void join_row(const CacheArgs &a, const float *from, int first, int last, int r,
+                                         uint16_t *out) {
+    const int lane = threadIdx.x & 63;
+    constexpr int kBatch = 8;
+    const int at = 2 * R + r * D + (D == 128 ? 2 * lane : lane & ~1);
+    float m = kNegInf, l = 0.0f, acc0 = 0.0f, acc1 = 0.0f;
+    for (int g0 = first; g0 <= last; g0 += 64) {
+        const int n = min(64, last + 1 - g0);
+        auto slot = [&](int i) { return g0 + i == first ? from : partial<R, D>(a, g0 + i, 0); };
+        float2 ml = make_float2(kNegInf, 0.0f);
+        if (lane < n) ml = load_agent(slot(lane) + 2 * r);
+        float m1 = ml.x;
+        for (int x = 32; x >= 1; x /= 2) m1 = fmaxf(m1, __shfl_xor(m1, x, 64));
+        m1 = fmaxf(m, m1);
+        const float old = m == kNegInf ? 0.0f : exp2_fast(m - m1);
+        const float f = ml.x == kNegInf ? 0.0f : exp2_fast(ml.x - m1);
+        float ls = f * ml.y;
+        for (int x = 32; x >= 1; x /= 2) ls += __shfl_xor(ls, x, 64);
+        m = m1;
+        l = l * old + ls;
+        acc0 *= old, acc1 *= old;
+        for (int i0 = 0; i0 < n; i0 += kBatch) {
+            float2 part[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) part[i] = load_agent(slot(min(i0 + i, n - 1)) + at);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const float fi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), min(i0 + i, n - 1)));
+                if (i0 + i < n) acc0 += fi * part[i].x, acc1 += fi * part[i].y;
+            }
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    if (D == 128)
+        *reinterpret_cast<uint32_t *>(out + 2 * lane) = pack_bf16(acc0 * inv, acc1 * inv);
+    else
+        out[lane] = (uint16_t)(pack_bf16((lane & 1 ? acc1 : acc0) * inv, 0.0f) & 0xffffu);
+}
+
+// Byte J of w, signed, as float.
+template <int J>
+__device__ __forceinline__ float byte_f32(uint32_t w) {
+    float f;
+    if (J == 0) asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0" : "=v"(f) : "v"(w));
+    if (J == 1) asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1" : "=v"(f) : "v"(w));
+    if (J == 2) asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2" : "=v"(f) : "v"(w));
+    if (J == 3) asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3" : "=v"(f) : "v"(w));
+    return f;
+}
+
+// Four codes to four bf16 (two words), exact in both types.
+template <bool E4M3>
+__device__ __forceinline__ uint2 decode4(uint32_t w) {
+    if (E4M3)
+        return make_uint2(
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true)));
+    return make_uint2(pack_bf16(byte_f32<0>(w), byte_f32<1>(w)), pack_bf16(byte_f32<2>(w), byte_f32<3>(w)));
+}
+template <bool E4M3>
+__device__ __forceinline__ bf8_t decode8(uint32_t lo, uint32_t hi) {
+    const uint2 a = decode4<E4M3>(lo), b = decode4<E4M3>(hi);
+    return __builtin_bit_cast(bf8_t, i4_t{(int)a.x, (int)a.y, (int)b.x, (int)b.y});
+}
+
+// Few rows: R = 16 or 32 query rows of an item.  Every wave takes all R rows
+// and 32 of the unit's keys; codes and scales go from memory to registers a
+// step ahead, K's straight as the matrix unit's operand, V's through a tile of
+// the wave's own in LDS that turns them.  The waves meet only at the end of an
+// item.
 template <int D, bool E4M3, int R>
-__global__ __launch_bounds__(256, R == 64 ? 1 : 2) void attn_cache_kernel(CacheArgs a) {
-    constexpr int kN = R / 16;              // blocks of 16 rows
-    constexpr int kStage = 2 * 32 * D;      // bytes of a step: 32 rows of K, 32 of V
-    constexpr int kCols = R == 16 ? D : R == 32 ? 64 : 32;  // channels joined at a time
+__global__ __launch_bounds__(256, R == 16 ? 3 : 2) void attn_few_kernel(CacheArgs a) {
+    constexpr int kN = R / 16;                   // blocks of 16 rows
+    constexpr int kCols = R == 16 ? D : 64;      // channels joined at a time
     constexpr int kPad = kCols + 4;
-    constexpr int kRing = 4 * 2 * kStage, kJoin = 4 * R * kPad * 4;
-    __shared__ __attribute__((aligned(1024))) char lds[kRing > kJoin ? kRing : kJoin];
+    constexpr int kTurn = 4 * 32 * D, kJoin = 4 * R * kPad * 4;
+    __shared__ __attribute__((aligned(1024))) char lds[kTurn > kJoin ? kTurn : kJoin];
     __shared__ float stat[2][4][R];
+    __shared__ int arrived;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), quarter = lane >> 4, col = lane & 15;
 
-    const int64_t total = total_units<R>(a), per = units_per_group(total, a.groups);
-    int64_t u = blockIdx.x * per;
-    const int64_t uend = min(u + per, total);
-    if (u >= uend) return;
-    int64_t before = 0;
-    int b = uniform(find_unit<R>(a, u, &before));
-    Seq<R> seq(a, b);
+    Run run = find_run<R>(a);
+    if (run.u >= run.end) return;
+    Seq<R> seq(a, run.b);
 
-    // lane's place in the LDS rows (see attn_prompt_kernel): D-byte rows, piece c of row r at c ^ f(r)
-    constexpr int kPieces = D / 16;
-    const int frow = lane / kPieces;  // row within a load of 1 KB
-    uint32_t vo[D / 64];
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-        const int r = frow + i * (64 / kPieces);
-        const int f = D == 128 ? ((r >> 1) & 7) : ((r >> 2) & 3);
-        vo[i] = (uint32_t)(r * D + ((lane % kPieces) ^ f) * 16);
-    }
-    char *ring = lds + wave * 2 * kStage;
-    const int xk = D == 128 ? ((col >> 1) & 7) : ((col >> 2) & 3);
+    constexpr int kPieces = D / 16, kVLoads = D / 32;
+    // V tile: row r, 16-byte piece c at place c ^ f(r), so that the turning reads spread over the banks
+    char *turn = lds + wave * 32 * D;
+    auto place = [](int r) { return D == 128 ? (r >> 1) & 7 : (r >> 2) & 3; };
+    const int vrow = lane / kPieces, vpiece = lane % kPieces;
 
-    while (u < uend) {
-        while (u - before >= seq.units) {  // next sequence (some have no rows)
-            before += seq.units;
-            ++b;
-            seq = Seq<R>(a, b);
+    struct Stage {
+        uint4 k[2][D / 64], v[kVLoads];
+        float4 ks[2], vs[2];
+    };
+
+    while (run.u < run.end) {
+        while (run.u - run.before >= seq.units) {  // next sequence (some have no rows)
+            run.before += seq.units;
+            ++run.b;
+            seq = Seq<R>(a, run.b);
         }
-        const int64_t local = u - before, item = local / seq.per_item;
-        const int64_t t0 = local - item * seq.per_item, t1 = min(seq.per_item, t0 + (uend - u));
-        const int h = (int)(item / seq.blocks), block = (int)(item - (int64_t)h * seq.blocks);
+        const int64_t local = run.u - run.before, item = quotient(local, seq.per_item);
+        const int64_t t0 = local - item * seq.per_item, t1 = min(seq.per_item, t0 + (run.end - run.u));
+        const int h = (int)quotient(item, seq.blocks), block = (int)(item - (int64_t)h * seq.blocks);
         const int rows = seq.nq * a.G, r0 = block * R, len = seq.len, ctx = len - seq.nq;
+
+        // the wave's keys: 32 from key0 + 128 s in step s
+        const int key0 = (int)t0 * kUnit + 32 * wave;
+        const int64_t room = (int64_t)len - key0;
+        const int steps = room <= 0 ? 0 : (int)min((int64_t)(t1 - t0), (room + kUnit - 1) / kUnit);
+
+        // pages of 32 steps: lane 2 s + g has the one of group g (16 keys) of step s
+        const int32_t *table = a.table + (int64_t)run.b * a.max_pages;
+        auto pages_of = [&](int s) {
+            const int pos = min(key0 + (s + (lane >> 1)) * kUnit + 16 * (lane & 1), len - 1);
+            return table[pos >> a.page_shift];
+        };
+        int ids = 0, ids_next = 0;
+        if (steps > 0) {
+            ids = pages_of(0);
+            if (steps > 32) ids_next = pages_of(32);
+        }
+        int ids_base = 0;
+        const int64_t page_rows = (int64_t)(2 * a.H) << a.page_shift, head_row = (int64_t)h << a.page_shift;
+        const int64_t to_v = (int64_t)a.H << a.page_shift;
+        auto page_of = [&](int s, int g) { return __builtin_amdgcn_readlane(ids, 2 * (s - ids_base) + g); };
+        Stage st;
+        auto fetch = [&](int s) {
+            const int key = key0 + s * kUnit;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                // a group past the end reads the last key's, a page that does not exist page 0: hidden below
+                const int pos = min(key + 16 * g, (len - 1) & ~15);
+                int page = page_of(s, g);
+                page = (uint32_t)page < (uint64_t)a.pages ? page : 0;
+                const int64_t row = page * page_rows + head_row + (pos & ((1 << a.page_shift) - 1));
+                const uint8_t *kp = a.codes + row * D, *vp = kp + to_v * D;
+                const float *sp = a.scales + row;
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    st.k[g][c] = *reinterpret_cast<const uint4 *>(kp + (uint32_t)(col * D + (quarter + 4 * c) * 16));
+#pragma unroll
+                for (int c = 0; c < kVLoads / 2; ++c)
+                    st.v[g * (kVLoads / 2) + c] = *reinterpret_cast<const uint4 *>(vp + (uint32_t)(c * 1024 + lane * 16));
+                st.ks[g] = *reinterpret_cast<const float4 *>(sp + (uint32_t)(4 * quarter));
+                st.vs[g] = *reinterpret_cast<const float4 *>(sp + to_v + (uint32_t)(4 * quarter));
+            }
+        };
+
+        if (steps > 0) fetch(0);
 
         // the rows' queries, as B operands with the channels in the order of K's pieces
         bf8_t qf[kN][D / 32];
@@ -515,58 +690,32 @@ __global__ __launch_bounds__(256, R == 64 ? 1 : 2) void attn_cache_kernel(CacheA
             for (int i = 0; i < D / 16; ++i) acc[x][i] = f4_t{};
         }
 
-        const int key0 = (int)t0 * kUnit + 32 * wave;
-        // steps of this wave: keys key0 + 128 s
-        const int64_t room = (int64_t)len - key0;
-        const int steps = room <= 0 ? 0 : (int)min((int64_t)(t1 - t0), (room + kUnit - 1) / kUnit);
-        // of the step to come: the scales of keys 4 quarter + r of its two 16-key
-        // groups, and whether a group's page does not exist (its keys are hidden)
-        float4 ks[2], vs[2];
-        bool none[2];
-        auto fetch = [&](int s, int buf) {
+        auto step = [&](int s, auto fetch_c) {
             const int key = key0 + s * kUnit;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const int pos = key + 16 * g;
-                const int idx = pos >> a.page_shift, in = pos & ((1 << a.page_shift) - 1);
-                const int page = pos < len ? uniform(a.table[(int64_t)b * a.max_pages + idx]) : -1;
-                const bool there = page >= 0 && page < a.pages;
-                const int64_t row = ((((int64_t)(there ? page : 0) * 2) * a.H + h) << a.page_shift) + in;
-                const int64_t vrow = row + ((int64_t)a.H << a.page_shift);
-                const uint32_t bytes = there ? (uint32_t)(min(16, len - pos) * D) : 0;
-                const desc_t dk = descriptor(a.codes + row * D, bytes), dv = descriptor(a.codes + vrow * D, bytes);
-#pragma unroll
-                for (int i = 0; i < D / 64; ++i) {
-                    load_to_lds(ring + buf * kStage + g * 16 * D + i * 1024, vo[i], dk);
-                    load_to_lds(ring + buf * kStage + (32 + g * 16) * D + i * 1024, vo[i], dv);
-                }
-                ks[g] = vs[g] = make_float4(0, 0, 0, 0);
-                none[g] = !there;
-                if (there) {
-                    ks[g] = *reinterpret_cast<const float4 *>(a.scales + row + 4 * quarter);
-                    vs[g] = *reinterpret_cast<const float4 *>(a.scales + vrow + 4 * quarter);
-                }
-            }
-        };
-
-        if (steps > 0) fetch(0, 0);
-        for (int s = 0; s < steps; ++s) {
-            wait_vm0();
-            float kc[2][4], vc[2][4];
             bool gone[2];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                asm volatile("" : "+v"(ks[g].x), "+v"(ks[g].y), "+v"(ks[g].z), "+v"(ks[g].w));
-                asm volatile("" : "+v"(vs[g].x), "+v"(vs[g].y), "+v"(vs[g].z), "+v"(vs[g].w));
-                gone[g] = none[g];
-                kc[g][0] = ks[g].x * a.scale, kc[g][1] = ks[g].y * a.scale;
-                kc[g][2] = ks[g].z * a.scale, kc[g][3] = ks[g].w * a.scale;
-                vc[g][0] = vs[g].x, vc[g][1] = vs[g].y, vc[g][2] = vs[g].z, vc[g][3] = vs[g].w;
+            for (int g = 0; g < 2; ++g) gone[g] = (uint32_t)page_of(s, g) >= (uint64_t)a.pages;
+            const bool masked = key + 31 >= min(ctx, len) || gone[0] || gone[1];
+            // V's codes into the turning tile
+#pragma unroll
+            for (int c = 0; c < kVLoads; ++c) {
+                const int r = vrow + c * (64 / kPieces);
+                uint4 w = st.v[c];
+                // p = 0 hides a row only if its codes are numbers: e4m3 garbage may be NaN
+                if (E4M3 && masked && (key + r >= len || gone[c / (kVLoads / 2)])) w = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(turn + r * D + ((vpiece ^ place(r)) << 4)) = w;
             }
-            if (s + 1 < steps) fetch(s + 1, (s + 1) & 1);
-            const char *kt = ring + (s & 1) * kStage, *vt = kt + 32 * D;
-            const int key = key0 + s * kUnit;
-
+            float kc[2][4], vc[2][4];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                kc[g][0] = st.ks[g].x * a.scale, kc[g][1] = st.ks[g].y * a.scale;
+                kc[g][2] = st.ks[g].z * a.scale, kc[g][3] = st.ks[g].w * a.scale;
+                vc[g][0] = st.vs[g].x, vc[g][1] = st.vs[g].y, vc[g][2] = st.vs[g].z, vc[g][3] = st.vs[g].w;
+                // copies, so that the next step's loads land in the same registers and
+                // are not waited for at the end of this one
+#pragma unroll
+                for (int r = 0; r < 4; ++r) asm volatile("" : "+v"(vc[g][r]));
+            }
             f4_t sc[kN][2];
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
@@ -574,8 +723,7 @@ __global__ __launch_bounds__(256, R == 64 ? 1 : 2) void attn_cache_kernel(CacheA
                 for (int x = 0; x < kN; ++x) sc[x][g] = f4_t{};
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(kt + (16 * g + col) * D +
-                                                                     (((quarter + 4 * c) ^ xk) << 4));
+                    const uint4 w = st.k[g][c];
                     const bf8_t k0 = decode8<E4M3>(w.x, w.y), k1 = decode8<E4M3>(w.z, w.w);
 #pragma unroll
                     for (int x = 0; x < kN; ++x) {
@@ -584,7 +732,13 @@ __global__ __launch_bounds__(256, R == 64 ? 1 : 2) void attn_cache_kernel(CacheA
                     }
                 }
             }
-            const bool masked = key + 31 >= min(ctx, len) || gone[0] || gone[1];
+            if (decltype(fetch_c)::value) {
+                if (s + 1 == ids_base + 32) {
+                    ids = ids_next, ids_base += 32;
+                    if (ids_base + 32 < steps) ids_next = pages_of(ids_base + 32);
+                }
+                fetch(s + 1);
+            }
             bf8_t pf[kN];
 #pragma unroll
             for (int x = 0; x < kN; ++x) {
@@ -636,18 +790,19 @@ __global__ __launch_bounds__(256, R == 64 ? 1 : 2) void attn_cache_kernel(CacheA
                 pf[x] = __builtin_bit_cast(bf8_t, i4_t{(int)p[0], (int)p[1], (int)p[2], (int)p[3]});
             }
             // V^T: keys 4 quarter + 0..3 and 16 + 4 quarter + 0..3 of 16 channels
-            const int vkey = 4 * quarter + ((col >> 1) & 3) + 16 * (col >> 3);
-            const int xv = D == 128 ? ((vkey >> 1) & 7) : ((vkey >> 2) & 3);
-            const char *vrow = vt + vkey * D + (col & 1) * 8;
+            const int vkey = 4 * quarter + ((col >> 1) & 3) + 16 * (col >> 3), xv = place(vkey);
+            const char *from = turn + vkey * D + (col & 1) * 8;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
-                const i2_t w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS_AS i2_t *)(vrow + ((i ^ xv) << 4)));
+                const i2_t w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS_AS i2_t *)(from + ((i ^ xv) << 4)));
                 const bf8_t vf = decode8<E4M3>((uint32_t)w[0], (uint32_t)w[1]);
 #pragma unroll
                 for (int x = 0; x < kN; ++x)
                     acc[x][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[x], acc[x][i], 0, 0, 0);
             }
-        }
+        };
+        for (int s = 0; s + 1 < steps; ++s) step(s, std::true_type{});
+        if (steps > 0) step(steps - 1, std::false_type{});
 
         // join the four waves
 #pragma unroll
@@ -656,11 +811,11 @@ __global__ __launch_bounds__(256, R == 64 ? 1 : 2) void attn_cache_kernel(CacheA
             if (quarter == 0) stat[0][wave][16 * x + col] = m[x], stat[1][wave][16 * x + col] = l[x];
         }
         const bool whole = t1 - t0 == seq.per_item;
-        float *out = whole ? nullptr : partial<R, D>(a, blockIdx.x, u == blockIdx.x * per ? 0 : 1);
+        float *out = partial<R, D>(a, blockIdx.x, run.u == blockIdx.x * run.per ? 0 : 1);
         float *join = reinterpret_cast<float *>(lds);
 #pragma unroll
         for (int c0 = 0; c0 < D; c0 += kCols) {
-            __syncthreads();  // the ring, or the channels before, are read
+            __syncthreads();  // the turning tiles, or the channels before, are read
 #pragma unroll
             for (int x = 0; x < kN; ++x)
 #pragma unroll
@@ -668,7 +823,7 @@ __global__ __launch_bounds__(256, R == 64 ? 1 : 2) void attn_cache_kernel(CacheA
                     *reinterpret_cast<f4_t *>(join + (wave * R + 16 * x + col) * kPad + 16 * i + 4 * quarter) =
                         acc[x][c0 / 16 + i];
             __syncthreads();
-            for (int e = tid; e < R * kCols / 4; e += 256) {
+            for (int e = tid; e < min(R, rows - r0) * kCols / 4; e += 256) {
                 const int r = e / (kCols / 4), c = 4 * (e % (kCols / 4));
                 float mm = kNegInf;
 #pragma unroll
@@ -681,100 +836,61 @@ __global__ __launch_bounds__(256, R == 64 ? 1 : 2) void attn_cache_kernel(CacheA
                     ll += f * stat[1][w][r];
                     sum += f * *reinterpret_cast<const f4_t *>(join + (w * R + r) * kPad + c);
                 }
-                if (r0 + r >= rows) continue;
                 if (whole) {
                     const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
                     const int i = (r0 + r) / a.G, g = r0 + r - i * a.G;
                     *reinterpret_cast<uint2 *>(a.o + ((int64_t)(seq.q0 + i) * a.Hq + h * a.G + g) * D + c0 + c) =
                         make_uint2(pack_bf16(sum[0] * inv, sum[1] * inv), pack_bf16(sum[2] * inv, sum[3] * inv));
                 } else {
-                    *reinterpret_cast<f4_t *>(out + 2 * R + r * D + c0 + c) = sum;
-                    if (c0 == 0 && c == 0) out[r] = mm, out[R + r] = ll;
+                    store_agent(out + 2 * R + r * D + c0 + c, sum[0], sum[1]);
+                    store_agent(out + 2 * R + r * D + c0 + c + 2, sum[2], sum[3]);
+                    if (c0 == 0 && c == 0) store_agent(out + 2 * r, mm, ll);
                 }
             }
         }
-        __syncthreads();
-        u += t1 - t0;
-    }
-}
-
-// Joins the partial results of the items that more than one workgroup worked
-// on, in the workgroups' order: one wave per query row and head.
-template <int D, int R>
-__global__ __launch_bounds__(256) void attn_cache_join_kernel(CacheArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);  // (token, head)
-    const int tok = uniform((int)(at / a.Hq)), head = uniform((int)(at % a.Hq));
-    if (tok >= a.Tq) return;
-    const int64_t total = total_units<R>(a), per = units_per_group(total, a.groups);
-    // the token's sequence, and the units before it
-    int b = -1;
-    int64_t before = 0;
-    for (int base = 0; base < a.B; base += 64) {
-        const int c = base + lane;
-        Seq<R> s;
-        s.q0 = 0, s.nq = 0, s.units = 0;
-        if (c < a.B) s = Seq<R>(a, c);
-        const int64_t upto = before + wave_scan(s.units);
-        const unsigned long long in = __ballot(tok >= s.q0 && tok < s.q0 + s.nq);
-        if (in) {
-            const int w = __builtin_ctzll(in);
-            b = uniform(base + w);
-            before = uniform((int64_t)__shfl(upto - s.units, w, 64));
-            break;
+        if (!whole) {
+            const int64_t ustart = run.u - t0;
+            const int first = (int)(ustart / run.per), last = (int)((ustart + seq.per_item - 1) / run.per);
+            wait_vm0();
+            __syncthreads();
+            if (tid == 0)
+                arrived = __hip_atomic_fetch_add(a.counts + first, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __syncthreads();
+            if (uniform(arrived) == last - first) {
+                for (int r = wave; r < min(R, rows - r0); r += 4) {
+                    const int i = (r0 + r) / a.G, g = r0 + r - i * a.G;
+                    join_row<R, D>(a, partial<R, D>(a, first, first * run.per >= ustart ? 0 : 1), first, last, r,
+                                   a.o + ((int64_t)(seq.q0 + i) * a.Hq + h * a.G + g) * D);
+                }
+                if (tid == 0) __hip_atomic_store(a.counts + first, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
         }
-        before = uniform((int64_t)__shfl(upto, 63, 64));
+        __syncthreads();
+        run.u += t1 - t0;
     }
-    if (b < 0) return;
-    const Seq<R> seq(a, b);
-    const int h = head / a.G, r = (tok - seq.q0) * a.G + head - h * a.G;
-    const int64_t ustart = before + ((int64_t)h * seq.blocks + r / R) * seq.per_item, uend = ustart + seq.per_item;
-    const int64_t first = ustart / per, last = (uend - 1) / per;
-    if (first == last) return;  // its workgroup wrote the output
-    constexpr int kPer = D / 64;
-    float m = kNegInf, l = 0.0f, acc[kPer] = {};
-    for (int64_t w = first; w <= last; ++w) {
-        const float *p = partial<R, D>(a, w, w * per >= ustart ? 0 : 1);
-        const float pm = p[r % R], pl = p[R + r % R];
-        if (pm == kNegInf) continue;
-        const float m1 = fmaxf(m, pm), f = exp2_fast(m - m1), g = exp2_fast(pm - m1);
-        m = m1;
-        l = l * f + pl * g;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) acc[i] = acc[i] * f + p[2 * R + (r % R) * D + lane * kPer + i] * g;
-    }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint16_t *o = a.o + (int64_t)at * D + lane * kPer;
-    if (kPer == 2)
-        *reinterpret_cast<uint32_t *>(o) = pack_bf16(acc[0] * inv, acc[kPer - 1] * inv);
-    else
-        *o = (uint16_t)(pack_bf16(acc[0] * inv, 0.0f) & 0xffffu);
 }
 
 template <int D, bool E4M3, int R>
-qw3_status launch_cache(CacheArgs a, hipStream_t stream) {
+qw3_status launch_few(CacheArgs a, hipStream_t stream) {
     int cus = 0;
     qw3_status st = cu_count(&cus);
     if (st != QW3_OK) return st;
-    a.groups = cus * (R == 64 ? 1 : 2);
+    a.groups = cus * (R == 16 ? 3 : 2);
     void *ws = nullptr;
     st = workspace(stream, (size_t)a.groups * 2 * R * (D + 2) * sizeof(float), &ws);
     if (st != QW3_OK) return st;
     a.part = static_cast<float *>(ws);
-    hipLaunchKernelGGL((attn_cache_kernel<D, E4M3, R>), dim3(a.groups), dim3(256), 0, stream, a);
-    st = check_launch();
+    st = counters(stream, a.groups, &a.counts);
     if (st != QW3_OK) return st;
-    hipLaunchKernelGGL((attn_cache_join_kernel<D, R>), dim3((unsigned)ceil_div((int64_t)a.Tq * a.Hq, 4)), dim3(256), 0,
-                       stream, a);
+    hipLaunchKernelGGL((attn_few_kernel<D, E4M3, R>), dim3(a.groups), dim3(256), 0, stream, a);
     return check_launch();
 }
 
 template <int D, bool E4M3>
 qw3_status launch_cache_rows(const CacheArgs &a, hipStream_t stream) {
     const int64_t rows = ceil_div(a.Tq, a.B) * a.G;  // of a sequence, on average
-    if (rows <= 16) return launch_cache<D, E4M3, 16>(a, stream);
-    if (rows <= 32) return launch_cache<D, E4M3, 32>(a, stream);
-    return launch_cache<D, E4M3, 64>(a, stream);
+    if (rows <= 16) return launch_few<D, E4M3, 16>(a, stream);
+    return launch_few<D, E4M3, 32>(a, stream);
 }
 
 bool strides_ok(int64_t ts, int64_t hs) { return ts >= 0 && hs >= 0 && ts < (1 << 23) && hs < (int64_t(1) << 40); }
@@ -786,6 +902,43 @@ qw3_status check_heads(int64_t Hq, int64_t H) {
 bool scale_ok(float s) { return s > 0.0f && s < __builtin_huge_valf(); }
 
 }  // namespace
+
+// One buffer per (device, stream handle), cleared by the first call on the
+// stream and never grown: kMaxCounts is more than any grid that counts.
+namespace {
+constexpr int kMaxCounts = 4096;
+struct Counters {
+    int dev;
+    hipStream_t stream;
+    int *ptr;
+};
+std::mutex g_counters_mutex;
+std::vector<Counters> g_counters;
+__global__ void clear_counts_kernel(int *p) { p[blockIdx.x * 256 + threadIdx.x] = 0; }
+}  // namespace
+
+qw3_status qw3_shared::counters(hipStream_t stream, int n, int **out) {
+    if (n > kMaxCounts) return hip_fail(hipErrorInvalidValue);
+    int dev = 0;
+    hipError_t err = hipGetDevice(&dev);
+    if (err != hipSuccess) return hip_fail(err);
+    std::lock_guard<std::mutex> lock(g_counters_mutex);
+    for (const auto &e : g_counters)
+        if (e.dev == dev && e.stream == stream) {
+            *out = e.ptr;
+            return QW3_OK;
+        }
+    if (stream_capturing(stream)) return QW3_ERR_CAPTURE;
+    void *p = nullptr;
+    err = hipMalloc(&p, kMaxCounts * sizeof(int));
+    if (err != hipSuccess) return hip_fail(err);
+    hipLaunchKernelGGL(clear_counts_kernel, dim3(kMaxCounts / 256), dim3(256), 0, stream, static_cast<int *>(p));
+    const qw3_status st = check_launch();
+    if (st != QW3_OK) return st;
+    g_counters.push_back(Counters{dev, stream, static_cast<int *>(p)});
+    *out = static_cast<int *>(p);
+    return QW3_OK;
+}
 
 extern "C" {
 
