@@ -413,10 +413,11 @@ struct CacheArgs {
 };
 
 constexpr int kUnit = 128;  // keys of a workgroup's step: 32 for each of its 4 waves
+constexpr int kSetup = 2;   // what beginning and ending an item costs, in such steps
 
 // What a sequence asks for.  An item is (sequence, kv head, block of R query
-// rows); its work is counted in units of kUnit keys, at least one, so that an
-// empty cache still writes its zeros.  All items of the call, laid end to end,
+// rows); its work is counted in units: kSetup, and one for each kUnit keys, at
+// least one, so that an empty cache still writes its zeros.  All items of the call, laid end to end,
 // are cut into equal runs of units, one per workgroup: a long sequence is split
 // over many workgroups and short ones share one, with no lengths known on the
 // host.
@@ -431,7 +432,7 @@ struct Seq {
         nq = max(nq, 0);
         len = a.pages == 0 ? 0 : (int)max((int64_t)0, min((int64_t)a.lens[b], a.max_pages << a.page_shift));
         blocks = (int)(((int64_t)nq * a.G + R - 1) / R);
-        per_item = max((len + (int64_t)kUnit - 1) / kUnit, (int64_t)1);
+        per_item = kSetup + max((len + (int64_t)kUnit - 1) / kUnit, (int64_t)1);
         units = per_item * blocks * a.H;
     }
 };
@@ -510,47 +511,79 @@ __device__ __forceinline__ float2 load_agent(const float *p) {
     return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
 }
 
-// Row r of an item, from the partial results of workgroups first..last in that
-// order; one wave.  `from` is the first one's slot, the others' are their first.
-// Maxima and sums are stored as pairs (m, l).
-template <int R, int D>
-__device__ __forceinline__ void join_row(const CacheArgs &a, const float *from, int first, int last, int r,
-                                         uint16_t *out) {
-    const int lane = threadIdx.x & 63;
-    constexpr int kBatch = 8;
-    const int at = 2 * R + r * D + (D == 128 ? 2 * lane : lane & ~1);
-    float m = kNegInf, l = 0.0f, acc0 = 0.0f, acc1 = 0.0f;
+// Reads of partial results that a wave has under way at once.
+constexpr int kFlight = 32;
+
+// An item's `rows` rows from the partial results of workgroups first..last in
+// that order, by the 4 waves of a workgroup: wave w takes rows w, w + 4, ...
+// together, so that their reads, each of which goes to memory, are under way at
+// once.  `from` is the first one's slot, the others' are their first.
+// Maxima and sums are stored as pairs (m, l).  row_out(r): where row r goes.
+template <int R, int D, int kRowsOfWave, class RowOut>
+__device__ __forceinline__ void join_rows(const CacheArgs &a, const float *from, int first, int last, int rows,
+                                          RowOut row_out) {
+    const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
+    constexpr int kBatch = kFlight / kRowsOfWave;
+    float m[kRowsOfWave], l[kRowsOfWave], f[kRowsOfWave];
+    float2 acc[kRowsOfWave];
+#pragma unroll
+    for (int k = 0; k < kRowsOfWave; ++k) m[k] = kNegInf, l[k] = 0.0f, acc[k] = make_float2(0.0f, 0.0f);
     for (int g0 = first; g0 <= last; g0 += 64) {
         const int n = min(64, last + 1 - g0);
         auto slot = [&](int i) { return g0 + i == first ? from : partial<R, D>(a, g0 + i, 0); };
-        float2 ml = make_float2(kNegInf, 0.0f);
-        if (lane < n) ml = load_agent(slot(lane) + 2 * r);
-        float m1 = ml.x;
-        for (int x = 32; x >= 1; x /= 2) m1 = fmaxf(m1, __shfl_xor(m1, x, 64));
-        m1 = fmaxf(m, m1);
-        const float old = m == kNegInf ? 0.0f : exp2_fast(m - m1);
-        const float f = ml.x == kNegInf ? 0.0f : exp2_fast(ml.x - m1);
-        float ls = f * ml.y;
-        for (int x = 32; x >= 1; x /= 2) ls += __shfl_xor(ls, x, 64);
-        m = m1;
-        l = l * old + ls;
-        acc0 *= old, acc1 *= old;
-        for (int i0 = 0; i0 < n; i0 += kBatch) {
-            float2 part[kBatch];
+        const float *mine = slot(min(lane, n - 1));
+        float2 ml[kRowsOfWave];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) part[i] = load_agent(slot(min(i0 + i, n - 1)) + at);
+        for (int k = 0; k < kRowsOfWave; ++k) ml[k] = load_agent(mine + 2 * min(wave + 4 * k, rows - 1));
+#pragma unroll
+        for (int k = 0; k < kRowsOfWave; ++k) {
+            float m1 = lane < n ? ml[k].x : kNegInf;
+            for (int x = 32; x >= 1; x /= 2) m1 = fmaxf(m1, __shfl_xor(m1, x, 64));
+            m1 = fmaxf(m[k], m1);
+            const float old = m[k] == kNegInf ? 0.0f : exp2_fast(m[k] - m1);
+            f[k] = lane >= n || ml[k].x == kNegInf ? 0.0f : exp2_fast(ml[k].x - m1);
+            float ls = f[k] == 0.0f ? 0.0f : f[k] * ml[k].y;
+            for (int x = 32; x >= 1; x /= 2) ls += __shfl_xor(ls, x, 64);
+            m[k] = m1;
+            l[k] = l[k] * old + ls;
+            acc[k].x *= old, acc[k].y *= old;
+        }
+        for (int i0 = 0; i0 < n; i0 += kBatch) {
+            float2 part[kBatch][kRowsOfWave];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                const float fi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), min(i0 + i, n - 1)));
-                if (i0 + i < n) acc0 += fi * part[i].x, acc1 += fi * part[i].y;
+                const float *p = slot(min(i0 + i, n - 1)) + 2 * R;
+#pragma unroll
+                for (int k = 0; k < kRowsOfWave; ++k) {
+                    const int at = min(wave + 4 * k, rows - 1) * D;
+                    if (D == 128)
+                        part[i][k] = load_agent(p + at + 2 * lane);
+                    else
+                        part[i][k].x = __hip_atomic_load(p + at + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                }
             }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                for (int k = 0; k < kRowsOfWave; ++k) {
+                    const float fi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f[k]), min(i0 + i, n - 1)));
+                    if (i0 + i < n) {
+                        acc[k].x += fi * part[i][k].x;
+                        if (D == 128) acc[k].y += fi * part[i][k].y;
+                    }
+                }
         }
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    if (D == 128)
-        *reinterpret_cast<uint32_t *>(out + 2 * lane) = pack_bf16(acc0 * inv, acc1 * inv);
-    else
-        out[lane] = (uint16_t)(pack_bf16((lane & 1 ? acc1 : acc0) * inv, 0.0f) & 0xffffu);
+#pragma unroll
+    for (int k = 0; k < kRowsOfWave; ++k) {
+        if (wave + 4 * k >= rows) continue;
+        const float inv = l[k] == 0.0f ? 0.0f : 1.0f / l[k];
+        uint16_t *out = row_out(wave + 4 * k);
+        if (D == 128)
+            *reinterpret_cast<uint32_t *>(out + 2 * lane) = pack_bf16(acc[k].x * inv, acc[k].y * inv);
+        else
+            out[lane] = (uint16_t)(pack_bf16(acc[k].x * inv, 0.0f) & 0xffffu);
+    }
 }
 
 // Byte J of w, signed, as float.
@@ -585,14 +618,14 @@ __device__ __forceinline__ bf8_t decode8(uint32_t lo, uint32_t hi) {
 // the wave's own in LDS that turns them.  The waves meet only at the end of an
 // item.
 template <int D, bool E4M3, int R>
-__global__ __launch_bounds__(256, R == 16 ? 3 : 2) void attn_few_kernel(CacheArgs a) {
+__global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
     constexpr int kN = R / 16;                   // blocks of 16 rows
     constexpr int kCols = R == 16 ? D : 64;      // channels joined at a time
     constexpr int kPad = kCols + 4;
     constexpr int kTurn = 4 * 32 * D, kJoin = 4 * R * kPad * 4;
     __shared__ __attribute__((aligned(1024))) char lds[kTurn > kJoin ? kTurn : kJoin];
     __shared__ float stat[2][4][R];
-    __shared__ int arrived;
+    __shared__ int arrived[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), quarter = lane >> 4, col = lane & 15;
 
     Run run = find_run<R>(a);
@@ -610,35 +643,47 @@ __global__ __launch_bounds__(256, R == 16 ? 3 : 2) void attn_few_kernel(CacheArg
         float4 ks[2], vs[2];
     };
 
-    while (run.u < run.end) {
+    // the portion of an item that is worked on: units t0.. of it, for the rows
+    // r0.. of kv head h of a sequence, the wave's keys 32 from key0 + 128 s in step s
+    int h, r0, rows, q0, len, ctx, key0, steps;
+    int64_t ustart, count;  // the item's first unit; units of the portion
+    const int32_t *table;
+    auto locate = [&]() {
         while (run.u - run.before >= seq.units) {  // next sequence (some have no rows)
             run.before += seq.units;
             ++run.b;
             seq = Seq<R>(a, run.b);
         }
         const int64_t local = run.u - run.before, item = quotient(local, seq.per_item);
-        const int64_t t0 = local - item * seq.per_item, t1 = min(seq.per_item, t0 + (run.end - run.u));
-        const int h = (int)quotient(item, seq.blocks), block = (int)(item - (int64_t)h * seq.blocks);
-        const int rows = seq.nq * a.G, r0 = block * R, len = seq.len, ctx = len - seq.nq;
-
-        // the wave's keys: 32 from key0 + 128 s in step s
-        const int key0 = (int)t0 * kUnit + 32 * wave;
+        const int64_t begin = run.before + item * seq.per_item;
+        ustart = begin + kSetup;
+        run.u = max(run.u, ustart);
+        const int64_t t0 = run.u - ustart;
+        count = min(begin + seq.per_item, run.end) - run.u;
+        if (count <= 0) return false;  // the run ends before the item's first keys
+        h = (int)quotient(item, seq.blocks);
+        r0 = (int)(item - (int64_t)h * seq.blocks) * R;
+        rows = seq.nq * a.G, q0 = seq.q0, len = seq.len, ctx = len - seq.nq;
+        key0 = (int)t0 * kUnit + 32 * wave;
         const int64_t room = (int64_t)len - key0;
-        const int steps = room <= 0 ? 0 : (int)min((int64_t)(t1 - t0), (room + kUnit - 1) / kUnit);
+        steps = room <= 0 ? 0 : (int)min(count, (room + kUnit - 1) / kUnit);
+        table = a.table + (int64_t)run.b * a.max_pages;
+        return true;
+    };
+    if (!locate()) return;
 
         // pages of 32 steps: lane 2 s + g has the one of group g (16 keys) of step s
-        const int32_t *table = a.table + (int64_t)run.b * a.max_pages;
         auto pages_of = [&](int s) {
             const int pos = min(key0 + (s + (lane >> 1)) * kUnit + 16 * (lane & 1), len - 1);
             return table[pos >> a.page_shift];
         };
-        int ids = 0, ids_next = 0;
-        if (steps > 0) {
-            ids = pages_of(0);
+        int ids = 0, ids_next = 0, ids_base = 0;
+        auto begin_ids = [&]() {
+            ids_base = 0;
+            if (steps > 0) ids = pages_of(0);
             if (steps > 32) ids_next = pages_of(32);
-        }
-        int ids_base = 0;
-        const int64_t page_rows = (int64_t)(2 * a.H) << a.page_shift, head_row = (int64_t)h << a.page_shift;
+        };
+        const int64_t page_rows = (int64_t)(2 * a.H) << a.page_shift;
         const int64_t to_v = (int64_t)a.H << a.page_shift;
         auto page_of = [&](int s, int g) { return __builtin_amdgcn_readlane(ids, 2 * (s - ids_base) + g); };
         Stage st;
@@ -650,59 +695,61 @@ __global__ __launch_bounds__(256, R == 16 ? 3 : 2) void attn_few_kernel(CacheArg
                 const int pos = min(key + 16 * g, (len - 1) & ~15);
                 int page = page_of(s, g);
                 page = (uint32_t)page < (uint64_t)a.pages ? page : 0;
-                const int64_t row = page * page_rows + head_row + (pos & ((1 << a.page_shift) - 1));
+                const int64_t row = page * page_rows + ((int64_t)h << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
                 const uint8_t *kp = a.codes + row * D, *vp = kp + to_v * D;
                 const float *sp = a.scales + row;
+                // a uniform base and a lane's offset: kept apart, or the compiler makes
+                // a 64-bit address for each lane and load
+                uint32_t ko = col * D + quarter * 16, vo = lane * 16, so = 4 * quarter;
+                asm("" : "+v"(ko), "+v"(vo), "+v"(so));
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                    st.k[g][c] = *reinterpret_cast<const uint4 *>(kp + (uint32_t)(col * D + (quarter + 4 * c) * 16));
+                for (int c = 0; c < D / 64; ++c) st.k[g][c] = *reinterpret_cast<const uint4 *>(kp + ko + 64 * c);
 #pragma unroll
                 for (int c = 0; c < kVLoads / 2; ++c)
-                    st.v[g * (kVLoads / 2) + c] = *reinterpret_cast<const uint4 *>(vp + (uint32_t)(c * 1024 + lane * 16));
-                st.ks[g] = *reinterpret_cast<const float4 *>(sp + (uint32_t)(4 * quarter));
-                st.vs[g] = *reinterpret_cast<const float4 *>(sp + to_v + (uint32_t)(4 * quarter));
+                    st.v[g * (kVLoads / 2) + c] = *reinterpret_cast<const uint4 *>(vp + vo + 1024 * c);
+                st.ks[g] = *reinterpret_cast<const float4 *>(sp + so);
+                st.vs[g] = *reinterpret_cast<const float4 *>(sp + to_v + so);
             }
         };
-
-        if (steps > 0) fetch(0);
 
         // the rows' queries, as B operands with the channels in the order of K's pieces
         bf8_t qf[kN][D / 32];
         int seen[kN];       // causal: the row's last visible key
         uint64_t tree[kN];  // otherwise the drafts it sees
+        auto begin_loads = [&]() {
+            if (steps > 0) fetch(0);
 #pragma unroll
-        for (int x = 0; x < kN; ++x) {
-            const int r = min(r0 + 16 * x + col, rows - 1), i = r / a.G, g = r - i * a.G;
-            const uint16_t *qp = a.q + (int64_t)(seq.q0 + i) * a.q_ts + (h * a.G + g) * a.q_hs;
+            for (int x = 0; x < kN; ++x) {
+                const int r = min(r0 + 16 * x + col, rows - 1), i = r / a.G, g = r - i * a.G;
+                const uint16_t *qp = a.q + (int64_t)(q0 + i) * a.q_ts + (h * a.G + g) * a.q_hs;
 #pragma unroll
-            for (int t = 0; t < D / 32; ++t)
-                qf[x][t] = *reinterpret_cast<const bf8_t *>(qp + 16 * (quarter + 4 * (t / 2)) + 8 * (t & 1));
-            seen[x] = a.tree ? ctx - 1 : ctx + i;
-            tree[x] = a.tree ? a.tree[seq.q0 + i] : 0;
-        }
+                for (int t = 0; t < D / 32; ++t)
+                    qf[x][t] = *reinterpret_cast<const bf8_t *>(qp + 16 * (quarter + 4 * (t / 2)) + 8 * (t & 1));
+                seen[x] = a.tree ? ctx - 1 : ctx + i;
+                tree[x] = a.tree ? a.tree[q0 + i] : 0;
+            }
+        };
+        begin_ids();
+        begin_loads();
 
         f4_t acc[kN][D / 16];
         float m[kN], l[kN];
-#pragma unroll
-        for (int x = 0; x < kN; ++x) {
-            m[x] = kNegInf, l[x] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) acc[x][i] = f4_t{};
-        }
 
-        auto step = [&](int s, auto fetch_c) {
+        auto step = [&](int s, auto masked_c) {
+            constexpr bool kMasked = decltype(masked_c)::value;
             const int key = key0 + s * kUnit;
-            bool gone[2];
+            bool gone[2] = {false, false};
+            if (kMasked) {
 #pragma unroll
-            for (int g = 0; g < 2; ++g) gone[g] = (uint32_t)page_of(s, g) >= (uint64_t)a.pages;
-            const bool masked = key + 31 >= min(ctx, len) || gone[0] || gone[1];
+                for (int g = 0; g < 2; ++g) gone[g] = (uint32_t)page_of(s, g) >= (uint64_t)a.pages;
+            }
             // V's codes into the turning tile
 #pragma unroll
             for (int c = 0; c < kVLoads; ++c) {
                 const int r = vrow + c * (64 / kPieces);
                 uint4 w = st.v[c];
                 // p = 0 hides a row only if its codes are numbers: e4m3 garbage may be NaN
-                if (E4M3 && masked && (key + r >= len || gone[c / (kVLoads / 2)])) w = make_uint4(0, 0, 0, 0);
+                if (E4M3 && kMasked && (key + r >= len || gone[c / (kVLoads / 2)])) w = make_uint4(0, 0, 0, 0);
                 *reinterpret_cast<uint4 *>(turn + r * D + ((vpiece ^ place(r)) << 4)) = w;
             }
             float kc[2][4], vc[2][4];
@@ -732,7 +779,7 @@ __global__ __launch_bounds__(256, R == 16 ? 3 : 2) void attn_few_kernel(CacheArg
                     }
                 }
             }
-            if (decltype(fetch_c)::value) {
+            if (!kMasked || s + 1 < steps) {
                 if (s + 1 == ids_base + 32) {
                     ids = ids_next, ids_base += 32;
                     if (ids_base + 32 < steps) ids_next = pages_of(ids_base + 32);
@@ -750,7 +797,7 @@ __global__ __launch_bounds__(256, R == 16 ? 3 : 2) void attn_few_kernel(CacheArg
                         sc[x][g][r] *= kc[g][r];
                         hid[g][r] = false;
                     }
-                if (masked) {
+                if (kMasked) {
 #pragma unroll
                     for (int g = 0; g < 2; ++g)
 #pragma unroll
@@ -783,7 +830,7 @@ __global__ __launch_bounds__(256, R == 16 ? 3 : 2) void attn_few_kernel(CacheArg
                         const float pe = exp2_fast(sc[x][g][r] - ms);
                         l[x] += pe;
                         // a hidden key's scale may be anything
-                        w[e] = masked && hid[g][r] ? 0.0f : pe * vc[g][r];
+                        w[e] = kMasked && hid[g][r] ? 0.0f : pe * vc[g][r];
                     }
                     p[i] = pack_bf16(w[0], w[1]);
                 }
@@ -801,29 +848,62 @@ __global__ __launch_bounds__(256, R == 16 ? 3 : 2) void attn_few_kernel(CacheArg
                     acc[x][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[x], acc[x][i], 0, 0, 0);
             }
         };
-        for (int s = 0; s + 1 < steps; ++s) step(s, std::true_type{});
-        if (steps > 0) step(steps - 1, std::false_type{});
+    // items shared with other workgroups (at most the first and the last)
+    struct Shared {
+        int first, last, slot, h, r0, n, q0;  // slot: where the first workgroup's part is
+    } shared[2];
+    int nshared = 0;
+    for (;;) {
+#pragma unroll
+        for (int x = 0; x < kN; ++x) {
+            m[x] = kNegInf, l[x] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) acc[x][i] = f4_t{};
+        }
+        // steps up to the first that can hold a draft, the end or a missing page, then the others
+        const int plain = min(steps - 1, (min(ctx, len) - key0 - 32 + kUnit) / kUnit);
+        int s = 0;
+        for (; s < plain; ++s) {
+            if ((uint32_t)page_of(s, 0) >= (uint64_t)a.pages || (uint32_t)page_of(s, 1) >= (uint64_t)a.pages) break;
+            step(s, std::false_type{});
+        }
+        for (; s < steps; ++s) step(s, std::true_type{});
 
-        // join the four waves
+        // the next portion's page numbers and then its first loads are on their way
+        // while this one's waves are joined
+        const int64_t first = quotient(ustart, run.per);
+        const Shared done = {(int)first, (int)quotient(ustart + seq.per_item - kSetup - 1, run.per),
+                             first * run.per == ustart ? 0 : 1, h, r0, min(R, rows - r0), q0};
+        float *out = nullptr;
+        if (done.first != done.last) {
+            out = partial<R, D>(a, blockIdx.x, first < blockIdx.x || first * run.per == ustart ? 0 : 1);
+            if (nshared == 0)
+                shared[0] = done;
+            else
+                shared[1] = done;
+            ++nshared;
+        }
+        run.u += count;
+        const bool more = run.u < run.end && locate();
+        if (more) begin_ids();
 #pragma unroll
         for (int x = 0; x < kN; ++x) {
             l[x] = sum_quarters(l[x]);
             if (quarter == 0) stat[0][wave][16 * x + col] = m[x], stat[1][wave][16 * x + col] = l[x];
         }
-        const bool whole = t1 - t0 == seq.per_item;
-        float *out = partial<R, D>(a, blockIdx.x, run.u == blockIdx.x * run.per ? 0 : 1);
         float *join = reinterpret_cast<float *>(lds);
 #pragma unroll
         for (int c0 = 0; c0 < D; c0 += kCols) {
-            __syncthreads();  // the turning tiles, or the channels before, are read
+            lds_barrier();  // the turning tiles, or the channels before, are read
 #pragma unroll
             for (int x = 0; x < kN; ++x)
 #pragma unroll
                 for (int i = 0; i < kCols / 16; ++i)
                     *reinterpret_cast<f4_t *>(join + (wave * R + 16 * x + col) * kPad + 16 * i + 4 * quarter) =
                         acc[x][c0 / 16 + i];
-            __syncthreads();
-            for (int e = tid; e < min(R, rows - r0) * kCols / 4; e += 256) {
+            if (more && c0 + kCols == D) begin_loads();
+            lds_barrier();
+            for (int e = tid; e < done.n * kCols / 4; e += 256) {
                 const int r = e / (kCols / 4), c = 4 * (e % (kCols / 4));
                 float mm = kNegInf;
 #pragma unroll
@@ -836,10 +916,10 @@ __global__ __launch_bounds__(256, R == 16 ? 3 : 2) void attn_few_kernel(CacheArg
                     ll += f * stat[1][w][r];
                     sum += f * *reinterpret_cast<const f4_t *>(join + (w * R + r) * kPad + c);
                 }
-                if (whole) {
+                if (out == nullptr) {
                     const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-                    const int i = (r0 + r) / a.G, g = r0 + r - i * a.G;
-                    *reinterpret_cast<uint2 *>(a.o + ((int64_t)(seq.q0 + i) * a.Hq + h * a.G + g) * D + c0 + c) =
+                    const int i = (done.r0 + r) / a.G, g = done.r0 + r - i * a.G;
+                    *reinterpret_cast<uint2 *>(a.o + ((int64_t)(done.q0 + i) * a.Hq + done.h * a.G + g) * D + c0 + c) =
                         make_uint2(pack_bf16(sum[0] * inv, sum[1] * inv), pack_bf16(sum[2] * inv, sum[3] * inv));
                 } else {
                     store_agent(out + 2 * R + r * D + c0 + c, sum[0], sum[1]);
@@ -848,25 +928,31 @@ __global__ __launch_bounds__(256, R == 16 ? 3 : 2) void attn_few_kernel(CacheArg
                 }
             }
         }
-        if (!whole) {
-            const int64_t ustart = run.u - t0;
-            const int first = (int)(ustart / run.per), last = (int)((ustart + seq.per_item - 1) / run.per);
-            wait_vm0();
-            __syncthreads();
-            if (tid == 0)
-                arrived = __hip_atomic_fetch_add(a.counts + first, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            __syncthreads();
-            if (uniform(arrived) == last - first) {
-                for (int r = wave; r < min(R, rows - r0); r += 4) {
-                    const int i = (r0 + r) / a.G, g = r0 + r - i * a.G;
-                    join_row<R, D>(a, partial<R, D>(a, first, first * run.per >= ustart ? 0 : 1), first, last, r,
-                                   a.o + ((int64_t)(seq.q0 + i) * a.Hq + h * a.G + g) * D);
-                }
-                if (tid == 0) __hip_atomic_store(a.counts + first, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            }
-        }
-        __syncthreads();
-        run.u += t1 - t0;
+        lds_barrier();
+        if (!more) break;
+    }
+
+    if (nshared == 0) return;
+    wait_vm0();
+    __syncthreads();
+    if (tid < nshared)
+        arrived[tid] = __hip_atomic_fetch_add(a.counts + (tid == 0 ? shared[0].first : shared[1].first), 1,
+                                              __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < nshared; ++i) {
+        const Shared s = i == 0 ? shared[0] : shared[1];
+        if (uniform(arrived[i]) != s.last - s.first) continue;
+        const float *from = partial<R, D>(a, s.first, s.slot);
+        auto row_out = [&](int r) {
+            const int i = (s.r0 + r) / a.G, g = s.r0 + r - i * a.G;
+            return a.o + ((int64_t)(s.q0 + i) * a.Hq + s.h * a.G + g) * D;
+        };
+        if (s.n <= R / 2)
+            join_rows<R, D, R / 8>(a, from, s.first, s.last, s.n, row_out);
+        else
+            join_rows<R, D, R / 4>(a, from, s.first, s.last, s.n, row_out);
+        if (tid == 0) __hip_atomic_store(a.counts + s.first, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 }
 
@@ -875,7 +961,7 @@ qw3_status launch_few(CacheArgs a, hipStream_t stream) {
     int cus = 0;
     qw3_status st = cu_count(&cus);
     if (st != QW3_OK) return st;
-    a.groups = cus * (R == 16 ? 3 : 2);
+    a.groups = cus * 2;
     void *ws = nullptr;
     st = workspace(stream, (size_t)a.groups * 2 * R * (D + 2) * sizeof(float), &ws);
     if (st != QW3_OK) return st;
