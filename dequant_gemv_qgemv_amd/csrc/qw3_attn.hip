@@ -412,11 +412,13 @@ struct CacheArgs {
     float scale;
 };
 
-constexpr int kUnit = 128;  // keys of a workgroup's step: 32 for each of its 4 waves
-constexpr int kSetup = 2;   // what beginning and ending an item costs, in such steps
+// Keys of a unit of work: with few rows 32 for each of a workgroup's 4 waves,
+// with many a tile that the waves share.
+constexpr int unit_of(int R) { return R <= 32 ? 128 : 64; }
+constexpr int kSetup = 2;  // what beginning and ending an item costs, in units
 
 // What a sequence asks for.  An item is (sequence, kv head, block of R query
-// rows); its work is counted in units: kSetup, and one for each kUnit keys, at
+// rows); its work is counted in units: kSetup, and one for each unit_of(R) keys, at
 // least one, so that an empty cache still writes its zeros.  All items of the call, laid end to end,
 // are cut into equal runs of units, one per workgroup: a long sequence is split
 // over many workgroups and short ones share one, with no lengths known on the
@@ -432,7 +434,7 @@ struct Seq {
         nq = max(nq, 0);
         len = a.pages == 0 ? 0 : (int)max((int64_t)0, min((int64_t)a.lens[b], a.max_pages << a.page_shift));
         blocks = (int)(((int64_t)nq * a.G + R - 1) / R);
-        per_item = kSetup + max((len + (int64_t)kUnit - 1) / kUnit, (int64_t)1);
+        per_item = kSetup + max((len + (int64_t)unit_of(R) - 1) / unit_of(R), (int64_t)1);
         units = per_item * blocks * a.H;
     }
 };
@@ -612,6 +614,15 @@ __device__ __forceinline__ bf8_t decode8(uint32_t lo, uint32_t hi) {
     return __builtin_bit_cast(bf8_t, i4_t{(int)a.x, (int)a.y, (int)b.x, (int)b.y});
 }
 
+// The keys base..base + 63 that a row sees, as bits: all up to `seen`, and of
+// the drafts, which begin at ctx, those of its word; none from len on.
+__device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
+__device__ __forceinline__ uint64_t visible(int base, int seen, uint64_t tree, int ctx, int len) {
+    const int at = ctx - base;
+    const uint64_t drafts = at >= 64 || at <= -64 ? 0 : at >= 0 ? tree << at : tree >> -at;
+    return (low_bits(seen + 1 - base) | drafts) & low_bits(len - base);
+}
+
 // Few rows: R = 16 or 32 query rows of an item.  Every wave takes all R rows
 // and 32 of the unit's keys; codes and scales go from memory to registers a
 // step ahead, K's straight as the matrix unit's operand, V's through a tile of
@@ -619,6 +630,7 @@ __device__ __forceinline__ bf8_t decode8(uint32_t lo, uint32_t hi) {
 // item.
 template <int D, bool E4M3, int R>
 __global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
+    constexpr int kUnit = unit_of(R);
     constexpr int kN = R / 16;                   // blocks of 16 rows
     constexpr int kCols = R == 16 ? D : 64;      // channels joined at a time
     constexpr int kPad = kCols + 4;
@@ -798,13 +810,15 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
                         hid[g][r] = false;
                     }
                 if (kMasked) {
+                    uint64_t vis = visible(key, seen[x], tree[x], ctx, len);
+                    if (gone[0]) vis &= ~0xffffull;
+                    if (gone[1]) vis &= ~0xffff0000ull;
+                    vis >>= 4 * quarter;
 #pragma unroll
                     for (int g = 0; g < 2; ++g)
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            const int pos = key + 16 * g + 4 * quarter + r, j = pos - ctx;
-                            const bool draft = j >= 0 && j < 64 && ((tree[x] >> (j & 63)) & 1);
-                            hid[g][r] = gone[g] || pos >= len || (pos > seen[x] && !draft);
+                            hid[g][r] = !((vis >> (16 * g + r)) & 1);
                             sc[x][g][r] = hid[g][r] ? kNegInf : sc[x][g][r];
                         }
                 }
@@ -903,27 +917,26 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
                         acc[x][c0 / 16 + i];
             if (more && c0 + kCols == D) begin_loads();
             lds_barrier();
-            for (int e = tid; e < done.n * kCols / 4; e += 256) {
-                const int r = e / (kCols / 4), c = 4 * (e % (kCols / 4));
+            for (int e = tid; e < done.n * kCols / 2; e += 256) {
+                const int r = e / (kCols / 2), c = 2 * (e % (kCols / 2));
                 float mm = kNegInf;
 #pragma unroll
                 for (int w = 0; w < 4; ++w) mm = fmaxf(mm, stat[0][w][r]);
                 float ll = 0.0f;
-                f4_t sum = {};
+                f2_t sum = {};
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const float f = stat[0][w][r] == kNegInf ? 0.0f : exp2_fast(stat[0][w][r] - mm);
                     ll += f * stat[1][w][r];
-                    sum += f * *reinterpret_cast<const f4_t *>(join + (w * R + r) * kPad + c);
+                    sum += f * *reinterpret_cast<const f2_t *>(join + (w * R + r) * kPad + c);
                 }
                 if (out == nullptr) {
                     const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
                     const int i = (done.r0 + r) / a.G, g = done.r0 + r - i * a.G;
-                    *reinterpret_cast<uint2 *>(a.o + ((int64_t)(done.q0 + i) * a.Hq + done.h * a.G + g) * D + c0 + c) =
-                        make_uint2(pack_bf16(sum[0] * inv, sum[1] * inv), pack_bf16(sum[2] * inv, sum[3] * inv));
+                    *reinterpret_cast<uint32_t *>(a.o + ((int64_t)(done.q0 + i) * a.Hq + done.h * a.G + g) * D + c0 + c) =
+                        pack_bf16(sum[0] * inv, sum[1] * inv);
                 } else {
                     store_agent(out + 2 * R + r * D + c0 + c, sum[0], sum[1]);
-                    store_agent(out + 2 * R + r * D + c0 + c + 2, sum[2], sum[3]);
                     if (c0 == 0 && c == 0) store_agent(out + 2 * r, mm, ll);
                 }
             }
@@ -956,8 +969,317 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
     }
 }
 
+// Many rows: R = 128 query rows of an item, 32 for each of 4 waves, which share
+// tiles of 64 keys.  The tile's codes come through registers a tile ahead and
+// are turned into bf16 once for all waves; the rest is attn_prompt_kernel's.
 template <int D, bool E4M3, int R>
-qw3_status launch_few(CacheArgs a, hipStream_t stream) {
+__global__ __launch_bounds__(256, 2) void attn_many_kernel(CacheArgs a) {
+    constexpr int kUnit = unit_of(R);             // 64
+    static_assert(R == 128, "a wave for each 32 rows");
+    constexpr int kRowBytes = D * 2, kTileBytes = kUnit * kRowBytes;
+    constexpr int kPieces = D / 16;               // 16-byte pieces of a row of codes
+    constexpr int kLoads = kUnit * kPieces / 256; // of a thread, for K and for V
+    __shared__ __attribute__((aligned(1024))) char lds[4 * kTileBytes];  // K, V of two tiles
+    __shared__ __attribute__((aligned(16))) float tile_scales[2][2][kUnit];
+    __shared__ int arrived[2];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), half = lane >> 5, col = lane & 31;
+
+    Run run = find_run<R>(a);
+    if (run.u >= run.end) return;
+    Seq<R> seq(a, run.b);
+
+    const int lrow = tid / kPieces, lpiece = tid % kPieces;  // of a thread's first load; the others 256 / kPieces rows on
+    const int xk = D == 128 ? (col & 15) : ((col >> 1) & 7);
+    const uint32_t kbase = col * kRowBytes + ((half ^ (xk & 1)) << 4);
+    const int vr = 4 * half + ((lane & 15) >> 2), xv = value_place<D>(vr);
+    const int vsub = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    const uint32_t vbase = vr * kRowBytes + ((vsub ^ (xv & 3)) << 4) + (lane & 1) * 8;
+
+    struct Shared {
+        int first, last, slot, h, r0, n, q0;  // slot: where the first workgroup's part is
+    } shared[2];
+    int nshared = 0;
+    while (run.u < run.end) {
+        while (run.u - run.before >= seq.units) {  // next sequence (some have no rows)
+            run.before += seq.units;
+            ++run.b;
+            seq = Seq<R>(a, run.b);
+        }
+        const int64_t local = run.u - run.before, item = quotient(local, seq.per_item);
+        const int64_t begin = run.before + item * seq.per_item, ustart = begin + kSetup;
+        run.u = max(run.u, ustart);
+        const int64_t t0 = run.u - ustart, count = min(begin + seq.per_item, run.end) - run.u;
+        if (count <= 0) break;  // the run ends before the item's first keys
+        const int h = (int)quotient(item, seq.blocks), r0 = (int)(item - (int64_t)h * seq.blocks) * R;
+        const int rows = seq.nq * a.G, q0 = seq.q0, len = seq.len, ctx = len - seq.nq;
+        const int key0 = (int)t0 * kUnit;
+        const int tiles = (int)min(count, ((int64_t)len - key0 + kUnit - 1) / kUnit);
+        const int32_t *table = a.table + (int64_t)run.b * a.max_pages;
+
+        // page numbers of 16 tiles: lane 4 t + g has the one of 16-key group g of tile t
+        int ids = 0, ids_next = 0, ids_base = 0;
+        auto pages_of = [&](int t) {
+            return table[min(key0 + (t + (lane >> 2)) * kUnit + 16 * (lane & 3), len - 1) >> a.page_shift];
+        };
+        if (tiles > 0) ids = pages_of(0);
+        if (tiles > 16) ids_next = pages_of(16);
+        const int64_t page_rows = (int64_t)(2 * a.H) << a.page_shift, to_v = (int64_t)a.H << a.page_shift;
+        const int in_page = (1 << a.page_shift) - 1;
+        auto row_of = [&](int t, int r) {  // row of the codes of key r of tile t; its page exists, or it is hidden
+            int page = __shfl(ids, 4 * (t - ids_base) + (r >> 4), 64);
+            page = (uint32_t)page < (uint64_t)a.pages ? page : 0;
+            return page * page_rows + ((int64_t)h << a.page_shift) + (min(key0 + t * kUnit + r, len - 1) & in_page);
+        };
+        uint4 kcode[kLoads], vcode[kLoads];
+        float scale_in = 0.0f;
+        uint32_t gone_in = 0;  // groups of the tile whose page does not exist
+        auto fetch = [&](int t) {
+            if (t == ids_base + 16) {
+                ids = ids_next, ids_base += 16;
+                if (ids_base + 16 < tiles) ids_next = pages_of(ids_base + 16);
+            }
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const uint8_t *at = a.codes + row_of(t, lrow + i * (256 / kPieces)) * D + lpiece * 16;
+                kcode[i] = *reinterpret_cast<const uint4 *>(at);
+                vcode[i] = *reinterpret_cast<const uint4 *>(at + to_v * D);
+            }
+            const int64_t srow = row_of(t, tid & 63);
+            if (tid < 128) scale_in = a.scales[srow + (tid < 64 ? 0 : to_v)];
+            const unsigned long long missing = __ballot((uint32_t)ids >= (uint64_t)a.pages);
+            gone_in = uniform((int)((missing >> (4 * (t - ids_base))) & 15));
+        };
+        uint32_t gone = 0;  // of the tile in LDS
+        auto place = [&](int t) {  // the fetched tile, as bf16, into its buffer
+            char *kt = lds + (2 * (t & 1)) * kTileBytes, *vt = kt + kTileBytes;
+            const bool partly = key0 + (t + 1) * kUnit > len || gone_in != 0;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int r = lrow + i * (256 / kPieces);
+                const int fk = D == 128 ? (r & 15) : ((r >> 1) & 7), fv = value_place<D>(r);
+                *reinterpret_cast<bf8_t *>(kt + r * kRowBytes + (((2 * lpiece) ^ fk) << 4)) =
+                    decode8<E4M3>(kcode[i].x, kcode[i].y);
+                *reinterpret_cast<bf8_t *>(kt + r * kRowBytes + (((2 * lpiece + 1) ^ fk) << 4)) =
+                    decode8<E4M3>(kcode[i].z, kcode[i].w);
+                uint4 w = vcode[i];
+                // a weight of zero hides a row only if its codes are numbers: e4m3 garbage may be NaN
+                if (E4M3 && partly && (key0 + t * kUnit + r >= len || ((gone_in >> (r >> 4)) & 1)))
+                    w = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<bf8_t *>(vt + r * kRowBytes + (((2 * lpiece) ^ fv) << 4)) = decode8<E4M3>(w.x, w.y);
+                *reinterpret_cast<bf8_t *>(vt + r * kRowBytes + (((2 * lpiece + 1) ^ fv) << 4)) =
+                    decode8<E4M3>(w.z, w.w);
+            }
+            if (tid < 128) tile_scales[t & 1][tid >> 6][tid & 63] = tid < 64 ? scale_in * a.scale : scale_in;
+        };
+
+        // the lane's query row
+        const int row = min(r0 + 32 * wave + col, rows - 1), tok = row / a.G;
+        const bool live = r0 + 32 * wave < rows;
+        const uint16_t *qp = a.q + (int64_t)(q0 + tok) * a.q_ts + (h * a.G + row - tok * a.G) * a.q_hs;
+        bf8_t qf[D / 16];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) qf[i] = *reinterpret_cast<const bf8_t *>(qp + 16 * i + 8 * half);
+        const int seen = a.tree ? ctx - 1 : ctx + tok;
+        const uint64_t tree = a.tree ? a.tree[q0 + tok] : 0;
+
+        f16_t acc[D / 32];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) acc[i] = f16_t{};
+        float m = kNegInf, l = 0.0f;
+
+        auto step = [&](int t, auto masked_c) {
+            constexpr bool kMasked = decltype(masked_c)::value;
+            const char *kt = lds + (2 * (t & 1)) * kTileBytes, *vt = kt + kTileBytes;
+            f16_t s[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                s[b] = f16_t{};
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const bf8_t kf =
+                        *reinterpret_cast<const bf8_t *>(kt + b * 32 * kRowBytes + kbase + (((2 * i) ^ (xk & ~1)) << 4));
+                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[i], s[b], 0, 0, 0);
+                }
+            }
+            uint64_t vis = 0;  // of the keys that the lane has, from bit 0 on
+            if (kMasked) {
+                vis = visible(key0 + t * kUnit, seen, tree, ctx, len);
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    if ((gone >> g) & 1) vis &= ~(0xffffull << (16 * g));
+                vis >>= 4 * half;
+            }
+            float top = kNegInf;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                for (int r = 0; r < 16; r += 4) {
+                    const f4_t ks = *reinterpret_cast<const f4_t *>(&tile_scales[t & 1][0][32 * b + 2 * r + 4 * half]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x = s[b][r + e] * ks[e];
+                        if (kMasked && !((vis >> (32 * b + 2 * r + e)) & 1)) x = kNegInf;
+                        s[b][r + e] = x;
+                        top = fmaxf(top, x);
+                    }
+                }
+            }
+            if (__any(top > m + kSlack)) {
+                const float m1 = fmaxf(m, max_halves(top));
+                const float f = m1 == kNegInf ? 1.0f : exp2_fast(m - m1);
+                m = m1;
+                l *= f;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) acc[i] *= f;
+            }
+            const float ms = m == kNegInf ? 0.0f : m;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t p[4];
+#pragma unroll
+                    for (int r = 0; r < 8; r += 4) {
+                        const f4_t vs = *reinterpret_cast<const f4_t *>(
+                            &tile_scales[t & 1][1][32 * b + 2 * (8 * u + r) + 4 * half]);
+                        float w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float x = s[b][8 * u + r + e], pe = exp2_fast(x - ms);
+                            l += pe;
+                            // a hidden key's scale may be anything
+                            w[e] = kMasked && x == kNegInf ? 0.0f : pe * vs[e];
+                        }
+                        p[r / 2] = pack_bf16(w[0], w[1]), p[r / 2 + 1] = pack_bf16(w[2], w[3]);
+                    }
+                    const bf8_t pf = __builtin_bit_cast(bf8_t, i4_t{(int)p[0], (int)p[1], (int)p[2], (int)p[3]});
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        const char *at = vt + (32 * b + 16 * u) * kRowBytes + vbase + (((4 * i) ^ (xv & ~3)) << 4);
+                        const s4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS s4_t *)at);
+                        const s4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS s4_t *)(at + 8 * kRowBytes));
+                        const s8_t vv = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8_t, vv), pf, acc[i], 0, 0, 0);
+                    }
+                }
+            }
+        };
+
+        if (tiles > 0) {
+            fetch(0);
+            place(0);
+            gone = gone_in;
+        }
+        auto iteration = [&](int t, auto masked_c) {
+            lds_barrier();  // tile t is in place; nobody reads the other buffer any more
+            if (t + 1 < tiles) fetch(t + 1);
+            if (live) step(t, masked_c);
+            if (t + 1 < tiles) {
+                place(t + 1);
+                gone = gone_in;
+            }
+        };
+        // tiles up to the first that can hold a draft, the end or a missing page, then the others
+        const int plain = min(tiles, (min(ctx, len) - key0) / kUnit);
+        int t = 0;
+        for (; t < plain && gone == 0; ++t) iteration(t, std::false_type{});
+        for (; t < tiles; ++t) iteration(t, std::true_type{});
+
+        const int64_t first = quotient(ustart, run.per), last = quotient(begin + seq.per_item - 1, run.per);
+        float *out = nullptr;
+        if (first != last) {
+            out = partial<R, D>(a, blockIdx.x, first < blockIdx.x || first * run.per == ustart ? 0 : 1);
+            const Shared mine = {(int)first, (int)last, first * run.per == ustart ? 0 : 1, h, r0, min(R, rows - r0), q0};
+            if (nshared == 0)
+                shared[0] = mine;
+            else
+                shared[1] = mine;
+            ++nshared;
+        }
+        l = sum_halves(l);
+        lds_barrier();  // the last tile is read
+        const int r = 32 * wave + col;  // of the item
+        if (r0 + r < rows) {
+            if (out == nullptr) {
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                uint16_t *op = a.o + ((int64_t)(q0 + tok) * a.Hq + h * a.G + row - tok * a.G) * D;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        *reinterpret_cast<uint2 *>(op + 32 * i + 2 * e + 4 * half) =
+                            make_uint2(pack_bf16(acc[i][e] * inv, acc[i][e + 1] * inv),
+                                       pack_bf16(acc[i][e + 2] * inv, acc[i][e + 3] * inv));
+            } else {
+                // in the order of the registers, so that a wave's stores are contiguous
+                float *at = out + 2 * R + wave * 32 * D + 2 * lane;
+#pragma unroll
+                for (int i = 0; i < D / 4; ++i)
+                    store_agent(at + i * 128, acc[i / 8][2 * (i % 8)], acc[i / 8][2 * (i % 8) + 1]);
+                if (half == 0) store_agent(out + 2 * r, m, l);
+            }
+        }
+        run.u += count;
+    }
+
+    if (nshared == 0) return;
+    wait_vm0();
+    __syncthreads();
+    if (tid < nshared)
+        arrived[tid] = __hip_atomic_fetch_add(a.counts + (tid == 0 ? shared[0].first : shared[1].first), 1,
+                                              __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < nshared; ++i) {
+        const Shared s = i == 0 ? shared[0] : shared[1];
+        if (uniform(arrived[i]) != s.last - s.first) continue;
+        const int r = 32 * wave + col;
+        if (32 * wave < s.n) {
+            // a lane joins what it and its like have stored, in the workgroups' order; the
+            // reads of the next part are under way while one is added
+            auto slot = [&](int g) { return partial<R, D>(a, g, g == s.first ? s.slot : 0); };
+            float2 ml, next_ml, part[D / 4], next[D / 4];
+            auto read = [&](int g) {
+                const float *p = slot(g), *at = p + 2 * R + wave * 32 * D + 2 * lane;
+                next_ml = load_agent(p + 2 * min(r, s.n - 1));
+#pragma unroll
+                for (int i = 0; i < D / 4; ++i) next[i] = load_agent(at + i * 128);
+            };
+            float m = kNegInf, l = 0.0f;
+            float2 sum[D / 4];
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) sum[i] = make_float2(0.0f, 0.0f);
+            read(s.first);
+#pragma unroll 1
+            for (int g = s.first; g <= s.last; ++g) {
+                ml = next_ml;
+#pragma unroll
+                for (int i = 0; i < D / 4; ++i) part[i] = next[i];
+                if (g < s.last) read(g + 1);
+                const float m1 = fmaxf(m, ml.x);
+                const float f0 = m == kNegInf ? 0.0f : exp2_fast(m - m1), f1 = ml.x == kNegInf ? 0.0f : exp2_fast(ml.x - m1);
+                m = m1, l = l * f0 + ml.y * f1;
+#pragma unroll
+                for (int i = 0; i < D / 4; ++i)
+                    sum[i] = make_float2(sum[i].x * f0 + part[i].x * f1, sum[i].y * f0 + part[i].y * f1);
+            }
+            if (r < s.n) {
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                const int i = (s.r0 + r) / a.G, g = s.r0 + r - i * a.G;
+                uint16_t *op = a.o + ((int64_t)(s.q0 + i) * a.Hq + s.h * a.G + g) * D;
+#pragma unroll
+                for (int e = 0; e < D / 4; e += 2)
+                    *reinterpret_cast<uint2 *>(op + 32 * (e / 8) + 4 * (e % 8) + 4 * half) =
+                        make_uint2(pack_bf16(sum[e].x * inv, sum[e].y * inv),
+                                   pack_bf16(sum[e + 1].x * inv, sum[e + 1].y * inv));
+            }
+        }
+        if (tid == 0) __hip_atomic_store(a.counts + s.first, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+}
+
+template <int D, bool E4M3, int R>
+qw3_status launch_cache(CacheArgs a, hipStream_t stream) {
     int cus = 0;
     qw3_status st = cu_count(&cus);
     if (st != QW3_OK) return st;
@@ -968,15 +1290,19 @@ qw3_status launch_few(CacheArgs a, hipStream_t stream) {
     a.part = static_cast<float *>(ws);
     st = counters(stream, a.groups, &a.counts);
     if (st != QW3_OK) return st;
-    hipLaunchKernelGGL((attn_few_kernel<D, E4M3, R>), dim3(a.groups), dim3(256), 0, stream, a);
+    if constexpr (R <= 32)
+        hipLaunchKernelGGL((attn_few_kernel<D, E4M3, R>), dim3(a.groups), dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((attn_many_kernel<D, E4M3, R>), dim3(a.groups), dim3(256), 0, stream, a);
     return check_launch();
 }
 
 template <int D, bool E4M3>
 qw3_status launch_cache_rows(const CacheArgs &a, hipStream_t stream) {
     const int64_t rows = ceil_div(a.Tq, a.B) * a.G;  // of a sequence, on average
-    if (rows <= 16) return launch_few<D, E4M3, 16>(a, stream);
-    return launch_few<D, E4M3, 32>(a, stream);
+    if (rows <= 16) return launch_cache<D, E4M3, 16>(a, stream);
+    if (rows <= 64) return launch_cache<D, E4M3, 32>(a, stream);
+    return launch_cache<D, E4M3, 128>(a, stream);
 }
 
 bool strides_ok(int64_t ts, int64_t hs) { return ts >= 0 && hs >= 0 && ts < (1 << 23) && hs < (int64_t(1) << 40); }
