@@ -76,7 +76,11 @@ __device__ __forceinline__ uint32_t lds_address(const void *p) {
 }
 
 __device__ __forceinline__ void wait_vm0() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
-__device__ __forceinline__ void wait_vm0_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// Until at most N of the wave's loads are on the way, then for the other waves.
+template <int N>
+__device__ __forceinline__ void wait_loads_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
 
 // x plus the two bf16 of p.
 __device__ __forceinline__ float add_pair(uint32_t p, float x) {
@@ -160,6 +164,73 @@ __device__ __forceinline__ void exact_row(const PromptArgs &a, const uint16_t *q
     }
 }
 
+__device__ __forceinline__ int wave_sum(int x) {  // over all 64 lanes, in every lane
+    x += (int)dpp_u32<0xB1>((uint32_t)x);   // quad_perm [1, 0, 3, 2]
+    x += (int)dpp_u32<0x4E>((uint32_t)x);   // quad_perm [2, 3, 0, 1]
+    x += (int)dpp_u32<0x141>((uint32_t)x);  // row_half_mirror
+    x += (int)dpp_u32<0x140>((uint32_t)x);  // row_mirror
+    auto r = __builtin_amdgcn_permlane16_swap((uint32_t)x, (uint32_t)x, false, false);
+    x = (int)(r[0] + r[1]);
+    r = __builtin_amdgcn_permlane32_swap((uint32_t)x, (uint32_t)x, false, false);
+    return (int)(r[0] + r[1]);
+}
+
+// The rank-th tile of the call: its sequence and its place there.  Workgroups
+// start in the order of the ranks, so the tiles with the most keys come first;
+// a light tile at the end fills a gap, a heavy one would be waited for.  With a
+// causal mask tile i of a sequence counts i + 1 + (prefix in tiles): F(x), the
+// number of tiles that count more than x, is summed over the sequences by the
+// lanes, and the x with F(x) <= rank < F(x - 1) found by halving.  Without one,
+// and beyond 64 sequences, sequence b owns the ranks from cu_q[b] / kRows + b on
+// (room for its rows whatever its length), last tiles first.
+template <bool CAUSAL>
+__device__ __forceinline__ bool find_tile(const PromptArgs &a, int rank, int *seq, int *tile) {
+    const int lane = threadIdx.x & 63;
+    if (CAUSAL && a.B <= 64) {
+        int n = 0, pre = 0;
+        if (lane < a.B) {
+            const int q0 = clamp_row(a.cu_q[lane], a.Tq), nq = max(clamp_row(a.cu_q[lane + 1], a.Tq) - q0, 0);
+            const int k0 = clamp_row(a.cu_k[lane], a.Tk), nk = max(clamp_row(a.cu_k[lane + 1], a.Tk) - k0, 0);
+            n = (nq + kRows - 1) / kRows, pre = max(nk - nq, 0) / kRows;
+        }
+        if (a.B == 1) {
+            *seq = 0, *tile = uniform(n) - 1 - rank;
+            return *tile >= 0;
+        }
+        auto above = [&](int x) { return uniform(wave_sum(min(max(n + pre - x, 0), n))); };
+        int lo = 0, hi = (a.Tq > a.Tk ? a.Tq : a.Tk) / kRows + 2;  // F(lo) > rank >= F(hi)
+        if (above(lo) <= rank) return false;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (above(mid) > rank)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        // the tiles that count hi: at most one of a sequence
+        const bool has = hi > pre && hi <= n + pre;
+        const unsigned long long mine = __ballot(has);
+        const int skip = rank - above(hi);
+        const bool it = has && __popcll(mine & ((1ull << lane) - 1)) == skip;
+        *seq = uniform(__builtin_ctzll(__ballot(it)));
+        *tile = hi - 1 - uniform(__shfl(pre, *seq, 64));
+        return true;
+    }
+    const int at = a.tiles - 1 - rank;
+    int b = -1;
+    for (int base = 0; base < a.B; base += 64) {
+        const unsigned long long in = __ballot(
+            base + lane < a.B && clamp_row(a.cu_q[min(base + lane, a.B - 1)], a.Tq) / kRows + base + lane <= at);
+        b += __popcll(in);
+        if (in != ~0ull) break;
+    }
+    b = uniform(b);
+    if (b < 0) return false;
+    *seq = b;
+    *tile = at - clamp_row(a.cu_q[b], a.Tq) / kRows - b;
+    return true;
+}
+
 // What row r of a V tile is exchanged by.  A transposing read takes 4 rows x 64
 // bytes for lanes 0..31 and the 4 rows behind for the others: the rows' 64-byte
 // pieces go to different banks, and the two halves to different 32 bytes.
@@ -174,34 +245,21 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
     constexpr int kRowBytes = D * 2;
     constexpr int kRowsPerLoad = 1024 / kRowBytes;       // rows that one wave-wide load covers
     constexpr int kLoads = kTileBytes / 1024 / 4;        // loads of one tile per wave
-    __shared__ __attribute__((aligned(1024))) char lds[4 * kTileBytes];  // K, V of the two tiles in flight
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5, col = lane & 31;
+    // Tiles of K and of V in the ring: 64 KB, so that two workgroups fit a CU.
+    constexpr int kStages = D == 128 ? 2 : 4;
+    __shared__ __attribute__((aligned(1024))) char lds[kStages * 2 * kTileBytes];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), half = lane >> 5, col = lane & 31;
 
-    // Workgroups go round the 8 XCDs; give each XCD a contiguous range of
-    // (kv head, tile, head of the group), so its L2 holds few heads' keys.
-    // Tiles run from the end: with a causal mask the last have the most keys.
-    const uint32_t n = gridDim.x, xcd = blockIdx.x & 7, q8 = n >> 3, r8 = n & 7;
-    const uint32_t idx = xcd * q8 + min(xcd, r8) + (blockIdx.x >> 3);
-    const int G = a.Hq / a.H;
-    const int kvh = idx / (uint32_t)(a.tiles * G);
-    const uint32_t rest = idx - (uint32_t)kvh * (a.tiles * G);
-    const int tile = a.tiles - 1 - (int)(rest / (uint32_t)G);
-    const int head = kvh * G + (int)(rest % (uint32_t)G);
-
-    // Sequence b owns the tiles from cu_q[b] / kRows + b on: room for all of
-    // its rows whatever its length, with no lengths known on the host.
-    int b = -1;
-    for (int base = 0; base < a.B; base += 64) {
-        const unsigned long long in = __ballot(
-            base + lane < a.B && clamp_row(a.cu_q[min(base + lane, a.B - 1)], a.Tq) / kRows + base + lane <= tile);
-        b += __popcll(in);
-        if (in != ~0ull) break;
-    }
-    b = uniform(b);
-    if (b < 0) return;
+    // Workgroups go round the 8 XCDs: where the heads divide by 8, each XCD takes
+    // the same ones of every tile, so that its L2 holds few heads' keys.
+    const int rank = (int)(blockIdx.x / (uint32_t)a.Hq), j = (int)(blockIdx.x - (uint32_t)rank * a.Hq);
+    const int head = a.Hq % 8 == 0 ? (j & 7) * (a.Hq / 8) + (j >> 3) : j;
+    const int kvh = head / (a.Hq / a.H);
+    int b, tile;
+    if (!find_tile<CAUSAL>(a, rank, &b, &tile)) return;
     const int q0 = clamp_row(a.cu_q[b], a.Tq), nq = clamp_row(a.cu_q[b + 1], a.Tq) - q0;
     const int k0 = clamp_row(a.cu_k[b], a.Tk), nk = max(clamp_row(a.cu_k[b + 1], a.Tk) - k0, 0);
-    const int row0 = (tile - q0 / kRows - b) * kRows;
+    const int row0 = tile * kRows;
     if (row0 >= nq) return;
 
     const int off = nk - nq;
@@ -235,18 +293,17 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
         vvo[i] = (uint32_t)((lrow + 4 * kRowsPerLoad * i) * a.v_ts * 2 + (lpiece ^ fv) * 16);
     }
     const uint32_t lds0 = lds_address(lds + wave * 1024);
+    // Past the last tile the loads give zeros, so that every wave has the same
+    // number of them on the way.
     auto fetch = [&](const char *base, const uint32_t (&vo)[kLoads], int64_t ts, int t, int which) {
         const int64_t j0 = (int64_t)t * kKeys, left = (nk - 1 - j0) * ts * 2 + kRowBytes;
-        const i4_t d = descriptor(base + j0 * ts * 2, (uint32_t)min(left, (int64_t)0x7fffffff));
+        const i4_t d = descriptor(base + j0 * ts * 2, t < ntiles ? (uint32_t)min(left, (int64_t)0x7fffffff) : 0);
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) load_to_lds(lds0 + (2 * (t & 1) + which) * kTileBytes + i * 4096, vo[i], d);
+        for (int i = 0; i < kLoads; ++i)
+            load_to_lds(lds0 + (2 * (t % kStages) + which) * kTileBytes + i * 4096, vo[i], d);
     };
-    auto fetch_k = [&](int t) {
-        if (t < ntiles) fetch(kp, kvo, a.k_ts, t, 0);
-    };
-    auto fetch_v = [&](int t) {
-        if (t < ntiles) fetch(vp, vvo, a.v_ts, t, 1);
-    };
+    auto fetch_k = [&](int t) { fetch(kp, kvo, a.k_ts, t, 0); };
+    auto fetch_v = [&](int t) { fetch(vp, vvo, a.v_ts, t, 1); };
 
     // reads: K piece 2 t + half of row 32 kb + col; V^T through 4-row blocks
     const int xk = D == 128 ? (col & 15) : ((col >> 1) & 7);
@@ -267,7 +324,7 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
         s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[i], s, 0, 0, 0);
     };
     auto scores = [&](f16_t (&s)[2], int t) {
-        const char *kt = lds + (2 * (t & 1)) * kTileBytes;
+        const char *kt = lds + (2 * (t % kStages)) * kTileBytes;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             s[kb] = f16_t{};
@@ -288,15 +345,13 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
     // vector unit works on the other.
     auto step = [&](f16_t (&s)[2], int t, auto masked_c, auto next_c) {
         constexpr bool kMasked = decltype(masked_c)::value, kNext = decltype(next_c)::value;
-        const char *vt = lds + (2 * (t & 1) + 1) * kTileBytes, *kt = lds + (2 * ((t + 1) & 1)) * kTileBytes;
+        const char *vt = lds + (2 * (t % kStages) + 1) * kTileBytes, *kt = lds + (2 * ((t + 1) % kStages)) * kTileBytes;
         if (kMasked) {
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int key = t * kKeys + 32 * kb + 8 * (r / 4) + 4 * half + (r & 3);
-                    s[kb][r] = key > last ? kNegInf : s[kb][r];
-                }
+                for (int r = 0; r < 16; ++r)
+                    s[kb][r] = 32 * kb + 8 * (r / 4) + (r & 3) > last - t * kKeys - 4 * half ? kNegInf : s[kb][r];
         }
         float top = s[0][0];
 #pragma unroll
@@ -342,31 +397,45 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
     };
 
     // The keys run one tile ahead of the values: iteration t reads V of tile t
-    // and K of t + 1 while V of t + 1 and K of t + 2 are on their way.
+    // and K of t + 1, and sends for V of t + kStages - 1 and K of t + kStages, into
+    // the places that iteration t - 1 has read.
     const int mine = live && whi >= 0 ? whi / kKeys + 1 : 0;  // tiles that a row of the wave sees
     f16_t s[2];
     fetch_k(0);
-    fetch_v(0);
-    wait_vm0_barrier();
+#pragma unroll
+    for (int i = 0; i + 1 < kStages; ++i) {
+        fetch_v(i);
+        fetch_k(i + 1);
+    }
+    wait_loads_barrier<(kStages - 1) * 2 * kLoads>();
     // the compiler sees the queries arrive here: it does not know of the loads
     // into LDS, and its waits for the queries inside the loop would wait for those
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) asm volatile("" : "+v"(qf[i]));
-    fetch_k(1);
     if (mine > 0) scores(s, 0);
-    for (int t = 0; t < ntiles; ++t) {
-        wait_vm0_barrier();  // K of t + 1 and V of t are here; nobody reads what the next loads replace
-        fetch_k(t + 2);
-        fetch_v(t + 1);
-        if (t + 1 < mine) {
-            if (t * kKeys + kKeys - 1 > wlo)
-                step(s, t, std::true_type{}, std::true_type{});
-            else
-                step(s, t, std::false_type{}, std::true_type{});
-        } else if (t < mine) {
-            step(s, t, std::true_type{}, std::false_type{});
-        }
+    auto arrive = [&](int t) {
+        wait_loads_barrier<(kStages - 2) * 2 * kLoads>();  // K of t + 1 and V of t are here
+        fetch_v(t + kStages - 1);
+        fetch_k(t + kStages);
+    };
+    // tiles that all rows of the wave see whole, then those that hold some row's
+    // end, then those that only other waves need
+    const int plain = min(mine - 1, (wlo + 1) / kKeys);
+    int t = 0;
+    for (; t < plain; ++t) {
+        arrive(t);
+        step(s, t, std::false_type{}, std::true_type{});
     }
+    for (; t < mine - 1; ++t) {
+        arrive(t);
+        step(s, t, std::true_type{}, std::true_type{});
+    }
+    if (t < mine) {
+        arrive(t);
+        step(s, t, std::true_type{}, std::false_type{});
+        ++t;
+    }
+    for (; t < ntiles; ++t) arrive(t);
     if (!live) return;
 
     l = sum_halves(l);
