@@ -118,8 +118,8 @@ struct PromptArgs {
     float scale;  // sm_scale log2(e)
 };
 
-// Query rows of a workgroup (4 waves x 32) and keys of a tile.
-constexpr int kRows = 128, kKeys = 64;
+constexpr int kKeys = 64;  // of a tile
+
 
 // One query row recomputed by a wave from the visible keys alone (keys 0..last).
 // The tiles multiply hidden keys by p = 0, which is not 0 where a hidden value
@@ -183,7 +183,7 @@ __device__ __forceinline__ int wave_sum(int x) {  // over all 64 lanes, in every
 // lanes, and the x with F(x) <= rank < F(x - 1) found by halving.  Without one,
 // and beyond 64 sequences, sequence b owns the ranks from cu_q[b] / kRows + b on
 // (room for its rows whatever its length), last tiles first.
-template <bool CAUSAL>
+template <bool CAUSAL, int kRows>
 __device__ __forceinline__ bool find_tile(const PromptArgs &a, int rank, int *seq, int *tile) {
     const int lane = threadIdx.x & 63;
     if (CAUSAL && a.B <= 64) {
@@ -239,8 +239,13 @@ __device__ __forceinline__ int value_place(int r) {
     return (D == 128 ? (r & 3) << 2 : ((r >> 1) & 1) << 2) | (((r >> 2) & 1) << 1);
 }
 
-template <int D, bool CAUSAL>
+// A workgroup takes 128 / W query rows of one head, 32 for each of 4 / W pairs
+// (W = 2) or single waves (W = 1).  The waves of a pair have the two halves of
+// every tile's keys and are joined at the end: twice the workgroups with half of
+// the work, for calls with few rows.
+template <int D, bool CAUSAL, int W>
 __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
+    constexpr int kRows = 128 / W, kBlocks = 2 / W;      // blocks of 32 keys of a wave and tile
     constexpr int kTileBytes = kKeys * D * 2;
     constexpr int kRowBytes = D * 2;
     constexpr int kRowsPerLoad = 1024 / kRowBytes;       // rows that one wave-wide load covers
@@ -249,6 +254,7 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
     constexpr int kStages = D == 128 ? 2 : 4;
     __shared__ __attribute__((aligned(1024))) char lds[kStages * 2 * kTileBytes];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), half = lane >> 5, col = lane & 31;
+    const int row_wave = wave / W, first_block = W == 1 ? 0 : wave % W;
 
     // Workgroups go round the 8 XCDs: where the heads divide by 8, each XCD takes
     // the same ones of every tile, so that its L2 holds few heads' keys.
@@ -256,7 +262,7 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
     const int head = a.Hq % 8 == 0 ? (j & 7) * (a.Hq / 8) + (j >> 3) : j;
     const int kvh = head / (a.Hq / a.H);
     int b, tile;
-    if (!find_tile<CAUSAL>(a, rank, &b, &tile)) return;
+    if (!find_tile<CAUSAL, kRows>(a, rank, &b, &tile)) return;
     const int q0 = clamp_row(a.cu_q[b], a.Tq), nq = clamp_row(a.cu_q[b + 1], a.Tq) - q0;
     const int k0 = clamp_row(a.cu_k[b], a.Tk), nk = max(clamp_row(a.cu_k[b + 1], a.Tk) - k0, 0);
     const int row0 = tile * kRows;
@@ -265,7 +271,7 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
     const int off = nk - nq;
     const int kend = CAUSAL ? min(nk, min(row0 + kRows, nq) + off) : nk;  // keys past every row of the workgroup
     const int ntiles = kend > 0 ? (kend + kKeys - 1) / kKeys : 0;
-    const int w0 = row0 + 32 * wave, row = w0 + col;
+    const int w0 = row0 + 32 * row_wave, row = w0 + col;
     const int last = CAUSAL ? min(nk - 1, row + off) : nk - 1;  // the row's last visible key
     const int wlo = CAUSAL ? min(nk - 1, w0 + off) : nk - 1;    // the same of the wave's first and last row
     const int whi = CAUSAL ? min(nk - 1, min(w0 + 31, nq - 1) + off) : nk - 1;
@@ -320,20 +326,20 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
 
     // scores of 4 of the D / 16 channel steps of a 32-key block
     auto score_step = [&](f16_t &s, const char *kt, int kb, int i) {
-        const bf8_t kf = *reinterpret_cast<const bf8_t *>(kt + kb * 32 * kRowBytes + kbase + (((2 * i) ^ (xk & ~1)) << 4));
+        const bf8_t kf = *reinterpret_cast<const bf8_t *>(kt + (first_block + kb) * 32 * kRowBytes + kbase + (((2 * i) ^ (xk & ~1)) << 4));
         s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[i], s, 0, 0, 0);
     };
-    auto scores = [&](f16_t (&s)[2], int t) {
+    auto scores = [&](f16_t (&s)[kBlocks], int t) {
         const char *kt = lds + (2 * (t % kStages)) * kTileBytes;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
+        for (int kb = 0; kb < kBlocks; ++kb) {
             s[kb] = f16_t{};
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) score_step(s[kb], kt, kb, i);
         }
     };
     auto value_step = [&](const char *vt, int u, int i, bf8_t pf) {
-        const char *at = vt + 16 * u * kRowBytes + vbase + (((4 * i) ^ (xv & ~3)) << 4);
+        const char *at = vt + (32 * first_block + 16 * u) * kRowBytes + vbase + (((4 * i) ^ (xv & ~3)) << 4);
         const s4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS s4_t *)at);
         const s4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS s4_t *)(at + 8 * kRowBytes));
         const s8_t vv = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -343,21 +349,20 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
     // Softmax and values of tile t, whose scores are in s, and beside it the
     // scores of tile t + 1 into s: the matrix unit works on one while the
     // vector unit works on the other.
-    auto step = [&](f16_t (&s)[2], int t, auto masked_c, auto next_c) {
+    auto step = [&](f16_t (&s)[kBlocks], int t, auto masked_c, auto next_c) {
         constexpr bool kMasked = decltype(masked_c)::value, kNext = decltype(next_c)::value;
         const char *vt = lds + (2 * (t % kStages) + 1) * kTileBytes, *kt = lds + (2 * ((t + 1) % kStages)) * kTileBytes;
         if (kMasked) {
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
+            for (int kb = 0; kb < kBlocks; ++kb)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    s[kb][r] = 32 * kb + 8 * (r / 4) + (r & 3) > last - t * kKeys - 4 * half ? kNegInf : s[kb][r];
+                    s[kb][r] =
+                        32 * kb + 8 * (r / 4) + (r & 3) > last - t * kKeys - 32 * first_block - 4 * half ? kNegInf : s[kb][r];
         }
         float top = s[0][0];
 #pragma unroll
-        for (int r = 1; r < 16; ++r) top = fmaxf(top, s[0][r]);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[1][r]);
+        for (int i = 1; i < 16 * kBlocks; ++i) top = fmaxf(top, s[i / 16][i % 16]);
         top *= a.scale;
         if (__any(top > m + kSlack)) {
             const float m1 = fmaxf(m, max_halves(top));
@@ -368,10 +373,14 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
             for (int i = 0; i < D / 32; ++i) acc[i] *= f;
         }
         const float ms = m == kNegInf ? 0.0f : m;
-        bf8_t pf[4];
-        f16_t n[2] = {f16_t{}, f16_t{}};
+        bf8_t pf[2 * kBlocks];
+        f16_t n[kBlocks];
+        auto values = [&](int u) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+            for (int i = 0; i < D / 32; ++i) value_step(vt, u, i, pf[u]);
+        };
+#pragma unroll
+        for (int u = 0; u < 2 * kBlocks; ++u) {
             uint32_t p[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -381,26 +390,27 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
                 l = add_pair(p[e], l);
             }
             pf[u] = __builtin_bit_cast(bf8_t, i4_t{(int)p[0], (int)p[1], (int)p[2], (int)p[3]});
-            if (kNext && u < 2) {
+            if (kNext && u < kBlocks) {
+                n[u] = f16_t{};
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) score_step(n[u], kt, u, i);
-            } else if (u >= 2) {
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) value_step(vt, u - 2, i, pf[u - 2]);
+            } else if (u >= kBlocks) {
+                values(u - kBlocks);
             }
         }
 #pragma unroll
-        for (int u = 2; u < 4; ++u)
+        for (int u = kBlocks; u < 2 * kBlocks; ++u) values(u);
+        if (kNext) {
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) value_step(vt, u, i, pf[u]);
-        if (kNext) s[0] = n[0], s[1] = n[1];
+            for (int kb = 0; kb < kBlocks; ++kb) s[kb] = n[kb];
+        }
     };
 
     // The keys run one tile ahead of the values: iteration t reads V of tile t
     // and K of t + 1, and sends for V of t + kStages - 1 and K of t + kStages, into
     // the places that iteration t - 1 has read.
     const int mine = live && whi >= 0 ? whi / kKeys + 1 : 0;  // tiles that a row of the wave sees
-    f16_t s[2];
+    f16_t s[kBlocks];
     fetch_k(0);
 #pragma unroll
     for (int i = 0; i + 1 < kStages; ++i) {
@@ -436,9 +446,36 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
         ++t;
     }
     for (; t < ntiles; ++t) arrive(t);
-    if (!live) return;
-
     l = sum_halves(l);
+    if (W == 2) {  // the second wave of a pair hands its part to the first
+        float *hand = reinterpret_cast<float *>(lds) + row_wave * 32 * (D + 4);
+        float *stat = reinterpret_cast<float *>(lds) + 2 * 32 * (D + 4) + row_wave * 64;
+        wait_vm0();  // the loads past the last tile, which write zeros
+        __syncthreads();
+        if (first_block == 1) {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; r += 4)
+                    *reinterpret_cast<f4_t *>(hand + col * (D + 4) + 32 * i + 2 * r + 4 * half) =
+                        f4_t{acc[i][r], acc[i][r + 1], acc[i][r + 2], acc[i][r + 3]};
+            if (half == 0) stat[col] = m, stat[32 + col] = l;
+        }
+        __syncthreads();
+        if (first_block == 1) return;
+        const float m2 = stat[col], l2 = stat[32 + col], m1 = fmaxf(m, m2);
+        const float f1 = m == kNegInf ? 0.0f : exp2_fast(m - m1), f2 = m2 == kNegInf ? 0.0f : exp2_fast(m2 - m1);
+        l = l * f1 + l2 * f2;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+                const f4_t o = *reinterpret_cast<const f4_t *>(hand + col * (D + 4) + 32 * i + 2 * r + 4 * half);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][r + e] = acc[i][r + e] * f1 + o[e] * f2;
+            }
+    }
+    if (!live) return;
     const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // l NaN stays NaN
     uint16_t *op = a.o + ((int64_t)(q0 + row) * a.Hq + head) * D;
     bool bad = false;
@@ -1437,16 +1474,30 @@ qw3_status qattn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v,
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_q, 4) ||
         !aligned(cu_k, 4) || q_ts % 8 || q_hs % 8 || k_ts % 8 || k_hs % 8 || v_ts % 8 || v_hs % 8)
         return QW3_ERR_ALIGN;
-    const int64_t tiles = Tq / kRows + B;
+    PromptArgs a{q,    k,    v,    out,  cu_q,   cu_k,    q_ts,    q_hs,   k_ts,       k_hs,
+                 v_ts, v_hs, (int)B, (int)Tq, (int)Tk, (int)Hq, (int)H, 0, sm_scale * 1.44269504088896341f};
+    int cus = 0;
+    const qw3_status st = cu_count(&cus);
+    if (st != QW3_OK) return st;
+    // room for every sequence's last, partly filled tile
+    // Halves of 64 rows while 128-row tiles leave CUs with less than two workgroups:
+    // measured at 288 tiles (64 channels, 6511 keys) 85 us whole, 79 halved; at 136
+    // (4000 tokens, 8 heads) 72 and 55; at 1040 (3..2500 tokens, 16 heads) 63 and 75.
+    const bool few = (Tq / 128 + B) * Hq <= 2 * (int64_t)cus;
+    const int64_t tiles = Tq / (few ? 64 : 128) + B;
     if (tiles * Hq > 0x7fffffff) return QW3_ERR_SHAPE;
-    const PromptArgs a{q,    k,    v,    out,  cu_q,   cu_k,    q_ts,    q_hs,   k_ts,       k_hs,
-                       v_ts, v_hs, (int)B, (int)Tq, (int)Tk, (int)Hq, (int)H, (int)tiles, sm_scale * 1.44269504088896341f};
-    const dim3 grid((unsigned)(tiles * Hq));
-    auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, (hipStream_t)hip_stream, a); };
-    if (D == 128)
-        causal ? run(attn_prompt_kernel<128, true>) : run(attn_prompt_kernel<128, false>);
-    else
-        causal ? run(attn_prompt_kernel<64, true>) : run(attn_prompt_kernel<64, false>);
+    a.tiles = (int)tiles;
+    auto run = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles * Hq)), dim3(256), 0, (hipStream_t)hip_stream, a);
+    };
+    auto by_mask = [&](auto d, auto w) {
+        constexpr int kD = decltype(d)::value, kW = decltype(w)::value;
+        causal ? run(attn_prompt_kernel<kD, true, kW>) : run(attn_prompt_kernel<kD, false, kW>);
+    };
+    auto by_rows = [&](auto d) {
+        few ? by_mask(d, std::integral_constant<int, 2>{}) : by_mask(d, std::integral_constant<int, 1>{});
+    };
+    D == 128 ? by_rows(std::integral_constant<int, 128>{}) : by_rows(std::integral_constant<int, 64>{});
     return check_launch();
 }
 

@@ -36,8 +36,7 @@ __global__ __launch_bounds__(256) void cache_write_kernel(const void *__restrict
     // every lane of a row takes the same branch, so the row's exchanges below stay whole
     if (row >= rows) return;
     const uint32_t t = row / (2 * H), wh = row - t * (2 * H), which = wh / H, h = wh - which * H;
-    const int64_t slot = slots[t];
-    if (slot < 0 || slot >= n_slots) return;
+    const int64_t slot = slots[t];  // read beside the row, checked below
     const int64_t at = which ? t * v_ts + h * v_hs : t * k_ts + h * k_hs;
     float x[8];
     if (F32) {
@@ -53,6 +52,7 @@ __global__ __launch_bounds__(256) void cache_write_kernel(const void *__restrict
             x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
+    if (slot < 0 || slot >= n_slots) return;
     // |x| as bits orders like the value, with infinities and NaN on top
     uint32_t top = 0;
 #pragma unroll
