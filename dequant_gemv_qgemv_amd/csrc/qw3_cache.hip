@@ -21,70 +21,127 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // ------------------------------------------------------------------ write --
-// A row is quantised by D / 8 lanes of one wave, 8 channels each; a wave holds
-// 64 / (D / 8) rows.  Rows run over (token, key or value, head), head fastest,
-// so a wave's loads are contiguous wherever the heads of a token are.
+// A row is quantised by D / 16 lanes of one wave, 16 channels each; a workgroup
+// has consecutive tokens of one head, keys and values, so its loads and stores
+// are whole rows, no lane divides to find its row, and both rows' loads are on
+// their way together.  Neighbouring workgroups have the heads of the same tokens:
+// what the card reads at one time lies together in memory.
+//
+// The quotients.  A row's 128 divisions by the same s cost more than all else
+// here.  With r the correctly rounded 1 / s, one division for the row, each
+// quotient is refined by its exact remainder: q = x r; q += (x - q s) r makes it
+// one of the two floats around x / s; q += (x - q s) r the correctly rounded one
+// (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990), where neither r nor a remainder leaves the normal numbers:
+// rows with s outside 2^-80..2^100 divide.  So codes are those of the IEEE
+// quotient for every input.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t codes4(const float (&y)[4]) {
+    if (E4M3) {
+        const int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
+    }
+    // 1.5 2^23 + y is rounded to a whole number, whose two's complement is its low byte
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(y[i] + 12582912.0f);
+    const uint32_t lo = __builtin_amdgcn_perm(w[1], w[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(w[3], w[2], 0x04000c0cu);
+    return lo | hi;
+}
+
+template <bool F32>
+struct Source {
+    uint4 w[F32 ? 4 : 2];
+    __device__ __forceinline__ void load(const void *p, int64_t at, int c) {
+        const uint4 *src = F32 ? reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + at)
+                               : reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at);
+#pragma unroll
+        for (int i = 0; i < (F32 ? 4 : 2); ++i) w[i] = src[(F32 ? 4 : 2) * c + i];
+    }
+    __device__ __forceinline__ void values(float (&x)[16]) const {
+#pragma unroll
+        for (int i = 0; i < (F32 ? 4 : 2); ++i) {
+            const uint32_t d[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (F32) {
+                    x[4 * i + e] = __uint_as_float(d[e]);
+                } else {
+                    x[8 * i + 2 * e] = __uint_as_float(d[e] << 16);
+                    x[8 * i + 2 * e + 1] = __uint_as_float(d[e] & 0xffff0000u);
+                }
+            }
+        }
+    }
+};
+
+template <int D, bool F32, bool E4M3>
+__device__ __forceinline__ float quantise(const Source<F32> &src, uint32_t (&out)[4]) {
+    constexpr int kLanes = D / 16;
+    constexpr float kLimit = E4M3 ? 448.0f : 127.0f;
+    float x[16];
+    src.values(x);
+    // |x| as bits orders like the value, with infinities and NaN on top
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+#pragma unroll
+    for (int m = kLanes / 2; m >= 1; m /= 2) top = max(top, (uint32_t)__shfl_xor((int)top, m, 64));
+    const bool finite = top < 0x7f800000u;
+    const float s = finite ? __uint_as_float(top) / kLimit : __uint_as_float(0x7fc00000u);
+    if (s > 0x1p-80f && s < 0x1p100f) {
+        const float r = 1.0f / s;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float v = x[4 * i + e];
+                float q = v * r;
+                q = fmaf(fmaf(-q, s, v), r, q);
+                y[e] = fmaf(fmaf(-q, s, v), r, q);
+            }
+            out[i] = codes4<E4M3>(y);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float y[4];
+            // past L only where s is a denormal and a / L was rounded down; no s, no codes
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = s > 0.0f ? fminf(fmaxf(x[4 * i + e] / s, -kLimit), kLimit) : 0.0f;
+            out[i] = codes4<E4M3>(y);
+        }
+    }
+    return s;
+}
+
 template <int D, bool F32, bool E4M3>
 __global__ __launch_bounds__(256) void cache_write_kernel(const void *__restrict__ k, const void *__restrict__ v,
                                                           const int64_t *__restrict__ slots,
                                                           uint8_t *__restrict__ codes, float *__restrict__ scales,
-                                                          uint32_t rows, uint32_t H, int page_shift, int64_t n_slots,
-                                                          int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs) {
-    constexpr uint32_t kLanes = D / 8;
-    const uint32_t row = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
-    const uint32_t c = threadIdx.x % kLanes;
-    // every lane of a row takes the same branch, so the row's exchanges below stay whole
-    if (row >= rows) return;
-    const uint32_t t = row / (2 * H), wh = row - t * (2 * H), which = wh / H, h = wh - which * H;
-    const int64_t slot = slots[t];  // read beside the row, checked below
-    const int64_t at = which ? t * v_ts + h * v_hs : t * k_ts + h * k_hs;
-    float x[8];
-    if (F32) {
-        const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(which ? v : k) + at) + 2 * c;
-        const float4 a = src[0], b = src[1];
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-        const uint4 a = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(which ? v : k) + at)[c];
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    }
+                                                          int T, int H, int page_shift, int64_t n_slots, int64_t k_ts,
+                                                          int64_t k_hs, int64_t v_ts, int64_t v_hs) {
+    constexpr int kLanes = D / 16;
+    const int group = (int)(blockIdx.x / (uint32_t)H), h = (int)blockIdx.x - group * H;
+    const int t = group * (256 / kLanes) + threadIdx.x / kLanes, c = threadIdx.x % kLanes;
+    // every lane of a row takes the same branch, so the row's exchanges stay whole
+    if (t >= T) return;
+    const int64_t slot = slots[t];
+    Source<F32> kx, vx;
+    kx.load(k, t * k_ts + h * k_hs, c);
+    vx.load(v, t * v_ts + h * v_hs, c);
     if (slot < 0 || slot >= n_slots) return;
-    // |x| as bits orders like the value, with infinities and NaN on top
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-#pragma unroll
-    for (int m = kLanes / 2; m >= 1; m /= 2) top = max(top, (uint32_t)__shfl_xor((int)top, m, 64));
-    const bool finite = top < 0x7f800000u;
-    const float s = finite ? __uint_as_float(top) / (E4M3 ? 448.0f : 127.0f) : __uint_as_float(0x7fc00000u);
-    uint32_t out[2] = {0, 0};
-    if (s > 0.0f) {
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            // the quotient can pass L only where s is a denormal and a / L was rounded down
-            const float lim = E4M3 ? 448.0f : 127.0f;
-            y[i] = fminf(fmaxf(x[i] / s, -lim), lim);
-        }
-        if (E4M3) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i], y[4 * i + 1], 0, false);
-                out[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2], y[4 * i + 3], w, true);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) out[i / 4] |= ((uint32_t)(int)rintf(y[i]) & 0xffu) << (8 * (i % 4));
-        }
-    }
     const int64_t page = slot >> page_shift;
-    const int64_t at_row = (((page * 2 + which) * H + h) << page_shift) + (slot - (page << page_shift));
-    reinterpret_cast<uint2 *>(codes + at_row * D)[c] = make_uint2(out[0], out[1]);
-    if (c == 0) scales[at_row] = s;
+    const int64_t at = ((page * 2 * H + h) << page_shift) + (slot - (page << page_shift));
+    const int64_t to_v = (int64_t)H << page_shift;
+    uint32_t out[4];
+    const float ks = quantise<D, F32, E4M3>(kx, out);
+    reinterpret_cast<uint4 *>(codes + at * D)[c] = make_uint4(out[0], out[1], out[2], out[3]);
+    if (c == 0) scales[at] = ks;
+    const float vs = quantise<D, F32, E4M3>(vx, out);
+    reinterpret_cast<uint4 *>(codes + (at + to_v) * D)[c] = make_uint4(out[0], out[1], out[2], out[3]);
+    if (c == 0) scales[at + to_v] = vs;
 }
 
 // ------------------------------------------------------------------- read --
@@ -166,11 +223,10 @@ qw3_status qcache_write(const void *k, const void *v, int32_t src_type, const in
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(slots, 8) ||
         k_ts % per || k_hs % per || v_ts % per || v_hs % per)
         return QW3_ERR_ALIGN;
-    const uint32_t rows = (uint32_t)(T * 2 * H);
-    const dim3 grid((unsigned)ceil_div(rows, 256 / (D / 8)));
+    const dim3 grid((unsigned)(ceil_div(T, 256 / (D / 16)) * H));
     auto run = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(256), 0, (hipStream_t)hip_stream, k, v, slots, (uint8_t *)codes, scales,
-                           rows, (uint32_t)H, shift, pages * page_size, k_ts, k_hs, v_ts, v_hs);
+                           (int)T, (int)H, shift, pages * page_size, k_ts, k_hs, v_ts, v_hs);
     };
     auto by_type = [&](auto d) {
         constexpr int kD = decltype(d)::value;
