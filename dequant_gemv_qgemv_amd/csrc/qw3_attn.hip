@@ -531,55 +531,50 @@ constexpr int kSetup = 2;  // what beginning and ending an item costs, in units
 // host.
 template <int R>
 struct Seq {
-    int q0, nq, len, blocks;
-    int64_t per_item, units;
+    int q0, nq, len, blocks, per_item, units;
     __device__ Seq() {}
     __device__ Seq(const CacheArgs &a, int b) {
         q0 = a.cu_q ? clamp_row(a.cu_q[b], a.Tq) : min(b, a.Tq);
         nq = (a.cu_q ? clamp_row(a.cu_q[b + 1], a.Tq) : min(b + 1, a.Tq)) - q0;
         nq = max(nq, 0);
         len = a.pages == 0 ? 0 : (int)max((int64_t)0, min((int64_t)a.lens[b], a.max_pages << a.page_shift));
-        blocks = (int)(((int64_t)nq * a.G + R - 1) / R);
-        per_item = kSetup + max((len + (int64_t)unit_of(R) - 1) / unit_of(R), (int64_t)1);
+        blocks = (nq * a.G + R - 1) / R;
+        per_item = kSetup + max((len + unit_of(R) - 1) / unit_of(R), 1);
         units = per_item * blocks * a.H;
     }
 };
 
-__device__ __forceinline__ int64_t wave_scan(int64_t x) {  // inclusive prefix sum over the wave
-    const int lane = threadIdx.x & 63;
-    for (int d = 1; d < 64; d *= 2) {
-        const int64_t y = __shfl_up(x, d, 64);
-        if (lane >= d) x += y;
-    }
+__device__ __forceinline__ int wave_scan(int x) {  // inclusive prefix sum over the wave
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, kDppRowBcast15, 0xA, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, kDppRowBcast31, 0xC, 0xF, false);
     return x;
-}
-
-__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {  // of values >= 0, mostly below 2^32
-    return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
 }
 
 // A workgroup's run of units: [u, end) of the call's total, beginning in
 // sequence b, before which there are `before` units.
 struct Run {
-    int64_t per, u, end, before;
-    int b;
+    int per, u, end, before, b;
 };
 template <int R>
 __device__ __forceinline__ Run find_run(const CacheArgs &a) {
     const int lane = threadIdx.x & 63;
     Run run;
-    int64_t total = 0, mine = 0, upto = 0;
+    int total = 0, mine = 0, upto = 0;
     for (int base = 0; base < a.B; base += 64) {
         mine = base + lane < a.B ? Seq<R>(a, base + lane).units : 0;
-        upto = total + (a.B > 1 ? wave_scan(mine) : mine);
-        total = uniform((int64_t)__shfl(upto, min(63, a.B - 1 - base), 64));
+        upto = total + wave_scan(mine);
+        total = __builtin_amdgcn_readlane(upto, 63);
     }
-    run.per = max((total + a.groups - 1) / a.groups, (int64_t)1);
-    run.u = blockIdx.x * run.per;
+    run.per = max((total + a.groups - 1) / a.groups, 1);
+    run.u = min((int64_t)blockIdx.x * run.per, (int64_t)total);
     run.end = min(run.u + run.per, total);
     run.b = 0, run.before = 0;
     if (run.u >= run.end || a.B == 1) return run;
-    int64_t done = 0;
+    int done = 0;
     for (int base = 0; base < a.B; base += 64) {
         if (a.B > 64) {
             mine = base + lane < a.B ? Seq<R>(a, base + lane).units : 0;
@@ -587,12 +582,12 @@ __device__ __forceinline__ Run find_run(const CacheArgs &a) {
         }
         const unsigned long long past = __ballot(upto > run.u);
         if (past) {
-            const int at = __builtin_ctzll(past);
-            run.b = uniform(base + at);
-            run.before = uniform((int64_t)__shfl(upto - mine, at, 64));
+            const int at = uniform(__builtin_ctzll(past));
+            run.b = base + at;
+            run.before = __builtin_amdgcn_readlane(upto - mine, at);
             break;
         }
-        done = uniform((int64_t)__shfl(upto, 63, 64));
+        done = __builtin_amdgcn_readlane(upto, 63);
     }
     return run;
 }
@@ -606,8 +601,8 @@ __device__ __forceinline__ Run find_run(const CacheArgs &a) {
 // The count belongs to the first workgroup of the item, and the joining
 // workgroup sets it back to zero for the next call.
 template <int R, int D>
-__device__ __forceinline__ float *partial(const CacheArgs &a, int64_t group, int which) {
-    return a.part + (group * 2 + which) * (int64_t)(R * (D + 2));
+__device__ __forceinline__ float *partial(const CacheArgs &a, int group, int which) {
+    return a.part + (int64_t)(group * 2 + which) * (R * (D + 2));
 }
 __device__ __forceinline__ void store_agent(float *p, float x, float y) {
     const uint64_t v = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
@@ -643,6 +638,22 @@ __device__ __forceinline__ void join_rows(const CacheArgs &a, const float *from,
         float2 ml[kRowsOfWave];
 #pragma unroll
         for (int k = 0; k < kRowsOfWave; ++k) ml[k] = load_agent(mine + 2 * min(wave + 4 * k, rows - 1));
+        float2 part[kBatch][kRowsOfWave];
+        auto read = [&](int i0) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const float *p = slot(min(i0 + i, n - 1)) + 2 * R;
+#pragma unroll
+                for (int k = 0; k < kRowsOfWave; ++k) {
+                    const int at = min(wave + 4 * k, rows - 1) * D;
+                    if (D == 128)
+                        part[i][k] = load_agent(p + at + 2 * lane);
+                    else
+                        part[i][k].x = __hip_atomic_load(p + at + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                }
+            }
+        };
+        read(0);  // beside the maxima and sums
 #pragma unroll
         for (int k = 0; k < kRowsOfWave; ++k) {
             float m1 = lane < n ? ml[k].x : kNegInf;
@@ -657,19 +668,7 @@ __device__ __forceinline__ void join_rows(const CacheArgs &a, const float *from,
             acc[k].x *= old, acc[k].y *= old;
         }
         for (int i0 = 0; i0 < n; i0 += kBatch) {
-            float2 part[kBatch][kRowsOfWave];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const float *p = slot(min(i0 + i, n - 1)) + 2 * R;
-#pragma unroll
-                for (int k = 0; k < kRowsOfWave; ++k) {
-                    const int at = min(wave + 4 * k, rows - 1) * D;
-                    if (D == 128)
-                        part[i][k] = load_agent(p + at + 2 * lane);
-                    else
-                        part[i][k].x = __hip_atomic_load(p + at + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                }
-            }
+            if (i0 > 0) read(i0);
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
 #pragma unroll
@@ -764,7 +763,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
     // the portion of an item that is worked on: units t0.. of it, for the rows
     // r0.. of kv head h of a sequence, the wave's keys 32 from key0 + 128 s in step s
     int h, r0, rows, q0, len, ctx, key0, steps;
-    int64_t ustart, count;  // the item's first unit; units of the portion
+    int ustart, count;  // the item's first unit; units of the portion
     const int32_t *table;
     auto locate = [&]() {
         while (run.u - run.before >= seq.units) {  // next sequence (some have no rows)
@@ -772,19 +771,18 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
             ++run.b;
             seq = Seq<R>(a, run.b);
         }
-        const int64_t local = run.u - run.before, item = quotient(local, seq.per_item);
-        const int64_t begin = run.before + item * seq.per_item;
+        const int item = (int)((uint32_t)(run.u - run.before) / (uint32_t)seq.per_item);
+        const int begin = run.before + item * seq.per_item;
         ustart = begin + kSetup;
         run.u = max(run.u, ustart);
-        const int64_t t0 = run.u - ustart;
+        const int t0 = run.u - ustart;
         count = min(begin + seq.per_item, run.end) - run.u;
         if (count <= 0) return false;  // the run ends before the item's first keys
-        h = (int)quotient(item, seq.blocks);
-        r0 = (int)(item - (int64_t)h * seq.blocks) * R;
+        h = (int)((uint32_t)item / (uint32_t)seq.blocks);
+        r0 = (item - h * seq.blocks) * R;
         rows = seq.nq * a.G, q0 = seq.q0, len = seq.len, ctx = len - seq.nq;
-        key0 = (int)t0 * kUnit + 32 * wave;
-        const int64_t room = (int64_t)len - key0;
-        steps = room <= 0 ? 0 : (int)min(count, (room + kUnit - 1) / kUnit);
+        key0 = t0 * kUnit + 32 * wave;
+        steps = len <= key0 ? 0 : min(count, (len - key0 + kUnit - 1) / kUnit);
         table = a.table + (int64_t)run.b * a.max_pages;
         return true;
     };
@@ -991,12 +989,12 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
 
         // the next portion's page numbers and then its first loads are on their way
         // while this one's waves are joined
-        const int64_t first = quotient(ustart, run.per);
-        const Shared done = {(int)first, (int)quotient(ustart + seq.per_item - kSetup - 1, run.per),
+        const int first = (int)((uint32_t)ustart / (uint32_t)run.per);
+        const Shared done = {first, (int)((uint32_t)(ustart + seq.per_item - kSetup - 1) / (uint32_t)run.per),
                              first * run.per == ustart ? 0 : 1, h, r0, min(R, rows - r0), q0};
         float *out = nullptr;
         if (done.first != done.last) {
-            out = partial<R, D>(a, blockIdx.x, first < blockIdx.x || first * run.per == ustart ? 0 : 1);
+            out = partial<R, D>(a, blockIdx.x, first < (int)blockIdx.x || first * run.per == ustart ? 0 : 1);
             if (nshared == 0)
                 shared[0] = done;
             else
@@ -1111,15 +1109,15 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(CacheArgs a) {
             ++run.b;
             seq = Seq<R>(a, run.b);
         }
-        const int64_t local = run.u - run.before, item = quotient(local, seq.per_item);
-        const int64_t begin = run.before + item * seq.per_item, ustart = begin + kSetup;
+        const int item = (int)((uint32_t)(run.u - run.before) / (uint32_t)seq.per_item);
+        const int begin = run.before + item * seq.per_item, ustart = begin + kSetup;
         run.u = max(run.u, ustart);
-        const int64_t t0 = run.u - ustart, count = min(begin + seq.per_item, run.end) - run.u;
+        const int t0 = run.u - ustart, count = min(begin + seq.per_item, run.end) - run.u;
         if (count <= 0) break;  // the run ends before the item's first keys
-        const int h = (int)quotient(item, seq.blocks), r0 = (int)(item - (int64_t)h * seq.blocks) * R;
+        const int h = (int)((uint32_t)item / (uint32_t)seq.blocks), r0 = (item - h * seq.blocks) * R;
         const int rows = seq.nq * a.G, q0 = seq.q0, len = seq.len, ctx = len - seq.nq;
-        const int key0 = (int)t0 * kUnit;
-        const int tiles = (int)min(count, ((int64_t)len - key0 + kUnit - 1) / kUnit);
+        const int key0 = t0 * kUnit;
+        const int tiles = min(count, (len - key0 + kUnit - 1) / kUnit);
         const int32_t *table = a.table + (int64_t)run.b * a.max_pages;
 
         // page numbers of 16 tiles: lane 4 t + g has the one of 16-key group g of tile t
@@ -1291,11 +1289,12 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(CacheArgs a) {
         for (; t < plain && gone == 0; ++t) iteration(t, std::false_type{});
         for (; t < tiles; ++t) iteration(t, std::true_type{});
 
-        const int64_t first = quotient(ustart, run.per), last = quotient(begin + seq.per_item - 1, run.per);
+        const int first = (int)((uint32_t)ustart / (uint32_t)run.per);
+        const int last = (int)((uint32_t)(begin + seq.per_item - 1) / (uint32_t)run.per);
         float *out = nullptr;
         if (first != last) {
-            out = partial<R, D>(a, blockIdx.x, first < blockIdx.x || first * run.per == ustart ? 0 : 1);
-            const Shared mine = {(int)first, (int)last, first * run.per == ustart ? 0 : 1, h, r0, min(R, rows - r0), q0};
+            out = partial<R, D>(a, blockIdx.x, first < (int)blockIdx.x || first * run.per == ustart ? 0 : 1);
+            const Shared mine = {first, last, first * run.per == ustart ? 0 : 1, h, r0, min(R, rows - r0), q0};
             if (nshared == 0)
                 shared[0] = mine;
             else
@@ -1386,6 +1385,10 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(CacheArgs a) {
 
 template <int D, bool E4M3, int R>
 qw3_status launch_cache(CacheArgs a, hipStream_t stream) {
+    // units of work are counted in 31 bits: a bound on them from what the host knows
+    const int64_t most = ceil_div((a.max_pages << a.page_shift) + unit_of(R), unit_of(R)) + kSetup;
+    const int64_t items = ((int64_t)a.Tq * a.G / R + a.B) * a.H;
+    if (most > 0x7fffffff / (items + 1)) return QW3_ERR_SHAPE;
     int cus = 0;
     qw3_status st = cu_count(&cus);
     if (st != QW3_OK) return st;
