@@ -49,6 +49,7 @@ def test_cache_shapes(call, bad):
     (read, dict(B=-1)), (read, dict(B=1 << 20)), (read, dict(total=-1)), (read, dict(total=1 << 31)), (read, dict(maxp=-1)),
     (cache, dict(B=-1)), (cache, dict(B=1 << 20)), (cache, dict(Tq=-1)), (cache, dict(Tq=1 << 27)), (cache, dict(Hq=7)),
     (cache, dict(Hq=0)), (cache, dict(maxp=-1)), (cache, dict(maxp=1 << 27)), (cache, dict(sm=0.0)), (cache, dict(sm=-1.0)),
+    (cache, dict(B=60000, Tq=1 << 20, maxp=1 << 20)),  # more work than is counted in 31 bits
     (cache, dict(sm=float("inf"))), (cache, dict(sm=float("nan"))), (cache, dict(ts=-8)), (cache, dict(cu=NULL)),
     (prompt, dict(D=80)), (prompt, dict(H=0)), (prompt, dict(Hq=9)), (prompt, dict(B=-1)), (prompt, dict(B=1 << 20)),
     (prompt, dict(Tq=-1)), (prompt, dict(Tk=-1)), (prompt, dict(Tk=1 << 27)), (prompt, dict(sm=0.0)),

@@ -105,6 +105,36 @@ def test_write_is_exact(kind, src, tokens, heads, dim, page):
     assert np.array_equal(got_c, want_c)
 
 
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+def test_quotients_at_rounding_boundaries(kind):
+    """Elements within a few floats of a boundary between two codes, for many scales, tiny and huge ones among them:
+    codes are those of the correctly rounded quotient."""
+    rng = np.random.default_rng(23)
+    tokens, heads, dim = 600, 1, 128
+    limit = np.float32(ref.LIMIT[kind])
+    if kind == "int8":
+        middle = rng.integers(-127, 127, (tokens, heads, dim)) + 0.5
+    else:
+        v = ref.e4m3_table()[:127]
+        at = rng.integers(0, 126, (tokens, heads, dim))
+        middle = (v[at] + v[at + 1]) / 2 * rng.choice([-1, 1], at.shape)
+    top = (limit * np.exp2(rng.integers(-100, 100, (tokens, heads, 1))) * rng.uniform(0.6, 1.9, (tokens, heads, 1))).astype(np.float32)
+    scale = top / limit
+    x = (middle * scale).astype(np.float32)
+    for _ in range(3):
+        x = np.nextafter(x, np.where(rng.random(x.shape) < 0.5, -np.inf, np.inf).astype(np.float32))
+    x[:, :, 0] = top[:, :, 0]
+    codes, scales = q().new_cache(tokens // 16 + 1, 16, heads, dim, TORCH[kind])
+    k = torch.tensor(x).cuda()
+    q().qcache_write(k, k, torch.arange(tokens, device="cuda"), codes, scales)
+    want_c, want_s = ref.quantise(x, kind)
+    got = codes.view(torch.uint8).cpu().numpy()[:, 0].transpose(0, 2, 1, 3).reshape(-1, heads, dim)[:tokens]
+    got_s = scales.cpu().numpy()[:, 0].transpose(0, 2, 1).reshape(-1, heads)[:tokens]
+    if kind == "e4m3":
+        got, want_c = np.where(got == 0x80, 0, got), np.where(want_c == 0x80, 0, want_c)
+    assert np.array_equal(got_s, want_s) and np.array_equal(got, want_c)
+
+
 def random_cache(rng, kind, pages, page, heads, dim):
     raw = torch.tensor(rng.integers(0, 256, (pages, 2, heads, page, dim)), dtype=torch.uint8)
     if kind == "int8":
@@ -227,6 +257,8 @@ def test_single_tokens(kind, dim, heads, group, page, lens):
     ("int8", 1, 8, 128, 16, [90, 64], [64, 33]),             # 64-row blocks, several per sequence
     ("e4m3", 2, 3, 128, 64, [129, 40, 31], [31, 0, 31]),     # a sequence with no new token, one with no context
     ("int8", 1, 1, 64, 16, [7, 5, 0, 100], [7, 9, 2, 70]),   # more new tokens than cached ones; more than 64
+    ("e4m3", 1, 8, 64, 32, [100, 65, 17], [30, 9, 17]),      # 128-row blocks, e4m3 codes
+    ("e4m3", 2, 5, 128, 16, [63, 200, 1], [40, 13, 1]),
 ])
 def test_drafts(tree, kind, heads, group, dim, page, lens, news):
     say("drafts", tree, kind, heads, group, dim, page, lens, news)
@@ -244,6 +276,14 @@ def test_many_sequences():
 def test_a_long_sequence_beside_short_ones():
     cache_case(np.random.default_rng(4), "int8", 1, 8, 128, 16, [20000, 3, 700], 1, False)
     cache_case(np.random.default_rng(5), "e4m3", 2, 2, 64, 64, [9000, 70], [3, 5], True)
+    cache_case(np.random.default_rng(55), "int8", 1, 24, 64, 32, [7000, 40, 900], [4, 3, 4], True)
+
+
+def test_many_rows_of_many_sequences():
+    """128-row blocks: items that share a workgroup, and items that several share."""
+    rng = np.random.default_rng(56)
+    lens = [int(x) for x in rng.integers(0, 90, 70)]
+    cache_case(rng, "int8", 1, 33, 64, 16, lens, [int(x) for x in rng.integers(1, 4, 70)], False)
 
 
 @pytest.mark.parametrize("scale", [0.01, 1.0, 40.0])
@@ -252,7 +292,8 @@ def test_other_scales(scale):
     cache_case(np.random.default_rng(6), "int8", 2, 4, 128, 16, [200, 37], 2, True, scale=scale)
 
 
-def test_what_is_hidden_has_no_influence():
+@pytest.mark.parametrize("group", [4, 20])
+def test_what_is_hidden_has_no_influence(group):
     """NaN scales of hidden drafts, garbage past the end (codes that are NaN in e4m3 too) and missing pages."""
     def touch(codes, scales, table, rq, words):
         raw = codes.view(torch.uint8)
@@ -269,25 +310,27 @@ def test_what_is_hidden_has_no_influence():
         table[2, 1] = -5
 
     for kind in ("int8", "e4m3"):
-        cache_case(np.random.default_rng(7), kind, 2, 4, 128, 16, [50, 40, 60], 4, True, touch=touch)
+        cache_case(np.random.default_rng(7), kind, 2, group, 128, 16, [50, 40, 60], 4, True, touch=touch)
 
 
-def test_nan_and_zero_rows_that_are_seen():
+@pytest.mark.parametrize("group", [2, 66])
+def test_nan_and_zero_rows_that_are_seen(group):
     def touch(codes, scales, table, rq, words):
         scales[int(table[0, 0]), 0, 0, 3] = float("nan")   # a key of head 0
         scales[int(table[1, 0]), 1, 1, 3] = float("nan")   # a value of head 1
         scales[int(table[2, 0])] = 0.0                     # rows of zeros
 
-    cache_case(np.random.default_rng(8), "int8", 2, 2, 64, 16, [20, 20, 16], 1, False, touch=touch)
+    cache_case(np.random.default_rng(8), "int8", 2, group, 64, 16, [20, 20, 16], 1, False, touch=touch)
 
 
-def test_scales_of_very_different_sizes():
+@pytest.mark.parametrize("group", [8, 66])
+def test_scales_of_very_different_sizes(group):
     """Value scales over 2^40: each weight is rounded relative to itself."""
     def touch(codes, scales, table, rq, words):
         e = torch.tensor(np.random.default_rng(1).integers(-20, 20, tuple(scales[:, 1].shape)), device="cuda")
         scales[:, 1] = torch.exp2(e.float())
 
-    cache_case(np.random.default_rng(9), "int8", 1, 8, 128, 16, [333], 1, False, touch=touch)
+    cache_case(np.random.default_rng(9), "int8", 1, group, 128, 16, [333], 1, False, touch=touch)
 
 
 def test_cache_beyond_4_gib():
@@ -509,6 +552,41 @@ def test_a_product_between_two_attention_calls():
     for _ in range(3):
         assert np.array_equal(want, bits(q().qattn_cache(rq, **c)))
         assert torch.equal(y, q().qgemm_w3g128_smallM(x, packed, s))
+
+
+@pytest.mark.parametrize("rows_per_head", [1, 40])
+def test_starts_and_lengths_out_of_range_are_clipped(rows_per_head):
+    """Starts past the rows, decreasing or negative; lengths past the table: nothing outside the arrays is touched."""
+    rng = np.random.default_rng(24)
+    codes, scales = random_cache(rng, "int8", 8, 16, 2, 64)
+    table = tables(rng, [30, 40, 20], 16, 8)
+    heads = 2 * rows_per_head
+    rq = rows(rng, 9, heads, 64)
+    guard = torch.full((9 + 4, heads, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    for cu in ([0, 2000, 4, 9], [-7, 3, 3, 1 << 30], [5, 2, 9, 9]):
+        c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        lens = torch.tensor([30, 1 << 30, -4], dtype=torch.int32, device="cuda")
+        q().qattn_cache(rq, codes, scales, table, lens, cu_q=c, out=guard[:9])
+        k = rows(rng, 9, 2, 64)
+        q().qattn_prompt(rq, k, k, c, out=guard[:9])
+        q().qattn_prompt(rq, k, k, c, causal=False, out=guard[:9])
+        out = [torch.full((13, 2, 64), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        q().qcache_read(codes, scales, table, c, 9, out=[t[:9] for t in out])
+        torch.cuda.synchronize()
+        assert (guard[9:] == 5).all() and all((t[9:] == 5).all() for t in out)
+
+
+@pytest.mark.parametrize("codes", [torch.int8, torch.float8_e4m3fn])
+def test_example(codes):
+    """The four calls together, as a server uses them: prompts in chunks, a drafted tree, the accepted path."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "attention_block.py")
+    spec = importlib.util.spec_from_file_location("attention_block", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    # 8-bit keys and values: int8 rounds by up to 1/254 of a row's largest element, e4m3 an element by up to 1/16
+    assert mod.demo(codes=codes, verbose=False) < (0.02 if codes is torch.int8 else 0.08)
 
 
 def test_refusals_on_the_gpu():
