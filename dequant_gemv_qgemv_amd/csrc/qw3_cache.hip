@@ -147,8 +147,10 @@ __global__ __launch_bounds__(256) void cache_write_kernel(const void *__restrict
 // ------------------------------------------------------------------- read --
 // A workgroup reads 16 consecutive rows of the packed output for every head,
 // of the keys or of the values; lanes run over a row's 16-byte pieces, then
-// over the tokens, so loads follow a page's tokens.
-template <int D, bool E4M3>
+// over the tokens, so loads follow a page's tokens.  kAtOnce heads' rows are on
+// their way together: 4 for many rows (60,000 tokens of 8 heads 119 us, 128 with
+// 1), 1 where a CU has only a few workgroups (8191 tokens 10 us, 11 with 4).
+template <int D, bool E4M3, int kAtOnce>
 __global__ __launch_bounds__(256) void cache_read_kernel(const uint8_t *__restrict__ codes,
                                                          const float *__restrict__ scales,
                                                          const int32_t *__restrict__ table,
@@ -176,32 +178,42 @@ __global__ __launch_bounds__(256) void cache_read_kernel(const uint8_t *__restri
     if (!there) page = 0;
     const int64_t row0 = ((page * 2 + which) * H << page_shift) + (pos & ((int64_t(1) << page_shift) - 1));
     uint16_t *out = (which ? v_out : k_out) + t * H * D + piece * 16;
-    for (int h = threadIdx.x / (16 * kPieces); h < H; h += 256 / (16 * kPieces)) {
-        const int64_t row = row0 + ((int64_t)h << page_shift);
-        uint4 c = make_uint4(0, 0, 0, 0);
-        float s = 0.0f;
-        if (there) {
-            c = *reinterpret_cast<const uint4 *>(codes + row * D + piece * 16);
-            s = scales[row];
-        }
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-        uint32_t o[8];
+    constexpr int kStep = 256 / (16 * kPieces);
+    for (int h0 = threadIdx.x / (16 * kPieces); h0 < H; h0 += kStep * kAtOnce) {
+        uint4 c[kAtOnce];
+        float s[kAtOnce];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float f[4];
-            if (E4M3) {
-                f[0] = __builtin_amdgcn_cvt_f32_fp8(w[i], 0), f[1] = __builtin_amdgcn_cvt_f32_fp8(w[i], 1);
-                f[2] = __builtin_amdgcn_cvt_f32_fp8(w[i], 2), f[3] = __builtin_amdgcn_cvt_f32_fp8(w[i], 3);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) f[j] = (float)(int8_t)(w[i] >> (8 * j));
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int64_t row = row0 + ((int64_t)(h0 + kStep * i) << page_shift);
+            c[i] = make_uint4(0, 0, 0, 0), s[i] = 0.0f;
+            if (there && h0 + kStep * i < H) {
+                c[i] = *reinterpret_cast<const uint4 *>(codes + row * D + piece * 16);
+                s[i] = scales[row];
             }
-            o[2 * i] = pack_bf16(f[0] * s, f[1] * s);
-            o[2 * i + 1] = pack_bf16(f[2] * s, f[3] * s);
         }
-        uint4 *dst = reinterpret_cast<uint4 *>(out + (int64_t)h * D);
-        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float f[4];
+                if (E4M3) {
+                    f[0] = __builtin_amdgcn_cvt_f32_fp8(w[j], 0), f[1] = __builtin_amdgcn_cvt_f32_fp8(w[j], 1);
+                    f[2] = __builtin_amdgcn_cvt_f32_fp8(w[j], 2), f[3] = __builtin_amdgcn_cvt_f32_fp8(w[j], 3);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[e] = (float)(int8_t)(w[j] >> (8 * e));
+                }
+                o[2 * j] = pack_bf16(f[0] * s[i], f[1] * s[i]);
+                o[2 * j + 1] = pack_bf16(f[2] * s[i], f[3] * s[i]);
+            }
+            if (h0 + kStep * i < H) {
+                uint4 *dst = reinterpret_cast<uint4 *>(out + (int64_t)(h0 + kStep * i) * D);
+                dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+        }
     }
 }
 
@@ -259,10 +271,15 @@ qw3_status qcache_read(const void *codes, const float *scales, int32_t code_type
         hipLaunchKernelGGL(kernel, grid, dim3(256), 0, (hipStream_t)hip_stream, (const uint8_t *)codes, scales,
                            block_table, cu, k_out, v_out, (int)B, max_pages, pages, total, (int)H, shift);
     };
-    if (D == 128)
-        code_type == QW3_CODES_E4M3 ? run(cache_read_kernel<128, true>) : run(cache_read_kernel<128, false>);
-    else
-        code_type == QW3_CODES_E4M3 ? run(cache_read_kernel<64, true>) : run(cache_read_kernel<64, false>);
+    auto by_size = [&](auto d, auto type) {
+        constexpr int kD = decltype(d)::value;
+        constexpr bool kType = decltype(type)::value;
+        total >= 16384 ? run(cache_read_kernel<kD, kType, 4>) : run(cache_read_kernel<kD, kType, 1>);
+    };
+    auto by_type = [&](auto d) {
+        code_type == QW3_CODES_E4M3 ? by_size(d, std::true_type{}) : by_size(d, std::false_type{});
+    };
+    D == 128 ? by_type(std::integral_constant<int, 128>{}) : by_type(std::integral_constant<int, 64>{});
     return check_launch();
 }
 

@@ -160,7 +160,8 @@ def tables(rng, lens, page, pages, spare=1):
 
 @pytest.mark.parametrize("kind,heads,dim,page,lens", [
     ("int8", 1, 64, 16, [1]), ("int8", 8, 128, 16, [0, 17, 0, 1, 130, 15]), ("e4m3", 3, 128, 64, [63, 64, 65]),
-    ("e4m3", 5, 64, 32, [33] * 70), ("int8", 2, 128, 128, [500, 3])])
+    ("e4m3", 5, 64, 32, [33] * 70), ("int8", 2, 128, 128, [500, 3]),
+    ("int8", 3, 64, 32, [9001, 5, 7500])])
 def test_read_is_exact(kind, heads, dim, page, lens):
     say("read", kind, heads, dim, page, lens[:8])
     rng = np.random.default_rng(len(lens))
