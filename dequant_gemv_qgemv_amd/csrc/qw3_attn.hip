@@ -1077,16 +1077,17 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
     }
 }
 
-// Many rows: R = 128 query rows of an item, 32 for each of 4 waves, which share
-// tiles of 64 keys.  The tile's codes come through registers a tile ahead and
-// are turned into bf16 once for all waves; the rest is attn_prompt_kernel's.
+// Many rows: R = 128 or 256 query rows of an item, 32 for each wave; the waves
+// share tiles of 64 keys.  The tile's codes come through registers a tile ahead
+// and are turned into bf16 once for all waves; the rest is attn_prompt_kernel's.
 template <int D, bool E4M3, int R>
-__global__ __launch_bounds__(256, 2) void attn_many_kernel(CacheArgs a) {
+__global__ __launch_bounds__(2 * R, 2) void attn_many_kernel(CacheArgs a) {
     constexpr int kUnit = unit_of(R);             // 64
-    static_assert(R == 128, "a wave for each 32 rows");
+    constexpr int kThreads = 2 * R;               // a wave for each 32 rows
+    static_assert(kUnit * (D / 16) % kThreads == 0, "every thread has the same pieces of a tile");
     constexpr int kRowBytes = D * 2, kTileBytes = kUnit * kRowBytes;
     constexpr int kPieces = D / 16;               // 16-byte pieces of a row of codes
-    constexpr int kLoads = kUnit * kPieces / 256; // of a thread, for K and for V
+    constexpr int kLoads = kUnit * kPieces / kThreads;  // of a thread, for K and for V
     __shared__ __attribute__((aligned(1024))) char lds[4 * kTileBytes];  // K, V of two tiles
     __shared__ __attribute__((aligned(16))) float tile_scales[2][2][kUnit];
     __shared__ int arrived[2];
@@ -1096,7 +1097,7 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(CacheArgs a) {
     if (run.u >= run.end) return;
     Seq<R> seq(a, run.b);
 
-    const int lrow = tid / kPieces, lpiece = tid % kPieces;  // of a thread's first load; the others 256 / kPieces rows on
+    const int lrow = tid / kPieces, lpiece = tid % kPieces;  // of a thread's first load; the others kThreads / kPieces rows on
     const int xk = D == 128 ? (col & 15) : ((col >> 1) & 7);
     const uint32_t kbase = col * kRowBytes + ((half ^ (xk & 1)) << 4);
     const int vr = 4 * half + ((lane & 15) >> 2), xv = value_place<D>(vr);
@@ -1149,7 +1150,7 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(CacheArgs a) {
             }
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                const uint8_t *at = a.codes + row_of(t, lrow + i * (256 / kPieces)) * D + lpiece * 16;
+                const uint8_t *at = a.codes + row_of(t, lrow + i * (kThreads / kPieces)) * D + lpiece * 16;
                 kcode[i] = *reinterpret_cast<const uint4 *>(at);
                 vcode[i] = *reinterpret_cast<const uint4 *>(at + to_v * D);
             }
@@ -1164,7 +1165,7 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(CacheArgs a) {
             const bool partly = key0 + (t + 1) * kUnit > len || gone_in != 0;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                const int r = lrow + i * (256 / kPieces);
+                const int r = lrow + i * (kThreads / kPieces);
                 const int fk = D == 128 ? (r & 15) : ((r >> 1) & 7), fv = value_place<D>(r);
                 *reinterpret_cast<bf8_t *>(kt + r * kRowBytes + (((2 * lpiece) ^ fk) << 4)) =
                     decode8<E4M3>(kcode[i].x, kcode[i].y);
@@ -1397,7 +1398,7 @@ qw3_status launch_cache(CacheArgs a, hipStream_t stream) {
     int cus = 0;
     qw3_status st = cu_count(&cus);
     if (st != QW3_OK) return st;
-    a.groups = cus * 2;
+    a.groups = cus * (R == 256 ? 1 : 2);
     void *ws = nullptr;
     st = workspace(stream, (size_t)a.groups * 2 * R * (D + 2) * sizeof(float), &ws);
     if (st != QW3_OK) return st;
@@ -1407,7 +1408,7 @@ qw3_status launch_cache(CacheArgs a, hipStream_t stream) {
     if constexpr (R <= 32)
         hipLaunchKernelGGL((attn_few_kernel<D, E4M3, R>), dim3(a.groups), dim3(256), 0, stream, a);
     else
-        hipLaunchKernelGGL((attn_many_kernel<D, E4M3, R>), dim3(a.groups), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((attn_many_kernel<D, E4M3, R>), dim3(a.groups), dim3(2 * R), 0, stream, a);
     return check_launch();
 }
 
@@ -1416,7 +1417,8 @@ qw3_status launch_cache_rows(const CacheArgs &a, hipStream_t stream) {
     const int64_t rows = ceil_div(a.Tq, a.B) * a.G;  // of a sequence, on average
     if (rows <= 16) return launch_cache<D, E4M3, 16>(a, stream);
     if (rows <= 64) return launch_cache<D, E4M3, 32>(a, stream);
-    return launch_cache<D, E4M3, 128>(a, stream);
+    if (D == 64 || rows <= 128) return launch_cache<D, E4M3, 128>(a, stream);
+    return launch_cache<D, E4M3, D == 128 ? 256 : 128>(a, stream);
 }
 
 bool strides_ok(int64_t ts, int64_t hs) { return ts >= 0 && hs >= 0 && ts < (1 << 23) && hs < (int64_t(1) << 40); }
