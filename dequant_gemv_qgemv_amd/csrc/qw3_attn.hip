@@ -906,7 +906,11 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
                 }
                 fetch(s + 1);
             }
-            bf8_t pf[kN];
+            // A weight is the sum of two bf16: its rounding and the rounding of what that
+            // leaves (16 bits).  One would do for a flat softmax; where one key decides a
+            // row, its error is that of every channel.  The second costs 8 of 24 matrix
+            // instructions of a kernel that waits for memory.
+            bf8_t pf[kN], pl[kN];
 #pragma unroll
             for (int x = 0; x < kN; ++x) {
                 bool hid[2][4];
@@ -942,7 +946,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
                     for (int i = 0; i < D / 16; ++i) acc[x][i] *= f;
                 }
                 const float ms = m[x] == kNegInf ? 0.0f : m[x];
-                uint32_t p[4];
+                uint32_t p[4], pr[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float w[2];
@@ -955,8 +959,10 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
                         w[e] = kMasked && hid[g][r] ? 0.0f : pe * vc[g][r];
                     }
                     p[i] = pack_bf16(w[0], w[1]);
+                    pr[i] = pack_bf16(w[0] - __uint_as_float(p[i] << 16), w[1] - __uint_as_float(p[i] & 0xffff0000u));
                 }
                 pf[x] = __builtin_bit_cast(bf8_t, i4_t{(int)p[0], (int)p[1], (int)p[2], (int)p[3]});
+                pl[x] = __builtin_bit_cast(bf8_t, i4_t{(int)pr[0], (int)pr[1], (int)pr[2], (int)pr[3]});
             }
             // V^T: keys 4 quarter + 0..3 and 16 + 4 quarter + 0..3 of 16 channels
             const int vkey = 4 * quarter + ((col >> 1) & 3) + 16 * (col >> 3), xv = place(vkey);
@@ -966,8 +972,10 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
                 const i2_t w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS_AS i2_t *)(from + ((i ^ xv) << 4)));
                 const bf8_t vf = decode8<E4M3>((uint32_t)w[0], (uint32_t)w[1]);
 #pragma unroll
-                for (int x = 0; x < kN; ++x)
+                for (int x = 0; x < kN; ++x) {
                     acc[x][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[x], acc[x][i], 0, 0, 0);
+                    acc[x][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pl[x], acc[x][i], 0, 0, 0);
+                }
             }
         };
     // items shared with other workgroups (at most the first and the last)
