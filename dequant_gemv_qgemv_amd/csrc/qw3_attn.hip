@@ -5,9 +5,9 @@
 //   o = sum_{j in V} p_j v_j / sum_{j in V} p_j,   p_j = 2^(c q.k_j - m),
 // c = sm_scale log2(e), m a running maximum over the keys read so far: one
 // pass over the keys, the sums rescaled by 2^(m - m') when m grows to m'.
-// Scores, m, the sum of p and the weighted sum of v stay in fp32; only p is
-// rounded, to bf16 for the matrix unit (at most 2^-8 of a term, the rounding
-// of the output itself).
+// Scores, m, the sum of p and the weighted sum of v stay in fp32; only the
+// weights of the v_j are rounded, to bf16 for the matrix unit (at most 2^-8 of a
+// term, the rounding of the output itself), and with few rows to two bf16 each.
 //
 // Orientation.  The matrix unit computes S^T = K Q^T, so a query row is a
 // column of the result: one lane holds many keys of one row, the row's maximum
@@ -107,6 +107,13 @@ __device__ __forceinline__ float sum_quarters(float x) {
 
 // cu[i] as a row number, whatever the array holds.
 __device__ __forceinline__ int clamp_row(int x, int total) { return min(max(x, 0), total); }
+
+// What the matrix-bound kernels cost.  On this card matrix and vector
+// instructions of a SIMD hardly run at the same time: for two waves of a SIMD,
+// 16 32x32x16 products each take 608 ns alone, 192 fma 449 ns alone, both 900 ns
+// mixed in one wave and 1041 ns from two.  So a kernel's time is the sum of the
+// two, and what counts is the number of vector instructions beside a product,
+// not their order (interleaving them by hand measured within 2 %).
 
 // ================================================================= prompt ==
 struct PromptArgs {
@@ -239,6 +246,18 @@ __device__ __forceinline__ int value_place(int r) {
     return (D == 128 ? (r & 3) << 2 : ((r >> 1) & 1) << 2) | (((r >> 2) & 1) << 1);
 }
 
+// Whole prompts.  K and V go from memory straight into LDS, in tiles of 64 keys
+// that the 4 waves of a workgroup share, one tile ahead; a wave keeps its 32 rows'
+// queries and sums in registers.  Two workgroups fit a CU, each with its own
+// barrier, so one computes while the other waits.  Bound by the matrix and vector
+// instructions together: for 64 rows of a SIMD and a tile 1.2 us of products, 0.7
+// of exponentials and the rest; the prompt of 8192 tokens (64 heads of 128
+// channels) runs in 1.03 ms, 1070 TFLOP/s, where a large bf16 product reaches
+// 1305.  With 64 channels half of the products stand beside as many exponentials:
+// 890 TFLOP/s.  Measured and left: 256 rows and 8 waves that share a tile (-1 %
+// and +1 % on long prompts, +13 % on packed ones), rings of 3 and 4 tiles (one
+// workgroup per CU: +20 to +70 %).
+//
 // A workgroup takes 128 / W query rows of one head, 32 for each of 4 / W pairs
 // (W = 2) or single waves (W = 1).  The waves of a pair have the two halves of
 // every tile's keys and are joined at the end: twice the workgroups with half of
@@ -736,7 +755,14 @@ __device__ __forceinline__ uint64_t visible(int base, int seen, uint64_t tree, i
 // and 32 of the unit's keys; codes and scales go from memory to registers a
 // step ahead, K's straight as the matrix unit's operand, V's through a tile of
 // the wave's own in LDS that turns them.  The waves meet only at the end of an
-// item.
+// item.  Bound by memory where there is much of it (64 sequences of 2048 tokens
+// 56 us, 4.9 TB/s, what a large copy reaches; one of 131071 tokens 61 us, of
+// which 8 join 62 parts a head), and by its own chain of dependent reads where
+// there is little: one token over 1000 keys 8.4 us in a graph, of which 1.1 find
+// the work, 0.8 a page number, 1.1 the codes, 1.6 the step with its instructions,
+// 1.2 join the waves, 2.6 the parts.  Three workgroups a CU (168 registers,
+// spills) measured 73 us where two measure 56; codes by direct loads into LDS,
+// with the compiler's waits for all of them, 104 us where 61 are measured now.
 template <int D, bool E4M3, int R>
 __global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
     constexpr int kUnit = unit_of(R);
@@ -1088,6 +1114,12 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
 // Many rows: R = 128 or 256 query rows of an item, 32 for each wave; the waves
 // share tiles of 64 keys.  The tile's codes come through registers a tile ahead
 // and are turned into bf16 once for all waves; the rest is attn_prompt_kernel's.
+// Bound by matrix and vector instructions: the two scales of a key and the
+// conversion make about 430 vector instructions beside 32 products (1.2 of the
+// 1.4 us that a tile takes a wave), 770 TFLOP/s on long caches, and 25 us of a
+// call are the exchange of partial results (trees of 64 drafts over 36,000
+// tokens, 512 rows a kv head: 130 us).  256 rows halve the conversion: 129 us
+// where 128 rows take 134.
 template <int D, bool E4M3, int R>
 __global__ __launch_bounds__(2 * R, 2) void attn_many_kernel(CacheArgs a) {
     constexpr int kUnit = unit_of(R);             // 64
@@ -1422,7 +1454,10 @@ qw3_status launch_cache(CacheArgs a, hipStream_t stream) {
 
 template <int D, bool E4M3>
 qw3_status launch_cache_rows(const CacheArgs &a, hipStream_t stream) {
-    const int64_t rows = ceil_div(a.Tq, a.B) * a.G;  // of a sequence, on average
+    // Rows of a sequence, on average.  16 drafts of 4 heads a kv head, 64 rows: 55
+    // us in blocks of 32, 54 in one of 64 with shared tiles; 52 rows of 64 channels
+    // 18 and 31 us.  512 rows of 128 channels: 210 us in blocks of 32, 134 of 128.
+    const int64_t rows = ceil_div(a.Tq, a.B) * a.G;
     if (rows <= 16) return launch_cache<D, E4M3, 16>(a, stream);
     if (rows <= 64) return launch_cache<D, E4M3, 32>(a, stream);
     if (D == 64 || rows <= 128) return launch_cache<D, E4M3, 128>(a, stream);

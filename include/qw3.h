@@ -65,8 +65,8 @@ enum {
     QW3_ERR_SHAPE = -2, /* negative size, K % 128 != 0, or K > QW3_MAX_K      */
     QW3_ERR_ALIGN = -3, /* a pointer is not aligned as stated above           */
     QW3_ERR_HIP = -4,   /* the HIP runtime reported an error                  */
-    QW3_ERR_CAPTURE = -5, /* qgemm_w3g128_smallM would have to allocate its
-                             workspace while the stream is being captured      */
+    QW3_ERR_CAPTURE = -5, /* qgemm_w3g128_smallM or qattn_cache would have to
+                             allocate while the stream is being captured       */
     QW3_ERR_SCRATCH = -6  /* qgemm_w3g128_smallM_noalloc needs more than
                              QW3_NOALLOC_SCRATCH_BYTES of scratch               */
 };
@@ -267,7 +267,11 @@ qw3_status qgemm_w3g128_smallM_noalloc(const uint16_t *x, const int32_t *packed,
  *     Hq a multiple of H, sm_scale > 0 and finite, else QW3_ERR_SHAPE.  B or
  *     the number of rows may be 0: no work.
  *   - Rows of a packed output that belong to no sequence are not written.
- *   - Deterministic and safe to capture, like the calls above.
+ *   - Deterministic: parts of a sequence that several workgroups worked on are
+ *     joined in a fixed order.  Safe to capture, like the calls above (qattn_cache
+ *     after one call of the size on the stream).
+ *   - Domain: |q|, |k|, |v|, s below 2^60.  NaN and infinities in what a row sees
+ *     make its output NaN or infinite; what it does not see has no influence on it.
  * ------------------------------------------------------------------------ */
 enum { QW3_CODES_INT8 = 0, QW3_CODES_E4M3 = 1 }; /* code_type */
 enum { QW3_SRC_BF16 = 0, QW3_SRC_F32 = 1 };      /* src_type */
@@ -319,9 +323,13 @@ qw3_status qcache_read(const void *codes, const float *scales, int32_t code_type
  *                 for a tree of drafted tokens each row's ancestors and itself.
  *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(sm_scale q.k_j - max_j)
  * over what the row sees; a row that sees nothing gets zeros.  fp32 scores and
- * sums; the weights p_j s_j are rounded to bf16 for the matrix unit.
- * Workspace: up to 2 x 2 x CUs x 64 (D + 2) floats per stream (68 MB at most),
- * by the rules of qgemm_w3g128_smallM.  max_pages * page_size <= 2^30.
+ * sums; the weights p_j s_j enter the matrix unit as two bf16 each where a
+ * sequence has up to 64 query rows per kv head on average, as one otherwise.
+ * Workspace, by the rules of qgemm_w3g128_smallM (the same buffer): 2 slots of R
+ * (D + 2) floats for each of 2 x CUs workgroups, R = 16, 32 or 128 (68 MB at most
+ * on 256 CUs), and 16 KB of counters for each stream, which a call leaves zero.
+ * max_pages * page_size <= 2^30, Tq * Hq <= 2^30, and (Tq Hq / (16 H) + B) H
+ * (max_pages * page_size / 64 + 4) < 2^31, else QW3_ERR_SHAPE.
  */
 qw3_status qattn_cache(const uint16_t *q, const void *codes, const float *scales, int32_t code_type,
                        const int32_t *block_table, const int32_t *lens, const int32_t *cu_q, const int64_t *tree,
@@ -336,8 +344,8 @@ qw3_status qattn_cache(const uint16_t *q, const void *codes, const float *scales
  * Row i of a sequence with nq queries and nk keys sees, with `causal`, the keys
  * j <= i + nk - nq (the last query sees the last key, so that a chunk of a
  * prompt attends to the whole prefix), else all nk keys.  Formula and empty
- * rows as for qattn_cache.  A key that a row does not see has no influence on
- * it, also where it holds an infinity or NaN.  No workspace.
+ * rows as for qattn_cache.  Rows that come out NaN or infinite are computed again
+ * from the keys they see alone, slowly.  No workspace.
  */
 qw3_status qattn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *cu_q,
                         const int32_t *cu_k, uint16_t *out, int64_t B, int64_t Tq, int64_t Tk, int64_t Hq,
