@@ -1565,7 +1565,7 @@ qw3_status qattn_cache(const uint16_t *q, const void *codes, const float *scales
     if (check_heads(Hq, H) != QW3_OK) return QW3_ERR_SHAPE;
     if (B < 0 || B > QW3_MAX_SEQS || Tq < 0 || Tq > QW3_MAX_TOKENS || max_pages < 0 || (!cu_q && Tq != B))
         return QW3_ERR_SHAPE;
-    if (max_pages * page_size > (int64_t(1) << 30) || Tq * Hq > (int64_t(1) << 30)) return QW3_ERR_SHAPE;
+    if (max_pages > (int64_t(1) << 30) / page_size || Tq * Hq > (int64_t(1) << 30)) return QW3_ERR_SHAPE;
     if (!scale_ok(sm_scale) || !strides_ok(q_ts, q_hs)) return QW3_ERR_SHAPE;
     if (B == 0 || Tq == 0) return QW3_OK;
     if (!q || !lens || !out || (max_pages > 0 && !block_table) || (pages > 0 && (!codes || !scales)))

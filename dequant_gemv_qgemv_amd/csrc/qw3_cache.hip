@@ -230,7 +230,7 @@ qw3_status qcache_write(const void *k, const void *v, int32_t src_type, const in
     const qw3_status st = check_cache(code_type, H, D, pages, page_size, &shift);
     if (st != QW3_OK) return st;
     if (src_type != QW3_SRC_BF16 && src_type != QW3_SRC_F32) return QW3_ERR_SHAPE;
-    if (T < 0 || T * H > (int64_t(1) << 28)) return QW3_ERR_SHAPE;
+    if (T < 0 || T > (int64_t(1) << 28) / H) return QW3_ERR_SHAPE;
     if (T == 0 || pages == 0) return QW3_OK;
     if (!k || !v || !slots || !codes || !scales) return QW3_ERR_NULL;
     const int per = src_type == QW3_SRC_F32 ? 4 : 8;  // elements of 16 bytes

@@ -326,8 +326,8 @@ qw3_status qcache_read(const void *codes, const float *scales, int32_t code_type
  * sums; the weights p_j s_j enter the matrix unit as two bf16 each where a
  * sequence has up to 64 query rows per kv head on average, as one otherwise.
  * Workspace, by the rules of qgemm_w3g128_smallM (the same buffer): 2 slots of R
- * (D + 2) floats for each of 2 x CUs workgroups, R = 16, 32 or 128 (68 MB at most
- * on 256 CUs), and 16 KB of counters for each stream, which a call leaves zero.
+ * (D + 2) floats for each of 2 x CUs workgroups, R = 16, 32 or 128, or 1 x CUs, R =
+ * 256 (68 MB at most on 256 CUs), and 16 KB of counters for each stream, which a call leaves zero.
  * max_pages * page_size <= 2^30, Tq * Hq <= 2^30, and (Tq Hq / (16 H) + B) H
  * (max_pages * page_size / 64 + 4) < 2^31, else QW3_ERR_SHAPE.
  */

@@ -58,6 +58,13 @@ def test_shapes(call, bad):
     assert call(**bad) == q.QW3_ERR_SHAPE
 
 
+@pytest.mark.parametrize("call,bad", [
+    (write, dict(T=1 << 62, H=4)), (write, dict(T=(1 << 63) - 1, H=1024)), (cache, dict(maxp=1 << 60)),
+    (cache, dict(maxp=(1 << 63) - 1)), (cache, dict(maxp=1 << 58, size=64))], ids=str)
+def test_sizes_whose_product_passes_64_bits(call, bad):
+    assert call(**bad) == q.QW3_ERR_SHAPE
+
+
 @pytest.mark.parametrize("call,names", [
     (write, ("k", "v", "slots", "codes", "scales")), (read, ("codes", "scales", "table", "cu", "k", "v")),
     (cache, ("qq", "codes", "scales", "table", "lens", "out")), (prompt, ("qq", "k", "v", "cu_q", "cu_k", "out"))])
