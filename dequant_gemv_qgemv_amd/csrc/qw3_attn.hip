@@ -545,9 +545,9 @@ constexpr int kSetup = 2;  // what beginning and ending an item costs, in units
 // What a sequence asks for.  An item is (sequence, kv head, block of R query
 // rows); its work is counted in units: kSetup, and one for each unit_of(R) keys, at
 // least one, so that an empty cache still writes its zeros.  All items of the call, laid end to end,
-// are cut into equal runs of units, one per workgroup: a long sequence is split
-// over many workgroups and short ones share one, with no lengths known on the
-// host.
+// are cut into equal runs of units, one per workgroup (fewer workgroups where the
+// runs would be too short for their join): a long sequence is split over many
+// workgroups and short ones share one, with no lengths known on the host.
 template <int R>
 struct Seq {
     int q0, nq, len, blocks, per_item, units;
@@ -573,6 +573,28 @@ __device__ __forceinline__ int wave_scan(int x) {  // inclusive prefix sum over 
     return x;
 }
 
+__device__ __forceinline__ int wave_max(int x) {  // over all 64 lanes, in every lane
+    x = max(x, (int)dpp_u32<0xB1>((uint32_t)x));   // as in wave_sum
+    x = max(x, (int)dpp_u32<0x4E>((uint32_t)x));
+    x = max(x, (int)dpp_u32<0x141>((uint32_t)x));
+    x = max(x, (int)dpp_u32<0x140>((uint32_t)x));
+    auto r = __builtin_amdgcn_permlane16_swap((uint32_t)x, (uint32_t)x, false, false);
+    x = max((int)r[0], (int)r[1]);
+    r = __builtin_amdgcn_permlane32_swap((uint32_t)x, (uint32_t)x, false, false);
+    return max((int)r[0], (int)r[1]);
+}
+
+// What adding one workgroup's part costs in the join, in units.  A run of u units
+// leaves an item of n units in n / u parts that one workgroup adds, u + kJoin n / u
+// in all, least at u = sqrt(kJoin n): runs are no shorter than that for the longest
+// item.  Without it a long sequence of few heads is cut for the whole card and
+// waits for its join.  Measured without, and with 0.07, 0.14, 0.8: one kv head, one
+// token over 30000 keys 32, 18, 17 and 25 us, over 131071 46, 32, 31, 48; with rows
+// of 128 or 256 without, and with 0.1, 0.5, 0.8, 1.0: trees of 64 over 6000 keys of
+// one kv head 193, 88, 62, 57, 71 us.  Short items lose 0.1 us to the root.
+template <int R>
+constexpr float kJoin = R <= 32 ? 0.14f : 0.8f;
+
 // A workgroup's run of units: [u, end) of the call's total, beginning in
 // sequence b, before which there are `before` units.
 struct Run {
@@ -582,13 +604,19 @@ template <int R>
 __device__ __forceinline__ Run find_run(const CacheArgs &a) {
     const int lane = threadIdx.x & 63;
     Run run;
-    int total = 0, mine = 0, upto = 0;
+    int total = 0, mine = 0, upto = 0, longest = 0;
     for (int base = 0; base < a.B; base += 64) {
-        mine = base + lane < a.B ? Seq<R>(a, base + lane).units : 0;
+        mine = 0;
+        if (base + lane < a.B) {
+            const Seq<R> seq(a, base + lane);
+            mine = seq.units;
+            if (mine > 0) longest = max(longest, seq.per_item);
+        }
         upto = total + wave_scan(mine);
         total = __builtin_amdgcn_readlane(upto, 63);
     }
-    run.per = max((total + a.groups - 1) / a.groups, 1);
+    const int least = uniform((int)__builtin_sqrtf(kJoin<R> * (float)wave_max(longest)));
+    run.per = max(max((total + a.groups - 1) / a.groups, least), 1);
     run.u = min((int64_t)blockIdx.x * run.per, (int64_t)total);
     run.end = min(run.u + run.per, total);
     run.b = 0, run.before = 0;

@@ -280,6 +280,13 @@ def test_a_long_sequence_beside_short_ones():
     cache_case(np.random.default_rng(55), "int8", 1, 24, 64, 32, [7000, 40, 900], [4, 3, 4], True)
 
 
+@pytest.mark.parametrize("kind,group,dim,length,news", [
+    ("int8", 8, 128, 9000, 1), ("e4m3", 5, 64, 5003, 4), ("int8", 2, 128, 2500, 50), ("e4m3", 4, 128, 2100, 40)])
+def test_long_sequences_of_one_head(kind, group, dim, length, news):
+    """Fewer workgroups than the card has: the runs are cut for the longest item's join."""
+    cache_case(np.random.default_rng(21), kind, 1, group, dim, 16, [length, 3 + news], news, news > 1)
+
+
 def test_many_rows_of_many_sequences():
     """128-row blocks: items that share a workgroup, and items that several share."""
     rng = np.random.default_rng(56)
