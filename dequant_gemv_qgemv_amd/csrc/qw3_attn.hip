@@ -105,6 +105,16 @@ __device__ __forceinline__ float sum_quarters(float x) {
     return sum_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
+__device__ __forceinline__ void store_agent(float *p, float x, float y) {
+    const uint64_t v = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
+    __hip_atomic_store(reinterpret_cast<uint64_t *>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 load_agent(const float *p) {
+    const uint64_t v =
+        __hip_atomic_load(reinterpret_cast<const uint64_t *>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+
 // cu[i] as a row number, whatever the array holds.
 __device__ __forceinline__ int clamp_row(int x, int total) { return min(max(x, 0), total); }
 
@@ -123,10 +133,20 @@ struct PromptArgs {
     int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;  // strides in elements
     int B, Tq, Tk, Hq, H, tiles;
     float scale;  // sm_scale log2(e)
+    int slices;   // with SPLIT: workgroups for one tile's keys, at most, ...
+    float *part;  // ... where they leave their parts, and ...
+    int *counts;  // ... how many have
 };
 
 constexpr int kKeys = 64;  // of a tile
 
+// Slices of a tile's keys.  A workgroup takes 0.6 us for a tile of keys, adding a
+// part costs about twice that: slices of u of n tiles are worth it from u = sqrt(2
+// n) on, and from 16 tiles on.  Measured whole, and with factors 0.3, 1 and 2: 1 row
+// of 8 heads of 128 channels against 6000 keys 59, 24, 20 and 20 us, 100 rows of 64
+// heads 61, 39, 39, 39; but against 700 keys 13.4 us whole, 16.6 in slices.
+constexpr float kSliceJoin = 2.0f;
+constexpr int kSliceLeast = 16;
 
 // One query row recomputed by a wave from the visible keys alone (keys 0..last).
 // The tiles multiply hidden keys by p = 0, which is not 0 where a hidden value
@@ -262,8 +282,13 @@ __device__ __forceinline__ int value_place(int r) {
 // (W = 2) or single waves (W = 1).  The waves of a pair have the two halves of
 // every tile's keys and are joined at the end: twice the workgroups with half of
 // the work, for calls with few rows.
-template <int D, bool CAUSAL, int W>
+//
+// SPLIT: a tile's keys are cut once more, into slices of whole tiles of keys for
+// workgroups of their own, for a few rows against many keys.  The one that
+// finishes last adds the parts in their order (see "Partial results" below).
+template <int D, bool CAUSAL, int W, bool SPLIT>
 __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
+    static_assert(W == 2 || !SPLIT, "all four waves join, two for 32 rows");
     constexpr int kRows = 128 / W, kBlocks = 2 / W;      // blocks of 32 keys of a wave and tile
     constexpr int kTileBytes = kKeys * D * 2;
     constexpr int kRowBytes = D * 2;
@@ -283,13 +308,22 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
     int b, tile;
     if (!find_tile<CAUSAL, kRows>(a, rank, &b, &tile)) return;
     const int q0 = clamp_row(a.cu_q[b], a.Tq), nq = clamp_row(a.cu_q[b + 1], a.Tq) - q0;
-    const int k0 = clamp_row(a.cu_k[b], a.Tk), nk = max(clamp_row(a.cu_k[b + 1], a.Tk) - k0, 0);
+    const int k0 = clamp_row(a.cu_k[b], a.Tk), keys = max(clamp_row(a.cu_k[b + 1], a.Tk) - k0, 0);
     const int row0 = tile * kRows;
     if (row0 >= nq) return;
 
-    const int off = nk - nq;
-    const int kend = CAUSAL ? min(nk, min(row0 + kRows, nq) + off) : nk;  // keys past every row of the workgroup
-    const int ntiles = kend > 0 ? (kend + kKeys - 1) / kKeys : 0;
+    const int kend = CAUSAL ? min(keys, min(row0 + kRows, nq) + keys - nq) : keys;  // past every row of the workgroup
+    int ntiles = kend > 0 ? (kend + kKeys - 1) / kKeys : 0, parts = 1, skip = 0;
+    if (SPLIT) {
+        const int worth = uniform((int)__builtin_sqrtf(kSliceJoin * (float)ntiles));
+        const int per = max(ntiles < kSliceLeast ? ntiles : max((ntiles + a.slices - 1) / a.slices, worth), 1);
+        parts = max((ntiles + per - 1) / per, 1);
+        if ((int)blockIdx.y >= parts) return;
+        const int first = per * (int)blockIdx.y;
+        ntiles = min(per, ntiles - first), skip = first * kKeys;
+    }
+    // from here on keys count from the first of the slice
+    const int nk = SPLIT ? min(keys - skip, max(ntiles, 0) * kKeys) : keys, off = keys - skip - nq;
     const int w0 = row0 + 32 * row_wave, row = w0 + col;
     const int last = CAUSAL ? min(nk - 1, row + off) : nk - 1;  // the row's last visible key
     const int wlo = CAUSAL ? min(nk - 1, w0 + off) : nk - 1;    // the same of the wave's first and last row
@@ -297,8 +331,8 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
     const bool live = w0 < nq;
 
     const uint16_t *qp = a.q + (int64_t)(q0 + min(row, nq - 1)) * a.q_ts + head * a.q_hs;
-    const char *kp = reinterpret_cast<const char *>(a.k + (int64_t)k0 * a.k_ts + kvh * a.k_hs);
-    const char *vp = reinterpret_cast<const char *>(a.v + (int64_t)k0 * a.v_ts + kvh * a.v_hs);
+    const char *kp = reinterpret_cast<const char *>(a.k + (int64_t)(k0 + skip) * a.k_ts + kvh * a.k_hs);
+    const char *vp = reinterpret_cast<const char *>(a.v + (int64_t)(k0 + skip) * a.v_ts + kvh * a.v_hs);
 
     bf8_t qf[D / 16];
 #pragma unroll
@@ -481,10 +515,21 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
             if (half == 0) stat[col] = m, stat[32 + col] = l;
         }
         __syncthreads();
-        if (first_block == 1) return;
+    }
+    auto redo_rows = [&](uint32_t todo) {  // of the wave's rows, those with a bit
+        for (; todo != 0; todo &= todo - 1) {
+            const int r = w0 + __builtin_ctz(todo);
+            exact_row<D>(a, a.q + (int64_t)(q0 + r) * a.q_ts + head * a.q_hs, a.k + (int64_t)k0 * a.k_ts + kvh * a.k_hs,
+                         a.v + (int64_t)k0 * a.v_ts + kvh * a.v_hs, a.o + ((int64_t)(q0 + r) * a.Hq + head) * D,
+                         CAUSAL ? min(keys - 1, r + keys - nq) : keys - 1);
+        }
+    };
+    if (W == 2 && first_block == 0) {
+        const float *hand = reinterpret_cast<const float *>(lds) + row_wave * 32 * (D + 4);
+        const float *stat = reinterpret_cast<const float *>(lds) + 2 * 32 * (D + 4) + row_wave * 64;
         const float m2 = stat[col], l2 = stat[32 + col], m1 = fmaxf(m, m2);
         const float f1 = m == kNegInf ? 0.0f : exp2_fast(m - m1), f2 = m2 == kNegInf ? 0.0f : exp2_fast(m2 - m1);
-        l = l * f1 + l2 * f2;
+        m = m1, l = l * f1 + l2 * f2;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -494,9 +539,76 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
                 for (int e = 0; e < 4; ++e) acc[i][r + e] = acc[i][r + e] * f1 + o[e] * f2;
             }
     }
-    if (!live) return;
-    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // l NaN stays NaN
     uint16_t *op = a.o + ((int64_t)(q0 + row) * a.Hq + head) * D;
+    if (SPLIT && parts > 1) {
+        __shared__ int arrived;
+        __shared__ uint32_t bad_rows[4];
+        constexpr int kSlot = kRows * (D + 2), kPart = D / 8;  // pairs of sums that a lane joins
+        const float *parts0 = a.part + (int64_t)blockIdx.x * a.slices * kSlot;
+        if (live && first_block == 0) {
+            float *at = a.part + ((int64_t)blockIdx.x * a.slices + blockIdx.y) * kSlot;
+            if (half == 0) store_agent(at + 2 * (32 * row_wave + col), m, l);
+            at += 2 * kRows + row_wave * 32 * D + 2 * lane;
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) store_agent(at + i * 128, acc[i / 8][2 * (i % 8)], acc[i / 8][2 * (i % 8) + 1]);
+        }
+        wait_vm0();
+        __syncthreads();
+        if (tid == 0)
+            arrived = __hip_atomic_fetch_add(a.counts + blockIdx.x, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        if (uniform(arrived) != parts - 1) return;
+        // each wave of a pair joins half of the channels, the next part's reads under way
+        uint32_t todo = 0;
+        if (live) {
+            float2 ml, next_ml, part[kPart], next[kPart], sum[kPart];
+            auto read = [&](int g) {
+                const float *p = parts0 + (int64_t)g * kSlot;
+                next_ml = load_agent(p + 2 * (32 * row_wave + col));
+                p += 2 * kRows + row_wave * 32 * D + 2 * lane + first_block * kPart * 128;
+#pragma unroll
+                for (int i = 0; i < kPart; ++i) next[i] = load_agent(p + i * 128);
+            };
+            m = kNegInf, l = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kPart; ++i) sum[i] = make_float2(0.0f, 0.0f);
+            read(0);
+#pragma unroll 1
+            for (int g = 0; g < parts; ++g) {
+                ml = next_ml;
+#pragma unroll
+                for (int i = 0; i < kPart; ++i) part[i] = next[i];
+                if (g + 1 < parts) read(g + 1);
+                const float m1 = fmaxf(m, ml.x);
+                const float f0 = m == kNegInf ? 0.0f : exp2_fast(m - m1), f1 = ml.x == kNegInf ? 0.0f : exp2_fast(ml.x - m1);
+                m = m1, l = l * f0 + ml.y * f1;
+#pragma unroll
+                for (int i = 0; i < kPart; ++i)
+                    sum[i] = make_float2(sum[i].x * f0 + part[i].x * f1, sum[i].y * f0 + part[i].y * f1);
+            }
+            const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+            bool bad = false;
+#pragma unroll
+            for (int e = 0; e < kPart; e += 2) {
+                const float x[4] = {sum[e].x * inv, sum[e].y * inv, sum[e + 1].x * inv, sum[e + 1].y * inv};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) bad |= !(fabsf(x[c]) < __builtin_huge_valf());
+                if (row < nq)
+                    *reinterpret_cast<uint2 *>(op + first_block * (D / 2) + 32 * (e / 8) + 4 * (e % 8) + 4 * half) =
+                        make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+            }
+            const unsigned long long redo = __ballot(bad && row < nq);
+            todo = (uint32_t)(redo | redo >> 32);
+        }
+        if (tid == 0) __hip_atomic_store(a.counts + blockIdx.x, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (lane == 0) bad_rows[wave] = todo;
+        wait_vm0();  // a row that is redone is written after both of its halves
+        __syncthreads();
+        if (first_block == 0) redo_rows(uniform((int)(bad_rows[wave] | bad_rows[wave + 1])));
+        return;
+    }
+    if (!live || first_block == 1) return;
+    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // l NaN stays NaN
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
@@ -513,13 +625,7 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
                     make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
         }
     unsigned long long redo = __ballot(bad && row < nq);
-    redo |= redo >> 32;
-    for (uint32_t todo = (uint32_t)redo; todo != 0; todo &= todo - 1) {
-        const int r = w0 + __builtin_ctz(todo);
-        exact_row<D>(a, a.q + (int64_t)(q0 + r) * a.q_ts + head * a.q_hs, reinterpret_cast<const uint16_t *>(kp),
-                     reinterpret_cast<const uint16_t *>(vp), a.o + ((int64_t)(q0 + r) * a.Hq + head) * D,
-                     CAUSAL ? min(nk - 1, r + off) : nk - 1);
-    }
+    redo_rows((uint32_t)(redo | redo >> 32));
 }
 
 // ================================================================== cache ==
@@ -651,16 +757,6 @@ template <int R, int D>
 __device__ __forceinline__ float *partial(const CacheArgs &a, int group, int which) {
     return a.part + (int64_t)(group * 2 + which) * (R * (D + 2));
 }
-__device__ __forceinline__ void store_agent(float *p, float x, float y) {
-    const uint64_t v = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
-    __hip_atomic_store(reinterpret_cast<uint64_t *>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float2 load_agent(const float *p) {
-    const uint64_t v =
-        __hip_atomic_load(reinterpret_cast<const uint64_t *>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
-}
-
 // Reads of partial results that a wave has under way at once: more of them make
 // the code longer, and a call on a short cache waits for its instructions
 // (measured with 16 rows: one token over 1000 keys 8.4 us at 16, 9.0 at 32, 10.8
@@ -1555,10 +1651,12 @@ qw3_status qattn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v,
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_q, 4) ||
         !aligned(cu_k, 4) || q_ts % 8 || q_hs % 8 || k_ts % 8 || k_hs % 8 || v_ts % 8 || v_hs % 8)
         return QW3_ERR_ALIGN;
-    PromptArgs a{q,    k,    v,    out,  cu_q,   cu_k,    q_ts,    q_hs,   k_ts,       k_hs,
-                 v_ts, v_hs, (int)B, (int)Tq, (int)Tk, (int)Hq, (int)H, 0, sm_scale * 1.44269504088896341f};
+    PromptArgs a{};
+    a.q = q, a.k = k, a.v = v, a.o = out, a.cu_q = cu_q, a.cu_k = cu_k, a.q_ts = q_ts, a.q_hs = q_hs;
+    a.k_ts = k_ts, a.k_hs = k_hs, a.v_ts = v_ts, a.v_hs = v_hs, a.B = (int)B, a.Tq = (int)Tq, a.Tk = (int)Tk;
+    a.Hq = (int)Hq, a.H = (int)H, a.scale = sm_scale * 1.44269504088896341f;
     int cus = 0;
-    const qw3_status st = cu_count(&cus);
+    qw3_status st = cu_count(&cus);
     if (st != QW3_OK) return st;
     // room for every sequence's last, partly filled tile
     // Halves of 64 rows while 128-row tiles leave CUs with less than two workgroups:
@@ -1568,15 +1666,31 @@ qw3_status qattn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v,
     const int64_t tiles = Tq / (few ? 64 : 128) + B;
     if (tiles * Hq > 0x7fffffff) return QW3_ERR_SHAPE;
     a.tiles = (int)tiles;
+    const hipStream_t stream = (hipStream_t)hip_stream;
+    // in slices while the tiles leave half of the CUs' places empty
+    a.slices = few && Tk > (kSliceLeast - 1) * kKeys ? (int)std::max<int64_t>(2 * cus / (tiles * Hq), 1) : 1;
+    if (a.slices > 1) {
+        void *ws = nullptr;
+        st = workspace(stream, (size_t)(tiles * Hq * a.slices) * 64 * (D + 2) * sizeof(float), &ws);
+        if (st != QW3_OK) return st;
+        a.part = static_cast<float *>(ws);
+        st = counters(stream, (int)(tiles * Hq), &a.counts);
+        if (st != QW3_OK) return st;
+    }
     auto run = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles * Hq)), dim3(256), 0, (hipStream_t)hip_stream, a);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles * Hq), (unsigned)a.slices), dim3(256), 0, stream, a);
     };
-    auto by_mask = [&](auto d, auto w) {
+    auto by_mask = [&](auto d, auto w, auto split) {
         constexpr int kD = decltype(d)::value, kW = decltype(w)::value;
-        causal ? run(attn_prompt_kernel<kD, true, kW>) : run(attn_prompt_kernel<kD, false, kW>);
+        constexpr bool kSplit = decltype(split)::value;
+        causal ? run(attn_prompt_kernel<kD, true, kW, kSplit>) : run(attn_prompt_kernel<kD, false, kW, kSplit>);
     };
     auto by_rows = [&](auto d) {
-        few ? by_mask(d, std::integral_constant<int, 2>{}) : by_mask(d, std::integral_constant<int, 1>{});
+        using One = std::integral_constant<int, 1>;
+        using Two = std::integral_constant<int, 2>;
+        a.slices > 1 ? by_mask(d, Two{}, std::true_type{})
+        : few        ? by_mask(d, Two{}, std::false_type{})
+                     : by_mask(d, One{}, std::false_type{});
     };
     D == 128 ? by_rows(std::integral_constant<int, 128>{}) : by_rows(std::integral_constant<int, 64>{});
     return check_launch();

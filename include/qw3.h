@@ -65,7 +65,7 @@ enum {
     QW3_ERR_SHAPE = -2, /* negative size, K % 128 != 0, or K > QW3_MAX_K      */
     QW3_ERR_ALIGN = -3, /* a pointer is not aligned as stated above           */
     QW3_ERR_HIP = -4,   /* the HIP runtime reported an error                  */
-    QW3_ERR_CAPTURE = -5, /* qgemm_w3g128_smallM or qattn_cache would have to
+    QW3_ERR_CAPTURE = -5, /* qgemm_w3g128_smallM, qattn_cache or qattn_prompt would have to
                              allocate while the stream is being captured       */
     QW3_ERR_SCRATCH = -6  /* qgemm_w3g128_smallM_noalloc needs more than
                              QW3_NOALLOC_SCRATCH_BYTES of scratch               */
@@ -269,7 +269,7 @@ qw3_status qgemm_w3g128_smallM_noalloc(const uint16_t *x, const int32_t *packed,
  *   - Rows of a packed output that belong to no sequence are not written.
  *   - Deterministic: parts of a sequence that several workgroups worked on are
  *     joined in a fixed order.  Safe to capture, like the calls above (qattn_cache
- *     after one call of the size on the stream).
+ *     and qattn_prompt after one call of the size on the stream).
  *   - Domain: |q|, |k|, |v|, s below 2^60.  NaN and infinities in what a row sees
  *     make its output NaN or infinite; what it does not see has no influence on it.
  * ------------------------------------------------------------------------ */
@@ -345,7 +345,10 @@ qw3_status qattn_cache(const uint16_t *q, const void *codes, const float *scales
  * j <= i + nk - nq (the last query sees the last key, so that a chunk of a
  * prompt attends to the whole prefix), else all nk keys.  Formula and empty
  * rows as for qattn_cache.  Rows that come out NaN or infinite are computed again
- * from the keys they see alone, slowly.  No workspace.
+ * from the keys they see alone, slowly.  Workspace, by the same rules as
+ * qattn_cache: none with fewer than 961 keys in all or with (Tq / 64 + B) Hq above
+ * the number of CUs; else parts of 64 (D + 2) floats for each of 2 x CUs workgroups
+ * at most (17 MB on 256 CUs), and the counters.
  */
 qw3_status qattn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *cu_q,
                         const int32_t *cu_k, uint16_t *out, int64_t B, int64_t Tq, int64_t Tk, int64_t Hq,

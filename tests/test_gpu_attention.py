@@ -416,6 +416,36 @@ def test_chunks(causal, dim, nq, nk):
     prompt_case(np.random.default_rng(sum(nk)), nq, nk, 2, 2, dim, causal, some=40)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim,nq,nk,heads,group", [
+    (128, [1], [4000], 1, 1), (64, [33, 2, 70], [1500, 0, 700], 1, 3), (128, [65], [2049], 2, 2),
+    (64, [64, 1], [129, 6000], 1, 1), (128, [90], [150], 1, 4)])
+def test_few_rows_against_many_keys(causal, dim, nq, nk, heads, group):
+    """The keys of a tile in slices: of one tile, of unequal length, past a row's last key."""
+    say("slices", causal, dim, nq, nk)
+    prompt_case(np.random.default_rng(sum(nk) + 1), nq, nk, heads, group, dim, causal, some=12)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_nonfinite_values_in_slices(dim, bad):
+    """A key in the middle that all rows see (one channel), the last ones that some see."""
+    rng = np.random.default_rng(22)
+    rq, rk, rv = rows(rng, 40, 2, dim), rows(rng, 1500, 1, dim), rows(rng, 1500, 1, dim)
+    rv[1490, 0, :] = bad
+    cu, cuk = starts([40]), starts([1500])
+    got = f64(q().qattn_prompt(rq, rk, rv, cu, cuk))
+    for i in (0, 13, 29):  # row i sees the keys up to 1460 + i
+        for h in (0, 1):
+            o, bound = ref.attend(f64(rq)[i, h], f64(rk)[:, 0], f64(rv)[:, 0], np.arange(1461 + i), dim ** -0.5)
+            check(got[i, h], o, bound, "row %d head %d" % (i, h))
+    assert not np.isfinite(got[30:]).any()
+    rv[700, 0, 5] = bad
+    again = f64(q().qattn_prompt(rq, rk, rv, cu, cuk))
+    assert not np.isfinite(again[:, :, 5]).any()
+    assert np.isfinite(np.delete(again[:30], 5, axis=2)).all()
+
+
 def test_many_prompts():
     rng = np.random.default_rng(11)
     nq = [int(x) for x in rng.integers(0, 30, 140)]
@@ -528,6 +558,26 @@ def test_streams_and_graph_replay():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert np.array_equal(a, b)
+
+
+def test_slices_repeat_and_replay():
+    """Parts joined by whoever finishes last: the same bits every time, eager and in a graph."""
+    rng = np.random.default_rng(23)
+    rq, rk, rv = rows(rng, 70, 4, 128), rows(rng, 5000, 1, 128), rows(rng, 5000, 1, 128)
+    cu, cuk = starts([50, 20]), starts([1800, 3200])
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        first = bits(q().qattn_prompt(rq, rk, rv, cu, cuk))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        out = q().qattn_prompt(rq, rk, rv, cu, cuk)
+    for _ in range(4):
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(bits(out), first)
+        assert np.array_equal(bits(q().qattn_prompt(rq, rk, rv, cu, cuk)), first)
 
 
 def test_two_streams_at_once():
