@@ -1580,12 +1580,25 @@ template <int D, bool E4M3>
 qw3_status launch_cache_rows(const CacheArgs &a, hipStream_t stream) {
     // Rows of a sequence, on average.  16 drafts of 4 heads a kv head, 64 rows: 55
     // us in blocks of 32, 54 in one of 64 with shared tiles; 52 rows of 64 channels
-    // 18 and 31 us.  512 rows of 128 channels: 210 us in blocks of 32, 134 of 128.
+    // 18 and 31 us.
     const int64_t rows = ceil_div(a.Tq, a.B) * a.G;
     if (rows <= 16) return launch_cache<D, E4M3, 16>(a, stream);
     if (rows <= 64) return launch_cache<D, E4M3, 32>(a, stream);
-    if (D == 64 || rows <= 128) return launch_cache<D, E4M3, 128>(a, stream);
-    return launch_cache<D, E4M3, D == 128 ? 256 : 128>(a, stream);
+    // Larger blocks read a key for more rows, smaller ones spread over more
+    // workgroups and have less to join.  The host knows the work only by the keys
+    // that the table can name.  Trees of 64, 512 rows a kv head of 128 channels, in
+    // blocks of 32, 128 and 256: 1 kv head over 1500 keys 17, 26 and 36 us, over 6000
+    // 30, 42, 57; 4 sequences of 8 over 1500 keys 39, 43, 54, over 6000 117, 88, 86; 8
+    // sequences of 8 over 1500..8000 214, 132, 129.  With 64 channels in blocks of 32
+    // and 128: 2 kv heads over 6000 keys 24 and 29 us, 8 39 and 35.
+    if (a.Tq * (int64_t)a.Hq * (a.max_pages << a.page_shift) <= (D == 128 ? 1 << 25 : 1 << 24))
+        return launch_cache<D, E4M3, 32>(a, stream);
+    int cus = 0;
+    const qw3_status st = cu_count(&cus);
+    if (st != QW3_OK) return st;
+    if (D == 128 && rows > 128 && (int64_t)a.Tq * a.Hq >= int64_t(256) * (cus / 2))  // blocks of 256 for half of the CUs
+        return launch_cache<D, E4M3, D == 128 ? 256 : 128>(a, stream);
+    return launch_cache<D, E4M3, 128>(a, stream);
 }
 
 bool strides_ok(int64_t ts, int64_t hs) { return ts >= 0 && hs >= 0 && ts < (1 << 23) && hs < (int64_t(1) << 40); }

@@ -324,7 +324,8 @@ qw3_status qcache_read(const void *codes, const float *scales, int32_t code_type
  *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(sm_scale q.k_j - max_j)
  * over what the row sees; a row that sees nothing gets zeros.  fp32 scores and
  * sums; the weights p_j s_j enter the matrix unit as two bf16 each where a
- * sequence has up to 64 query rows per kv head on average, as one otherwise.
+ * sequence has up to 64 query rows per kv head on average or Tq Hq max_pages
+ * page_size is at most 2^25 (D = 64: 2^24), as one otherwise.
  * Workspace, by the rules of qgemm_w3g128_smallM (the same buffer): 2 slots of R
  * (D + 2) floats for each of 2 x CUs workgroups, R = 16, 32 or 128, or 1 x CUs, R =
  * 256 (68 MB at most on 256 CUs), and 16 KB of counters for each stream, which a call leaves zero.

@@ -203,8 +203,9 @@ def check(got, want, bound, what):
         what, bad.sum(), np.nanmax(np.where(bad, err / np.maximum(bound, 1e-300), 0)))
 
 
-def cache_case(rng, kind, heads, group, dim, page, lens, news, tree, scale=None, touch=None, pages=None, lift=0):
-    """One qattn_cache call against the oracle, every row and head."""
+def cache_case(rng, kind, heads, group, dim, page, lens, news, tree, scale=None, touch=None, pages=None, some=None):
+    """One qattn_cache call against the oracle, every row and head (`some`: that many rows of each sequence).
+    With many rows a second one, whose table is wide enough for the kernels of large calls."""
     news = [news] * len(lens) if isinstance(news, int) else news
     pages = pages or sum(-(-n // page) for n in lens) + 2
     codes, scales = random_cache(rng, kind, pages, page, heads, dim)
@@ -224,7 +225,15 @@ def cache_case(rng, kind, heads, group, dim, page, lens, news, tree, scale=None,
     out = torch.full(rq.shape, 77.0, dtype=torch.bfloat16, device="cuda")
     q().qattn_cache(rq, codes, scales, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
                     tree=words.cuda() if words is not None else None, out=out, **kw)
-    got, qq = f64(out), f64(rq)
+    outs, qq = [f64(out)], f64(rq)
+    if -(-sum(news) // len(lens)) * group > 64:
+        width = (1 << 25) // (page * rq.shape[0] * rq.shape[1]) + 1
+        wide = torch.full((len(lens), max(width, table.shape[1])), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+        wide[:, :table.shape[1]] = table
+        out.fill_(77.0)
+        q().qattn_cache(rq, codes, scales, wide, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                        tree=words.cuda() if words is not None else None, out=out, **kw)
+        outs.append(f64(out))
     val = ref.code_values(codes.view(torch.uint8).cpu().numpy(), kind) * scales.cpu().numpy().astype(np.float64)[..., None]
     tab, at = table.cpu().numpy(), 0
     for b, (n, length) in enumerate(zip(news, lens)):
@@ -232,13 +241,14 @@ def cache_case(rng, kind, heads, group, dim, page, lens, news, tree, scale=None,
         page_of = tab[b, tokens // page] if length else np.zeros(0, int)
         there = (page_of >= 0) & (page_of < pages)
         kv = val[np.where(there, page_of, 0), :, :, tokens % page]  # [len, 2, H, D]
-        for i in range(n):
+        for i in range(n) if some is None or n <= some else sorted(rng.choice(n, some, replace=False).tolist()):
             sees = ref.cache_sees(i, n, length, int(words[at + i]) & (2 ** 64 - 1) if tree else None)
             sees = sees[there[sees]] if len(sees) else sees
             for h in range(heads * group):
                 o, bound = ref.attend(qq[at + i, h], kv[:, 0, h // group], kv[:, 1, h // group], sees,
                                       dim ** -0.5 if scale is None else scale)
-                check(got[at + i, h], o, bound, "sequence %d row %d head %d" % (b, i, h))
+                for got in outs:
+                    check(got[at + i, h], o, bound, "sequence %d row %d head %d" % (b, i, h))
         at += n
 
 
@@ -285,6 +295,11 @@ def test_a_long_sequence_beside_short_ones():
 def test_long_sequences_of_one_head(kind, group, dim, length, news):
     """Fewer workgroups than the card has: the runs are cut for the longest item's join."""
     cache_case(np.random.default_rng(21), kind, 1, group, dim, 16, [length, 3 + news], news, news > 1)
+
+
+@pytest.mark.parametrize("kind,lens", [("int8", [300, 1100]), ("e4m3", [64, 777])])
+def test_more_rows_than_the_card_has_workgroups(kind, lens):
+    cache_case(np.random.default_rng(25), kind, 2, 128, 128, 16, lens, 64, True, some=5)
 
 
 def test_many_rows_of_many_sequences():
@@ -620,11 +635,14 @@ def test_starts_and_lengths_out_of_range_are_clipped(rows_per_head):
     table = tables(rng, [30, 40, 20], 16, 8)
     heads = 2 * rows_per_head
     rq = rows(rng, 9, heads, 64)
+    wide = torch.full((3, (1 << 24) // (16 * 9 * heads) + 1), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table  # with many rows: the kernel of large calls
     guard = torch.full((9 + 4, heads, 64), 5.0, dtype=torch.bfloat16, device="cuda")
     for cu in ([0, 2000, 4, 9], [-7, 3, 3, 1 << 30], [5, 2, 9, 9]):
         c = torch.tensor(cu, dtype=torch.int32, device="cuda")
         lens = torch.tensor([30, 1 << 30, -4], dtype=torch.int32, device="cuda")
-        q().qattn_cache(rq, codes, scales, table, lens, cu_q=c, out=guard[:9])
+        for t in (table, wide):
+            q().qattn_cache(rq, codes, scales, t, lens, cu_q=c, out=guard[:9])
         k = rows(rng, 9, 2, 64)
         q().qattn_prompt(rq, k, k, c, out=guard[:9])
         q().qattn_prompt(rq, k, k, c, causal=False, out=guard[:9])
