@@ -1553,12 +1553,16 @@ __global__ __launch_bounds__(2 * R, 2) void attn_many_kernel(CacheArgs a) {
     }
 }
 
-template <int D, bool E4M3, int R>
-qw3_status launch_cache(CacheArgs a, hipStream_t stream) {
-    // units of work are counted in 31 bits: a bound on them from what the host knows
+// Units of work are counted in 31 bits: whether what the host knows keeps them there.
+bool units_fit(const CacheArgs &a, int R) {
     const int64_t most = ceil_div((a.max_pages << a.page_shift) + unit_of(R), unit_of(R)) + kSetup;
     const int64_t items = ((int64_t)a.Tq * a.G / R + a.B) * a.H;
-    if (most > 0x7fffffff / (items + 1)) return QW3_ERR_SHAPE;
+    return most <= 0x7fffffff / (items + 1);
+}
+
+template <int D, bool E4M3, int R>
+qw3_status launch_cache(CacheArgs a, hipStream_t stream) {
+    if (!units_fit(a, R)) return QW3_ERR_SHAPE;
     int cus = 0;
     qw3_status st = cu_count(&cus);
     if (st != QW3_OK) return st;
@@ -1593,6 +1597,7 @@ qw3_status launch_cache_rows(const CacheArgs &a, hipStream_t stream) {
     // and 128: 2 kv heads over 6000 keys 24 and 29 us, 8 39 and 35.
     if (a.Tq * (int64_t)a.Hq * (a.max_pages << a.page_shift) <= (D == 128 ? 1 << 25 : 1 << 24))
         return launch_cache<D, E4M3, 32>(a, stream);
+    if (!units_fit(a, 128)) return QW3_ERR_SHAPE;  // before the device is asked: no device decides on a refusal
     int cus = 0;
     const qw3_status st = cu_count(&cus);
     if (st != QW3_OK) return st;
