@@ -16,10 +16,12 @@
 // rescale factor of a row is then one value per lane.  V^T comes from row-major
 // tiles in LDS through the transposing LDS reads.
 #include "qw3_common.h"
+#include "qw3_units.h"
 
 #include <vector>
 
 using namespace qw3_shared;
+using namespace qw3_units;
 
 namespace {
 
@@ -115,8 +117,16 @@ __device__ __forceinline__ float2 load_agent(const float *p) {
     return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
 }
 
-// cu[i] as a row number, whatever the array holds.
-__device__ __forceinline__ int clamp_row(int x, int total) { return min(max(x, 0), total); }
+// Inclusive maximum over the wave's lanes up to one's own, of values >= 0.
+__device__ __forceinline__ int wave_scan_max(int x) {
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false));  // row_shr 1, 2, 4, 8
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, kDppRowBcast15, 0xA, 0xF, false));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, kDppRowBcast31, 0xC, 0xF, false));
+    return x;
+}
 
 // What the matrix-bound kernels cost.  On this card matrix and vector
 // instructions of a SIMD hardly run at the same time: for two waves of a SIMD,
@@ -208,20 +218,23 @@ __device__ __forceinline__ int wave_sum(int x) {  // over all 64 lanes, in every
 // causal mask tile i of a sequence counts i + 1 + (prefix in tiles): F(x), the
 // number of tiles that count more than x, is summed over the sequences by the
 // lanes, and the x with F(x) <= rank < F(x - 1) found by halving.  Without one,
-// and beyond 64 sequences, sequence b owns the ranks from cu_q[b] / kRows + b on
-// (room for its rows whatever its length), last tiles first.
+// and beyond 64 sequences, sequence b owns the ranks from q0 / kRows + b on, q0 its
+// first row (room for its rows whatever its length), last tiles first.
 template <bool CAUSAL, int kRows>
-__device__ __forceinline__ bool find_tile(const PromptArgs &a, int rank, int *seq, int *tile) {
+__device__ __forceinline__ bool find_tile(const PromptArgs &a, int rank, int *seq, int *tile, Rows *rows) {
     const int lane = threadIdx.x & 63;
     if (CAUSAL && a.B <= 64) {
-        int n = 0, pre = 0;
+        int n = 0, pre = 0, start = lane < a.B ? clamp_row(a.cu_q[lane], a.Tq) : 0;
+        if (a.B > 1) start = wave_scan_max(start);
+        Rows of = {0, 0};
         if (lane < a.B) {
-            const int q0 = clamp_row(a.cu_q[lane], a.Tq), nq = max(clamp_row(a.cu_q[lane + 1], a.Tq) - q0, 0);
+            of = rows_of(start, a.cu_q[lane + 1], start, a.Tq);
             const int k0 = clamp_row(a.cu_k[lane], a.Tk), nk = max(clamp_row(a.cu_k[lane + 1], a.Tk) - k0, 0);
-            n = (nq + kRows - 1) / kRows, pre = max(nk - nq, 0) / kRows;
+            n = (of.n + kRows - 1) / kRows, pre = max(nk - of.n, 0) / kRows;
         }
         if (a.B == 1) {
             *seq = 0, *tile = uniform(n) - 1 - rank;
+            *rows = Rows{uniform(of.first), uniform(of.n)};
             return *tile >= 0;
         }
         auto above = [&](int x) { return uniform(wave_sum(min(max(n + pre - x, 0), n))); };
@@ -241,20 +254,26 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int rank, int *se
         const bool it = has && __popcll(mine & ((1ull << lane) - 1)) == skip;
         *seq = uniform(__builtin_ctzll(__ballot(it)));
         *tile = hi - 1 - uniform(__shfl(pre, *seq, 64));
+        *rows = Rows{uniform(__shfl(of.first, *seq, 64)), uniform(__shfl(of.n, *seq, 64))};
         return true;
     }
     const int at = a.tiles - 1 - rank;
-    int b = -1;
+    int b = -1, first = 0, floor = 0;
     for (int base = 0; base < a.B; base += 64) {
-        const unsigned long long in = __ballot(
-            base + lane < a.B && clamp_row(a.cu_q[min(base + lane, a.B - 1)], a.Tq) / kRows + base + lane <= at);
-        b += __popcll(in);
+        const int start =
+            max(floor, wave_scan_max(base + lane < a.B ? clamp_row(a.cu_q[min(base + lane, a.B - 1)], a.Tq) : 0));
+        const unsigned long long in = __ballot(base + lane < a.B && start / kRows + base + lane <= at);
+        if (in == 0) break;
+        b = base + __popcll(in) - 1;  // the starts do not fall, so these are the first lanes
+        first = __builtin_amdgcn_readlane(start, b - base);
+        floor = __builtin_amdgcn_readlane(start, 63);
         if (in != ~0ull) break;
     }
     b = uniform(b);
     if (b < 0) return false;
     *seq = b;
-    *tile = at - clamp_row(a.cu_q[b], a.Tq) / kRows - b;
+    *tile = at - first / kRows - b;
+    *rows = rows_of(first, a.cu_q[b + 1], first, a.Tq);
     return true;
 }
 
@@ -306,8 +325,9 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
     const int head = a.Hq % 8 == 0 ? (j & 7) * (a.Hq / 8) + (j >> 3) : j;
     const int kvh = head / (a.Hq / a.H);
     int b, tile;
-    if (!find_tile<CAUSAL, kRows>(a, rank, &b, &tile)) return;
-    const int q0 = clamp_row(a.cu_q[b], a.Tq), nq = clamp_row(a.cu_q[b + 1], a.Tq) - q0;
+    Rows of;
+    if (!find_tile<CAUSAL, kRows>(a, rank, &b, &tile, &of)) return;
+    const int q0 = of.first, nq = of.n;
     const int k0 = clamp_row(a.cu_k[b], a.Tk), keys = max(clamp_row(a.cu_k[b + 1], a.Tk) - k0, 0);
     const int row0 = tile * kRows;
     if (row0 >= nq) return;
@@ -643,28 +663,21 @@ struct CacheArgs {
     float scale;
 };
 
-// Keys of a unit of work: with few rows 32 for each of a workgroup's 4 waves,
-// with many a tile that the waves share.
-constexpr int unit_of(int R) { return R <= 32 ? 128 : 64; }
-constexpr int kSetup = 2;  // what beginning and ending an item costs, in units
-
-// What a sequence asks for.  An item is (sequence, kv head, block of R query
-// rows); its work is counted in units: kSetup, and one for each unit_of(R) keys, at
-// least one, so that an empty cache still writes its zeros.  All items of the call, laid end to end,
-// are cut into equal runs of units, one per workgroup (fewer workgroups where the
-// runs would be too short for their join): a long sequence is split over many
-// workgroups and short ones share one, with no lengths known on the host.
+// What a sequence asks for: its rows, and the units of its items (qw3_units.h).
+// All items of the call, laid end to end, are cut into equal runs of units, one
+// per workgroup (fewer workgroups where the runs would be too short for their
+// join): a long sequence is split over many workgroups and short ones share one,
+// with no lengths known on the host.
 template <int R>
 struct Seq {
     int q0, nq, len, blocks, per_item, units;
     __device__ Seq() {}
-    __device__ Seq(const CacheArgs &a, int b) {
-        q0 = a.cu_q ? clamp_row(a.cu_q[b], a.Tq) : min(b, a.Tq);
-        nq = (a.cu_q ? clamp_row(a.cu_q[b + 1], a.Tq) : min(b + 1, a.Tq)) - q0;
-        nq = max(nq, 0);
+    __device__ Seq(const CacheArgs &a, int b, int floor) {  // floor: the largest start before (without cu_q: any)
+        const Rows rows = a.cu_q ? rows_of(a.cu_q[b], a.cu_q[b + 1], floor, a.Tq) : Rows{b, 1};
+        q0 = rows.first, nq = rows.n;
         len = a.pages == 0 ? 0 : (int)max((int64_t)0, min((int64_t)a.lens[b], a.max_pages << a.page_shift));
-        blocks = (nq * a.G + R - 1) / R;
-        per_item = kSetup + max((len + unit_of(R) - 1) / unit_of(R), 1);
+        blocks = blocks_of(nq * a.G, R);
+        per_item = units_of_item(len, R);
         units = per_item * blocks * a.H;
     }
 };
@@ -702,47 +715,53 @@ template <int R>
 constexpr float kJoin = R <= 32 ? 0.14f : 0.8f;
 
 // A workgroup's run of units: [u, end) of the call's total, beginning in
-// sequence b, before which there are `before` units.
-struct Run {
-    int per, u, end, before, b;
+// sequence b, before which there are `before` units and whose starts' floor is `floor`.
+struct Work {
+    int per, u, end, before, b, floor;
 };
 template <int R>
-__device__ __forceinline__ Run find_run(const CacheArgs &a) {
+__device__ __forceinline__ Work find_work(const CacheArgs &a) {
     const int lane = threadIdx.x & 63;
-    Run run;
-    int total = 0, mine = 0, upto = 0, longest = 0;
-    for (int base = 0; base < a.B; base += 64) {
+    int total = 0, mine = 0, upto = 0, longest = 0, floor = 0, start = 0;
+    // the lane's sequence of 64: its units, and the largest start up to its own
+    auto sequence = [&](int b) {
+        if (a.cu_q) start = max(floor, wave_scan_max(b < a.B ? clamp_row(a.cu_q[min(b, a.B)], a.Tq) : 0));
         mine = 0;
-        if (base + lane < a.B) {
-            const Seq<R> seq(a, base + lane);
+        if (b < a.B) {
+            const Seq<R> seq(a, b, start);
             mine = seq.units;
             if (mine > 0) longest = max(longest, seq.per_item);
         }
+    };
+    for (int base = 0; base < a.B; base += 64) {
+        sequence(base + lane);
         upto = total + wave_scan(mine);
         total = __builtin_amdgcn_readlane(upto, 63);
+        if (a.B > 64) floor = __builtin_amdgcn_readlane(start, 63);
     }
     const int least = uniform((int)__builtin_sqrtf(kJoin<R> * (float)wave_max(longest)));
-    run.per = max(max((total + a.groups - 1) / a.groups, least), 1);
-    run.u = min((int64_t)blockIdx.x * run.per, (int64_t)total);
-    run.end = min(run.u + run.per, total);
-    run.b = 0, run.before = 0;
-    if (run.u >= run.end || a.B == 1) return run;
+    const Run run = run_of(total, a.groups, least, blockIdx.x);
+    Work work = {run.per, run.begin, run.end, 0, 0, 0};
+    if (work.u >= work.end || a.B == 1) return work;
     int done = 0;
+    floor = 0;
     for (int base = 0; base < a.B; base += 64) {
         if (a.B > 64) {
-            mine = base + lane < a.B ? Seq<R>(a, base + lane).units : 0;
+            sequence(base + lane);
             upto = done + wave_scan(mine);
         }
-        const unsigned long long past = __ballot(upto > run.u);
+        const unsigned long long past = __ballot(upto > work.u);
         if (past) {
             const int at = uniform(__builtin_ctzll(past));
-            run.b = base + at;
-            run.before = __builtin_amdgcn_readlane(upto - mine, at);
+            work.b = base + at;
+            work.before = __builtin_amdgcn_readlane(upto - mine, at);
+            work.floor = __builtin_amdgcn_readlane(start, at);
             break;
         }
         done = __builtin_amdgcn_readlane(upto, 63);
+        floor = __builtin_amdgcn_readlane(start, 63);
     }
-    return run;
+    return work;
 }
 
 // Partial results.  An item that several workgroups worked on is joined by the
@@ -899,9 +918,9 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
     __shared__ int arrived[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), quarter = lane >> 4, col = lane & 15;
 
-    Run run = find_run<R>(a);
+    Work run = find_work<R>(a);
     if (run.u >= run.end) return;
-    Seq<R> seq(a, run.b);
+    Seq<R> seq(a, run.b, run.floor);
 
     constexpr int kPieces = D / 16, kVLoads = D / 32;
     // V tile: row r, 16-byte piece c at place c ^ f(r), so that the turning reads spread over the banks
@@ -922,8 +941,8 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
     auto locate = [&]() {
         while (run.u - run.before >= seq.units) {  // next sequence (some have no rows)
             run.before += seq.units;
-            if (++run.b >= a.B) return false;  // starts that overlap can count past the end
-            seq = Seq<R>(a, run.b);
+            if (++run.b >= a.B) return false;  // only if the arrays change under the call
+            seq = Seq<R>(a, run.b, seq.q0 + seq.nq);
         }
         const int item = (int)((uint32_t)(run.u - run.before) / (uint32_t)seq.per_item);
         const int begin = run.before + item * seq.per_item;
@@ -1151,8 +1170,8 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
 
         // the next portion's page numbers and then its first loads are on their way
         // while this one's waves are joined
-        const int first = (int)((uint32_t)ustart / (uint32_t)run.per);
-        const Shared done = {first, (int)((uint32_t)(ustart + seq.per_item - kSetup - 1) / (uint32_t)run.per),
+        const int first = group_of(ustart, run.per);
+        const Shared done = {first, group_of(ustart + seq.per_item - kSetup - 1, run.per),
                              first * run.per == ustart ? 0 : 1, h, r0, min(R, rows - r0), q0};
         float *out = nullptr;
         if (done.first != done.last) {
@@ -1257,9 +1276,9 @@ __global__ __launch_bounds__(2 * R, 2) void attn_many_kernel(CacheArgs a) {
     __shared__ int arrived[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), half = lane >> 5, col = lane & 31;
 
-    Run run = find_run<R>(a);
+    Work run = find_work<R>(a);
     if (run.u >= run.end) return;
-    Seq<R> seq(a, run.b);
+    Seq<R> seq(a, run.b, run.floor);
 
     const int lrow = tid / kPieces, lpiece = tid % kPieces;  // of a thread's first load; the others kThreads / kPieces rows on
     const int xk = D == 128 ? (col & 15) : ((col >> 1) & 7);
@@ -1275,8 +1294,8 @@ __global__ __launch_bounds__(2 * R, 2) void attn_many_kernel(CacheArgs a) {
     while (run.u < run.end) {
         while (run.u - run.before >= seq.units) {  // next sequence (some have no rows)
             run.before += seq.units;
-            if (++run.b >= a.B) break;  // starts that overlap can count past the end
-            seq = Seq<R>(a, run.b);
+            if (++run.b >= a.B) break;  // only if the arrays change under the call
+            seq = Seq<R>(a, run.b, seq.q0 + seq.nq);
         }
         if (run.b >= a.B) break;
         const int item = (int)((uint32_t)(run.u - run.before) / (uint32_t)seq.per_item);
@@ -1459,8 +1478,7 @@ __global__ __launch_bounds__(2 * R, 2) void attn_many_kernel(CacheArgs a) {
         for (; t < plain && gone == 0; ++t) iteration(t, std::false_type{});
         for (; t < tiles; ++t) iteration(t, std::true_type{});
 
-        const int first = (int)((uint32_t)ustart / (uint32_t)run.per);
-        const int last = (int)((uint32_t)(begin + seq.per_item - 1) / (uint32_t)run.per);
+        const int first = group_of(ustart, run.per), last = group_of(begin + seq.per_item - 1, run.per);
         float *out = nullptr;
         if (first != last) {
             out = partial<R, D>(a, blockIdx.x, first < (int)blockIdx.x || first * run.per == ustart ? 0 : 1);
@@ -1553,11 +1571,8 @@ __global__ __launch_bounds__(2 * R, 2) void attn_many_kernel(CacheArgs a) {
     }
 }
 
-// Units of work are counted in 31 bits: whether what the host knows keeps them there.
 bool units_fit(const CacheArgs &a, int R) {
-    const int64_t most = ceil_div((a.max_pages << a.page_shift) + unit_of(R), unit_of(R)) + kSetup;
-    const int64_t items = ((int64_t)a.Tq * a.G / R + a.B) * a.H;
-    return most <= 0x7fffffff / (items + 1);
+    return qw3_units::units_fit(a.Tq, a.G, a.B, a.H, a.max_pages << a.page_shift, R);
 }
 
 template <int D, bool E4M3, int R>

@@ -162,18 +162,30 @@ __global__ __launch_bounds__(256) void cache_read_kernel(const uint8_t *__restri
     constexpr int kPieces = D / 16;
     const int lane = threadIdx.x & 63, which = blockIdx.y;
     const int64_t t0 = (int64_t)blockIdx.x * 16;
-    // sequences that end at or before t0
-    int b = 0;
+    // b: the first sequence that ends past t; start: the largest start up to its own
+    int b = 0, start = cu[0];
     for (int base = 0; base < B; base += 64) {
-        const unsigned long long in = __ballot(base + lane < B && cu[base + lane + 1] <= t0);
-        b += __popcll(in);
-        if (in != ~0ull) break;
+        const int end = base + lane < B ? cu[base + lane + 1] : 0x7fffffff;
+        const unsigned long long past = __ballot(end > t0);
+        const int n = past ? __builtin_ctzll(past) : 64;
+        int top = n > 0 ? __builtin_amdgcn_readlane(end, n - 1) : start;
+        if (__any(lane < n && end > top)) {  // starts that fall
+            top = lane < n ? end : start;
+            for (int m = 32; m >= 1; m /= 2) top = max(top, __shfl_xor(top, m, 64));
+        }
+        start = max(start, top);
+        b += n;
+        if (past) break;
     }
     const int tok = (threadIdx.x / kPieces) & 15, piece = threadIdx.x % kPieces;
     const int64_t t = t0 + tok;
-    while (b < B && cu[b + 1] <= t) ++b;
+    for (; b < B; ++b) {
+        const int end = cu[b + 1];
+        if (end > t) break;
+        start = max(start, end);
+    }
     if (b >= B || t >= total) return;
-    const int64_t pos = t - cu[b], idx = pos >> page_shift;
+    const int64_t pos = t - start, idx = pos >> page_shift;
     if (pos < 0) return;
     int64_t page = idx < max_pages ? table[b * max_pages + idx] : -1;
     const bool there = page >= 0 && page < pages;

@@ -262,7 +262,9 @@ qw3_status qgemm_w3g128_smallM_noalloc(const uint16_t *x, const int32_t *packed,
  *     packed array.  Arrays of starts, lengths, tables, slots and trees are
  *     read on the device: a call never waits for them.  Entries out of range
  *     are clipped and never read or write out of bounds: a token whose page is
- *     not in 0..pages-1 is not attended to and reads back as zeros.
+ *     not in 0..pages-1 is not attended to and reads back as zeros.  A start of
+ *     rows (cu_q, cu) below an earlier one counts as that one, so no row belongs to
+ *     two sequences; the keys of two sequences (cu_k) may overlap.
  *   - 1 <= B <= QW3_MAX_SEQS, at most QW3_MAX_TOKENS rows, QW3_MAX_HEADS heads,
  *     Hq a multiple of H, sm_scale > 0 and finite, else QW3_ERR_SHAPE.  B or
  *     the number of rows may be 0: no work.
