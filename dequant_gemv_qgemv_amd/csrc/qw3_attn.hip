@@ -885,6 +885,24 @@ __device__ __forceinline__ bf8_t decode8(uint32_t lo, uint32_t hi) {
     return __builtin_bit_cast(bf8_t, i4_t{(int)a.x, (int)a.y, (int)b.x, (int)b.y});
 }
 
+// NaN among e4m3 codes.  A place that was never written may hold one, and a weight
+// of zero does not hide it (0 NaN = NaN).  So where a tile has keys that some row
+// may not see, the codes that are NaN go to the matrix unit as zeros, and NaN goes
+// into just the sums of the rows that see them: what a row does not see has no
+// influence on it, and one that sees a NaN has it in that channel.
+
+// The bytes of w that are NaN (0x7f, 0xff), each with its highest bit.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t without_codes(uint32_t w, uint32_t n) { return w & ~(n | (n - (n >> 7))); }
+__device__ __forceinline__ uint4 nan_codes(uint4 w) {
+    return make_uint4(nan_codes(w.x), nan_codes(w.y), nan_codes(w.z), nan_codes(w.w));
+}
+__device__ __forceinline__ uint4 without_codes(uint4 w, uint4 n) {
+    return make_uint4(without_codes(w.x, n.x), without_codes(w.y, n.y), without_codes(w.z, n.z), without_codes(w.w, n.w));
+}
+__device__ __forceinline__ uint32_t any_of(uint4 n) { return n.x | n.y | n.z | n.w; }
+constexpr float kNaN = __builtin_nanf("");
+
 // The keys base..base + 63 that a row sees, as bits: all up to `seen`, and of
 // the drafts, which begin at ctx, those of its word; none from len on.
 __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
@@ -1033,13 +1051,45 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
                 for (int g = 0; g < 2; ++g) gone[g] = (uint32_t)page_of(s, g) >= (uint64_t)a.pages;
             }
             // V's codes into the turning tile
+            uint32_t nans_here = 0;
 #pragma unroll
             for (int c = 0; c < kVLoads; ++c) {
                 const int r = vrow + c * (64 / kPieces);
-                uint4 w = st.v[c];
-                // p = 0 hides a row only if its codes are numbers: e4m3 garbage may be NaN
-                if (E4M3 && kMasked && (key + r >= len || gone[c / (kVLoads / 2)])) w = make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4 *>(turn + r * D + ((vpiece ^ place(r)) << 4)) = w;
+                if (E4M3 && kMasked) {
+                    if (key + r >= len || gone[c / (kVLoads / 2)]) st.v[c] = make_uint4(0, 0, 0, 0);
+                    nans_here |= nan_codes(st.v[c].x) | nan_codes(st.v[c].y) | nan_codes(st.v[c].z) | nan_codes(st.v[c].w);
+                }
+                *reinterpret_cast<uint4 *>(turn + r * D + ((vpiece ^ place(r)) << 4)) = st.v[c];
+            }
+            if (E4M3 && kMasked && __any(nans_here != 0)) {
+                uint32_t nan_keys = 0;  // of the wave's 32, as bits
+#pragma unroll
+                for (int c = 0; c < kVLoads; ++c) {
+                    const int r = vrow + c * (64 / kPieces);
+                    const uint4 w = st.v[c], nans = nan_codes(w);
+                    *reinterpret_cast<uint4 *>(turn + r * D + ((vpiece ^ place(r)) << 4)) = without_codes(w, nans);
+                    for (unsigned long long lanes = __ballot(any_of(nans) != 0); lanes != 0;) {
+                        const int row = __builtin_ctzll(lanes) / kPieces;
+                        nan_keys |= 1u << (row + c * (64 / kPieces));
+                        lanes &= ~(((1ull << kPieces) - 1) << (row * kPieces));
+                    }
+                }
+                for (; nan_keys != 0; nan_keys &= nan_keys - 1) {
+                    const int r = __builtin_ctz(nan_keys);  // its page exists, or its codes were taken as zeros
+                    const int64_t row = page_of(s, r >> 4) * page_rows + ((int64_t)h << a.page_shift) + to_v +
+                                        ((key + r) & ((1 << a.page_shift) - 1));
+                    const uint8_t *at = a.codes + row * D + 4 * quarter;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint32_t nans = nan_codes(*reinterpret_cast<const uint32_t *>(at + 16 * i));
+#pragma unroll
+                        for (int x = 0; x < kN; ++x)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if ((nans >> (8 * e + 7)) & (uint32_t)(visible(key, seen[x], tree[x], ctx, len) >> r) & 1)
+                                    acc[x][i][e] = kNaN;
+                    }
+                }
             }
             float kc[2][4], vc[2][4];
 #pragma unroll
@@ -1273,6 +1323,7 @@ __global__ __launch_bounds__(2 * R, 2) void attn_many_kernel(CacheArgs a) {
     constexpr int kLoads = kUnit * kPieces / kThreads;  // of a thread, for K and for V
     __shared__ __attribute__((aligned(1024))) char lds[4 * kTileBytes];  // K, V of two tiles
     __shared__ __attribute__((aligned(16))) float tile_scales[2][2][kUnit];
+    __shared__ uint32_t tile_nans[E4M3 ? 2 : 1][kUnit];  // keys with values that are NaN
     __shared__ int arrived[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), half = lane >> 5, col = lane & 31;
 
@@ -1343,9 +1394,11 @@ __global__ __launch_bounds__(2 * R, 2) void attn_many_kernel(CacheArgs a) {
             gone_in = uniform((int)((missing >> (4 * (t - ids_base))) & 15));
         };
         uint32_t gone = 0;  // of the tile in LDS
+        auto partly = [&](int t) { return key0 + (t + 1) * kUnit > min(ctx, len) || gone_in != 0; };  // of the fetched tile
+        bool mixed = false;  // the tile in LDS has keys that some row may not see
         auto place = [&](int t) {  // the fetched tile, as bf16, into its buffer
             char *kt = lds + (2 * (t & 1)) * kTileBytes, *vt = kt + kTileBytes;
-            const bool partly = key0 + (t + 1) * kUnit > len || gone_in != 0;
+            const bool clean = E4M3 && partly(t);
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
                 const int r = lrow + i * (kThreads / kPieces);
@@ -1354,13 +1407,27 @@ __global__ __launch_bounds__(2 * R, 2) void attn_many_kernel(CacheArgs a) {
                     decode8<E4M3>(kcode[i].x, kcode[i].y);
                 *reinterpret_cast<bf8_t *>(kt + r * kRowBytes + (((2 * lpiece + 1) ^ fk) << 4)) =
                     decode8<E4M3>(kcode[i].z, kcode[i].w);
-                uint4 w = vcode[i];
-                // a weight of zero hides a row only if its codes are numbers: e4m3 garbage may be NaN
-                if (E4M3 && partly && (key0 + t * kUnit + r >= len || ((gone_in >> (r >> 4)) & 1)))
-                    w = make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<bf8_t *>(vt + r * kRowBytes + (((2 * lpiece) ^ fv) << 4)) = decode8<E4M3>(w.x, w.y);
-                *reinterpret_cast<bf8_t *>(vt + r * kRowBytes + (((2 * lpiece + 1) ^ fv) << 4)) =
-                    decode8<E4M3>(w.z, w.w);
+                uint4 w = vcode[i], nans = make_uint4(0, 0, 0, 0);
+                if (clean) {
+                    if (key0 + t * kUnit + r >= len || ((gone_in >> (r >> 4)) & 1)) w = make_uint4(0, 0, 0, 0);
+                    nans = nan_codes(w);
+                    w = without_codes(w, nans);
+                    const unsigned long long lanes = __ballot(any_of(nans) != 0);
+                    if (lpiece == 0) tile_nans[t & 1][r] = (uint32_t)(lanes >> lane) & ((1u << kPieces) - 1);
+                }
+                bf8_t v0 = decode8<E4M3>(w.x, w.y), v1 = decode8<E4M3>(w.z, w.w);
+                if (clean && __any(any_of(nans) != 0)) {
+                    // in the tile such a value is 2^-133, which no code stands for
+                    auto mark = [](bf8_t v, uint32_t lo, uint32_t hi) {
+                        i4_t x = __builtin_bit_cast(i4_t, v);
+                        x[0] |= (int)((lo >> 7 & 1) | (lo >> 15 & 1) << 16), x[1] |= (int)((lo >> 23 & 1) | (lo >> 31 & 1) << 16);
+                        x[2] |= (int)((hi >> 7 & 1) | (hi >> 15 & 1) << 16), x[3] |= (int)((hi >> 23 & 1) | (hi >> 31 & 1) << 16);
+                        return __builtin_bit_cast(bf8_t, x);
+                    };
+                    v0 = mark(v0, nans.x, nans.y), v1 = mark(v1, nans.z, nans.w);
+                }
+                *reinterpret_cast<bf8_t *>(vt + r * kRowBytes + (((2 * lpiece) ^ fv) << 4)) = v0;
+                *reinterpret_cast<bf8_t *>(vt + r * kRowBytes + (((2 * lpiece + 1) ^ fv) << 4)) = v1;
             }
             if (tid < 128) tile_scales[t & 1][tid >> 6][tid & 63] = tid < 64 ? scale_in * a.scale : scale_in;
         };
@@ -1400,6 +1467,21 @@ __global__ __launch_bounds__(2 * R, 2) void attn_many_kernel(CacheArgs a) {
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
                     if ((gone >> g) & 1) vis &= ~(0xffffull << (16 * g));
+                if (E4M3 && mixed) {
+                    for (unsigned long long left = __ballot(tile_nans[t & 1][lane] != 0); left != 0; left &= left - 1) {
+                        const int r = uniform(__builtin_ctzll(left));
+                        const char *at = vt + r * kRowBytes + 8 * half;
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4) {
+                                const s4_t v = *reinterpret_cast<const s4_t *>(at + (((4 * i + e / 4) ^ value_place<D>(r)) << 4));
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    if (v[c] == 1 && ((vis >> r) & 1)) acc[i][e + c] = kNaN;
+                            }
+                    }
+                }
                 vis >>= 4 * half;
             }
             float top = kNegInf;
@@ -1461,7 +1543,7 @@ __global__ __launch_bounds__(2 * R, 2) void attn_many_kernel(CacheArgs a) {
         if (tiles > 0) {
             fetch(0);
             place(0);
-            gone = gone_in;
+            gone = gone_in, mixed = partly(0);
         }
         auto iteration = [&](int t, auto masked_c) {
             lds_barrier();  // tile t is in place; nobody reads the other buffer any more
@@ -1469,7 +1551,7 @@ __global__ __launch_bounds__(2 * R, 2) void attn_many_kernel(CacheArgs a) {
             if (live) step(t, masked_c);
             if (t + 1 < tiles) {
                 place(t + 1);
-                gone = gone_in;
+                gone = gone_in, mixed = partly(t + 1);
             }
         };
         // tiles up to the first that can hold a draft, the end or a missing page, then the others

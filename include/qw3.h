@@ -273,7 +273,8 @@ qw3_status qgemm_w3g128_smallM_noalloc(const uint16_t *x, const int32_t *packed,
  *     joined in a fixed order.  Safe to capture, like the calls above (qattn_cache
  *     and qattn_prompt after one call of the size on the stream).
  *   - Domain: |q|, |k|, |v|, s below 2^60.  NaN and infinities in what a row sees
- *     make its output NaN or infinite; what it does not see has no influence on it.
+ *     make its output NaN or infinite; what it does not see has no influence on it,
+ *     whatever it is (e4m3 codes of NaN in places that were never written, too).
  * ------------------------------------------------------------------------ */
 enum { QW3_CODES_INT8 = 0, QW3_CODES_E4M3 = 1 }; /* code_type */
 enum { QW3_SRC_BF16 = 0, QW3_SRC_F32 = 1 };      /* src_type */

@@ -82,3 +82,67 @@ def test_falling_starts_of_reads_and_decodes():
         assert np.array_equal(*decodes), cu
         if len(reads) == 2:
             assert np.array_equal(*reads), cu
+
+
+# ------------------------------------------------- codes that are NaN (e4m3) ---
+def plant(codes, table, seq, token, which, head, channels, code):
+    size = codes.shape[3]
+    codes.view(torch.uint8)[int(table[seq, token // size]), which, head, token % size, channels] = code
+
+
+@pytest.mark.parametrize("tree", [True, False])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group", [2, 4, 20])
+def test_nan_codes_reach_only_rows_that_see_them(group, dim, tree):
+    """Places of drafts that were never written, or hold another writer's NaN: values and keys, seen by some rows of a
+    block and hidden from others; behind them a context that all rows see and what lies past the end."""
+    def touch(codes, scales, table, rq, words):
+        if words is not None:
+            words[:] = torch.tensor([1, 3, 5, 9, 17] * 3)  # each its own and the first draft
+            words[12] = 1  # sees nothing of the draft that is its own
+        # sequence 0: drafts are tokens 43..47; draft 2 has NaN in three channels of head 0, draft 4 in all of head 1
+        for c, code in ((0, 0x7F), (5, 0xFF), (dim - 1, 0x7F)):
+            plant(codes, table, 0, 45, 1, 0, c, code)
+        plant(codes, table, 0, 47, 1, 1, slice(None), 0x7F)
+        # sequence 1: draft 1 (token 56) has a key that is NaN, draft 3 a value; a context token (3) a value in one channel
+        plant(codes, table, 1, 56, 0, 0, 7, 0xFF)
+        plant(codes, table, 1, 58, 1, 0, slice(10, 20), 0xFF)
+        plant(codes, table, 1, 3, 1, 1, 33, 0x7F)
+        # sequence 2: every place of draft 2 (token 63, the last of its page) and all past the end
+        plant(codes, table, 2, 63, 0, slice(None), slice(None), 0x7F)
+        plant(codes, table, 2, 63, 1, slice(None), slice(None), 0x7F)
+        codes.view(torch.uint8)[int(table[2, 4]), :, :, 2:] = 0xFF
+        scales[int(table[2, 4]), :, :, 2:] = float("nan")
+
+    say("nan codes", group, dim, tree)
+    cache_case(np.random.default_rng(41), "e4m3", 2, group, dim, 16, [48, 60, 66], 5, tree, touch=touch)
+
+
+def test_nan_codes_among_many_rows():
+    """Blocks of 256 rows: 64 drafts of which some are NaN."""
+    def touch(codes, scales, table, rq, words):
+        for seq, token in ((0, 300 - 64 + 10), (0, 299), (1, 1100 - 30)):
+            plant(codes, table, seq, token, 1, slice(None), slice(3, 90), 0x7F)
+        plant(codes, table, 1, 1100 - 64, 0, 1, 0, 0xFF)
+
+    cache_case(np.random.default_rng(42), "e4m3", 2, 128, 128, 16, [300, 1100], 64, True, touch=touch, some=6)
+
+
+def test_padded_drafts_over_a_cache_that_was_never_cleared():
+    """A tree of three padded to eight with slots of -1, in memory that holds 0x7f everywhere."""
+    rng = np.random.default_rng(43)
+    codes = torch.full((8, 2, 2, 16, 128), 0x7F, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    scales = torch.full((8, 2, 2, 16), 1.0, dtype=torch.float32, device="cuda")
+    table = ints([[5, 2, 7]])
+    k, v, rq = rows(rng, 33, 2, 128), rows(rng, 33, 2, 128), rows(rng, 8, 8, 128)
+    slot = [int(table[0, t // 16]) * 16 + t % 16 for t in range(33)]
+    q().qcache_write(k, v, torch.tensor(slot, device="cuda"), codes, scales)
+    words = torch.tensor([1, 3, 5, 0, 0, 0, 0, 0], dtype=torch.int64, device="cuda")
+    got = f64(q().qattn_cache(rq, codes, scales, table, ints([38]), cu_q=ints([0, 8]), tree=words))
+    c, s = ref.quantise(np.stack([k.float().cpu().numpy(), v.float().cpu().numpy()]), "e4m3")
+    val = ref.code_values(c, "e4m3") * s.astype(np.float64)[..., None]
+    for i in range(8):
+        sees = ref.cache_sees(i, 8, 38, int(words[i]))
+        for h in range(8):
+            o, bound = ref.attend(f64(rq)[i, h], val[0][:, h // 4], val[1][:, h // 4], sees, 128 ** -0.5)
+            check(got[i, h], o, bound, "row %d head %d" % (i, h))
