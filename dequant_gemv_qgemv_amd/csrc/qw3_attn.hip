@@ -117,6 +117,14 @@ __device__ __forceinline__ float2 load_agent(const float *p) {
     return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
 }
 
+// By one workgroup of a call that counts: the next call's counters (qw3_units.h).
+template <int kThreads>
+__device__ __forceinline__ void clear_next(int *counts) {
+#pragma unroll
+    for (int i = 0; i < kCounts / 2; i += kThreads)
+        store_agent(reinterpret_cast<float *>(counts) + 2 * (i + threadIdx.x), 0.0f, 0.0f);
+}
+
 // Inclusive maximum over the wave's lanes up to one's own, of values >= 0.
 __device__ __forceinline__ int wave_scan_max(int x) {
     x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false));  // row_shr 1, 2, 4, 8
@@ -146,6 +154,7 @@ struct PromptArgs {
     int slices;   // with SPLIT: workgroups for one tile's keys, at most, ...
     float *part;  // ... where they leave their parts, and ...
     int *counts;  // ... how many have
+    int *clear;   // the next call's counters
 };
 
 constexpr int kKeys = 64;  // of a tile
@@ -318,6 +327,7 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
     __shared__ __attribute__((aligned(1024))) char lds[kStages * 2 * kTileBytes];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), half = lane >> 5, col = lane & 31;
     const int row_wave = wave / W, first_block = W == 1 ? 0 : wave % W;
+    if (SPLIT && blockIdx.x == 0 && (int)blockIdx.y == a.slices - 1) clear_next<256>(a.clear);
 
     // Workgroups go round the 8 XCDs: where the heads divide by 8, each XCD takes
     // the same ones of every tile, so that its L2 holds few heads' keys.
@@ -658,6 +668,7 @@ struct CacheArgs {
     uint16_t *o;
     float *part;   // partial results
     int *counts;   // workgroups that have finished with an item, by the first of them
+    int *clear;    // the next call's counters
     int64_t q_ts, q_hs, max_pages, pages;
     int B, Tq, Hq, H, G, page_shift, groups;
     float scale;
@@ -937,6 +948,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(CacheArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), quarter = lane >> 4, col = lane & 15;
 
     Work run = find_work<R>(a);
+    if ((int)blockIdx.x == a.groups - 1) clear_next<R <= 32 ? 256 : 2 * R>(a.clear);  // it has work in large calls only
     if (run.u >= run.end) return;
     Seq<R> seq(a, run.b, run.floor);
 
@@ -1328,6 +1340,7 @@ __global__ __launch_bounds__(2 * R, 2) void attn_many_kernel(CacheArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), half = lane >> 5, col = lane & 31;
 
     Work run = find_work<R>(a);
+    if ((int)blockIdx.x == a.groups - 1) clear_next<R <= 32 ? 256 : 2 * R>(a.clear);  // it has work in large calls only
     if (run.u >= run.end) return;
     Seq<R> seq(a, run.b, run.floor);
 
@@ -1668,7 +1681,7 @@ qw3_status launch_cache(CacheArgs a, hipStream_t stream) {
     st = workspace(stream, (size_t)a.groups * 2 * R * (D + 2) * sizeof(float), &ws);
     if (st != QW3_OK) return st;
     a.part = static_cast<float *>(ws);
-    st = counters(stream, a.groups, &a.counts);
+    st = counters(stream, a.groups, &a.counts, &a.clear);
     if (st != QW3_OK) return st;
     if constexpr (R <= 32)
         hipLaunchKernelGGL((attn_few_kernel<D, E4M3, R>), dim3(a.groups), dim3(256), 0, stream, a);
@@ -1713,41 +1726,54 @@ bool scale_ok(float s) { return s > 0.0f && s < __builtin_huge_valf(); }
 
 }  // namespace
 
-// One buffer per (device, stream handle), cleared by the first call on the
-// stream and never grown: kMaxCounts is more than any grid that counts.
+// Four banks per (device, stream handle), cleared by the first call on the stream
+// and never grown: kCounts is more than any grid that counts.
 namespace {
-constexpr int kMaxCounts = 4096;
 struct Counters {
     int dev;
     hipStream_t stream;
     int *ptr;
+    Banks banks;
 };
 std::mutex g_counters_mutex;
 std::vector<Counters> g_counters;
 __global__ void clear_counts_kernel(int *p) { p[blockIdx.x * 256 + threadIdx.x] = 0; }
+
+qw3_status clear_counts(int *p, int banks, hipStream_t stream) {
+    hipLaunchKernelGGL(clear_counts_kernel, dim3(banks * kCounts / 256), dim3(256), 0, stream, p);
+    return check_launch();
+}
 }  // namespace
 
-qw3_status qw3_shared::counters(hipStream_t stream, int n, int **out) {
-    if (n > kMaxCounts) return hip_fail(hipErrorInvalidValue);
+qw3_status qw3_shared::counters(hipStream_t stream, int n, int **use, int **clear) {
+    if (n > kCounts) return hip_fail(hipErrorInvalidValue);
     int dev = 0;
     hipError_t err = hipGetDevice(&dev);
     if (err != hipSuccess) return hip_fail(err);
+    hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    if (hipStreamGetCaptureInfo(stream, &capture, &id) != hipSuccess) {
+        (void)hipGetLastError();
+        capture = hipStreamCaptureStatusNone;
+    }
+    const bool capturing = capture != hipStreamCaptureStatusNone;
     std::lock_guard<std::mutex> lock(g_counters_mutex);
-    for (const auto &e : g_counters)
-        if (e.dev == dev && e.stream == stream) {
-            *out = e.ptr;
-            return QW3_OK;
-        }
-    if (stream_capturing(stream)) return QW3_ERR_CAPTURE;
-    void *p = nullptr;
-    err = hipMalloc(&p, kMaxCounts * sizeof(int));
-    if (err != hipSuccess) return hip_fail(err);
-    hipLaunchKernelGGL(clear_counts_kernel, dim3(kMaxCounts / 256), dim3(256), 0, stream, static_cast<int *>(p));
-    const qw3_status st = check_launch();
-    if (st != QW3_OK) return st;
-    g_counters.push_back(Counters{dev, stream, static_cast<int *>(p)});
-    *out = static_cast<int *>(p);
-    return QW3_OK;
+    Counters *mine = nullptr;
+    for (auto &e : g_counters)
+        if (e.dev == dev && e.stream == stream) mine = &e;
+    if (mine == nullptr) {
+        if (capturing) return QW3_ERR_CAPTURE;
+        void *p = nullptr;
+        err = hipMalloc(&p, 4 * kCounts * sizeof(int));
+        if (err != hipSuccess) return hip_fail(err);
+        const qw3_status st = clear_counts(static_cast<int *>(p), 4, stream);
+        if (st != QW3_OK) return st;
+        g_counters.push_back(Counters{dev, stream, static_cast<int *>(p), Banks{}});
+        mine = &g_counters.back();
+    }
+    const BankChoice choice = mine->banks.choose(capturing, id);
+    *use = mine->ptr + choice.use * kCounts, *clear = mine->ptr + choice.clear * kCounts;
+    return choice.fresh ? clear_counts(mine->ptr + 2 * kCounts, 2, stream) : QW3_OK;
 }
 
 extern "C" {
@@ -1789,7 +1815,7 @@ qw3_status qattn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v,
         st = workspace(stream, (size_t)(tiles * Hq * a.slices) * 64 * (D + 2) * sizeof(float), &ws);
         if (st != QW3_OK) return st;
         a.part = static_cast<float *>(ws);
-        st = counters(stream, (int)(tiles * Hq), &a.counts);
+        st = counters(stream, (int)(tiles * Hq), &a.counts, &a.clear);
         if (st != QW3_OK) return st;
     }
     auto run = [&](auto kernel) {

@@ -603,9 +603,9 @@ inline qw3_status blocks_per_cu(const void *kernel, int wgs, size_t lds, int *ou
 
 // Scratch of `stream` on the current device, at least `bytes` (qw3.hip).
 qw3_status workspace(hipStream_t stream, size_t bytes, void **out);
-// Counters of `stream` on the current device, zero between calls: a kernel that
-// counts in them sets them back (qw3_attn.hip).
-qw3_status counters(hipStream_t stream, int n, int **out);
+// Counters of `stream` on the current device for one call, zero when it runs, and
+// those of the next, which the call clears (qw3_attn.hip).
+qw3_status counters(hipStream_t stream, int n, int **use, int **clear);
 bool stream_capturing(hipStream_t stream);
 
 // The batch-1 launches (qw3_gemv.hip).  launch_gemv: y = dequant(W) x for M

@@ -60,4 +60,36 @@ constexpr Run run_of(int total, int groups, int least, int group) {
 // The workgroup whose run holds a unit.
 constexpr int group_of(int unit, int per) { return (int)((uint32_t)unit / (uint32_t)per); }
 
+// The counters of a stream: four banks of kCounts.  A call counts in one bank and
+// clears the other of its pair for the call behind it, which runs later: what a
+// bank holds from before, whatever that is, lasts for no more than one call.
+// Calls that a graph captures have a pair of their own, cleared by a launch of its
+// own (`fresh`) before the first of a capture: a replay starts from zeros, however
+// the one before it ended, and leaves the eager calls' banks alone.  That launch
+// costs a replay 4 us, once whatever the number of its calls (80 decodes of one
+// token: 664 -> 674 us).  Counts are set
+// back to zero by the call itself too, so the order in which threads enqueue on one
+// stream does not matter.
+constexpr int kCounts = 1024;
+struct BankChoice {
+    int use, clear;
+    bool fresh;
+};
+struct Banks {
+    int eager = 0, captured = 2;
+    unsigned long long capture = 0;  // the last capture's id
+    bool captures = false;           // there was one
+    constexpr BankChoice choose(bool capturing, unsigned long long id) {
+        if (!capturing) {
+            const int use = eager;
+            eager = 1 - use;
+            return BankChoice{use, eager, false};
+        }
+        const bool fresh = !captures || capture != id;
+        const int use = fresh ? 2 : captured;
+        captures = true, capture = id, captured = 5 - use;
+        return BankChoice{use, captured, fresh};
+    }
+};
+
 }  // namespace qw3_units

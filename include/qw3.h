@@ -174,6 +174,11 @@ qw3_status qgemv_w3g128_multi(const uint16_t *x, int32_t count, const int32_t *c
  *     told apart by handle: before destroying a stream that has calls of this
  *     library queued, wait for them (hipStreamSynchronize), since a stream
  *     created later at the same address takes over the same buffer.
+ *   - What shares a buffer must not overlap in time: calls on its stream never do,
+ *     but replays of graphs captured on the stream use it too, wherever they are
+ *     launched.  Order them, on other streams by events.  Calls that overlap all
+ *     the same spoil each other's results, not those of later calls.  The handle
+ *     hipStreamPerThread counts as one stream: threads that use it share a buffer.
  *   - Graph capture: a call captured on a stream uses that stream's buffer as
  *     it is at capture time.  If the buffer would have to grow during capture
  *     the call returns QW3_ERR_CAPTURE and enqueues nothing; make one call of
@@ -272,6 +277,9 @@ qw3_status qgemm_w3g128_smallM_noalloc(const uint16_t *x, const int32_t *packed,
  *   - Deterministic: parts of a sequence that several workgroups worked on are
  *     joined in a fixed order.  Safe to capture, like the calls above (qattn_cache
  *     and qattn_prompt after one call of the size on the stream).
+ *   - qattn_cache and qattn_prompt share their stream's buffer and counters with
+ *     other calls by the rules of qgemm_w3g128_smallM: calls and replays that share
+ *     them must not overlap in time.
  *   - Domain: |q|, |k|, |v|, s below 2^60.  NaN and infinities in what a row sees
  *     make its output NaN or infinite; what it does not see has no influence on it,
  *     whatever it is (e4m3 codes of NaN in places that were never written, too).

@@ -74,17 +74,29 @@ extern "C" int walk(const int *cu, const int *lens, int B, int Tq, int G, int H,
     for (int b = 0; b < B; ++b) items += (int64_t)blocks_of(rows[b].n * G, R) * H;
     return (int64_t)expects.size() == items ? 0 : 10;
 }
+
+extern "C" void *banks_new() { return new Banks(); }
+extern "C" void banks_delete(void *b) { delete static_cast<Banks *>(b); }
+extern "C" void banks_choose(void *b, int capturing, unsigned long long id, int *out) {
+    const BankChoice c = static_cast<Banks *>(b)->choose(capturing != 0, id);
+    out[0] = c.use, out[1] = c.clear, out[2] = c.fresh;
+}
 """
 
 
 @pytest.fixture(scope="module")
-def walk(tmp_path_factory):
+def shim(tmp_path_factory):
     d = tmp_path_factory.mktemp("units")
     src, lib = d / "shim.cpp", d / "shim.so"
     src.write_text(SHIM)
     subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-shared", "-fPIC", "-I", CSRC, "-o", str(lib), str(src)],
                    check=True)
-    fn = ctypes.CDLL(str(lib)).walk
+    return ctypes.CDLL(str(lib))
+
+
+@pytest.fixture(scope="module")
+def walk(shim):
+    fn = shim.walk
     p = np.ctypeslib.ndpointer
 
     def call(cu, lens, Tq, G, H, keys, R, groups=512, join=0.14):
@@ -139,3 +151,95 @@ def test_the_largest_totals(walk):
     # the host's bound just holds: 255 sequences of one row, 2^29 keys each, blocks of 256
     status, total, rows = walk(np.arange(256), [(1 << 29) - 300] * 255, 255, 1, 1, (1 << 29) - 300, 256, 512, 0.8)
     assert status == 0 and total > 2 ** 31 - 2 ** 24
+
+
+# --------------------------------------------------------------- counters ---
+class Chooser:
+    """The banks of one stream, by the library's own choice."""
+
+    def __init__(self, lib):
+        lib.banks_new.restype = ctypes.c_void_p
+        self.lib, self.at = lib, ctypes.c_void_p(lib.banks_new())
+
+    def __call__(self, capture=None):
+        out = (ctypes.c_int * 3)()
+        self.lib.banks_choose(self.at, capture is not None, ctypes.c_ulonglong(capture or 0), out)
+        return tuple(out)
+
+
+class OneBank:
+    """One bank for all, set back to zero by whoever is last and by nobody else."""
+
+    def __call__(self, capture=None):
+        return 0, None, 0
+
+
+ITEMS = 4
+
+
+def run_calls(memory, calls, rng):
+    """Runs calls at the same time: each a choice of banks and its items' numbers of parts, its steps taken in turn at
+    random; a joined item's count is set back a step later. Returns, for each call, how many of its items were joined
+    when all their parts were there, and how many joins came too early."""
+    done = [[0, 0] for _ in calls]
+    queues, arrived = [], [[0] * ITEMS for _ in calls]
+    for (_, _, fresh), parts in calls:
+        work = [("count", item) for item, n in enumerate(parts) for _ in range(n)] + [("clear", 0)]
+        queues.append([("fresh", 0)] * fresh + [work[i] for i in rng.permutation(len(work))])
+    while any(queues):
+        n = rng.choice([i for i, s in enumerate(queues) if s])
+        (use, clear, _), parts = calls[n]
+        step, item = queues[n].pop(0)
+        if step == "fresh":
+            memory[2][:] = memory[3][:] = [0] * ITEMS
+        elif step == "clear" and clear is not None:
+            memory[clear][:] = [0] * ITEMS
+        elif step == "reset":
+            memory[use][item] = 0
+        elif step == "count":
+            arrived[n][item] += 1
+            memory[use][item] += 1
+            if memory[use][item] == parts[item]:
+                done[n][0 if arrived[n][item] == parts[item] else 1] += 1
+                queues[n].insert(0, ("reset", item))
+    return done
+
+
+def counts_after_a_race(chooser, seed):
+    """Two graphs captured on one stream, replayed at once with each other and with an eager call; then everything in
+    order. Returns how many of the ordered calls joined every item once and in time, of how many."""
+    rng = np.random.default_rng(seed)
+    memory = [[0] * ITEMS for _ in range(4)]
+    parts = lambda: [int(x) for x in rng.integers(1, 6, ITEMS)]  # noqa: E731
+    alone = lambda call: run_calls(memory, [call], rng)[0] == [ITEMS, 0]  # noqa: E731
+    assert alone((chooser(), parts()))
+    graphs = [[(chooser(capture=c), parts()) for _ in range(rng.integers(1, 4))] for c in (7, 8)]
+    assert alone((chooser(), parts()))
+    for _ in range(3):  # the race: a call of each at a time
+        run_calls(memory, [g[rng.integers(0, len(g))] for g in graphs], rng)
+    run_calls(memory, [graphs[0][0], (chooser(), parts())], rng)
+    good = total = 0
+    for _ in range(4):
+        for call in [None] + graphs[rng.integers(0, 2)] + [None, None]:
+            good, total = good + alone(call or (chooser(), parts())), total + 1
+    return good, total
+
+
+def test_counters_survive_calls_that_overlapped(shim):
+    """Calls that share a stream's counters must not overlap; if they do all the same, later ones are right again."""
+    for seed in range(60):
+        good, total = counts_after_a_race(Chooser(shim), seed)
+        assert good == total, seed
+
+
+def test_the_model_sees_counters_that_stay_damaged():
+    spoiled = sum(good != total for good, total in (counts_after_a_race(OneBank(), seed) for seed in range(60)))
+    assert spoiled > 30
+
+
+def test_banks_in_order(shim):
+    choose = Chooser(shim)
+    assert choose() == (0, 1, 0) and choose() == (1, 0, 0) and choose() == (0, 1, 0)
+    assert choose(capture=0) == (2, 3, 1) and choose(capture=0) == (3, 2, 0) and choose(capture=0) == (2, 3, 0)
+    assert choose() == (1, 0, 0)
+    assert choose(capture=5) == (2, 3, 1) and choose() == (0, 1, 0) and choose(capture=5) == (3, 2, 0)

@@ -146,3 +146,42 @@ def test_padded_drafts_over_a_cache_that_was_never_cleared():
         for h in range(8):
             o, bound = ref.attend(f64(rq)[i, h], val[0][:, h // 4], val[1][:, h // 4], sees, 128 ** -0.5)
             check(got[i, h], o, bound, "row %d head %d" % (i, h))
+
+
+# ---------------------------------------------------------------- counters ---
+def test_graphs_of_one_stream_replayed_on_others():
+    """Two graphs captured on one stream, of two and of three calls that join parts, replayed in turn on other streams,
+    with eager calls on the first between them: ordered by events, each gives the eager call's bits every time."""
+    rng = np.random.default_rng(51)
+    codes, scales = random_cache(rng, "int8", 900, 16, 2, 128)
+    lens = [6000, 5000, 40]
+    table, n = tables(rng, lens, 16, 900), ints(lens)
+    few, many = rows(rng, 3, 16, 128), rows(rng, 48, 32, 128)
+    cu, cuq, cuk = starts([16, 20, 12]), starts([10, 4]), starts([2500, 1500])
+    pq, pk = rows(rng, 14, 4, 128), rows(rng, 4000, 1, 128)
+    wide = torch.full((3, (1 << 25) // (16 * 48 * 32) + 1), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    calls = [lambda: q().qattn_cache(few, codes, scales, table, n), lambda: q().qattn_prompt(pq, pk, pk, cuq, cuk),
+             lambda: q().qattn_cache(many, codes, scales, wide, n, cu_q=cu)]
+    home, away = torch.cuda.Stream(), [torch.cuda.Stream(), torch.cuda.Stream()]
+    home.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(home):
+        want = [bits(c()) for c in calls]
+    graphs, outs = [], []
+    for chain in ([0, 1, 2], [2, 0]):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=home):
+            outs.append([(i, calls[i]()) for i in chain])
+        graphs.append(g)
+    for turn in range(6):
+        for i, out in outs[turn % 2]:
+            out.fill_(3.0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(away[turn % 2]):
+            graphs[turn % 2].replay()
+        home.wait_stream(away[turn % 2])
+        with torch.cuda.stream(home):
+            eager = [c() for c in calls[:1 + turn % 3]]
+        torch.cuda.synchronize()
+        for i, out in outs[turn % 2] + list(enumerate(eager)):
+            assert np.array_equal(bits(out), want[i]), (turn, i)
