@@ -107,6 +107,11 @@ __device__ __forceinline__ float sum_quarters(float x) {
     return sum_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
+__device__ __forceinline__ float wave_max_f(float x) {  // over all 64 lanes, in every lane
+    for (int d = 8; d >= 1; d /= 2) x = fmaxf(x, __shfl_xor(x, d, 64));
+    return max_quarters(x);
+}
+
 __device__ __forceinline__ void store_agent(float *p, float x, float y) {
     const uint64_t v = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
     __hip_atomic_store(reinterpret_cast<uint64_t *>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -167,42 +172,101 @@ constexpr int kKeys = 64;  // of a tile
 constexpr float kSliceJoin = 2.0f;
 constexpr int kSliceLeast = 16;
 
-// One query row recomputed by a wave from the visible keys alone (keys 0..last).
-// The tiles multiply hidden keys by p = 0, which is not 0 where a hidden value
-// row holds an infinity or NaN; rows that come out non-finite are redone here,
-// so such a value reaches only the rows that see its key.
+// Hidden values that are not numbers.  The tiles multiply hidden keys by p = 0,
+// which is not 0 where a hidden value row holds an infinity or NaN.  A row whose
+// outputs come out non-finite is computed again from the keys it sees alone, but
+// only if such a value lies among the hidden keys of its tiles (at most 94 behind
+// its last): otherwise what it sees made it so, and it is right as it is.  8192
+// tokens of 64 heads, NaN in a value of one kv head: as without (1.0 ms) for most
+// tokens, 14 ms for the last one's (a wave computes its 31 other rows one by one).
+
+// The last of the keys first..end - 1 whose value row is not finite, or -1.
+template <int D>
+__device__ __forceinline__ int last_nonfinite(const uint16_t *v, int64_t ts, int first, int end) {
+    int found = -1;
+    for (int j0 = first; j0 < end; j0 += 64) {
+        const int j = j0 + (int)(threadIdx.x & 63);
+        uint32_t bad = 0;  // an exponent of ones carries into the bit above
+        if (j < end) {
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(v + j * ts + 8 * c);
+                const uint32_t d[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) bad |= (d[e] & 0x7f807f80u) + 0x00800080u;
+            }
+        }
+        const unsigned long long lanes = __ballot((bad & 0x80008000u) != 0);
+        if (lanes != 0) found = j0 + 63 - __builtin_clzll(lanes);
+    }
+    return found;
+}
+
+// One query row by a wave from the keys 0..last: 64 keys at a time, a key for each
+// lane in the scores, channels for each lane in the weighted sum; a step's keys
+// and values are on their way together.
 template <int D>
 __device__ __forceinline__ void exact_row(const PromptArgs &a, const uint16_t *q, const uint16_t *k, const uint16_t *v,
                                        uint16_t *o, int last) {
     const int lane = threadIdx.x & 63;
     constexpr int kPer = D / 64;
-    auto score = [&](int j) {
-        float s = 0.0f;
-        const uint16_t *kr = k + (int64_t)j * a.k_ts;
-        for (int d = 0; d < D; ++d) s += bf16_to_f32(q[d]) * bf16_to_f32(kr[d]);
-        return s * a.scale;
-    };
-    float m = kNegInf;
-    bool nan = false;
-    for (int j = lane; j <= last; j += 64) {
-        const float s = score(j);
-        nan |= s != s;
-        m = fmaxf(m, s);
-    }
-    for (int x = 32; x >= 1; x /= 2) m = fmaxf(m, __shfl_xor(m, x, 64));
-    if (__any(nan)) m = __uint_as_float(0x7fc00000u);
-    if (m == kNegInf) m = 0.0f;  // every visible score is -inf
-    float l = 0.0f, acc[kPer] = {};
-    for (int j0 = 0; j0 <= last; j0 += 64) {
-        const int j = j0 + lane;
-        const float p = j <= last ? exp2_fast(score(j) - m) : 0.0f;
-        l += p;
-        for (int i = 0; i < 64 && j0 + i <= last; ++i) {
-            const float pi = __shfl(p, i, 64);
-            for (int x = 0; x < kPer; ++x)
-                acc[x] += pi * bf16_to_f32(v[(int64_t)(j0 + i) * a.v_ts + lane * kPer + x]);
+    uint32_t qw = reinterpret_cast<const uint32_t *>(q)[lane % (D / 2)];  // two channels for each lane
+    float m = kNegInf, l = 0.0f, acc[kPer] = {};
+    auto chunk = [&](int j0, auto whole_c) {
+        constexpr bool kWhole = decltype(whole_c)::value;
+        const bool mine = kWhole || j0 + lane <= last;
+        const uint4 *kr = reinterpret_cast<const uint4 *>(k + (int64_t)(mine ? j0 + lane : last) * a.k_ts);
+        uint4 kw[D / 8];
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) kw[c] = kr[c];
+        const uint16_t *at = v + (int64_t)j0 * a.v_ts + lane * kPer;
+        auto value = [&]() {
+            asm("" : "+v"(at));  // one address of the lane's, not 64 of the wave's
+            const uint32_t w = kPer == 2 ? *reinterpret_cast<const uint32_t *>(at) : *at;
+            at += a.v_ts;
+            return w;
+        };
+        uint32_t vw[kWhole ? 64 : 1];
+        if (kWhole) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) vw[i] = value();
         }
-    }
+        float s = 0.0f;
+        asm("" : "+v"(qw));  // read out anew in each step, not kept in scalar registers
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+            const uint32_t kd[4] = {kw[c].x, kw[c].y, kw[c].z, kw[c].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t qd = (uint32_t)__builtin_amdgcn_readlane((int)qw, 4 * c + e);
+                s = fmaf(__uint_as_float(qd << 16), __uint_as_float(kd[e] << 16), s);
+                s = fmaf(__uint_as_float(qd & 0xffff0000u), __uint_as_float(kd[e] & 0xffff0000u), s);
+            }
+        }
+        s = mine ? s * a.scale : kNegInf;
+        const float m1 = fmaxf(m, wave_max_f(s));
+        const float f = m1 == kNegInf ? 1.0f : exp2_fast(m - m1);
+        m = m1;
+        const float p = mine ? exp2_fast(s - (m == kNegInf ? 0.0f : m)) : 0.0f;
+        l = l * f + p;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) acc[x] *= f;
+        auto add = [&](int i, uint32_t w) {
+            const float pi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(p), i));
+            acc[0] = fmaf(pi, __uint_as_float(w << 16), acc[0]);
+            if (kPer == 2) acc[kPer - 1] = fmaf(pi, __uint_as_float(w & 0xffff0000u), acc[kPer - 1]);
+        };
+        if (kWhole) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) add(i, vw[kWhole ? i : 0]);
+        } else {
+#pragma unroll 1
+            for (int i = 0; j0 + i <= last; ++i) add(i, value());
+        }
+    };
+    int j0 = 0;
+    for (; j0 + 63 <= last; j0 += 64) chunk(j0, std::true_type{});
+    if (j0 <= last) chunk(j0, std::false_type{});
     for (int x = 32; x >= 1; x /= 2) l += __shfl_xor(l, x, 64);
     for (int x = 0; x < kPer; ++x) {
         const float r = l != 0.0f ? acc[x] / l : 0.0f;
@@ -327,7 +391,7 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
     __shared__ __attribute__((aligned(1024))) char lds[kStages * 2 * kTileBytes];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), half = lane >> 5, col = lane & 31;
     const int row_wave = wave / W, first_block = W == 1 ? 0 : wave % W;
-    if (SPLIT && blockIdx.x == 0 && (int)blockIdx.y == a.slices - 1) clear_next<256>(a.clear);
+    if (SPLIT && (int)blockIdx.x == a.tiles * a.Hq - 1 && (int)blockIdx.y == a.slices - 1) clear_next<256>(a.clear);
 
     // Workgroups go round the 8 XCDs: where the heads divide by 8, each XCD takes
     // the same ones of every tile, so that its L2 holds few heads' keys.
@@ -546,12 +610,18 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(PromptArgs a) {
         }
         __syncthreads();
     }
-    auto redo_rows = [&](uint32_t todo) {  // of the wave's rows, those with a bit
+    auto redo_rows = [&](uint32_t todo) {  // of the wave's rows, those with a bit, where hidden values may be why
+        if (!CAUSAL || todo == 0) return;
+        const uint16_t *values = a.v + (int64_t)k0 * a.v_ts + kvh * a.v_hs;
+        auto last_of = [&](int r) { return min(keys - 1, r + keys - nq); };
+        // past the keys of the wave's last tile
+        const int past = min(keys, (max(last_of(min(w0 + 31, nq - 1)), -1) / kKeys + 1) * kKeys);
+        const int hidden = last_nonfinite<D>(values, a.v_ts, max(last_of(w0), -1) + 1, past);
         for (; todo != 0; todo &= todo - 1) {
-            const int r = w0 + __builtin_ctz(todo);
+            const int r = w0 + __builtin_ctz(todo), last_key = last_of(r);
+            if (last_key >= hidden) continue;
             exact_row<D>(a, a.q + (int64_t)(q0 + r) * a.q_ts + head * a.q_hs, a.k + (int64_t)k0 * a.k_ts + kvh * a.k_hs,
-                         a.v + (int64_t)k0 * a.v_ts + kvh * a.v_hs, a.o + ((int64_t)(q0 + r) * a.Hq + head) * D,
-                         CAUSAL ? min(keys - 1, r + keys - nq) : keys - 1);
+                         values, a.o + ((int64_t)(q0 + r) * a.Hq + head) * D, last_key);
         }
     };
     if (W == 2 && first_block == 0) {

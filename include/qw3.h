@@ -356,8 +356,9 @@ qw3_status qattn_cache(const uint16_t *q, const void *codes, const float *scales
  * Row i of a sequence with nq queries and nk keys sees, with `causal`, the keys
  * j <= i + nk - nq (the last query sees the last key, so that a chunk of a
  * prompt attends to the whole prefix), else all nk keys.  Formula and empty
- * rows as for qattn_cache.  Rows that come out NaN or infinite are computed again
- * from the keys they see alone, slowly.  Workspace, by the same rules as
+ * rows as for qattn_cache.  Rows before a NaN or infinite value (up to 94 before it)
+ * are computed again from the keys they see alone: 0.1 ms for 2000 keys and row.
+ * Workspace, by the same rules as
  * qattn_cache: none with fewer than 961 keys in all or with (Tq / 64 + B) Hq above
  * the number of CUs; else parts of 64 (D + 2) floats for each of 2 x CUs workgroups
  * at most (17 MB on 256 CUs), and the counters.

@@ -185,3 +185,60 @@ def test_graphs_of_one_stream_replayed_on_others():
         torch.cuda.synchronize()
         for i, out in outs[turn % 2] + list(enumerate(eager)):
             assert np.array_equal(bits(out), want[i]), (turn, i)
+
+
+# ------------------------------------------------- values that are not numbers ---
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("shape", ["whole tiles", "paired waves", "slices"])
+def test_a_value_that_is_not_a_number_at_any_place(shape, dim):
+    """NaN or an infinity in one channel of one value, at places on both sides of tile and block ends: rows that see it
+    are not finite in that channel and right in the others, rows that do not are right."""
+    rng = np.random.default_rng(61)
+    nq, nk, heads, group = {"whole tiles": (1200, 1200, 2, 32), "paired waves": (300, 333, 1, 2),
+                            "slices": (40, 2100, 1, 2)}[shape]
+    rq, rk, rv = rows(rng, nq, heads * group, dim), rows(rng, nk, heads, dim), rows(rng, nk, heads, dim)
+    off = nk - nq
+    clean = f64(q().qattn_prompt(rq, rk, rv, starts([nq]), starts([nk])))
+    kk, vv, qq = f64(rk), f64(rv), f64(rq)
+    for at in (0, off + 1, off + 5, off + 31, off + 32, off + 33, nk - 64, nk - 2, nk - 1):
+        bad = (float("nan"), float("inf"), -float("inf"))[at % 3]
+        v = rv.clone()
+        v[at, 0, 7] = bad
+        got = f64(q().qattn_prompt(rq, rk, v, starts([nq]), starts([nk])))
+        first = max(0, at - off)  # the first row that sees it
+        for h in range(group):
+            assert not np.isfinite(got[first:, h, 7]).any(), (at, h)
+            assert np.isfinite(got[:first, h]).all() and np.isfinite(np.delete(got[first:, h], 7, axis=1)).all(), (at, h)
+            assert np.array_equal(np.delete(got[first:, h], 7, axis=1), np.delete(clean[first:, h], 7, axis=1)), (at, h)
+        assert np.array_equal(got[:, group:], clean[:, group:]), at
+        for i in sorted({0, max(first - 1, 0), max(first - 17, 0), max(first - 40, 0)}):
+            if i >= first:
+                continue
+            for h in (0, group - 1):
+                o, bound = ref.attend(qq[i, h], kk[:, 0], vv[:, 0], np.arange(i + off + 1), dim ** -0.5)
+                check(got[i, h], o, bound, "value %d row %d head %d" % (at, i, h))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_nan_that_rows_see_costs_no_second_pass(causal):
+    """One NaN in the first value, or in the middle: the call takes about the time it takes without."""
+    rng = np.random.default_rng(62)
+    rq, rk, rv = rows(rng, 2048, 32, 128), rows(rng, 2048, 4, 128), rows(rng, 2048, 4, 128)
+    cu = starts([2048])
+
+    def time_of(v):
+        best = []
+        for _ in range(8):
+            a, b = torch.cuda.Event(True), torch.cuda.Event(True)
+            a.record()
+            q().qattn_prompt(rq, rk, v, cu, causal=causal)
+            b.record()
+            b.synchronize()
+            best.append(a.elapsed_time(b))
+        return sorted(best)[3]
+
+    clean = time_of(rv)
+    for at in (0, 1024):
+        v = rv.clone()
+        v[at, :, 3] = float("nan")
+        assert time_of(v) < 4 * clean
