@@ -132,7 +132,7 @@ def new_cache(pages: int, page_size: int, heads: int, dim: int, dtype: torch.dty
 def qcache_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, codes: torch.Tensor,
                  scales: torch.Tensor) -> None:
     """Quantise k and v [T, H, D] (bf16 or float32) into the cache at slots
-    [T] (int64, page * page_size + place; negative: skip the token)."""
+    [T] (int64, page * page_size + place, each at most once; negative: skip the token)."""
     kind, dev, pages, heads, size, dim = _cache(codes, scales)
     kts, khs = _rows(k, "k", _SRC_TYPES, dev)
     vts, vhs = _rows(v, "v", (k.dtype,), dev)

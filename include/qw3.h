@@ -295,7 +295,8 @@ enum { QW3_SRC_BF16 = 0, QW3_SRC_F32 = 1 };      /* src_type */
  *   k, v  [T, H, D] bf16 or float32 (src_type), strided
  *   slots [T] int64: where each token goes; an entry outside 0 ..
  *         pages * page_size - 1 stores nothing (-1 for padding rows).  Slots
- *         named twice hold one of the rows for each head, unspecified which.
+ *         that store are named once: one that is named twice holds an unspecified
+ *         mix of its rows (codes of one under the scale of another).
  * For each row, with a = max |x_d| and L = 127 (int8) or 448 (e4m3):
  *   s = a / L (float32), c_d = x_d / s rounded to the nearest code, ties to even;
  *   a = 0 gives s = 0 and c = 0.  A row that holds an infinity or NaN gets

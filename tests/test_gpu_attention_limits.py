@@ -242,3 +242,29 @@ def test_a_nan_that_rows_see_costs_no_second_pass(causal):
         v = rv.clone()
         v[at, :, 3] = float("nan")
         assert time_of(v) < 4 * clean
+
+
+# ------------------------------------------------------------------- slots ---
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+def test_a_slot_named_twice_touches_no_other(kind):
+    """Tokens 0..99 again as 100..199 at the same slots (equal rows, so that the content is known), padding between:
+    what these slots hold is right, and all others are as they were."""
+    rng = np.random.default_rng(71)
+    codes, scales = q().new_cache(14, 16, 3, 128, {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}[kind])
+    codes.view(torch.uint8).fill_(0x5A)
+    scales.fill_(-7.0)
+    x = rows(rng, 100, 3, 128, torch.float32)
+    twice = torch.cat([x, x])
+    at = rng.permutation(14 * 16)[:100]
+    slots = np.concatenate([at, at])
+    slots[[7, 107, 50, 150]] = -1
+    q().qcache_write(twice, -twice, torch.tensor(slots, device="cuda"), codes, scales)
+    got_c, got_s = codes.view(torch.uint8).cpu().numpy(), scales.cpu().numpy()
+    want_c, want_s = np.full_like(got_c, 0x5A), np.full_like(got_s, -7.0)
+    for which, sign in ((0, 1), (1, -1)):
+        c, s = ref.quantise(sign * x.cpu().numpy(), kind)
+        for t, slot in enumerate(slots[:100]):
+            if slot >= 0:
+                want_c[slot // 16, which, :, slot % 16], want_s[slot // 16, which, :, slot % 16] = c[t], s[t]
+    assert np.array_equal(got_s, want_s)
+    assert np.array_equal(np.where(got_c == 0x80, 0, got_c), np.where(want_c == 0x80, 0, want_c))
