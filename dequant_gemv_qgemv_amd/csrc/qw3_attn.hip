@@ -1786,7 +1786,8 @@ qw3_status launch_cache_rows(const CacheArgs &a, hipStream_t stream) {
     return launch_cache<D, E4M3, 128>(a, stream);
 }
 
-bool strides_ok(int64_t ts, int64_t hs) { return ts >= 0 && hs >= 0 && ts < (1 << 23) && hs < (int64_t(1) << 40); }
+// Row strides: 64 rows' offsets stay in a buffer descriptor's 31 bits.
+bool strides_ok(int64_t ts, int64_t hs) { return qw3_shared::strides_ok(ts, hs, 1 << 23); }
 
 qw3_status check_heads(int64_t Hq, int64_t H) {
     return H < 1 || Hq < 1 || Hq % H != 0 || Hq > QW3_MAX_HEADS ? QW3_ERR_SHAPE : QW3_OK;
@@ -1857,6 +1858,7 @@ qw3_status qattn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v,
         return QW3_ERR_SHAPE;
     if (!scale_ok(sm_scale) || !strides_ok(q_ts, q_hs) || !strides_ok(k_ts, k_hs) || !strides_ok(v_ts, v_hs))
         return QW3_ERR_SHAPE;
+    if ((Tq / 128 + B) * Hq >= kMaxGroups) return QW3_ERR_SHAPE;
     if (B == 0 || Tq == 0) return QW3_OK;
     if (!q || !cu_q || !cu_k || !out || (Tk > 0 && (!k || !v))) return QW3_ERR_NULL;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_q, 4) ||
@@ -1875,7 +1877,6 @@ qw3_status qattn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v,
     // (4000 tokens, 8 heads) 72 and 55; at 1040 (3..2500 tokens, 16 heads) 63 and 75.
     const bool few = (Tq / 128 + B) * Hq <= 2 * (int64_t)cus;
     const int64_t tiles = Tq / (few ? 64 : 128) + B;
-    if (tiles * Hq > 0x7fffffff) return QW3_ERR_SHAPE;
     a.tiles = (int)tiles;
     const hipStream_t stream = (hipStream_t)hip_stream;
     // in slices while the tiles leave half of the CUs' places empty

@@ -242,14 +242,18 @@ qw3_status qcache_write(const void *k, const void *v, int32_t src_type, const in
     const qw3_status st = check_cache(code_type, H, D, pages, page_size, &shift);
     if (st != QW3_OK) return st;
     if (src_type != QW3_SRC_BF16 && src_type != QW3_SRC_F32) return QW3_ERR_SHAPE;
-    if (T < 0 || T > (int64_t(1) << 28) / H) return QW3_ERR_SHAPE;
+    if (T < 0 || T > QW3_MAX_TOKENS) return QW3_ERR_SHAPE;
+    const int64_t groups = ceil_div(T, 256 / (D / 16)) * H;
+    if (groups >= kMaxGroups) return QW3_ERR_SHAPE;
+    const int64_t widest = int64_t(1) << 32;  // a row's address stays in 64 bits
+    if (!strides_ok(k_ts, k_hs, widest) || !strides_ok(v_ts, v_hs, widest)) return QW3_ERR_SHAPE;
     if (T == 0 || pages == 0) return QW3_OK;
     if (!k || !v || !slots || !codes || !scales) return QW3_ERR_NULL;
     const int per = src_type == QW3_SRC_F32 ? 4 : 8;  // elements of 16 bytes
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(slots, 8) ||
         k_ts % per || k_hs % per || v_ts % per || v_hs % per)
         return QW3_ERR_ALIGN;
-    const dim3 grid((unsigned)(ceil_div(T, 256 / (D / 16)) * H));
+    const dim3 grid((unsigned)groups);
     auto run = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(256), 0, (hipStream_t)hip_stream, k, v, slots, (uint8_t *)codes, scales,
                            (int)T, (int)H, shift, pages * page_size, k_ts, k_hs, v_ts, v_hs);
@@ -273,7 +277,8 @@ qw3_status qcache_read(const void *codes, const float *scales, int32_t code_type
     int shift = 0;
     const qw3_status st = check_cache(code_type, H, D, pages, page_size, &shift);
     if (st != QW3_OK) return st;
-    if (B < 0 || B > QW3_MAX_SEQS || max_pages < 0 || total < 0 || total >= (int64_t(1) << 31)) return QW3_ERR_SHAPE;
+    if (B < 0 || B > QW3_MAX_SEQS || max_pages < 0 || total < 0 || total > QW3_MAX_TOKENS)
+        return QW3_ERR_SHAPE;
     if (B == 0 || total == 0) return QW3_OK;
     if (!cu || !k_out || !v_out || (max_pages > 0 && !block_table) || (pages > 0 && (!codes || !scales)))
         return QW3_ERR_NULL;

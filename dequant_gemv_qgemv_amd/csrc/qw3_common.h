@@ -571,6 +571,14 @@ inline qw3_status check_cache(int32_t code_type, int64_t H, int64_t D, int64_t p
     return QW3_OK;
 }
 
+// Strides of a [rows, heads, channels] operand, in elements: row stride below `rows`.
+inline bool strides_ok(int64_t ts, int64_t hs, int64_t rows) {
+    return ts >= 0 && hs >= 0 && ts < rows && hs < (int64_t(1) << 40);
+}
+
+// Workgroups of 256 threads along one dimension of a grid: its threads are counted in 32 bits.
+constexpr int64_t kMaxGroups = int64_t(1) << 24;
+
 inline std::mutex g_dev_mutex;  // guards the per-device tables
 inline int g_cu_count[64];
 

@@ -258,8 +258,9 @@ qw3_status qgemm_w3g128_smallM_noalloc(const uint16_t *x, const int32_t *packed,
  * Shared by the four calls:
  *   - Strides (_ts: from token to token, _hs: from head to head) are in
  *     elements; channels are contiguous.  So q, k and v may be views of one
- *     fused projection output.  Strides are >= 0, and token strides of bf16
- *     operands below 2^23.
+ *     fused projection output.  Strides are >= 0; token strides are below 2^23 in
+ *     qattn_cache and qattn_prompt, 2^32 in qcache_write, head strides below 2^40;
+ *     else QW3_ERR_SHAPE.
  *   - Alignment: 16 bytes for every array, except block tables, lengths and
  *     starts (4) and slots and trees (8); strides are multiples of 16 bytes.
  *     Otherwise QW3_ERR_ALIGN.
@@ -273,6 +274,7 @@ qw3_status qgemm_w3g128_smallM_noalloc(const uint16_t *x, const int32_t *packed,
  *   - 1 <= B <= QW3_MAX_SEQS, at most QW3_MAX_TOKENS rows, QW3_MAX_HEADS heads,
  *     Hq a multiple of H, sm_scale > 0 and finite, else QW3_ERR_SHAPE.  B or
  *     the number of rows may be 0: no work.
+ *   - Outputs do not overlap inputs.
  *   - Rows of a packed output that belong to no sequence are not written.
  *   - Deterministic: parts of a sequence that several workgroups worked on are
  *     joined in a fixed order.  Safe to capture, like the calls above (qattn_cache
@@ -302,6 +304,8 @@ enum { QW3_SRC_BF16 = 0, QW3_SRC_F32 = 1 };      /* src_type */
  *   a = 0 gives s = 0 and c = 0.  A row that holds an infinity or NaN gets
  *   s = NaN and c = 0, so that it stays visible as NaN to whoever attends to it.
  * Float32 sources are the outputs of the products above as they are.
+ * ceil(T D / 4096) H < 2^24, else QW3_ERR_SHAPE (T H below 2^29 or, with 64
+ * channels, 2^30).
  */
 qw3_status qcache_write(const void *k, const void *v, int32_t src_type, const int64_t *slots, void *codes,
                         float *scales, int32_t code_type, int64_t T, int64_t H, int64_t D, int64_t pages,
@@ -362,7 +366,8 @@ qw3_status qattn_cache(const uint16_t *q, const void *codes, const float *scales
  * Workspace, by the same rules as
  * qattn_cache: none with fewer than 961 keys in all or with (Tq / 64 + B) Hq above
  * the number of CUs; else parts of 64 (D + 2) floats for each of 2 x CUs workgroups
- * at most (17 MB on 256 CUs), and the counters.
+ * at most (17 MB on 256 CUs), and the counters.  (floor(Tq / 128) + B) Hq < 2^24,
+ * else QW3_ERR_SHAPE.
  */
 qw3_status qattn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *cu_q,
                         const int32_t *cu_k, uint16_t *out, int64_t B, int64_t Tq, int64_t Tk, int64_t Hq,
