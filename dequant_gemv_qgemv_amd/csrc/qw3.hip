@@ -6,6 +6,7 @@
 #include <vector>
 
 #include "qw3_common.h"
+#include "qw3_host.h"
 
 using namespace qw3_shared;
 
@@ -1436,6 +1437,8 @@ qw3_status qw3_shared::workspace(hipStream_t stream, size_t bytes, void **out) {
     if (stream_capturing(stream)) return QW3_ERR_CAPTURE;
     size_t grow = (bytes + (size_t(1) << 20) - 1) & ~((size_t(1) << 20) - 1);
     if (w && grow < 2 * w->bytes) grow = 2 * w->bytes;
+    if (w ? !qw3_host::room_for_one(g_ws_retired) : !qw3_host::room_for_one(g_ws))
+        return hip_fail(hipErrorOutOfMemory);
     void *p = nullptr;
     err = hipMalloc(&p, grow);
     if (err != hipSuccess) return hip_fail(err);

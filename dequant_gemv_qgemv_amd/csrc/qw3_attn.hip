@@ -16,6 +16,7 @@
 // rescale factor of a row is then one value per lane.  V^T comes from row-major
 // tiles in LDS through the transposing LDS reads.
 #include "qw3_common.h"
+#include "qw3_host.h"
 #include "qw3_units.h"
 
 #include <vector>
@@ -1834,11 +1835,15 @@ qw3_status qw3_shared::counters(hipStream_t stream, int n, int **use, int **clea
         if (e.dev == dev && e.stream == stream) mine = &e;
     if (mine == nullptr) {
         if (capturing) return QW3_ERR_CAPTURE;
+        if (!qw3_host::room_for_one(g_counters)) return hip_fail(hipErrorOutOfMemory);
         void *p = nullptr;
         err = hipMalloc(&p, 4 * kCounts * sizeof(int));
         if (err != hipSuccess) return hip_fail(err);
         const qw3_status st = clear_counts(static_cast<int *>(p), 4, stream);
-        if (st != QW3_OK) return st;
+        if (st != QW3_OK) {
+            (void)hipFree(p);
+            return st;
+        }
         g_counters.push_back(Counters{dev, stream, static_cast<int *>(p), Banks{}});
         mine = &g_counters.back();
     }
