@@ -69,13 +69,14 @@ def quantise(rows, kind):
     return codes, scales
 
 
-def attend(q, k, v, sees, scale):
+def attend(q, k, v, sees, scale, weight_error=2.0 ** -8):
     """One query row over the keys it sees: (output [D], bound [D]).
 
     q [D], k and v [n, D] in float64, `sees` the indexes of the visible keys.
     The bound is on what a kernel may be off that multiplies exact operands, holds scores and sums in fp32 and rounds
     each weight and the output to bf16 (8 significant bits, so by at most 2^-8 of their size each): with w_j the normalised weights and A = sum w_j |v_j|,
-      2^-8 (A + |o|)          the weights' and the output's rounding,
+      2^-8 (A + |o|)          the weights' and the output's rounding (weight_error A + 2^-8 |o| where
+                              weights keep more bits: 2^-16 for two bf16 each),
       A (2 d + (n + 64) 2^-23) scores off by d, and the order of n additions in fp32 twice (numerator, denominator),
     d = 2 D 2^-24 scale max_j sum |q k_j|."""
     dim = q.shape[0]
@@ -89,7 +90,8 @@ def attend(q, k, v, sees, scale):
     w /= w.sum()
     o, a = w @ v, w @ np.abs(v)
     d = 2 * dim * 2.0 ** -24 * scale * (np.abs(k) @ np.abs(q)).max()
-    return o, 1.02 * 2.0 ** -8 * (a + np.abs(o)) + a * (2 * d + (len(sees) + 64) * 2.0 ** -23) + 1e-37
+    rounding = weight_error * a + 2.0 ** -8 * np.abs(o)
+    return o, 1.02 * rounding + a * (2 * d + (len(sees) + 64) * 2.0 ** -23) + 1e-37
 
 
 def prompt_sees(i, nq, nk, causal):
@@ -105,3 +107,37 @@ def cache_sees(i, n, length, word=None):
         if 0 <= ctx + j < length and (j <= i if word is None else j < 64 and (int(word) >> j) & 1):
             seen.append(ctx + j)
     return np.array(seen, int)
+
+
+# Counting keys.  With q = 0 every weight is one, and with values that are one in
+# one channel and zero elsewhere an output is the share of the row's keys that have
+# their one there.  32 neighbouring keys share a channel, so that a lost run of keys
+# is not lost from all channels alike, and a channel has at most 96 keys, so that one
+# lost or counted twice (1 / 96 of it) is more than bf16 rounds away.
+
+def counting_parts(n, dim):
+    """How many sets of values it takes for channels of at most 96 of n keys."""
+    return max(1, -(-n // (96 * dim)))
+
+
+def counting_values(n, dim, part, parts):
+    """Values [n, dim]: key j has its one in channel (j // 32) % dim, in set (j // (32 dim)) % parts only."""
+    v = np.zeros((n, dim))
+    j = np.arange(n)
+    j = j[(j // (32 * dim)) % parts == part]
+    v[j, (j // 32) % dim] = 1.0
+    return v
+
+
+def miscounted(got, seen, values):
+    """Outputs [rows, dim] that are not the shares of the keys `seen` [rows, n]: off by more than the rounding to bf16
+    (2^-8) and of one reciprocal and product in fp32."""
+    seen = np.asarray(seen, np.float64)
+    total = seen.sum(axis=1, keepdims=True)
+    want = np.where(total > 0, seen @ values / np.maximum(total, 1), 0.0)
+    return ~(np.abs(got - want) <= want * (2.0 ** -8 + 2.0 ** -20))
+
+
+# Two weights whose rounding to one bf16 shows: keys of score 0 and of score ln p,
+# p = 0.75 + 2^-9 half way between two bf16, whose values cancel.
+HALF_WAY = float(np.log(0.75 + 2.0 ** -9))
