@@ -63,6 +63,8 @@ def _rows(t, name, dtypes, index):
     token, head, channel = t.stride()
     if channel != 1 and t.shape[2] > 1:
         raise ValueError("%s must be contiguous in its channels" % name)
+    if (token | head) & 7:  # a dimension of one may have any stride; the others are the library's to check
+        token, head = token if t.shape[0] > 1 else 0, head if t.shape[1] > 1 else 0
     return token, head
 
 

@@ -268,3 +268,32 @@ def test_a_slot_named_twice_touches_no_other(kind):
                 want_c[slot // 16, which, :, slot % 16], want_s[slot // 16, which, :, slot % 16] = c[t], s[t]
     assert np.array_equal(got_s, want_s)
     assert np.array_equal(np.where(got_c == 0x80, 0, got_c), np.where(want_c == 0x80, 0, want_c))
+
+
+# ----------------------------------------------------------------- strides ---
+def test_dimensions_of_one_may_have_any_stride():
+    """One token, or one head, with the strides that a transposed or expanded vector leaves there."""
+    rng = np.random.default_rng(91)
+
+    def odd(t, dim):  # the same values, a stride of 1 in a dimension of one
+        strides = list(t.stride())
+        strides[dim] = 1
+        return t.as_strided(t.shape, strides)
+
+    codes, scales = random_cache(rng, "int8", 4, 16, 1, 64)
+    table = tables(rng, [40], 16, 4)
+    one, k, v = rows(rng, 1, 4, 64), rows(rng, 9, 1, 64), rows(rng, 9, 1, 64)
+    want = bits(q().qattn_cache(one, codes, scales, table, ints([40])))
+    assert np.array_equal(want, bits(q().qattn_cache(odd(one, 0), codes, scales, table, ints([40]))))
+    cu, cuk = starts([1]), starts([9])
+    want = bits(q().qattn_prompt(one, k, v, cu, cuk))
+    assert np.array_equal(want, bits(q().qattn_prompt(odd(one, 0), odd(k, 1), odd(v, 1), cu, cuk)))
+    slots = torch.arange(9, device="cuda")
+    for x in (k, k.float()):
+        caches = [q().new_cache(1, 16, 1, 64) for _ in range(2)]
+        q().qcache_write(x, x, slots, *caches[0])
+        q().qcache_write(odd(x, 1), odd(x, 1), slots, *caches[1])
+        assert torch.equal(caches[0][0], caches[1][0]) and torch.equal(caches[0][1], caches[1][1])
+    with pytest.raises(q().Qw3Error):
+        wide = torch.zeros(2, 4 * 64 + 1, dtype=torch.bfloat16, device="cuda")[:, :256].view(2, 4, 64)
+        q().qattn_prompt(wide, k, v, starts([2]), cuk)
