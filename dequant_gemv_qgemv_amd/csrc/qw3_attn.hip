@@ -365,8 +365,8 @@ __device__ __forceinline__ int value_place(int r) {
 // barrier, so one computes while the other waits.  Bound by the matrix and vector
 // instructions together: for 64 rows of a SIMD and a tile 1.2 us of products, 0.7
 // of exponentials and the rest; the prompt of 8192 tokens (64 heads of 128
-// channels) runs in 1.03 ms, 1070 TFLOP/s, where a large bf16 product reaches
-// 1305.  With 64 channels half of the products stand beside as many exponentials:
+// channels) runs in 1.00 to 1.07 ms by the card, 1030 to 1100 TFLOP/s, where a large
+// bf16 product reaches 1305.  With 64 channels half of the products stand beside as many exponentials:
 // 890 TFLOP/s.  Measured and left: 256 rows and 8 waves that share a tile (-1 %
 // and +1 % on long prompts, +13 % on packed ones), rings of 3 and 4 tiles (one
 // workgroup per CU: +20 to +70 %).
@@ -852,8 +852,8 @@ __device__ __forceinline__ Work find_work(const CacheArgs &a) {
 // its own).  Slots are written and read by atomic 8-byte accesses of agent
 // scope, which go past the per-XCD L2s, so no cache has to be flushed; every
 // thread's stores are complete (vmcnt 0) before its workgroup counts itself.
-// The count belongs to the first workgroup of the item, and the joining
-// workgroup sets it back to zero for the next call.
+// The count belongs to the first workgroup of the item; the joining workgroup sets
+// it back to zero, and the call clears the bank that the next one counts in.
 template <int R, int D>
 __device__ __forceinline__ float *partial(const CacheArgs &a, int group, int which) {
     return a.part + (int64_t)(group * 2 + which) * (R * (D + 2));
@@ -1001,7 +1001,7 @@ __device__ __forceinline__ uint64_t visible(int base, int seen, uint64_t tree, i
 // item.  Bound by memory where there is much of it (64 sequences of 2048 tokens
 // 56 us, 4.9 TB/s, what a large copy reaches; one of 131071 tokens 61 us, of
 // which 8 join 62 parts a head), and by its own chain of dependent reads where
-// there is little: one token over 1000 keys 8.4 us in a graph, of which 1.1 find
+// there is little: one token over 1000 keys 8.5 us in a graph, of which 1.1 find
 // the work, 0.8 a page number, 1.1 the codes, 1.6 the step with its instructions,
 // 1.2 join the waves, 2.6 the parts.  Three workgroups a CU (168 registers,
 // spills) measured 73 us where two measure 56; codes by direct loads into LDS,

@@ -341,7 +341,8 @@ qw3_status qcache_read(const void *codes, const float *scales, int32_t code_type
  * over what the row sees; a row that sees nothing gets zeros.  fp32 scores and
  * sums; the weights p_j s_j enter the matrix unit as two bf16 each where a
  * sequence has up to 64 query rows per kv head on average or Tq Hq max_pages
- * page_size is at most 2^25 (D = 64: 2^24), as one otherwise.
+ * page_size is at most 2^25 (D = 64: 2^24), as one otherwise.  So the width of the
+ * table, used or not, is part of what the bits of such calls depend on.
  * Workspace, by the rules of qgemm_w3g128_smallM (the same buffer): 2 slots of R
  * (D + 2) floats for each of 2 x CUs workgroups, R = 16, 32 or 128, or 1 x CUs, R =
  * 256 (68 MB at most on 256 CUs), and 16 KB of counters for each stream, which a call leaves zero.
@@ -361,13 +362,12 @@ qw3_status qattn_cache(const uint16_t *q, const void *codes, const float *scales
  * Row i of a sequence with nq queries and nk keys sees, with `causal`, the keys
  * j <= i + nk - nq (the last query sees the last key, so that a chunk of a
  * prompt attends to the whole prefix), else all nk keys.  Formula and empty
- * rows as for qattn_cache.  Rows before a NaN or infinite value (up to 94 before it)
- * are computed again from the keys they see alone: 0.1 ms for 2000 keys and row.
- * Workspace, by the same rules as
- * qattn_cache: none with fewer than 961 keys in all or with (Tq / 64 + B) Hq above
- * the number of CUs; else parts of 64 (D + 2) floats for each of 2 x CUs workgroups
- * at most (17 MB on 256 CUs), and the counters.  (floor(Tq / 128) + B) Hq < 2^24,
- * else QW3_ERR_SHAPE.
+ * rows as for qattn_cache.  Rows up to 94 places before a NaN or infinite value are
+ * computed again from the keys they see alone (0.1 ms for a row of 2000 keys).
+ * Workspace, by the same rules as qattn_cache: none with fewer than 961 keys in all
+ * or with (Tq / 64 + B) Hq above the number of CUs; else parts of 64 (D + 2) floats
+ * for each of 2 x CUs workgroups at most (17 MB on 256 CUs), and the counters.
+ * (floor(Tq / 128) + B) Hq < 2^24, else QW3_ERR_SHAPE.
  */
 qw3_status qattn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *cu_q,
                         const int32_t *cu_k, uint16_t *out, int64_t B, int64_t Tq, int64_t Tk, int64_t Hq,
