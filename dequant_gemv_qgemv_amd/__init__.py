@@ -19,8 +19,9 @@ import os
 
 import torch
 
-from . import _attention
+from . import _attention, _rope
 from ._attention import new_cache, qattn_cache, qattn_prompt, qcache_read, qcache_write
+from ._rope import qrope, qrope_write
 
 __all__ = [
     "qpack_uint3",
@@ -35,6 +36,8 @@ __all__ = [
     "qcache_read",
     "qattn_cache",
     "qattn_prompt",
+    "qrope",
+    "qrope_write",
     "qstatus_str",
     "check_quantization_config",
     "library_path",
@@ -64,7 +67,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libqw3.so")
 _EXPORTS = ("qpack_uint3", "qrepack_w4c_uint3", "qdequant_bf16", "qgemv_w3g128", "qgemv_w3g128_multi",
             "qgemm_w3g128_smallM", "qgemm_w3g128_smallM_noalloc", "qgemm_w3g128_batch_invariant",
-            "qcache_write", "qcache_read", "qattn_cache", "qattn_prompt", "qstatus_str",
+            "qcache_write", "qcache_read", "qattn_cache", "qattn_prompt",
+            "qrope", "qrope_write", "qstatus_str",
             "qw3_last_hip_error",
             "qw3_abi_version")
 
@@ -131,6 +135,7 @@ def _raise(status: int, where: str):
 
 
 _attention._bind(_lib, _raise)
+_rope._bind(_lib)
 
 
 def _stream():

@@ -29,6 +29,7 @@ UNITS = [
     ("qw3_gemv.hip", ["-mllvm", "--amdgpu-sched-strategy=max-ilp"]),
     ("qw3.hip", []),
     ("qw3_cache.hip", []),
+    ("qw3_rope.hip", []),
     ("qw3_attn.hip", []),
 ]
 

@@ -374,6 +374,58 @@ qw3_status qattn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v,
                         int64_t H, int64_t D, int64_t q_ts, int64_t q_hs, int64_t k_ts, int64_t k_hs, int64_t v_ts,
                         int64_t v_hs, int32_t causal, float sm_scale, void *hip_stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions.  What stands between the q/k/v products and the cache and
+ * attention calls; strides, alignment and slots as there.
+ *
+ * A token has a position on each of A axes (one for text; time, height and width
+ * for images and video): positions [A, T] int32, any values.  The first R of a
+ * row's D channels are R / 2 pairs; pair i is turned by
+ *   t_i = positions[axis[i]][token] * rates[i]   radians
+ *   (x, y) -> (x cos t - y sin t, y cos t + x sin t),
+ * with x and y the channels i and i + R / 2 (QW3_ROPE_HALVES) or 2 i and 2 i + 1
+ * (QW3_ROPE_PAIRS); channels R .. D - 1 stay as they are.
+ *   rates [R / 2] float64, axis [R / 2] int32 or NULL (every pair on axis 0; an
+ *   entry outside 0 .. A - 1 counts as the nearest of those): device arrays.
+ * t is formed in 64 bits (its error is 2^-51 |t|), sine, cosine and the products
+ * in fp32; outputs are rounded once.
+ *   - R a multiple of 16, 16 <= R <= D, D = 64 or 128, 1 <= A <= QW3_MAX_AXES,
+ *     T < 2^24, else QW3_ERR_SHAPE.
+ *   - Alignment: 8 bytes for rates, 4 for positions and axis.
+ * Both calls use no device memory beyond their arguments and may be captured.
+ * ------------------------------------------------------------------------ */
+enum { QW3_ROPE_HALVES = 0, QW3_ROPE_PAIRS = 1 }; /* style */
+#define QW3_MAX_AXES 8
+
+/*
+ * qrope -- rotate rows.
+ *   x   [T, H, D] bf16 or float32 (src_type), strided
+ *   out [T, H, D] bf16, contiguous, written
+ */
+qw3_status qrope(const void *x, int32_t src_type, const int32_t *positions, const double *rates, const int32_t *axis,
+                 int32_t style, uint16_t *out, int64_t T, int64_t H, int64_t D, int64_t R, int64_t A, int64_t x_ts,
+                 int64_t x_hs, void *hip_stream);
+
+/*
+ * qrope_write -- rotate q and k of a layer and store k and v in the cache, in
+ * one pass over them: qrope of q, and qcache_write of the rotated k (in fp32, not
+ * rounded to bf16 first) and of v.
+ *   q [T, Hq, D], k, v [T, H, D] bf16 or float32 (src_type, of all three), strided
+ *   slots [T] int64: as in qcache_write, each named once; a token whose slot stores
+ *         nothing still has its rows in the outputs
+ *   q_out [T, Hq, D] bf16, contiguous, written
+ *   k_out, v_out [T, H, D] bf16, contiguous: the rotated k and v, dense, for
+ *         qattn_prompt; written where not NULL
+ *   codes, scales: the cache
+ * Hq a multiple of H.
+ */
+qw3_status qrope_write(const void *q, const void *k, const void *v, int32_t src_type, const int32_t *positions,
+                       const double *rates, const int32_t *axis, int32_t style, const int64_t *slots, uint16_t *q_out,
+                       uint16_t *k_out, uint16_t *v_out, void *codes, float *scales, int32_t code_type, int64_t T,
+                       int64_t Hq, int64_t H, int64_t D, int64_t R, int64_t A, int64_t pages, int64_t page_size,
+                       int64_t q_ts, int64_t q_hs, int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs,
+                       void *hip_stream);
+
 /* Text for a status code (static storage, never NULL). */
 const char *qstatus_str(qw3_status status);
 
