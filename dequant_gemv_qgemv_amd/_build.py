@@ -30,6 +30,7 @@ UNITS = [
     ("qw3.hip", []),
     ("qw3_cache.hip", []),
     ("qw3_rope.hip", []),
+    ("qw3_pages.hip", []),
     ("qw3_attn.hip", []),
 ]
 

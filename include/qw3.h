@@ -426,6 +426,100 @@ qw3_status qrope_write(const void *q, const void *k, const void *v, int32_t src_
                        int64_t q_ts, int64_t q_hs, int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs,
                        void *hip_stream);
 
+/* ---------------------------------------------------------------------------
+ * The cache's pages.  Who holds a page is counted on the device:
+ *   refs [pages] int32: how many entries of the block table name a page; 0: free
+ * so that room for new tokens, beams that follow others and sequences that end
+ * need no reading back, and can be captured.  An entry of a block table outside
+ * 0 .. pages - 1 names no page (-1 is what these calls write).  A page with a
+ * count of more than one is shared: nothing may be written into it, and
+ * qcache_reserve sees to that.
+ *   - max_pages * page_size <= 2^30, B * max_pages < 2^32, else QW3_ERR_SHAPE.
+ *   - Lengths are clipped to 0 .. max_pages * page_size; starts (cu) as above.
+ *   - Alignment: 16 bytes for refs, codes and scales, 8 for slots and copies, 4
+ *     for the other arrays.
+ *   - Outputs do not overlap inputs or each other.
+ * Whole caches: codes and scales may have layers in front, [layers, pages, 2, H,
+ * page_size, D] and [layers, pages, 2, H, page_size]: the page of a number is the
+ * same in every layer.  layers <= QW3_MAX_LAYERS.
+ * ------------------------------------------------------------------------ */
+#define QW3_MAX_LAYERS 1024
+
+/*
+ * qcache_reserve -- room for new tokens behind each sequence's last, and their slots.
+ *   refs        [pages] int32, updated
+ *   block_table [B, max_pages] int32, updated
+ *   lens        [B] int32: tokens that each sequence has
+ *   cu          [B + 1] int32: the new tokens of each sequence; NULL: one each (total == B)
+ *   slots       [total] int64, written: where qcache_write and qrope_write put each
+ *               new token; -1 for tokens of sequences that got no room, and for rows of no sequence
+ *   lens_out    [B] int32, written: lens with the new tokens, or lens where there was no room
+ *   copies      [B, 2] int32, written: (page, its copy) for qcache_copy, or (-1, -1)
+ * The new tokens of a sequence reach the entries lens / page_size up to the one of
+ * its last token.  An entry there that names no page, or a shared one, needs a new
+ * page: in order of sequences and entries, the k-th need gets the k-th free page,
+ * lowest number first.  A shared page that is given up counts one holder less; if it
+ * holds tokens of the sequence (lens is not a multiple of page_size, first entry), the
+ * pair goes into copies, and qcache_copy has to run, for every layer, before the new
+ * tokens are written and before the next qcache_reserve.
+ * No room: a sequence that would pass max_pages * page_size tokens needs nothing and
+ * gets nothing.  Where free pages run out, the first sequence whose needs are not all
+ * met and every later one that needs a page get nothing and stay as they are; later ones that
+ * need none are served.
+ */
+qw3_status qcache_reserve(int32_t *refs, int32_t *block_table, const int32_t *lens, const int32_t *cu, int64_t *slots,
+                          int32_t *lens_out, int32_t *copies, int64_t B, int64_t max_pages, int64_t total,
+                          int64_t pages, int64_t page_size, void *hip_stream);
+
+/*
+ * qcache_fork -- rows of a block table that follow others: beams that follow their
+ * best parents, samples that start from one prompt, sequences that end.
+ *   refs        [pages] int32, updated
+ *   block_table [B, max_pages], lens [B], parents [B_out] int32
+ *   table_out   [B_out, max_pages], lens_out [B_out] int32, written
+ * Row b of the result has the length of row parents[b] and shares its pages that
+ * hold tokens, the first ceil(length / page_size) entries; the others are -1.  A
+ * parent outside 0 .. B - 1 gives an empty sequence.  refs then counts the new
+ * table in place of the old: a row that nobody follows frees its pages.
+ */
+qw3_status qcache_fork(int32_t *refs, const int32_t *block_table, const int32_t *lens, const int32_t *parents,
+                       int32_t *table_out, int32_t *lens_out, int64_t B, int64_t B_out, int64_t max_pages, int64_t pages,
+                       int64_t page_size, void *hip_stream);
+
+/*
+ * qcache_copy -- copy whole pages, in every layer.
+ *   codes, scales: the cache, updated
+ *   copies [n, 2] int32: (from, to); a pair with an entry outside 0 .. pages - 1, or of
+ *          one page with itself, copies nothing
+ * A page that is written by one pair is written by no other, and read by none: else
+ * what it and its copies then hold is a mix.
+ * n layers ceil(2 H page_size D / 16384) < 2^24, else QW3_ERR_SHAPE.
+ */
+qw3_status qcache_copy(void *codes, float *scales, const int32_t *copies, int64_t n, int64_t layers, int64_t H, int64_t D,
+                       int64_t pages, int64_t page_size, void *hip_stream);
+
+/*
+ * qcache_compact -- drop some of each sequence's last tokens, in every layer: drafts
+ * that were not accepted, tokens of a context that are no longer attended to.
+ *   codes, scales: the cache, updated
+ *   block_table [B, max_pages], lens [B] int32
+ *   cu_q     [B + 1] int32: how many last tokens of each sequence `keep` speaks of, as
+ *            the new tokens of qattn_cache; NULL: one each (Tq == B)
+ *   keep     [Tq] uint8: not 0 for a token that stays
+ *   lens_out [B] int32, written: lens without the dropped tokens
+ * Token i of the n stands at lens - n + i; the kept ones move, in order, to lens - n
+ * and behind.  Tokens at negative places are not there and are dropped; a kept one
+ * whose page is not there is zeros where it goes.  Pages are neither taken nor given
+ * back: those behind the new length are used again by qcache_reserve and given up by
+ * qcache_fork.  Pages that are written must not be shared.
+ * Workspace, by the rules of qgemm_w3g128_smallM: none where Tq <= 512 B; else 16 Tq
+ * bytes and the rows on the way, 64 MiB or 16 tokens of one layer if that is more.
+ * layers B H < 2^23, else QW3_ERR_SHAPE.
+ */
+qw3_status qcache_compact(void *codes, float *scales, const int32_t *block_table, const int32_t *lens, const int32_t *cu_q,
+                          const uint8_t *keep, int32_t *lens_out, int64_t B, int64_t max_pages, int64_t Tq,
+                          int64_t layers, int64_t H, int64_t D, int64_t pages, int64_t page_size, void *hip_stream);
+
 /* Text for a status code (static storage, never NULL). */
 const char *qstatus_str(qw3_status status);
 
