@@ -19,8 +19,9 @@ import os
 
 import torch
 
-from . import _attention, _pages, _rope
+from . import _attention, _blocks, _pages, _rope
 from ._attention import new_cache, qattn_cache, qattn_prompt, qcache_read, qcache_write
+from ._blocks import new_bounds, qattn_blocks, qblock_select, qcache_bounds
 from ._pages import qcache_compact, qcache_copy, qcache_fork, qcache_reserve
 from ._rope import qrope, qrope_write
 
@@ -43,6 +44,10 @@ __all__ = [
     "qcache_fork",
     "qcache_copy",
     "qcache_compact",
+    "new_bounds",
+    "qcache_bounds",
+    "qblock_select",
+    "qattn_blocks",
     "qstatus_str",
     "check_quantization_config",
     "library_path",
@@ -73,7 +78,8 @@ _LIB_PATH = os.path.join(_HERE, "libqw3.so")
 _EXPORTS = ("qpack_uint3", "qrepack_w4c_uint3", "qdequant_bf16", "qgemv_w3g128", "qgemv_w3g128_multi",
             "qgemm_w3g128_smallM", "qgemm_w3g128_smallM_noalloc", "qgemm_w3g128_batch_invariant",
             "qcache_write", "qcache_read", "qattn_cache", "qattn_prompt",
-            "qrope", "qrope_write", "qcache_reserve", "qcache_fork", "qcache_copy", "qcache_compact", "qstatus_str",
+            "qrope", "qrope_write", "qcache_reserve", "qcache_fork", "qcache_copy", "qcache_compact",
+            "qcache_bounds", "qblock_select", "qattn_blocks", "qstatus_str",
             "qw3_last_hip_error",
             "qw3_abi_version")
 
@@ -140,6 +146,7 @@ def _raise(status: int, where: str):
 
 
 _attention._bind(_lib, _raise)
+_blocks._bind(_lib)
 _pages._bind(_lib)
 _rope._bind(_lib)
 

@@ -31,6 +31,7 @@ UNITS = [
     ("qw3_cache.hip", []),
     ("qw3_rope.hip", []),
     ("qw3_pages.hip", []),
+    ("qw3_blocks.hip", []),
     ("qw3_attn.hip", []),
 ]
 

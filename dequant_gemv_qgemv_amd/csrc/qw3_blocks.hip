@@ -1,0 +1,910 @@
+// Attention over some of the cache's pages: the bounds of each page's keys
+// (qcache_bounds), the pages that a cheap score by them selects for each query and
+// kv head (qblock_select), and attention over those (qattn_blocks).  C ABI in
+// include/qw3.h.
+//
+// Bounds.  Per page and kv head, channel d of the keys' values x = c s (fp32) lies
+// between mn_d and mx_d; both are kept as int8 under one scale S = max |.| / 127.
+// Score.  With u_d = sum over the head's queries of max(q_d, 0) and n_d of min(q_d,
+// 0), sum_d u_d mx_d + n_d mn_d is at least the sum of their scores of any key of
+// the page.  u and n are kept as int8 under one scale too, which does not change
+// the order of the pages; so a score is a whole number below 2^24 times S, one
+// rounding, the same in whatever order it is summed: the selection is a matter of
+// definition, not of the kernel.
+#include "qw3_attn_dev.h"
+
+using namespace qw3_shared;
+
+namespace {
+
+// The sequence, the place in it and the position of a packed row: the row is token
+// len - n + i.  A wave's lanes together; b < 0: a row of no sequence.
+struct Row {
+    int b, pos, len;
+};
+__device__ __forceinline__ Row find_row(const int32_t *cu, const int32_t *lens, int B, int total, int64_t room, int t) {
+    const int lane = threadIdx.x & 63;
+    auto length = [&](int b) { return (int)max((int64_t)0, min((int64_t)lens[b], room)); };
+    if (cu == nullptr) {
+        const int len = length(t);
+        return Row{t, len - 1, len};
+    }
+    Row row = {-1, 0, 0};
+    int floor = 0;
+    for (int base = 0; base < B; base += 64) {
+        const int start = max(floor, wave_scan_max(base + lane < B ? clamp_row(cu[min(base + lane, B - 1)], total) : 0));
+        const unsigned long long in = __ballot(base + lane < B && start <= t);
+        if (in == 0) break;
+        const int at = __popcll(in) - 1;  // the starts do not fall, so these are the first lanes
+        row.b = base + at, row.pos = __builtin_amdgcn_readlane(start, at);
+        floor = __builtin_amdgcn_readlane(start, 63);
+        if (in != ~0ull) break;
+    }
+    row.b = uniform(row.b);
+    if (row.b < 0) return row;
+    const int first = uniform(row.pos), end = clamp_row(cu[row.b + 1], total);
+    row.len = length(row.b);
+    row.pos = row.len - (end - first) + t - first;
+    if (t >= end) row.b = -1;
+    return row;
+}
+
+// ----------------------------------------------------------------- bounds --
+struct BoundsArgs {
+    const uint8_t *codes;
+    const float *scales;
+    const int32_t *table, *lens, *cu;
+    int8_t *bounds;
+    float *steps;
+    int B, Tq, H, shift, items;
+    int64_t max_pages, pages;
+};
+
+// The larger of what lanes l and l ^ 8 (l ^ 4) of each 16 hold, in both.
+__device__ __forceinline__ float max_ror8(float x) { return fmaxf(x, dpp_f32<0x128>(x)); }
+__device__ __forceinline__ float max_ror4(float x) { return fmaxf(x, dpp_f32<0x124>(x)); }
+
+// A wave has one page and head.  D / 16 lanes take a row, 16 channels each, and the
+// wave 1024 / D rows at a time; what lanes of the same channels hold is joined at the
+// end, halving in each step the channels that a lane stands for.
+template <int D, bool E4M3>
+__global__ __launch_bounds__(256) void bounds_kernel(BoundsArgs a) {
+    constexpr int kPieces = D / 16, kRows = 64 / kPieces;
+    const int lane = threadIdx.x & 63;
+    const int unit = (int)blockIdx.x * 4 + uniform((int)threadIdx.x >> 6);
+    const int item = (int)((uint32_t)unit / (uint32_t)a.H), h = unit - item * a.H;
+    if (item >= a.items) return;
+    // Sequence b owns the items from start / page_size + 2 b on: room for its pages whatever its length.
+    const int64_t room = a.max_pages << a.shift;
+    int b = item, n = 1, at = 0;
+    if (a.cu != nullptr) {
+        int first = 0, floor = 0;
+        b = -1;
+        for (int base = 0; base < a.B; base += 64) {
+            const int start =
+                max(floor, wave_scan_max(base + lane < a.B ? clamp_row(a.cu[min(base + lane, a.B - 1)], a.Tq) : 0));
+            const unsigned long long in = __ballot(base + lane < a.B && (start >> a.shift) + 2 * (base + lane) <= item);
+            if (in == 0) break;
+            const int i = __popcll(in) - 1;
+            b = base + i, first = __builtin_amdgcn_readlane(start, i);
+            floor = __builtin_amdgcn_readlane(start, 63);
+            if (in != ~0ull) break;
+        }
+        b = uniform(b), first = uniform(first);
+        if (b < 0) return;
+        n = clamp_row(a.cu[b + 1], a.Tq) - first;
+        at = item - (first >> a.shift) - 2 * b;
+    }
+    if (n <= 0) return;
+    const int len = (int)max((int64_t)0, min((int64_t)a.lens[b], room));
+    const int64_t col = (max(len - n, 0) >> a.shift) + (int64_t)at;
+    if (col << a.shift >= len) return;
+    const uint32_t page = (uint32_t)a.table[b * a.max_pages + col];
+    if (page >= (uint64_t)a.pages) return;
+    const int count = min(1 << a.shift, len - (int)(col << a.shift));
+
+    const int piece = lane % kPieces;
+    const int64_t row0 = ((int64_t)page * 2 * a.H + h) << a.shift;
+    const uint8_t *codes = a.codes + row0 * D + piece * 16;
+    const float *scales = a.scales + row0;
+    float v[32];  // the channels' largest values, then those of the values' opposites
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = kNegInf;
+    uint32_t nans = 0;
+    bool bad = false;
+    for (int r0 = lane / kPieces; r0 < count; r0 += 2 * kRows) {
+        uint4 w[2];
+        float s[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int r = min(r0 + k * kRows, count - 1);  // the last row again does no harm
+            w[k] = *reinterpret_cast<const uint4 *>(codes + (int64_t)r * D);
+            s[k] = scales[r];
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t d[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+            bad |= !(fabsf(s[k]) < __builtin_huge_valf());
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float f[4];
+                if (E4M3) {
+                    nans |= ((d[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                    f[0] = __builtin_amdgcn_cvt_f32_fp8(d[i], 0), f[1] = __builtin_amdgcn_cvt_f32_fp8(d[i], 1);
+                    f[2] = __builtin_amdgcn_cvt_f32_fp8(d[i], 2), f[3] = __builtin_amdgcn_cvt_f32_fp8(d[i], 3);
+                } else {
+                    f[0] = byte_f32<0>(d[i]), f[1] = byte_f32<1>(d[i]), f[2] = byte_f32<2>(d[i]), f[3] = byte_f32<3>(d[i]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x = f[e] * s[k];
+                    v[4 * i + e] = fmaxf(v[4 * i + e], x);
+                    v[16 + 4 * i + e] = fmaxf(v[16 + 4 * i + e], -x);
+                }
+            }
+        }
+    }
+    // lanes 0..31 keep the maxima, the others those of the opposites; then the even
+    // sixteens of lanes the first 8 channels, the odd ones the last
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[16 + i]), false, false);
+        v[i] = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[8 + i]), false, false);
+        v[i] = max_ror8(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+        if (D == 64) v[i] = max_ror4(v[i]);
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    top = (uint32_t)wave_max((int)top);
+    const bool finite = top < 0x7f800000u && !__any(bad || nans != 0);
+    const float step = finite ? __uint_as_float(top) / 127.0f : __uint_as_float(0x7fc00000u);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = lane < 32 ? v[i] : -v[i];
+        y[i] = step > 0.0f ? fminf(fmaxf(x / step, -127.0f), 127.0f) : 0.0f;
+    }
+    const uint32_t lo = codes4<false>({y[0], y[1], y[2], y[3]}), hi = codes4<false>({y[4], y[5], y[6], y[7]});
+    const int64_t to = (int64_t)page * a.H + h;
+    if ((lane & 15) < kPieces)
+        *reinterpret_cast<uint2 *>(a.bounds + (to * 2 + (lane >> 5)) * D + 16 * piece + 8 * ((lane >> 4) & 1)) = make_uint2(lo, hi);
+    if (lane == 0) a.steps[to] = step;
+}
+
+// ----------------------------------------------------------------- select --
+struct SelectArgs {
+    const uint16_t *q;
+    const int8_t *bounds;
+    const float *steps;
+    const int32_t *table, *lens, *cu;
+    int32_t *picks;
+    uint32_t *keys;  // in memory: those of the rows t0 .. t0 + rows - 1, [rows, H, pitch]
+    int64_t q_ts, q_hs, max_pages, pages;
+    int B, Tq, H, G, shift, count, first, recent, pitch, t0, rows;
+};
+
+// A score as a number that orders like it; NaN above all, 0 for a page that is not there.
+__device__ __forceinline__ uint32_t key_of(float score) {
+    const uint32_t u = __float_as_uint(score + 0.0f);  // no negative zero
+    if ((u & 0x7fffffffu) > 0x7f800000u) return ~0u;
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+constexpr uint32_t kNoPage = ~0u;  // in the place of a page's step
+
+// The w of rows first .. first + n - 1 for kv head h as int8 [kRows][2 D] in LDS, by D / 8
+// threads for a row.
+template <int D, int kRows>
+__device__ __forceinline__ void query_codes(const SelectArgs &a, int first, int n, int h, uint8_t *w) {
+    constexpr int kLanes = D / 8;
+    const int r = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
+    if (r >= kRows) return;
+    double u[8], l[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = l[i] = 0.0;
+    if (r < n) {
+        const uint16_t *q = a.q + (int64_t)(first + r) * a.q_ts + (int64_t)h * a.G * a.q_hs + 8 * c;
+        // in 64 bits: exact for all that bf16 adds up to, so the order does not matter
+#pragma unroll 4
+        for (int g = 0; g < a.G; ++g) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(q + g * a.q_hs);
+            const uint32_t d[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float f = __uint_as_float(i & 1 ? d[i / 2] & 0xffff0000u : d[i / 2] << 16);
+                // a NaN into both sums
+                u[i] += f < 0.0f ? 0.0 : (double)f;
+                l[i] += f > 0.0f ? 0.0 : (double)f;
+            }
+        }
+    }
+    float x[16];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        x[i] = (float)u[i], x[8 + i] = (float)l[i];
+        top = max(top, max(__float_as_uint(x[i]) & 0x7fffffffu, __float_as_uint(x[8 + i]) & 0x7fffffffu));
+    }
+#pragma unroll
+    for (int m = kLanes / 2; m >= 1; m /= 2) top = max(top, (uint32_t)__shfl_xor((int)top, m, 64));
+    const float s = top < 0x7f800000u ? __uint_as_float(top) / 127.0f : 0.0f;
+    uint32_t out[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = s > 0.0f ? fminf(fmaxf(x[4 * i + e] / s, -127.0f), 127.0f) : 0.0f;
+        out[i] = codes4<false>(y);
+    }
+    *reinterpret_cast<uint2 *>(w + r * 2 * D + 8 * c) = make_uint2(out[0], out[1]);
+    *reinterpret_cast<uint2 *>(w + r * 2 * D + D + 8 * c) = make_uint2(out[2], out[3]);
+}
+
+// Keys of the pages 16 p, p = p0, p0 + stride .. below `pages16`, by one wave, 16 pages
+// with the kRows rows' w at a time: the matrix unit's rows are pages, its columns rows.
+// to(row, page): where the keys of 4 pages go, for the first n rows.
+template <int D, int kRows, class To>
+__device__ __forceinline__ void score_pages(const SelectArgs &a, int b, int h, int p0, int stride, int pages, int n,
+                                            const uint8_t *w, To to) {
+    constexpr int kSteps = 2 * D / 64;
+    const int lane = threadIdx.x & 63, col = lane & 15, quarter = lane >> 4;
+    const int32_t *table = a.table + b * a.max_pages;
+    i4_t wf[kSteps];
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k)
+        wf[k] = *reinterpret_cast<const i4_t *>(w + (kRows == 1 ? 0 : col) * 2 * D + 64 * k + 16 * quarter);
+    // two of them at a time, so that one's loads are on their way beside the other's
+    for (int p = 16 * p0; p < pages; p += 32 * stride) {
+        i4_t kf[2][kSteps];
+        uint32_t step[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t page = (uint32_t)table[min(p + 16 * stride * j + col, pages - 1)];
+            step[j] = kNoPage;
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) kf[j][k] = i4_t{};
+            if (page < (uint64_t)a.pages) {
+                const int64_t at = (int64_t)page * a.H + h;
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k)
+                    kf[j][k] = *reinterpret_cast<const i4_t *>(a.bounds + at * 2 * D + 64 * k + 16 * quarter);
+                step[j] = __float_as_uint(a.steps[at]);
+                if (step[j] == kNoPage) step[j] = 0x7fc00000u;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int at = p + 16 * stride * j;
+            i4_t sum = {};
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) sum = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[j][k], wf[k], sum, 0, 0, 0);
+            uint32_t key[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const uint32_t s = (uint32_t)__shfl((int)step[j], 4 * quarter + r, 64);
+                key[r] = s == kNoPage ? 0u : key_of((float)sum[r] * __uint_as_float(s));
+            }
+            if (col < n && at < pages) *reinterpret_cast<uint4 *>(to(col, at + 4 * quarter)) = make_uint4(key[0], key[1], key[2], key[3]);
+        }
+    }
+}
+
+template <int T>
+__device__ __forceinline__ void group_sync() {
+    if constexpr (T > 64) {
+        __syncthreads();
+    } else {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// What T threads need to pick: a histogram of 256, and sums that waves exchange.
+struct PickSpace {
+    int bins[256];
+    int waves[16], bin, left;
+};
+
+// A row's picks out of `seen` pages, by T threads whose number among them is tid.
+// All if there are at most count; else the first ones, the last ones, and of those
+// between the `left` with the largest keys: the key that is the left-th largest is
+// found by its bytes, from the highest on, in counts of what has the bytes found so far;
+// then the pages are gone through in order, and of those with that key the first are taken.
+template <int T>
+__device__ __forceinline__ void pick(const SelectArgs &a, const uint32_t *keys, int seen, int32_t *out, PickSpace &space, int tid) {
+    if (seen <= a.count) {
+        for (int i = tid; i < a.count; i += T) out[i] = i < seen ? i : -1;
+        return;
+    }
+    const int lane = tid & 63, lo = a.first, hi = seen - a.recent;
+    int left = a.count - a.first - a.recent;
+    uint32_t prefix = 0, mask = 0;
+    for (int shift = 24; shift >= 0 && left > 0; shift -= 8) {
+        group_sync<T>();
+        for (int i = tid; i < 256; i += T) space.bins[i] = 0;
+        group_sync<T>();
+        for (int i = lo + tid; i < hi; i += T) {
+            const uint32_t key = keys[i];
+            if ((key & mask) == prefix) atomicAdd(&space.bins[(key >> shift) & 255], 1);
+        }
+        group_sync<T>();
+        if (tid < 64) {  // lane l has the bins 255 - 4 l and the three below
+            int c[4], sum = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[j] = space.bins[255 - 4 * lane - j], sum += c[j];
+            const int upto = wave_scan(sum);
+            int before = upto - sum;
+            if (before < left && left <= upto) {
+                int j = 0;
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    if (j == k && before + c[k] < left) before += c[k], ++j;
+                space.bin = 255 - 4 * lane - j, space.left = left - before;
+            }
+        }
+        group_sync<T>();
+        prefix |= (uint32_t)space.bin << shift, mask |= 255u << shift;
+        left = space.left;
+    }
+    // place: of the next pick; equals: how many with the key have been passed
+    const bool none = left <= 0;
+    int place = a.first, equals = 0;
+    for (int i = tid; i < a.first; i += T) out[i] = i;
+    for (int i0 = lo; i0 < hi; i0 += T) {
+        const int i = i0 + tid;
+        const uint32_t key = i < hi ? keys[i] : 0;
+        const bool more = !none && i < hi && key > prefix, equal = !none && i < hi && key == prefix;
+        const unsigned long long m = __ballot(more), e = __ballot(equal), below = (1ull << lane) - 1;
+        int mores = __popcll(m), same = __popcll(e);  // of the wave, then of all
+        int m_before = __popcll(m & below), e_before = __popcll(e & below);
+        if constexpr (T > 64) {
+            group_sync<T>();
+            if (lane == 0) space.waves[tid >> 6] = mores << 16 | same;
+            group_sync<T>();
+            mores = same = 0;
+#pragma unroll
+            for (int x = 0; x < T / 64; ++x) {
+                const int s = space.waves[x];
+                if (x < tid >> 6) m_before += s >> 16, e_before += s & 0xffff;
+                mores += s >> 16, same += s & 0xffff;
+            }
+        }
+        const int taken = min(equals, left), e_taken = min(equals + e_before, left) - taken;
+        if (more || (equal && equals + e_before < left)) out[place + m_before + e_taken] = i;
+        place += mores + min(equals + same, left) - taken;
+        equals += same;
+    }
+    for (int i = tid; i < a.recent; i += T) out[a.count - a.recent + i] = hi + i;
+}
+
+// Pages that a row at a position sees.
+__device__ __forceinline__ int pages_seen(const SelectArgs &a, int pos) { return pos < 0 ? 0 : (pos >> a.shift) + 1; }
+
+// One row and kv head: scores and picks in one workgroup, the keys in LDS.
+template <int D, int T>
+__global__ __launch_bounds__(T) void select_row_kernel(SelectArgs a) {
+    extern __shared__ __attribute__((aligned(16))) uint32_t keys[];
+    __shared__ __attribute__((aligned(16))) uint8_t w[2 * D];
+    __shared__ PickSpace space;
+    const int t = (int)(blockIdx.x / (uint32_t)a.H), h = (int)blockIdx.x - t * a.H;
+    const Row row = find_row(a.cu, a.lens, a.B, a.Tq, a.max_pages << a.shift, t);
+    if (row.b < 0) return;
+    const int seen = pages_seen(a, row.pos);
+    if (seen > a.count) {
+        query_codes<D, 1>(a, t, 1, h, w);
+        __syncthreads();
+        score_pages<D, 1>(a, row.b, h, uniform((int)threadIdx.x >> 6), T / 64, seen, 1, w, [&](int, int p) { return keys + p; });
+        __syncthreads();
+    }
+    pick<T>(a, keys, seen, a.picks + ((int64_t)t * a.H + h) * a.count, space, threadIdx.x);
+}
+
+// The rank-th tile of 16 rows: sequence b owns the ranks from start / 16 + b on (room
+// for its rows whatever their number).  n: the tile's rows, 0 if there are none.
+struct Tile {
+    int b, first, n, pos;  // its first row and that row's position
+};
+__device__ __forceinline__ Tile find_tile(const SelectArgs &a, int rank) {
+    const int lane = threadIdx.x & 63;
+    const int64_t room = a.max_pages << a.shift;
+    auto length = [&](int b) { return (int)max((int64_t)0, min((int64_t)a.lens[b], room)); };
+    if (a.cu == nullptr) return Tile{rank, rank, 1, length(rank) - 1};
+    int b = -1, first = 0, floor = 0;
+    for (int base = 0; base < a.B; base += 64) {
+        const int start = max(floor, wave_scan_max(base + lane < a.B ? clamp_row(a.cu[min(base + lane, a.B - 1)], a.Tq) : 0));
+        const unsigned long long in = __ballot(base + lane < a.B && start / 16 + base + lane <= rank);
+        if (in == 0) break;
+        const int i = __popcll(in) - 1;
+        b = base + i, first = __builtin_amdgcn_readlane(start, i);
+        floor = __builtin_amdgcn_readlane(start, 63);
+        if (in != ~0ull) break;
+    }
+    b = uniform(b), first = uniform(first);
+    if (b < 0) return Tile{0, 0, 0, 0};
+    const int n = clamp_row(a.cu[b + 1], a.Tq) - first, skip = 16 * (rank - first / 16 - b);
+    return Tile{b, first + skip, max(min(16, n - skip), 0), length(b) - n + skip};
+}
+
+// 16 rows of a sequence and a kv head: the pages' bounds are read once for all of
+// them, and each wave picks for 4.
+template <int D>
+__global__ __launch_bounds__(256) void select_tile_kernel(SelectArgs a) {
+    extern __shared__ __attribute__((aligned(16))) uint32_t keys[];
+    __shared__ __attribute__((aligned(16))) uint8_t w[16 * 2 * D];
+    __shared__ PickSpace space[4];
+    const int rank = (int)(blockIdx.x / (uint32_t)a.H), h = (int)blockIdx.x - rank * a.H;
+    const int wave = uniform((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const Tile tile = find_tile(a, rank);
+    if (tile.n <= 0) return;
+    const int most = pages_seen(a, tile.pos + tile.n - 1);
+    if (most > a.count) {
+        query_codes<D, 16>(a, tile.first, tile.n, h, w);
+        __syncthreads();
+        score_pages<D, 16>(a, tile.b, h, wave, 4, most, tile.n, w, [&](int r, int p) { return keys + r * a.pitch + p; });
+        __syncthreads();
+    }
+    for (int r = wave; r < tile.n; r += 4)
+        pick<64>(a, keys + r * a.pitch, pages_seen(a, tile.pos + r), a.picks + ((int64_t)(tile.first + r) * a.H + h) * a.count,
+                 space[wave], lane);
+}
+
+// Scores alone, into memory: 16 rows of a sequence, a kv head and every
+// gridDim.y-th 64 pages.
+template <int D>
+__global__ __launch_bounds__(256) void score_kernel(SelectArgs a) {
+    __shared__ __attribute__((aligned(16))) uint8_t w[16 * 2 * D];
+    const int rank = (int)(blockIdx.x / (uint32_t)a.H), h = (int)blockIdx.x - rank * a.H;
+    Tile tile = find_tile(a, rank);
+    // of the tile's rows those of this launch
+    const int skip = max(a.t0 - tile.first, 0);
+    tile.n = min(tile.n, a.t0 + a.rows - tile.first) - skip, tile.first += skip, tile.pos += skip;
+    if (tile.n <= 0) return;
+    const int most = pages_seen(a, tile.pos + tile.n - 1);
+    if (most <= a.count) return;
+    query_codes<D, 16>(a, tile.first, tile.n, h, w);
+    __syncthreads();
+    const int wave = uniform((int)threadIdx.x >> 6);
+    score_pages<D, 16>(a, tile.b, h, (int)blockIdx.y * 4 + wave, 4 * (int)gridDim.y, most, tile.n, w,
+                       [&](int r, int p) { return a.keys + ((int64_t)(tile.first - a.t0 + r) * a.H + h) * a.pitch + p; });
+}
+
+template <int T>
+__global__ __launch_bounds__(T) void pick_kernel(SelectArgs a) {
+    __shared__ PickSpace space;
+    const int r = (int)(blockIdx.x / (uint32_t)a.H), h = (int)blockIdx.x - r * a.H, t = a.t0 + r;
+    const Row row = find_row(a.cu, a.lens, a.B, a.Tq, a.max_pages << a.shift, t);
+    if (row.b < 0) return;
+    pick<T>(a, a.keys + ((int64_t)r * a.H + h) * a.pitch, pages_seen(a, row.pos), a.picks + ((int64_t)t * a.H + h) * a.count, space,
+            threadIdx.x);
+}
+
+// -------------------------------------------------------------- attention --
+struct BlocksArgs {
+    const uint16_t *q;
+    const uint8_t *codes;
+    const float *scales;
+    const int32_t *table, *lens, *cu, *picks;
+    uint16_t *o;
+    float *part;  // split: where workgroups leave their parts, ...
+    int *counts;  // ... how many of an item have, ...
+    int *clear;   // ... and the next call's counters
+    int64_t q_ts, q_hs, max_pages, pages;
+    int B, Tq, Hq, H, G, shift, count, parts, blocks;  // blocks: of 16 of a kv head's queries
+    float scale;                                       // sm_scale log2(e)
+};
+
+// An item is a row, a kv head and 16 of its queries: 16 columns of the matrix unit's
+// result.  Its keys are the picked pages' in groups of 16, which lie in one page
+// whatever its size; a wave takes two groups at a time, a step.  W waves of a
+// workgroup, and the workgroups of `parts`, take an item's steps in turn.
+// W = 4: one item a workgroup, joined in LDS, and over the parts by the one that
+// finishes last; W = 1: an item for each wave, the same kv head of neighbouring rows.
+template <int D, bool E4M3, int W>
+__global__ __launch_bounds__(256, 2) void attn_blocks_kernel(BlocksArgs a) {
+    constexpr int R = 16, kPad = D + 4;
+    constexpr int kPieces = D / 16, kVLoads = D / 32;
+    constexpr int kTurn = 4 * 32 * D, kJoin = W == 4 ? 4 * R * kPad * 4 : 0;
+    __shared__ __attribute__((aligned(1024))) char lds[kTurn > kJoin ? kTurn : kJoin];
+    __shared__ float stat[2][4][R];
+    __shared__ int arrived;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), quarter = lane >> 4, col = lane & 15;
+    if (W == 4 && a.parts > 1 && blockIdx.x == 0) clear_next<256>(a.clear);
+
+    const int part = W == 4 ? (int)(blockIdx.x % (uint32_t)a.parts) : 0;
+    const int item = W == 4 ? (int)(blockIdx.x / (uint32_t)a.parts) : (int)blockIdx.x;
+    const int per_row = a.H * a.blocks;
+    const int t = item / per_row * (4 / W) + (W == 1 ? wave : 0), hb = item % per_row;
+    const int h = hb / a.blocks, g0 = (hb - h * a.blocks) * R, rows = min(R, a.G - g0);
+    Row row = {-1, 0, 0};
+    if (W == 4 || t < a.Tq) row = find_row(a.cu, a.lens, a.B, a.Tq, a.max_pages << a.shift, t);
+    if (row.b < 0) return;  // with W = 4 all waves, and all parts
+    const int pos = row.pos;
+    const int32_t *table = a.table + row.b * a.max_pages, *picks = a.picks + ((int64_t)t * a.H + h) * a.count;
+    const int mask = (1 << a.shift) - 1;
+
+    // Steps of the wave: first, first + stride, ...; 32 of them at a time lane 2 s + g has of
+    // group g of step s the page (-1: none that the row sees) and its first token's position.
+    const int groups = a.count << (a.shift - 4), stride = W * a.parts, first = part * W + (W == 4 ? wave : 0);
+    const int steps = first < (groups + 1) / 2 ? ((groups + 1) / 2 - first + stride - 1) / stride : 0;
+    int ids = -1, bases = 0;
+    auto look_up = [&](int s0) {
+        const int64_t g = 2 * (first + (int64_t)(s0 + (lane >> 1)) * stride) + (lane & 1);
+        ids = -1, bases = 0;
+        if (g < groups) {
+            const int pick = picks[g >> (a.shift - 4)];
+            const int64_t base = ((int64_t)pick << a.shift) + ((g << 4) & mask);
+            if (pick >= 0 && pick < a.max_pages && base <= pos) {
+                const int page = table[pick];
+                if ((uint32_t)page < (uint64_t)a.pages) ids = page, bases = (int)base;
+            }
+        }
+    };
+    if (steps > 0) look_up(0);
+
+    struct Stage {
+        uint4 k[2][D / 64], v[kVLoads];
+        float4 ks[2], vs[2];
+    } st = {};
+    auto page_of = [&](int s, int g) { return __builtin_amdgcn_readlane(ids, 2 * (s & 31) + g); };
+    auto base_of = [&](int s, int g) { return __builtin_amdgcn_readlane(bases, 2 * (s & 31) + g); };
+    const int64_t page_rows = (int64_t)(2 * a.H) << a.shift, to_v = (int64_t)a.H << a.shift;
+    auto fetch = [&](int s) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int page = page_of(s, g);
+            if (page < 0) continue;
+            const int64_t at = page * page_rows + ((int64_t)h << a.shift) + (base_of(s, g) & mask);
+            const uint8_t *kp = a.codes + at * D, *vp = kp + to_v * D;
+            const float *sp = a.scales + at;
+            // a uniform base and a lane's offset
+            uint32_t ko = col * D + quarter * 16, vo = lane * 16, so = 4 * quarter;
+            asm("" : "+v"(ko), "+v"(vo), "+v"(so));
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) st.k[g][c] = *reinterpret_cast<const uint4 *>(kp + ko + 64 * c);
+#pragma unroll
+            for (int c = 0; c < kVLoads / 2; ++c)
+                st.v[g * (kVLoads / 2) + c] = *reinterpret_cast<const uint4 *>(vp + vo + 1024 * c);
+            st.ks[g] = *reinterpret_cast<const float4 *>(sp + so);
+            st.vs[g] = *reinterpret_cast<const float4 *>(sp + to_v + so);
+        }
+    };
+
+    // the queries, as B operands with the channels in the order of K's pieces
+    bf8_t qf[D / 32];
+    {
+        const uint16_t *qp = a.q + (int64_t)t * a.q_ts + (h * a.G + g0 + min(col, rows - 1)) * a.q_hs;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+            qf[i] = *reinterpret_cast<const bf8_t *>(qp + 16 * (quarter + 4 * (i / 2)) + 8 * (i & 1));
+    }
+    if (steps > 0) fetch(0);
+
+    // V tile: row r, 16-byte piece c at place c ^ f(r), so that the turning reads spread over the banks
+    const int vrow = lane / kPieces, vpiece = lane % kPieces;
+    char *turn = lds + wave * 32 * D;
+    auto place = [](int r) { return D == 128 ? (r >> 1) & 7 : (r >> 2) & 3; };
+    f4_t acc[D / 16];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) acc[i] = f4_t{};
+    float m = kNegInf, l = 0.0f;
+
+    // A step; masked: of some group not all 16 keys are seen.  What is hidden is
+    // hidden from all columns, which are queries of one token: its values are taken as zeros.
+    auto step = [&](int s, uint32_t seen, auto masked_c) {
+        constexpr bool kMasked = decltype(masked_c)::value;
+#pragma unroll
+        for (int c = 0; c < kVLoads; ++c) {
+            const int r = vrow + c * (64 / kPieces);
+            if (E4M3 && kMasked && !((seen >> r) & 1)) st.v[c] = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(turn + r * D + ((vpiece ^ place(r)) << 4)) = st.v[c];
+        }
+        float kc[2][4], vc[2][4];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            kc[g][0] = st.ks[g].x * a.scale, kc[g][1] = st.ks[g].y * a.scale;
+            kc[g][2] = st.ks[g].z * a.scale, kc[g][3] = st.ks[g].w * a.scale;
+            vc[g][0] = st.vs[g].x, vc[g][1] = st.vs[g].y, vc[g][2] = st.vs[g].z, vc[g][3] = st.vs[g].w;
+            // copies, so that the next step's loads are not waited for at the end of this one
+#pragma unroll
+            for (int r = 0; r < 4; ++r) asm volatile("" : "+v"(vc[g][r]));
+        }
+        f4_t sc[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            sc[g] = f4_t{};
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                const uint4 w = st.k[g][c];
+                sc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8<E4M3>(w.x, w.y), qf[2 * c], sc[g], 0, 0, 0);
+                sc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8<E4M3>(w.z, w.w), qf[2 * c + 1], sc[g], 0, 0, 0);
+            }
+        }
+        if (s + 1 < steps) {
+            if (((s + 1) & 31) == 0) look_up(s + 1);
+            fetch(s + 1);
+        }
+        bool hid[2][4];
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                sc[g][r] *= kc[g][r];
+                hid[g][r] = kMasked && !((seen >> (16 * g + 4 * quarter + r)) & 1);
+                if (kMasked) sc[g][r] = hid[g][r] ? kNegInf : sc[g][r];
+            }
+        float top = sc[0][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) top = fmaxf(top, sc[i / 4][i % 4]);
+        if (__any(top > m + kSlack)) {
+            const float m1 = fmaxf(m, max_quarters(top));
+            const float f = m1 == kNegInf ? 1.0f : exp2_fast(m - m1);
+            m = m1;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) acc[i] *= f;
+        }
+        const float ms = m == kNegInf ? 0.0f : m;
+        // a weight is the sum of two bf16: its rounding and the rounding of what that leaves
+        uint32_t p[4], pr[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int g = i / 2, r = 2 * (i & 1) + e;
+                const float pe = exp2_fast(sc[g][r] - ms);
+                l += pe;
+                w[e] = hid[g][r] ? 0.0f : pe * vc[g][r];  // a hidden key's scale may be anything
+            }
+            p[i] = pack_bf16(w[0], w[1]);
+            pr[i] = pack_bf16(w[0] - __uint_as_float(p[i] << 16), w[1] - __uint_as_float(p[i] & 0xffff0000u));
+        }
+        const bf8_t pf = __builtin_bit_cast(bf8_t, i4_t{(int)p[0], (int)p[1], (int)p[2], (int)p[3]});
+        const bf8_t pl = __builtin_bit_cast(bf8_t, i4_t{(int)pr[0], (int)pr[1], (int)pr[2], (int)pr[3]});
+        // V^T: keys 4 quarter + 0..3 and 16 + 4 quarter + 0..3 of 16 channels
+        const int vkey = 4 * quarter + ((col >> 1) & 3) + 16 * (col >> 3), xv = place(vkey);
+        const char *from = turn + vkey * D + (col & 1) * 8;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            const i2_t w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS_AS i2_t *)(from + ((i ^ xv) << 4)));
+            const bf8_t vf = decode8<E4M3>((uint32_t)w[0], (uint32_t)w[1]);
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf, acc[i], 0, 0, 0);
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pl, acc[i], 0, 0, 0);
+        }
+    };
+    auto low_bits = [](int n) { return n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1; };
+    for (int s = 0; s < steps; ++s) {
+        uint32_t seen = page_of(s, 0) < 0 ? 0u : low_bits(pos + 1 - base_of(s, 0));
+        seen |= (page_of(s, 1) < 0 ? 0u : low_bits(pos + 1 - base_of(s, 1))) << 16;
+        if (seen == ~0u) {
+            step(s, seen, std::false_type{});
+        } else if (seen != 0) {
+            step(s, seen, std::true_type{});
+        } else if (s + 1 < steps) {  // nothing here
+            if (((s + 1) & 31) == 0) look_up(s + 1);
+            fetch(s + 1);
+        }
+    }
+    l = sum_quarters(l);
+
+    uint16_t *op = a.o + ((int64_t)t * a.Hq + h * a.G + g0) * D;
+    if (W == 1) {
+        if (col < rows) {
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                *reinterpret_cast<uint2 *>(op + col * D + 16 * i + 4 * quarter) =
+                    make_uint2(pack_bf16(acc[i][0] * inv, acc[i][1] * inv), pack_bf16(acc[i][2] * inv, acc[i][3] * inv));
+        }
+        return;
+    }
+    float *join = reinterpret_cast<float *>(lds);
+    if (quarter == 0) stat[0][wave][col] = m, stat[1][wave][col] = l;
+    __syncthreads();  // the turning tiles are read
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+        *reinterpret_cast<f4_t *>(join + (wave * R + col) * kPad + 16 * i + 4 * quarter) = acc[i];
+    __syncthreads();
+    float *out = a.part + (int64_t)(item * a.parts + part) * (R * (D + 2));
+    for (int e = tid; e < rows * D / 2; e += 256) {
+        const int r = e / (D / 2), c = 2 * (e % (D / 2));
+        float mm = kNegInf;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) mm = fmaxf(mm, stat[0][w][r]);
+        float ll = 0.0f;
+        f2_t sum = {};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float f = stat[0][w][r] == kNegInf ? 0.0f : exp2_fast(stat[0][w][r] - mm);
+            ll += f * stat[1][w][r];
+            sum += f * *reinterpret_cast<const f2_t *>(join + (w * R + r) * kPad + c);
+        }
+        if (a.parts == 1) {
+            const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+            *reinterpret_cast<uint32_t *>(op + r * D + c) = pack_bf16(sum[0] * inv, sum[1] * inv);
+        } else {
+            store_agent(out + 2 * R + r * D + c, sum[0], sum[1]);
+            if (c == 0) store_agent(out + 2 * r, mm, ll);
+        }
+    }
+    if (a.parts == 1) return;
+    wait_vm0();
+    __syncthreads();
+    if (tid == 0) arrived = __hip_atomic_fetch_add(a.counts + item, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (uniform(arrived) != a.parts - 1) return;
+    const float *parts0 = a.part + (int64_t)item * a.parts * (R * (D + 2));
+    auto slot_of = [&](int g) { return parts0 + (int64_t)g * (R * (D + 2)); };
+    auto row_out = [&](int r) { return op + r * D; };
+    if (rows <= R / 2)
+        join_rows<R, D, R / 8>(slot_of, 0, a.parts - 1, rows, row_out);
+    else
+        join_rows<R, D, R / 4>(slot_of, 0, a.parts - 1, rows, row_out);
+    if (tid == 0) __hip_atomic_store(a.counts + item, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+template <int D, bool E4M3>
+qw3_status launch_blocks(BlocksArgs a, hipStream_t stream) {
+    int cus = 0;
+    qw3_status st = cu_count(&cus);
+    if (st != QW3_OK) return st;
+    const int64_t items = (int64_t)a.Tq * a.H * a.blocks;
+    // An item of n units of 128 keys in parts of u: u + c n / u, as in qattn_cache, and
+    // no more parts than twice the CUs have room for.
+    const float units = (float)(((int64_t)a.count << a.shift) / 128 + 1);
+    const int most = (int)(units / __builtin_sqrtf(0.14f * units));
+    const int64_t room = items < 2 * (int64_t)cus ? 2 * (int64_t)cus / items : 1;
+    a.parts = (int)(room < most ? room : most);
+    if (a.parts < 1 || items > kCounts) a.parts = 1;
+    if (items >= 8 * (int64_t)cus) {  // an item for each wave
+        const int64_t wgs = ceil_div(a.Tq, 4) * a.H * a.blocks;
+        hipLaunchKernelGGL((attn_blocks_kernel<D, E4M3, 1>), dim3((unsigned)wgs), dim3(256), 0, stream, a);
+        return check_launch();
+    }
+    if (a.parts > 1) {
+        void *ws = nullptr;
+        st = workspace(stream, (size_t)(items * a.parts) * 16 * (D + 2) * sizeof(float), &ws);
+        if (st != QW3_OK) return st;
+        a.part = static_cast<float *>(ws);
+        st = counters(stream, (int)items, &a.counts, &a.clear);
+        if (st != QW3_OK) return st;
+    }
+    hipLaunchKernelGGL((attn_blocks_kernel<D, E4M3, 4>), dim3((unsigned)(items * a.parts)), dim3(256), 0, stream, a);
+    return check_launch();
+}
+
+constexpr int64_t kTileKeys = 12288, kRowKeys = 4100;  // words of LDS for the keys of 16 rows, of one
+constexpr int64_t kKeyBytes = int64_t(64) << 20;  // of keys in memory at a time
+
+template <int D>
+qw3_status launch_select(SelectArgs a, hipStream_t stream) {
+    a.pitch = (int)(ceil_div(a.max_pages, 16) * 16 + 4);  // rows of the keys begin in different banks
+    const int64_t tiles = a.cu ? a.Tq / 16 + a.B : a.B;
+    if (a.cu && a.Tq >= 4 * (int64_t)a.B && 16 * a.pitch <= kTileKeys) {
+        hipLaunchKernelGGL((select_tile_kernel<D>), dim3((unsigned)(tiles * a.H)), dim3(256), 16 * a.pitch * 4, stream, a);
+        return check_launch();
+    }
+    if (a.pitch <= kRowKeys) {
+        hipLaunchKernelGGL((select_row_kernel<D, 1024>), dim3((unsigned)(a.Tq * a.H)), dim3(1024), a.pitch * 4, stream, a);
+        return check_launch();
+    }
+    int64_t rows = kKeyBytes / (4 * (int64_t)a.pitch * a.H);
+    rows = rows < 16 ? 16 : rows;
+    rows = rows < a.Tq ? rows : a.Tq;
+    void *ws = nullptr;
+    const qw3_status st = workspace(stream, (size_t)(rows * a.H * a.pitch) * 4, &ws);
+    if (st != QW3_OK) return st;
+    a.keys = static_cast<uint32_t *>(ws);
+    int64_t some = ceil_div(a.max_pages, 64);  // workgroups of a tile
+    some = some < 64 ? some : 64;
+    for (int64_t t = 0; t < a.Tq; t += rows) {
+        a.t0 = (int)t, a.rows = (int)(rows < a.Tq - t ? rows : a.Tq - t);
+        hipLaunchKernelGGL((score_kernel<D>), dim3((unsigned)(tiles * a.H), (unsigned)some), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((pick_kernel<1024>), dim3((unsigned)(a.rows * a.H)), dim3(1024), 0, stream, a);
+    }
+    return check_launch();
+}
+
+// What the three calls check of sequences; *shift = log2(page_size).
+qw3_status check_sequences(int64_t B, int64_t max_pages, int64_t Tq, bool starts, int64_t H, int64_t D, int64_t pages,
+                           int64_t page_size, int *shift) {
+    const qw3_status st = check_cache(QW3_CODES_INT8, H, D, pages, page_size, shift);
+    if (st != QW3_OK) return st;
+    if (B < 0 || B > QW3_MAX_SEQS || Tq < 0 || Tq > QW3_MAX_TOKENS || max_pages < 0 || (!starts && Tq != B)) return QW3_ERR_SHAPE;
+    return max_pages > (int64_t(1) << 30) / page_size ? QW3_ERR_SHAPE : QW3_OK;
+}
+
+qw3_status check_picks(int64_t Tq, int64_t Hq, int64_t H, int64_t count, int64_t q_ts, int64_t q_hs) {
+    if (Hq < 1 || Hq % H != 0 || Hq > QW3_MAX_HEADS || count < 1 || count > QW3_MAX_PICKS) return QW3_ERR_SHAPE;
+    if ((Tq + 4) * H * ceil_div(Hq / H, 16) >= 4 * kMaxGroups) return QW3_ERR_SHAPE;  // a wave for each item
+    return strides_ok(q_ts, q_hs, int64_t(1) << 32) ? QW3_OK : QW3_ERR_SHAPE;
+}
+
+}  // namespace
+
+extern "C" {
+
+qw3_status qcache_bounds(const void *codes, const float *scales, int32_t code_type, const int32_t *block_table,
+                         const int32_t *lens, const int32_t *cu_q, int8_t *bounds, float *bound_scales, int64_t B,
+                         int64_t max_pages, int64_t Tq, int64_t H, int64_t D, int64_t pages, int64_t page_size,
+                         void *hip_stream) {
+    int shift = 0;
+    if (code_type != QW3_CODES_INT8 && code_type != QW3_CODES_E4M3) return QW3_ERR_SHAPE;
+    const qw3_status st = check_sequences(B, max_pages, Tq, cu_q != nullptr, H, D, pages, page_size, &shift);
+    if (st != QW3_OK) return st;
+    const int64_t items = cu_q ? (Tq >> shift) + 2 * B : B;
+    if (items * H >= 4 * kMaxGroups) return QW3_ERR_SHAPE;
+    if (B == 0 || Tq == 0 || max_pages == 0 || pages == 0) return QW3_OK;
+    if (!codes || !scales || !block_table || !lens || !bounds || !bound_scales) return QW3_ERR_NULL;
+    if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(block_table, 4) || !aligned(lens, 4) || !aligned(cu_q, 4) ||
+        !aligned(bounds, 16) || !aligned(bound_scales, 4))
+        return QW3_ERR_ALIGN;
+    BoundsArgs a{};
+    a.codes = static_cast<const uint8_t *>(codes), a.scales = scales, a.table = block_table, a.lens = lens, a.cu = cu_q;
+    a.bounds = bounds, a.steps = bound_scales, a.B = (int)B, a.Tq = (int)Tq, a.H = (int)H, a.shift = shift;
+    a.items = (int)items, a.max_pages = max_pages, a.pages = pages;
+    auto run = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)ceil_div(items * H, 4)), dim3(256), 0, (hipStream_t)hip_stream, a);
+    };
+    if (D == 128)
+        code_type == QW3_CODES_E4M3 ? run(bounds_kernel<128, true>) : run(bounds_kernel<128, false>);
+    else
+        code_type == QW3_CODES_E4M3 ? run(bounds_kernel<64, true>) : run(bounds_kernel<64, false>);
+    return check_launch();
+}
+
+qw3_status qblock_select(const uint16_t *q, const int8_t *bounds, const float *bound_scales, const int32_t *block_table,
+                         const int32_t *lens, const int32_t *cu_q, int32_t *picks, int64_t B, int64_t max_pages, int64_t Tq,
+                         int64_t Hq, int64_t H, int64_t D, int64_t pages, int64_t page_size, int64_t count, int64_t first,
+                         int64_t recent, int64_t q_ts, int64_t q_hs, void *hip_stream) {
+    int shift = 0;
+    qw3_status st = check_sequences(B, max_pages, Tq, cu_q != nullptr, H, D, pages, page_size, &shift);
+    if (st != QW3_OK) return st;
+    st = check_picks(Tq, Hq, H, count, q_ts, q_hs);
+    if (st != QW3_OK) return st;
+    if (first < 0 || recent < 1 || first > count || recent > count - first) return QW3_ERR_SHAPE;
+    if ((Tq + B) * H >= kMaxGroups / 4) return QW3_ERR_SHAPE;  // of workgroups of 1024 threads
+    if (B == 0 || Tq == 0) return QW3_OK;
+    if (!q || !lens || !picks || (max_pages > 0 && !block_table) || (pages > 0 && (!bounds || !bound_scales))) return QW3_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(bounds, 16) || !aligned(bound_scales, 4) || !aligned(block_table, 4) || !aligned(lens, 4) ||
+        !aligned(cu_q, 4) || !aligned(picks, 4) || q_ts % 8 || q_hs % 8)
+        return QW3_ERR_ALIGN;
+    SelectArgs a{};
+    a.q = q, a.bounds = bounds, a.steps = bound_scales, a.table = block_table, a.lens = lens, a.cu = cu_q, a.picks = picks;
+    a.q_ts = q_ts, a.q_hs = q_hs, a.max_pages = max_pages, a.pages = pages, a.B = (int)B, a.Tq = (int)Tq, a.H = (int)H;
+    a.G = (int)(Hq / H), a.shift = shift, a.count = (int)count, a.first = (int)first, a.recent = (int)recent;
+    return D == 128 ? launch_select<128>(a, (hipStream_t)hip_stream) : launch_select<64>(a, (hipStream_t)hip_stream);
+}
+
+qw3_status qattn_blocks(const uint16_t *q, const void *codes, const float *scales, int32_t code_type,
+                        const int32_t *block_table, const int32_t *lens, const int32_t *cu_q, const int32_t *picks,
+                        uint16_t *out, int64_t B, int64_t max_pages, int64_t Tq, int64_t Hq, int64_t H, int64_t D,
+                        int64_t pages, int64_t page_size, int64_t count, int64_t q_ts, int64_t q_hs, float sm_scale,
+                        void *hip_stream) {
+    int shift = 0;
+    if (code_type != QW3_CODES_INT8 && code_type != QW3_CODES_E4M3) return QW3_ERR_SHAPE;
+    qw3_status st = check_sequences(B, max_pages, Tq, cu_q != nullptr, H, D, pages, page_size, &shift);
+    if (st != QW3_OK) return st;
+    st = check_picks(Tq, Hq, H, count, q_ts, q_hs);
+    if (st != QW3_OK) return st;
+    if (count > (int64_t(1) << 30) / page_size || !(sm_scale > 0.0f && sm_scale < __builtin_huge_valf())) return QW3_ERR_SHAPE;
+    if (B == 0 || Tq == 0) return QW3_OK;
+    if (!q || !lens || !picks || !out || (max_pages > 0 && !block_table) || (pages > 0 && (!codes || !scales))) return QW3_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(block_table, 4) || !aligned(lens, 4) ||
+        !aligned(cu_q, 4) || !aligned(picks, 4) || !aligned(out, 16) || q_ts % 8 || q_hs % 8)
+        return QW3_ERR_ALIGN;
+    BlocksArgs a{};
+    a.q = q, a.codes = static_cast<const uint8_t *>(codes), a.scales = scales, a.table = block_table, a.lens = lens;
+    a.cu = cu_q, a.picks = picks, a.o = out, a.q_ts = q_ts, a.q_hs = q_hs, a.max_pages = max_pages, a.pages = pages;
+    a.B = (int)B, a.Tq = (int)Tq, a.Hq = (int)Hq, a.H = (int)H, a.G = (int)(Hq / H), a.shift = shift, a.count = (int)count;
+    a.blocks = (int)ceil_div(Hq / H, 16), a.scale = sm_scale * 1.44269504088896341f;
+    const hipStream_t stream = (hipStream_t)hip_stream;
+    if (D == 128) return code_type == QW3_CODES_E4M3 ? launch_blocks<128, true>(a, stream) : launch_blocks<128, false>(a, stream);
+    return code_type == QW3_CODES_E4M3 ? launch_blocks<64, true>(a, stream) : launch_blocks<64, false>(a, stream);
+}
+
+}  // extern "C"

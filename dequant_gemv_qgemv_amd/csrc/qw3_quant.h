@@ -8,11 +8,11 @@
 namespace {
 
 typedef float f2_t __attribute__((ext_vector_type(2)));
-typedef __bf16 bfx2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const f2_t f = {lo, hi};
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bfx2_t));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf2_t));
 }
 
 // The quotients.  A row's 128 divisions by the same s cost more than all else of

@@ -520,6 +520,85 @@ qw3_status qcache_compact(void *codes, float *scales, const int32_t *block_table
                           const uint8_t *keep, int32_t *lens_out, int64_t B, int64_t max_pages, int64_t Tq,
                           int64_t layers, int64_t H, int64_t D, int64_t pages, int64_t page_size, void *hip_stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention over some of the cache's pages.  A query reads, for each kv head, the
+ * pages that a cheap score selects out of those it sees, in place of all of them.
+ *   bounds       [pages, H, 2, D] int8, caller-owned, beside a layer's cache: for each
+ *                page, kv head and channel the largest (0) and smallest (1) value of its keys
+ *   bound_scales [pages, H] float32: what the int8 values are multiplied by
+ * Sequences, tables, lengths and starts as for qattn_cache: row i of a sequence's n new
+ * tokens is its token lens - n + i, and sees the tokens up to itself, that is
+ * the pages (places in the block table) 0 .. (lens - n + i) / page_size.  Rows of
+ * trees are not offered.  Strides as there, below 2^32 for tokens.
+ * ------------------------------------------------------------------------ */
+#define QW3_MAX_PICKS 65536
+
+/*
+ * qcache_bounds -- the bounds of the pages that new tokens have reached.
+ *   codes, scales: the cache of a layer
+ *   block_table [B, max_pages], lens [B], cu_q [B + 1] int32 or NULL (one new token each)
+ *   bounds, bound_scales: updated
+ * After qcache_write or qrope_write, with the lengths that count the new tokens.  For
+ * each page of a sequence that holds one of its last n tokens, over all the page's
+ * tokens below lens: mx_d = max c_d s, mn_d = min c_d s (float32 products),
+ * S = max_d max(|mx_d|, |mn_d|) / 127 (a float32 quotient), and mx_d / S and mn_d / S
+ * rounded to the nearest whole number, ties to even, at most 127 in size; zeros where S is zero.  A page
+ * whose keys hold an infinity or NaN gets S = NaN and zeros.
+ * The pages of two sequences are different, or hold the same tokens.
+ * Tq is the number of rows that cu_q speaks of.
+ * (Tq / page_size + 2 B) H < 2^26 (B H < 2^26 without cu_q), else QW3_ERR_SHAPE.
+ */
+qw3_status qcache_bounds(const void *codes, const float *scales, int32_t code_type, const int32_t *block_table,
+                         const int32_t *lens, const int32_t *cu_q, int8_t *bounds, float *bound_scales, int64_t B,
+                         int64_t max_pages, int64_t Tq, int64_t H, int64_t D, int64_t pages, int64_t page_size,
+                         void *hip_stream);
+
+/*
+ * qblock_select -- the pages that each row attends to, for each kv head.
+ *   q     [Tq, Hq, D] bf16, strided
+ *   picks [Tq, H, count] int32, written: places in the row's block table, ascending, -1
+ *         behind the last; rows of no sequence are not written
+ * A row that sees at most `count` pages gets all of them.  Otherwise the first `first`
+ * and the last `recent` (its own among them), and of the others the
+ * count - first - recent with the highest scores, of equal ones the lower place:
+ *   u_d = sum of max(q_d, 0), n_d = sum of min(q_d, 0) over the kv head's queries (exact,
+ *   then float32), both as int8 under one scale, max / 127, rounded as the bounds are;
+ *   score = float(sum_d u_d mx_d + n_d mn_d) * S   in float32: a whole number, one rounding.
+ * NaN is the highest score; a page that is not there comes last.  With NaN or an
+ * infinity in a row's queries its u and n are zeros.
+ * 1 <= count <= QW3_MAX_PICKS, first >= 0, recent >= 1, first + recent <= count,
+ * (Tq + B) H < 2^22, else QW3_ERR_SHAPE.
+ * Workspace, by the rules of qgemm_w3g128_smallM: none with at most 752 pages in the
+ * table's width for sequences of 4 new tokens and more on average, or with at most
+ * 4096; else the scores of at least 16 rows, 4 H (max_pages + 20) bytes each, 64 MiB
+ * where that is more.
+ */
+qw3_status qblock_select(const uint16_t *q, const int8_t *bounds, const float *bound_scales, const int32_t *block_table,
+                         const int32_t *lens, const int32_t *cu_q, int32_t *picks, int64_t B, int64_t max_pages, int64_t Tq,
+                         int64_t Hq, int64_t H, int64_t D, int64_t pages, int64_t page_size, int64_t count, int64_t first,
+                         int64_t recent, int64_t q_ts, int64_t q_hs, void *hip_stream);
+
+/*
+ * qattn_blocks -- attention of new tokens over the pages picked for them.
+ *   q     [Tq, Hq, D] bf16, strided; query head h reads kv head h / (Hq / H)
+ *   picks [Tq, H, count] int32: places in the row's block table, in any order; one
+ *         outside 0 .. max_pages - 1, or of a page behind the row, counts for nothing; one
+ *         named twice counts twice
+ *   out   [Tq, Hq, D] bf16, contiguous, written
+ * The formula of qattn_cache over the tokens of the picked pages up to the row's own;
+ * a row that sees nothing gets zeros.  fp32 scores and sums, the weights as two
+ * bf16 each.
+ * Workspace and counters, by the rules of qattn_cache: none with Tq H ceil(Hq / H / 16)
+ * at twice the number of CUs or above; else at most 2 x CUs parts of 16 (D + 2) floats.
+ * 1 <= count <= QW3_MAX_PICKS, count * page_size <= 2^30, (Tq + 4) H ceil(Hq / H / 16)
+ * < 2^26, else QW3_ERR_SHAPE.
+ */
+qw3_status qattn_blocks(const uint16_t *q, const void *codes, const float *scales, int32_t code_type,
+                        const int32_t *block_table, const int32_t *lens, const int32_t *cu_q, const int32_t *picks,
+                        uint16_t *out, int64_t B, int64_t max_pages, int64_t Tq, int64_t Hq, int64_t H, int64_t D,
+                        int64_t pages, int64_t page_size, int64_t count, int64_t q_ts, int64_t q_hs, float sm_scale,
+                        void *hip_stream);
+
 /* Text for a status code (static storage, never NULL). */
 const char *qstatus_str(qw3_status status);
 
