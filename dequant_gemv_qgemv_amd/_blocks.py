@@ -116,8 +116,9 @@ def qattn_blocks(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, blo
                  lens: torch.Tensor, picks: torch.Tensor, cu_q: torch.Tensor | None = None, sm_scale: float | None = None,
                  out: torch.Tensor | None = None) -> torch.Tensor:
     """Attention of new tokens q [Tq, Hq, D] (bf16) over the tokens, up to their own,
-    of the pages picks [Tq, H, count] (places in their sequence's block table in
-    any order, others than 0 .. its width - 1: none). Sequences as in qattn_cache."""
+    of the pages picks [Tq, H, count]: places in their sequence's block table in
+    any order, of which as many are read as the row sees pages (others than 0 ..
+    the table's width - 1: none). Sequences as in qattn_cache."""
     kind, dev, pages, heads, size, dim = _cache(codes, scales)
     qts, qhs = _rows(q, "q", _BF16, dev)
     rows, hq, d = shape = q.shape

@@ -76,30 +76,34 @@ __global__ __launch_bounds__(256) void bounds_kernel(BoundsArgs a) {
     if (item >= a.items) return;
     // Sequence b owns the items from start / page_size + 2 b on: room for its pages whatever its length.
     const int64_t room = a.max_pages << a.shift;
-    int b = item, n = 1, at = 0;
+    int b = item, n = 1, at = 0, len = 0;
     if (a.cu != nullptr) {
-        int first = 0, floor = 0;
+        int first = 0, end = 0, floor = 0;
         b = -1;
         for (int base = 0; base < a.B; base += 64) {
-            const int start =
-                max(floor, wave_scan_max(base + lane < a.B ? clamp_row(a.cu[min(base + lane, a.B - 1)], a.Tq) : 0));
+            // what a lane's sequence would need, read at once
+            const int mine = min(base + lane, a.B - 1), until = clamp_row(a.cu[mine + 1], a.Tq), length = a.lens[mine];
+            const int start = max(floor, wave_scan_max(base + lane < a.B ? clamp_row(a.cu[mine], a.Tq) : 0));
             const unsigned long long in = __ballot(base + lane < a.B && (start >> a.shift) + 2 * (base + lane) <= item);
             if (in == 0) break;
             const int i = __popcll(in) - 1;
-            b = base + i, first = __builtin_amdgcn_readlane(start, i);
+            b = base + i, first = __builtin_amdgcn_readlane(start, i), end = __builtin_amdgcn_readlane(until, i);
+            len = __builtin_amdgcn_readlane(length, i);
             floor = __builtin_amdgcn_readlane(start, 63);
             if (in != ~0ull) break;
         }
         b = uniform(b), first = uniform(first);
         if (b < 0) return;
-        n = clamp_row(a.cu[b + 1], a.Tq) - first;
+        n = uniform(end) - first;
         at = item - (first >> a.shift) - 2 * b;
+    } else {
+        len = a.lens[b];
     }
     if (n <= 0) return;
-    const int len = (int)max((int64_t)0, min((int64_t)a.lens[b], room));
+    len = uniform((int)max((int64_t)0, min((int64_t)len, room)));
     const int64_t col = (max(len - n, 0) >> a.shift) + (int64_t)at;
     if (col << a.shift >= len) return;
-    const uint32_t page = (uint32_t)a.table[b * a.max_pages + col];
+    const uint32_t page = (uint32_t)uniform(a.table[b * a.max_pages + col]);
     if (page >= (uint64_t)a.pages) return;
     const int count = min(1 << a.shift, len - (int)(col << a.shift));
 
@@ -111,39 +115,46 @@ __global__ __launch_bounds__(256) void bounds_kernel(BoundsArgs a) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = kNegInf;
     uint32_t nans = 0;
-    bool bad = false;
-    for (int r0 = lane / kPieces; r0 < count; r0 += 2 * kRows) {
-        uint4 w[2];
-        float s[2];
+    float worst = 0.0f;
+    constexpr int kAt = 32 / kRows;  // 32 rows on their way together, compared in twos
+    for (int base = 0; base < count; base += 32) {
+        uint4 w[kAt];
+        float s[kAt];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int r = min(r0 + k * kRows, count - 1);  // the last row again does no harm
+        for (int k = 0; k < kAt; ++k) {
+            const int r = min(base + k * kRows + lane / kPieces, count - 1);  // the last row again does no harm
             w[k] = *reinterpret_cast<const uint4 *>(codes + (int64_t)r * D);
             s[k] = scales[r];
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const uint32_t d[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-            bad |= !(fabsf(s[k]) < __builtin_huge_valf());
+        for (int k = 0; k < kAt; k += 2) {
+            if (base + k * kRows >= count) break;
+            const uint32_t d[2][4] = {{w[k].x, w[k].y, w[k].z, w[k].w}, {w[k + 1].x, w[k + 1].y, w[k + 1].z, w[k + 1].w}};
+            worst += s[k] * 0.0f + s[k + 1] * 0.0f;  // stays 0 unless a scale is not finite
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float f[4];
-                if (E4M3) {
-                    nans |= ((d[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                    f[0] = __builtin_amdgcn_cvt_f32_fp8(d[i], 0), f[1] = __builtin_amdgcn_cvt_f32_fp8(d[i], 1);
-                    f[2] = __builtin_amdgcn_cvt_f32_fp8(d[i], 2), f[3] = __builtin_amdgcn_cvt_f32_fp8(d[i], 3);
-                } else {
-                    f[0] = byte_f32<0>(d[i]), f[1] = byte_f32<1>(d[i]), f[2] = byte_f32<2>(d[i]), f[3] = byte_f32<3>(d[i]);
+                float f[2][4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (E4M3) {
+                        nans |= ((d[j][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                        const f2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8(d[j][i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(d[j][i], true);
+                        f[j][0] = lo[0], f[j][1] = lo[1], f[j][2] = hi[0], f[j][3] = hi[1];
+                    } else {
+                        f[j][0] = byte_f32<0>(d[j][i]), f[j][1] = byte_f32<1>(d[j][i]);
+                        f[j][2] = byte_f32<2>(d[j][i]), f[j][3] = byte_f32<3>(d[j][i]);
+                    }
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float x = f[e] * s[k];
-                    v[4 * i + e] = fmaxf(v[4 * i + e], x);
-                    v[16 + 4 * i + e] = fmaxf(v[16 + 4 * i + e], -x);
+                    const float x = f[0][e] * s[k], y = f[1][e] * s[k + 1];
+                    v[4 * i + e] = fmaxf(fmaxf(x, y), v[4 * i + e]);
+                    v[16 + 4 * i + e] = fmaxf(fmaxf(-x, -y), v[16 + 4 * i + e]);
                 }
             }
         }
     }
+    const bool bad = !(worst == 0.0f);
     // lanes 0..31 keep the maxima, the others those of the opposites; then the even
     // sixteens of lanes the first 8 channels, the odd ones the last
 #pragma unroll
@@ -196,100 +207,109 @@ __device__ __forceinline__ uint32_t key_of(float score) {
 }
 constexpr uint32_t kNoPage = ~0u;  // in the place of a page's step
 
-// The w of rows first .. first + n - 1 for kv head h as int8 [kRows][2 D] in LDS, by D / 8
-// threads for a row.
-template <int D, int kRows>
-__device__ __forceinline__ void query_codes(const SelectArgs &a, int first, int n, int h, uint8_t *w) {
-    constexpr int kLanes = D / 8;
-    const int r = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
-    if (r >= kRows) return;
-    double u[8], l[8];
+// The w of row `row` for kv head h as int8 [2 D] in LDS, by one wave, D / 64 channels
+// of every query a lane.
+template <int D>
+__device__ __forceinline__ void query_codes(const SelectArgs &a, int row, int h, uint8_t *w) {
+    constexpr int kPer = D / 64;
+    const int lane = threadIdx.x & 63;
+    double u[kPer] = {}, l[kPer] = {};
+    const uint16_t *q = a.q + (int64_t)row * a.q_ts + (int64_t)h * a.G * a.q_hs + kPer * lane;
+    // in 64 bits: exact for all that bf16 adds up to, so the order does not matter
+#pragma unroll 8
+    for (int g = 0; g < a.G; ++g) {
+        const uint32_t d = kPer == 2 ? *reinterpret_cast<const uint32_t *>(q + g * a.q_hs) : (uint32_t)q[g * a.q_hs] << 16;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = l[i] = 0.0;
-    if (r < n) {
-        const uint16_t *q = a.q + (int64_t)(first + r) * a.q_ts + (int64_t)h * a.G * a.q_hs + 8 * c;
-        // in 64 bits: exact for all that bf16 adds up to, so the order does not matter
-#pragma unroll 4
-        for (int g = 0; g < a.G; ++g) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(q + g * a.q_hs);
-            const uint32_t d[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float f = __uint_as_float(i & 1 ? d[i / 2] & 0xffff0000u : d[i / 2] << 16);
-                // a NaN into both sums
-                u[i] += f < 0.0f ? 0.0 : (double)f;
-                l[i] += f > 0.0f ? 0.0 : (double)f;
-            }
+        for (int i = 0; i < kPer; ++i) {
+            const float f = __uint_as_float(kPer == 2 && i == 0 ? d << 16 : d & 0xffff0000u);
+            // a NaN into both sums
+            u[i] += f < 0.0f ? 0.0 : (double)f;
+            l[i] += f > 0.0f ? 0.0 : (double)f;
         }
     }
-    float x[16];
+    float x[2][kPer];
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[i] = (float)u[i], x[8 + i] = (float)l[i];
-        top = max(top, max(__float_as_uint(x[i]) & 0x7fffffffu, __float_as_uint(x[8 + i]) & 0x7fffffffu));
+    for (int i = 0; i < kPer; ++i) {
+        x[0][i] = (float)u[i], x[1][i] = (float)l[i];
+        top = max(top, max(__float_as_uint(x[0][i]) & 0x7fffffffu, __float_as_uint(x[1][i]) & 0x7fffffffu));
     }
-#pragma unroll
-    for (int m = kLanes / 2; m >= 1; m /= 2) top = max(top, (uint32_t)__shfl_xor((int)top, m, 64));
+    top = (uint32_t)wave_max((int)top);
     const float s = top < 0x7f800000u ? __uint_as_float(top) / 127.0f : 0.0f;
-    uint32_t out[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float y[4];
+    for (int k = 0; k < 2; ++k) {
+        float y[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = s > 0.0f ? fminf(fmaxf(x[4 * i + e] / s, -127.0f), 127.0f) : 0.0f;
-        out[i] = codes4<false>(y);
+        for (int i = 0; i < kPer; ++i) y[i] = s > 0.0f ? fminf(fmaxf(x[k][i] / s, -127.0f), 127.0f) : 0.0f;
+        const uint32_t c = codes4<false>({y[0], y[1], 0.0f, 0.0f});
+        if (kPer == 2)
+            *reinterpret_cast<uint16_t *>(w + k * D + 2 * lane) = (uint16_t)c;
+        else
+            w[k * D + lane] = (uint8_t)c;
     }
-    *reinterpret_cast<uint2 *>(w + r * 2 * D + 8 * c) = make_uint2(out[0], out[1]);
-    *reinterpret_cast<uint2 *>(w + r * 2 * D + D + 8 * c) = make_uint2(out[2], out[3]);
 }
 
-// Keys of the pages 16 p, p = p0, p0 + stride .. below `pages16`, by one wave, 16 pages
-// with the kRows rows' w at a time: the matrix unit's rows are pages, its columns rows.
+// The page numbers of a wave's 64 pages from p on, one for each lane.
+__device__ __forceinline__ uint32_t page_at(const SelectArgs &a, const int32_t *table, int p) {
+    return a.max_pages == 0 ? kNoPage : (uint32_t)table[min((int64_t)p + (threadIdx.x & 63), a.max_pages - 1)];
+}
+
+// Keys of the pages from p on below `pages`, 64 for each step of `stride` pages, by one wave;
+// page: page_at(p).  The matrix unit's rows are 16 pages, its columns the kRows rows' w,
+// which prepare() sees to, once the first pages are on their way.
 // to(row, page): where the keys of 4 pages go, for the first n rows.
-template <int D, int kRows, class To>
-__device__ __forceinline__ void score_pages(const SelectArgs &a, int b, int h, int p0, int stride, int pages, int n,
-                                            const uint8_t *w, To to) {
+template <int D, int kRows, class Prepare, class To>
+__device__ __forceinline__ void score_pages(const SelectArgs &a, const int32_t *table, int h, int p, int stride, int pages, int n,
+                                            uint32_t page, const uint8_t *w, Prepare prepare, To to) {
     constexpr int kSteps = 2 * D / 64;
     const int lane = threadIdx.x & 63, col = lane & 15, quarter = lane >> 4;
-    const int32_t *table = a.table + b * a.max_pages;
+    uint32_t step;
+    i4_t kf[4][kSteps];
+    auto load = [&]() {  // one page's step a lane, then the bounds of 64 pages on their way together
+        step = kNoPage;
+        if (page < (uint64_t)a.pages) {
+            step = __float_as_uint(a.steps[(int64_t)page * a.H + h]);
+            if (step == kNoPage) step = 0x7fc00000u;
+        } else {
+            page = kNoPage;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t id = (uint32_t)__shfl((int)page, 16 * j + col, 64);
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) kf[j][k] = i4_t{};
+            if (id != kNoPage && p + 16 * j < pages) {
+                const int8_t *at = a.bounds + ((int64_t)id * a.H + h) * 2 * D + 16 * quarter;
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) kf[j][k] = *reinterpret_cast<const i4_t *>(at + 64 * k);
+            }
+        }
+    };
+    if (p < pages) load();
+    prepare();
     i4_t wf[kSteps];
 #pragma unroll
     for (int k = 0; k < kSteps; ++k)
         wf[k] = *reinterpret_cast<const i4_t *>(w + (kRows == 1 ? 0 : col) * 2 * D + 64 * k + 16 * quarter);
-    // two of them at a time, so that one's loads are on their way beside the other's
-    for (int p = 16 * p0; p < pages; p += 32 * stride) {
-        i4_t kf[2][kSteps];
-        uint32_t step[2];
+    while (p < pages) {
+        const int at = p;
+        p += stride;
+        if (p < pages) page = page_at(a, table, p);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t page = (uint32_t)table[min(p + 16 * stride * j + col, pages - 1)];
-            step[j] = kNoPage;
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k) kf[j][k] = i4_t{};
-            if (page < (uint64_t)a.pages) {
-                const int64_t at = (int64_t)page * a.H + h;
-#pragma unroll
-                for (int k = 0; k < kSteps; ++k)
-                    kf[j][k] = *reinterpret_cast<const i4_t *>(a.bounds + at * 2 * D + 64 * k + 16 * quarter);
-                step[j] = __float_as_uint(a.steps[at]);
-                if (step[j] == kNoPage) step[j] = 0x7fc00000u;
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int at = p + 16 * stride * j;
+        for (int j = 0; j < 4; ++j) {
             i4_t sum = {};
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) sum = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[j][k], wf[k], sum, 0, 0, 0);
             uint32_t key[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const uint32_t s = (uint32_t)__shfl((int)step[j], 4 * quarter + r, 64);
+                const uint32_t s = (uint32_t)__shfl((int)step, 16 * j + 4 * quarter + r, 64);
                 key[r] = s == kNoPage ? 0u : key_of((float)sum[r] * __uint_as_float(s));
             }
-            if (col < n && at < pages) *reinterpret_cast<uint4 *>(to(col, at + 4 * quarter)) = make_uint4(key[0], key[1], key[2], key[3]);
+            if (col < n && at + 16 * j < pages)
+                *reinterpret_cast<uint4 *>(to(col, at + 16 * j + 4 * quarter)) = make_uint4(key[0], key[1], key[2], key[3]);
         }
+        if (p < pages) load();
     }
 }
 
@@ -303,73 +323,104 @@ __device__ __forceinline__ void group_sync() {
     }
 }
 
-// What T threads need to pick: a histogram of 256, and sums that waves exchange.
+// What T threads need to pick: a histogram of 256 for each byte, and what waves exchange.
+template <int T>
 struct PickSpace {
-    int bins[256];
-    int waves[16], bin, left;
+    int bins[T > 64 ? 4 : 1][256];
+    uint32_t waves[2][T / 64];
 };
 
 // A row's picks out of `seen` pages, by T threads whose number among them is tid.
 // All if there are at most count; else the first ones, the last ones, and of those
-// between the `left` with the largest keys: the key that is the left-th largest is
-// found by its bytes, from the highest on, in counts of what has the bytes found so far;
-// then the pages are gone through in order, and of those with that key the first are taken.
+// between the `left` with the largest keys.  The left-th largest key is found by 8 bits at
+// a time, below the bits that all keys have in common, in counts of the keys that have the
+// bits found so far; then the pages are gone through in order, and of those with that key
+// the first are taken.
 template <int T>
-__device__ __forceinline__ void pick(const SelectArgs &a, const uint32_t *keys, int seen, int32_t *out, PickSpace &space, int tid) {
+__device__ __forceinline__ void pick(const SelectArgs &a, const uint32_t *keys, int seen, int32_t *out, PickSpace<T> &space, int tid) {
     if (seen <= a.count) {
         for (int i = tid; i < a.count; i += T) out[i] = i < seen ? i : -1;
         return;
     }
-    const int lane = tid & 63, lo = a.first, hi = seen - a.recent;
+    const int lane = tid & 63, wave = tid >> 6, lo = a.first, hi = seen - a.recent;
     int left = a.count - a.first - a.recent;
-    uint32_t prefix = 0, mask = 0;
-    for (int shift = 24; shift >= 0 && left > 0; shift -= 8) {
-        group_sync<T>();
-        for (int i = tid; i < 256; i += T) space.bins[i] = 0;
-        group_sync<T>();
-        for (int i = lo + tid; i < hi; i += T) {
-            const uint32_t key = keys[i];
-            if ((key & mask) == prefix) atomicAdd(&space.bins[(key >> shift) & 255], 1);
-        }
-        group_sync<T>();
-        if (tid < 64) {  // lane l has the bins 255 - 4 l and the three below
-            int c[4], sum = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) c[j] = space.bins[255 - 4 * lane - j], sum += c[j];
-            const int upto = wave_scan(sum);
-            int before = upto - sum;
-            if (before < left && left <= upto) {
-                int j = 0;
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    if (j == k && before + c[k] < left) before += c[k], ++j;
-                space.bin = 255 - 4 * lane - j, space.left = left - before;
-            }
-        }
-        group_sync<T>();
-        prefix |= (uint32_t)space.bin << shift, mask |= 255u << shift;
-        left = space.left;
-    }
-    // place: of the next pick; equals: how many with the key have been passed
     const bool none = left <= 0;
+    // a few keys are kept, more are read anew in each pass
+    constexpr int kHeld = 4;
+    const bool held = hi - lo <= kHeld * T;
+    uint32_t kept[kHeld];
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) kept[j] = keys[min(lo + tid + T * j, hi - 1)];
+    auto each = [&](auto f) {
+        if (held) {
+#pragma unroll
+            for (int j = 0; j < kHeld; ++j)
+                if (lo + tid + T * j < hi) f(kept[j]);
+        } else {
+            for (int i = lo + tid; i < hi; i += T) f(keys[i]);
+        }
+    };
+    uint32_t prefix = 0, mask = 0;
+    if (!none) {
+        uint32_t all = ~0u, any = 0;
+        each([&](uint32_t key) { all &= key, any |= key; });
+#pragma unroll
+        for (int m = 32; m >= 1; m /= 2) all &= (uint32_t)__shfl_xor((int)all, m, 64), any |= (uint32_t)__shfl_xor((int)any, m, 64);
+        if constexpr (T > 64) {
+            if (lane == 0) space.waves[0][wave] = all, space.waves[1][wave] = any;
+            for (int i = tid; i < 4 * 256; i += T) space.bins[0][i] = 0;
+            __syncthreads();
+#pragma unroll
+            for (int x = 0; x < T / 64; ++x) all &= space.waves[0][x], any |= space.waves[1][x];
+        }
+        int shift = 32 - (all == any ? 32 : __builtin_clz(all ^ any));  // of the lowest bit found so far
+        mask = shift == 32 ? 0u : ~0u << shift, prefix = all & mask;
+        for (int pass = 0; shift > 0; ++pass) {
+            const int width = min(shift, 8);
+            shift -= width;
+            int *bins = space.bins[T > 64 ? pass : 0];
+            if constexpr (T == 64) {
+                group_sync<T>();
+                *reinterpret_cast<int4 *>(bins + 4 * lane) = make_int4(0, 0, 0, 0);
+                group_sync<T>();
+            }
+            each([&](uint32_t key) {
+                if ((key & mask) == prefix) atomicAdd(bins + (key >> shift & ((1u << width) - 1)), 1);
+            });
+            group_sync<T>();
+            // by every wave: lane l has the bins 255 - 4 l and the three below
+            const int4 c = *reinterpret_cast<const int4 *>(bins + 252 - 4 * lane);
+            const int sum = c.x + c.y + c.z + c.w, upto = wave_scan(sum);
+            int before = upto - sum, bin = 255 - 4 * lane, count = c.w;
+            if (before + count < left) before += count, --bin, count = c.z;
+            if (before + count < left) before += count, --bin, count = c.y;
+            if (before + count < left) before += count, --bin, count = c.x;
+            const int owner = uniform(__builtin_ctzll(__ballot(upto >= left)));
+            bin = __builtin_amdgcn_readlane(bin, owner);
+            left -= __builtin_amdgcn_readlane(before, owner);
+            count = __builtin_amdgcn_readlane(count, owner);
+            prefix |= (uint32_t)bin << shift, mask |= ((1u << width) - 1) << shift;
+            if (count == left) break;  // all keys with these bits are taken
+        }
+    }
+    // place: of the next pick; equals: how many with the bits have been passed
     int place = a.first, equals = 0;
     for (int i = tid; i < a.first; i += T) out[i] = i;
-    for (int i0 = lo; i0 < hi; i0 += T) {
-        const int i = i0 + tid;
-        const uint32_t key = i < hi ? keys[i] : 0;
-        const bool more = !none && i < hi && key > prefix, equal = !none && i < hi && key == prefix;
+    auto take = [&](int i, uint32_t key) {  // T pages in order, of which the thread has page i
+        key &= mask;
+        const bool more = i < hi && key > prefix, equal = i < hi && key == prefix;
         const unsigned long long m = __ballot(more), e = __ballot(equal), below = (1ull << lane) - 1;
         int mores = __popcll(m), same = __popcll(e);  // of the wave, then of all
         int m_before = __popcll(m & below), e_before = __popcll(e & below);
         if constexpr (T > 64) {
-            group_sync<T>();
-            if (lane == 0) space.waves[tid >> 6] = mores << 16 | same;
-            group_sync<T>();
+            __syncthreads();
+            if (lane == 0) space.waves[0][wave] = mores << 16 | same;
+            __syncthreads();
             mores = same = 0;
 #pragma unroll
             for (int x = 0; x < T / 64; ++x) {
-                const int s = space.waves[x];
-                if (x < tid >> 6) m_before += s >> 16, e_before += s & 0xffff;
+                const int s = (int)space.waves[0][x];
+                if (x < wave) m_before += s >> 16, e_before += s & 0xffff;
                 mores += s >> 16, same += s & 0xffff;
             }
         }
@@ -377,6 +428,13 @@ __device__ __forceinline__ void pick(const SelectArgs &a, const uint32_t *keys, 
         if (more || (equal && equals + e_before < left)) out[place + m_before + e_taken] = i;
         place += mores + min(equals + same, left) - taken;
         equals += same;
+    };
+    if (held) {
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j)
+            if (lo + T * j < hi && !none) take(lo + tid + T * j, kept[j]);
+    } else {
+        for (int i0 = lo; i0 < hi && !none; i0 += T) take(i0 + tid, keys[min(i0 + tid, hi - 1)]);
     }
     for (int i = tid; i < a.recent; i += T) out[a.count - a.recent + i] = hi + i;
 }
@@ -385,22 +443,27 @@ __device__ __forceinline__ void pick(const SelectArgs &a, const uint32_t *keys, 
 __device__ __forceinline__ int pages_seen(const SelectArgs &a, int pos) { return pos < 0 ? 0 : (pos >> a.shift) + 1; }
 
 // One row and kv head: scores and picks in one workgroup, the keys in LDS.
-template <int D, int T>
-__global__ __launch_bounds__(T) void select_row_kernel(SelectArgs a) {
+template <int D>
+__global__ __launch_bounds__(256) void select_row_kernel(SelectArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint32_t keys[];
     __shared__ __attribute__((aligned(16))) uint8_t w[2 * D];
-    __shared__ PickSpace space;
-    const int t = (int)(blockIdx.x / (uint32_t)a.H), h = (int)blockIdx.x - t * a.H;
+    __shared__ PickSpace<256> space;
+    const int t = (int)(blockIdx.x / (uint32_t)a.H), h = (int)blockIdx.x - t * a.H, wave = uniform((int)threadIdx.x >> 6);
+    uint32_t page = a.cu ? kNoPage : page_at(a, a.table + t * a.max_pages, 64 * wave);  // beside the length
     const Row row = find_row(a.cu, a.lens, a.B, a.Tq, a.max_pages << a.shift, t);
     if (row.b < 0) return;
     const int seen = pages_seen(a, row.pos);
     if (seen > a.count) {
-        query_codes<D, 1>(a, t, 1, h, w);
-        __syncthreads();
-        score_pages<D, 1>(a, row.b, h, uniform((int)threadIdx.x >> 6), T / 64, seen, 1, w, [&](int, int p) { return keys + p; });
+        const int32_t *table = a.table + row.b * a.max_pages;
+        if (a.cu) page = page_at(a, table, 64 * wave);
+        auto prepare = [&]() {
+            if (wave == 3) query_codes<D>(a, t, h, w);  // the wave with the fewest pages
+            __syncthreads();
+        };
+        score_pages<D, 1>(a, table, h, 64 * wave, 256, seen, 1, page, w, prepare, [&](int, int p) { return keys + p; });
         __syncthreads();
     }
-    pick<T>(a, keys, seen, a.picks + ((int64_t)t * a.H + h) * a.count, space, threadIdx.x);
+    pick<256>(a, keys, seen, a.picks + ((int64_t)t * a.H + h) * a.count, space, threadIdx.x);
 }
 
 // The rank-th tile of 16 rows: sequence b owns the ranks from start / 16 + b on (room
@@ -430,56 +493,65 @@ __device__ __forceinline__ Tile find_tile(const SelectArgs &a, int rank) {
 }
 
 // 16 rows of a sequence and a kv head: the pages' bounds are read once for all of
-// them, and each wave picks for 4.
+// them, and each wave picks for one.
 template <int D>
-__global__ __launch_bounds__(256) void select_tile_kernel(SelectArgs a) {
+__global__ __launch_bounds__(1024) void select_tile_kernel(SelectArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint32_t keys[];
     __shared__ __attribute__((aligned(16))) uint8_t w[16 * 2 * D];
-    __shared__ PickSpace space[4];
+    __shared__ PickSpace<64> space[16];
     const int rank = (int)(blockIdx.x / (uint32_t)a.H), h = (int)blockIdx.x - rank * a.H;
     const int wave = uniform((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
     const Tile tile = find_tile(a, rank);
     if (tile.n <= 0) return;
     const int most = pages_seen(a, tile.pos + tile.n - 1);
     if (most > a.count) {
-        query_codes<D, 16>(a, tile.first, tile.n, h, w);
-        __syncthreads();
-        score_pages<D, 16>(a, tile.b, h, wave, 4, most, tile.n, w, [&](int r, int p) { return keys + r * a.pitch + p; });
+        const int32_t *table = a.table + tile.b * a.max_pages;
+        auto prepare = [&]() {
+            if (wave < tile.n) query_codes<D>(a, tile.first + wave, h, w + wave * 2 * D);
+            __syncthreads();
+        };
+        score_pages<D, 16>(a, table, h, 64 * wave, 1024, most, tile.n, page_at(a, table, 64 * wave), w, prepare, [&](int r, int p) { return keys + r * a.pitch + p; });
         __syncthreads();
     }
-    for (int r = wave; r < tile.n; r += 4)
-        pick<64>(a, keys + r * a.pitch, pages_seen(a, tile.pos + r), a.picks + ((int64_t)(tile.first + r) * a.H + h) * a.count,
-                 space[wave], lane);
+    if (wave < tile.n)
+        pick<64>(a, keys + wave * a.pitch, pages_seen(a, tile.pos + wave),
+                 a.picks + ((int64_t)(tile.first + wave) * a.H + h) * a.count, space[wave], lane);
 }
 
-// Scores alone, into memory: 16 rows of a sequence, a kv head and every
-// gridDim.y-th 64 pages.
+// Scores alone, into memory: 16 rows of a sequence, a kv head and 256 of every
+// 256 gridDim.y pages.
 template <int D>
 __global__ __launch_bounds__(256) void score_kernel(SelectArgs a) {
     __shared__ __attribute__((aligned(16))) uint8_t w[16 * 2 * D];
     const int rank = (int)(blockIdx.x / (uint32_t)a.H), h = (int)blockIdx.x - rank * a.H;
+    const int wave = uniform((int)threadIdx.x >> 6);
+    const int p = 256 * (int)blockIdx.y + 64 * wave;
+    uint32_t page = a.cu ? kNoPage : page_at(a, a.table + rank * a.max_pages, p);  // beside the length
     Tile tile = find_tile(a, rank);
     // of the tile's rows those of this launch
     const int skip = max(a.t0 - tile.first, 0);
     tile.n = min(tile.n, a.t0 + a.rows - tile.first) - skip, tile.first += skip, tile.pos += skip;
     if (tile.n <= 0) return;
     const int most = pages_seen(a, tile.pos + tile.n - 1);
-    if (most <= a.count) return;
-    query_codes<D, 16>(a, tile.first, tile.n, h, w);
-    __syncthreads();
-    const int wave = uniform((int)threadIdx.x >> 6);
-    score_pages<D, 16>(a, tile.b, h, (int)blockIdx.y * 4 + wave, 4 * (int)gridDim.y, most, tile.n, w,
-                       [&](int r, int p) { return a.keys + ((int64_t)(tile.first - a.t0 + r) * a.H + h) * a.pitch + p; });
+    if (most <= a.count || 256 * (int)blockIdx.y >= most) return;
+    const int32_t *table = a.table + tile.b * a.max_pages;
+    if (a.cu) page = page_at(a, table, p);
+    auto prepare = [&]() {
+        for (int r = 3 - wave; r < tile.n; r += 4) query_codes<D>(a, tile.first + r, h, w + r * 2 * D);
+        __syncthreads();
+    };
+    score_pages<D, 16>(a, table, h, p, 256 * (int)gridDim.y, most, tile.n, page, w, prepare,
+                       [&](int r, int k) { return a.keys + ((int64_t)(tile.first - a.t0 + r) * a.H + h) * a.pitch + k; });
 }
 
 template <int T>
 __global__ __launch_bounds__(T) void pick_kernel(SelectArgs a) {
-    __shared__ PickSpace space;
+    __shared__ PickSpace<T> space;
     const int r = (int)(blockIdx.x / (uint32_t)a.H), h = (int)blockIdx.x - r * a.H, t = a.t0 + r;
     const Row row = find_row(a.cu, a.lens, a.B, a.Tq, a.max_pages << a.shift, t);
     if (row.b < 0) return;
-    pick<T>(a, a.keys + ((int64_t)r * a.H + h) * a.pitch, pages_seen(a, row.pos), a.picks + ((int64_t)t * a.H + h) * a.count, space,
-            threadIdx.x);
+    pick<T>(a, a.keys + ((int64_t)r * a.H + h) * a.pitch, pages_seen(a, row.pos), a.picks + ((int64_t)t * a.H + h) * a.count,
+            space, threadIdx.x);
 }
 
 // -------------------------------------------------------------- attention --
@@ -489,125 +561,113 @@ struct BlocksArgs {
     const float *scales;
     const int32_t *table, *lens, *cu, *picks;
     uint16_t *o;
-    float *part;  // split: where workgroups leave their parts, ...
-    int *counts;  // ... how many of an item have, ...
+    float *part;  // where workgroups leave their parts of an item, ...
+    int *counts;  // ... how many have, ...
     int *clear;   // ... and the next call's counters
     int64_t q_ts, q_hs, max_pages, pages;
-    int B, Tq, Hq, H, G, shift, count, parts, blocks;  // blocks: of 16 of a kv head's queries
+    int B, Tq, Hq, H, G, shift, count, blocks, parts;  // blocks: of 16 of a kv head's queries
     float scale;                                       // sm_scale log2(e)
 };
 
-// An item is a row, a kv head and 16 of its queries: 16 columns of the matrix unit's
-// result.  Its keys are the picked pages' in groups of 16, which lie in one page
-// whatever its size; a wave takes two groups at a time, a step.  W waves of a
-// workgroup, and the workgroups of `parts`, take an item's steps in turn.
-// W = 4: one item a workgroup, joined in LDS, and over the parts by the one that
-// finishes last; W = 1: an item for each wave, the same kv head of neighbouring rows.
-template <int D, bool E4M3, int W>
-__global__ __launch_bounds__(256, 2) void attn_blocks_kernel(BlocksArgs a) {
-    constexpr int R = 16, kPad = D + 4;
-    constexpr int kPieces = D / 16, kVLoads = D / 32;
-    constexpr int kTurn = 4 * 32 * D, kJoin = W == 4 ? 4 * R * kPad * 4 : 0;
-    __shared__ __attribute__((aligned(1024))) char lds[kTurn > kJoin ? kTurn : kJoin];
-    __shared__ float stat[2][4][R];
-    __shared__ int arrived;
-    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), quarter = lane >> 4, col = lane & 15;
-    if (W == 4 && a.parts > 1 && blockIdx.x == 0) clear_next<256>(a.clear);
+// The pages that a row reads: entries of its picks, no more than it sees.
+__device__ __forceinline__ int entries(const BlocksArgs &a, int pos) { return pos < 0 || a.pages == 0 ? 0 : min(a.count, (pos >> a.shift) + 1); }
 
-    const int part = W == 4 ? (int)(blockIdx.x % (uint32_t)a.parts) : 0;
-    const int item = W == 4 ? (int)(blockIdx.x / (uint32_t)a.parts) : (int)blockIdx.x;
-    const int per_row = a.H * a.blocks;
-    const int t = item / per_row * (4 / W) + (W == 1 ? wave : 0), hb = item % per_row;
-    const int h = hb / a.blocks, g0 = (hb - h * a.blocks) * R, rows = min(R, a.G - g0);
-    Row row = {-1, 0, 0};
-    if (W == 4 || t < a.Tq) row = find_row(a.cu, a.lens, a.B, a.Tq, a.max_pages << a.shift, t);
-    if (row.b < 0) return;  // with W = 4 all waves, and all parts
-    const int pos = row.pos;
-    const int32_t *table = a.table + row.b * a.max_pages, *picks = a.picks + ((int64_t)t * a.H + h) * a.count;
-    const int mask = (1 << a.shift) - 1;
+// An item is a row, a kv head and up to 16 of its queries: 16 columns of the matrix
+// unit's result.  Its keys are the picked pages' in groups of 16, which lie in one
+// page whatever its size; a wave takes two groups at a time, a step.  What a wave
+// has of an item: the steps' pages, the codes and scales on their way, and the sums.
+template <int D, bool E4M3>
+struct Walk {
+    static constexpr int kPieces = D / 16, kVLoads = D / 32;
+    const BlocksArgs &a;
+    char *turn;  // the wave's V tile in LDS: row r, 16-byte piece c at place c ^ f(r), so that the turning reads spread over the banks
+    int lane, quarter, col;
+    // the item: its kv head, the row's position and number of entries; step s has groups g0 + stride s and the next
+    int h, pos, groups, g0, stride, steps;
+    const int32_t *table, *picks;
+    int ids, bases;  // of 32 steps: lane 2 s + g has of group g of step s the page (-1: none that the row sees) and its first token's position
+    uint4 k[2][D / 64], v[kVLoads];
+    float4 ks[2], vs[2];
+    bf8_t qf[D / 32];
+    f4_t acc[D / 16];
+    float m, l;
 
-    // Steps of the wave: first, first + stride, ...; 32 of them at a time lane 2 s + g has of
-    // group g of step s the page (-1: none that the row sees) and its first token's position.
-    const int groups = a.count << (a.shift - 4), stride = W * a.parts, first = part * W + (W == 4 ? wave : 0);
-    const int steps = first < (groups + 1) / 2 ? ((groups + 1) / 2 - first + stride - 1) / stride : 0;
-    int ids = -1, bases = 0;
-    auto look_up = [&](int s0) {
-        const int64_t g = 2 * (first + (int64_t)(s0 + (lane >> 1)) * stride) + (lane & 1);
+    __device__ __forceinline__ Walk(const BlocksArgs &args, char *lds) : a(args), turn(lds) {
+        lane = threadIdx.x & 63, quarter = lane >> 4, col = lane & 15;
+        steps = 0;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) k[g][c] = make_uint4(0, 0, 0, 0);
+            ks[g] = vs[g] = make_float4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int c = 0; c < kVLoads; ++c) v[c] = make_uint4(0, 0, 0, 0);
+    }
+
+    __device__ __forceinline__ static int place(int r) { return D == 128 ? (r >> 1) & 7 : (r >> 2) & 3; }
+
+    // The lane's entry of the 32 steps from s0 on, and what it says once the row is known.
+    __device__ __forceinline__ int entry(int s0) const {
+        const int64_t g = (g0 + (int64_t)(s0 + (lane >> 1)) * stride + (lane & 1)) >> (a.shift - 4);
+        return picks[min(g, (int64_t)a.count - 1)];
+    }
+    __device__ __forceinline__ void look_up(int s0, int pick) {
+        const int64_t g = g0 + (int64_t)(s0 + (lane >> 1)) * stride + (lane & 1);
         ids = -1, bases = 0;
         if (g < groups) {
-            const int pick = picks[g >> (a.shift - 4)];
-            const int64_t base = ((int64_t)pick << a.shift) + ((g << 4) & mask);
+            const int64_t base = ((int64_t)pick << a.shift) + ((g << 4) & ((1 << a.shift) - 1));
             if (pick >= 0 && pick < a.max_pages && base <= pos) {
                 const int page = table[pick];
                 if ((uint32_t)page < (uint64_t)a.pages) ids = page, bases = (int)base;
             }
         }
-    };
-    if (steps > 0) look_up(0);
+    }
+    __device__ __forceinline__ int page_of(int s, int g) const { return __builtin_amdgcn_readlane(ids, 2 * (s & 31) + g); }
+    __device__ __forceinline__ int base_of(int s, int g) const { return __builtin_amdgcn_readlane(bases, 2 * (s & 31) + g); }
 
-    struct Stage {
-        uint4 k[2][D / 64], v[kVLoads];
-        float4 ks[2], vs[2];
-    } st = {};
-    auto page_of = [&](int s, int g) { return __builtin_amdgcn_readlane(ids, 2 * (s & 31) + g); };
-    auto base_of = [&](int s, int g) { return __builtin_amdgcn_readlane(bases, 2 * (s & 31) + g); };
-    const int64_t page_rows = (int64_t)(2 * a.H) << a.shift, to_v = (int64_t)a.H << a.shift;
-    auto fetch = [&](int s) {
+    __device__ __forceinline__ void fetch(int s) {
+        const int64_t page_rows = (int64_t)(2 * a.H) << a.shift, to_v = (int64_t)a.H << a.shift;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            const int page = page_of(s, g);
-            if (page < 0) continue;
-            const int64_t at = page * page_rows + ((int64_t)h << a.shift) + (base_of(s, g) & mask);
+            const int page = max(page_of(s, g), 0);  // one that does not exist reads page 0: hidden below
+            const int64_t at = uniform(page * page_rows + ((int64_t)h << a.shift) + (base_of(s, g) & ((1 << a.shift) - 1)));
             const uint8_t *kp = a.codes + at * D, *vp = kp + to_v * D;
             const float *sp = a.scales + at;
             // a uniform base and a lane's offset
             uint32_t ko = col * D + quarter * 16, vo = lane * 16, so = 4 * quarter;
             asm("" : "+v"(ko), "+v"(vo), "+v"(so));
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) st.k[g][c] = *reinterpret_cast<const uint4 *>(kp + ko + 64 * c);
+            for (int c = 0; c < D / 64; ++c) k[g][c] = *reinterpret_cast<const uint4 *>(kp + ko + 64 * c);
 #pragma unroll
-            for (int c = 0; c < kVLoads / 2; ++c)
-                st.v[g * (kVLoads / 2) + c] = *reinterpret_cast<const uint4 *>(vp + vo + 1024 * c);
-            st.ks[g] = *reinterpret_cast<const float4 *>(sp + so);
-            st.vs[g] = *reinterpret_cast<const float4 *>(sp + to_v + so);
+            for (int c = 0; c < kVLoads / 2; ++c) v[g * (kVLoads / 2) + c] = *reinterpret_cast<const uint4 *>(vp + vo + 1024 * c);
+            ks[g] = *reinterpret_cast<const float4 *>(sp + so);
+            vs[g] = *reinterpret_cast<const float4 *>(sp + to_v + so);
         }
-    };
-
-    // the queries, as B operands with the channels in the order of K's pieces
-    bf8_t qf[D / 32];
-    {
-        const uint16_t *qp = a.q + (int64_t)t * a.q_ts + (h * a.G + g0 + min(col, rows - 1)) * a.q_hs;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-            qf[i] = *reinterpret_cast<const bf8_t *>(qp + 16 * (quarter + 4 * (i / 2)) + 8 * (i & 1));
     }
-    if (steps > 0) fetch(0);
 
-    // V tile: row r, 16-byte piece c at place c ^ f(r), so that the turning reads spread over the banks
-    const int vrow = lane / kPieces, vpiece = lane % kPieces;
-    char *turn = lds + wave * 32 * D;
-    auto place = [](int r) { return D == 128 ? (r >> 1) & 7 : (r >> 2) & 3; };
-    f4_t acc[D / 16];
+    // the queries t, h G + first .. + rows - 1, as B operands with the channels in the order of K's pieces
+    __device__ __forceinline__ void queries(int t, int first, int rows) {
+        const uint16_t *qp = a.q + (int64_t)t * a.q_ts + (int64_t)(h * a.G + first + min(col, rows - 1)) * a.q_hs;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) acc[i] = f4_t{};
-    float m = kNegInf, l = 0.0f;
+        for (int i = 0; i < D / 32; ++i) qf[i] = *reinterpret_cast<const bf8_t *>(qp + 16 * (quarter + 4 * (i / 2)) + 8 * (i & 1));
+    }
 
     // A step; masked: of some group not all 16 keys are seen.  What is hidden is
     // hidden from all columns, which are queries of one token: its values are taken as zeros.
-    auto step = [&](int s, uint32_t seen, auto masked_c) {
-        constexpr bool kMasked = decltype(masked_c)::value;
+    template <bool kMasked>
+    __device__ __forceinline__ void step(int s, uint32_t seen) {
 #pragma unroll
         for (int c = 0; c < kVLoads; ++c) {
-            const int r = vrow + c * (64 / kPieces);
-            if (E4M3 && kMasked && !((seen >> r) & 1)) st.v[c] = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(turn + r * D + ((vpiece ^ place(r)) << 4)) = st.v[c];
+            const int r = lane / kPieces + c * (64 / kPieces);
+            if (E4M3 && kMasked && !((seen >> r) & 1)) v[c] = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(turn + r * D + (((lane % kPieces) ^ place(r)) << 4)) = v[c];
         }
         float kc[2][4], vc[2][4];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            kc[g][0] = st.ks[g].x * a.scale, kc[g][1] = st.ks[g].y * a.scale;
-            kc[g][2] = st.ks[g].z * a.scale, kc[g][3] = st.ks[g].w * a.scale;
-            vc[g][0] = st.vs[g].x, vc[g][1] = st.vs[g].y, vc[g][2] = st.vs[g].z, vc[g][3] = st.vs[g].w;
+            kc[g][0] = ks[g].x * a.scale, kc[g][1] = ks[g].y * a.scale, kc[g][2] = ks[g].z * a.scale, kc[g][3] = ks[g].w * a.scale;
+            vc[g][0] = vs[g].x, vc[g][1] = vs[g].y, vc[g][2] = vs[g].z, vc[g][3] = vs[g].w;
             // copies, so that the next step's loads are not waited for at the end of this one
 #pragma unroll
             for (int r = 0; r < 4; ++r) asm volatile("" : "+v"(vc[g][r]));
@@ -618,22 +678,20 @@ __global__ __launch_bounds__(256, 2) void attn_blocks_kernel(BlocksArgs a) {
             sc[g] = f4_t{};
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
-                const uint4 w = st.k[g][c];
+                const uint4 w = k[g][c];
                 sc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8<E4M3>(w.x, w.y), qf[2 * c], sc[g], 0, 0, 0);
                 sc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8<E4M3>(w.z, w.w), qf[2 * c + 1], sc[g], 0, 0, 0);
             }
         }
-        if (s + 1 < steps) {
-            if (((s + 1) & 31) == 0) look_up(s + 1);
-            fetch(s + 1);
-        }
+        ahead(s);
         bool hid[2][4];
+        const uint32_t vis = seen >> (4 * quarter);
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 sc[g][r] *= kc[g][r];
-                hid[g][r] = kMasked && !((seen >> (16 * g + 4 * quarter + r)) & 1);
+                hid[g][r] = kMasked && !((vis >> (16 * g + r)) & 1);
                 if (kMasked) sc[g][r] = hid[g][r] ? kNegInf : sc[g][r];
             }
         float top = sc[0][0];
@@ -666,62 +724,124 @@ __global__ __launch_bounds__(256, 2) void attn_blocks_kernel(BlocksArgs a) {
         const bf8_t pf = __builtin_bit_cast(bf8_t, i4_t{(int)p[0], (int)p[1], (int)p[2], (int)p[3]});
         const bf8_t pl = __builtin_bit_cast(bf8_t, i4_t{(int)pr[0], (int)pr[1], (int)pr[2], (int)pr[3]});
         // V^T: keys 4 quarter + 0..3 and 16 + 4 quarter + 0..3 of 16 channels
-        const int vkey = 4 * quarter + ((col >> 1) & 3) + 16 * (col >> 3), xv = place(vkey);
+        const int vkey = 4 * quarter + ((col >> 1) & 3) + 16 * (col >> 3);
+        int xv = place(vkey) << 4;
+        asm("" : "+v"(xv));  // 8 addresses made anew in each step, not kept
         const char *from = turn + vkey * D + (col & 1) * 8;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-            const i2_t w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS_AS i2_t *)(from + ((i ^ xv) << 4)));
+            const i2_t w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS_AS i2_t *)(from + ((i << 4) ^ xv)));
             const bf8_t vf = decode8<E4M3>((uint32_t)w[0], (uint32_t)w[1]);
             acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf, acc[i], 0, 0, 0);
             acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pl, acc[i], 0, 0, 0);
         }
-    };
-    auto low_bits = [](int n) { return n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1; };
-    for (int s = 0; s < steps; ++s) {
-        uint32_t seen = page_of(s, 0) < 0 ? 0u : low_bits(pos + 1 - base_of(s, 0));
-        seen |= (page_of(s, 1) < 0 ? 0u : low_bits(pos + 1 - base_of(s, 1))) << 16;
-        if (seen == ~0u) {
-            step(s, seen, std::false_type{});
-        } else if (seen != 0) {
-            step(s, seen, std::true_type{});
-        } else if (s + 1 < steps) {  // nothing here
-            if (((s + 1) & 31) == 0) look_up(s + 1);
-            fetch(s + 1);
-        }
     }
-    l = sum_quarters(l);
 
-    uint16_t *op = a.o + ((int64_t)t * a.Hq + h * a.G + g0) * D;
-    if (W == 1) {
-        if (col < rows) {
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-                *reinterpret_cast<uint2 *>(op + col * D + 16 * i + 4 * quarter) =
-                    make_uint2(pack_bf16(acc[i][0] * inv, acc[i][1] * inv), pack_bf16(acc[i][2] * inv, acc[i][3] * inv));
-        }
-        return;
+    __device__ __forceinline__ void ahead(int s) {  // the loads of the step behind s
+        if (s + 1 >= steps) return;
+        if (((s + 1) & 31) == 0) look_up(s + 1, entry(s + 1));
+        fetch(s + 1);
     }
-    float *join = reinterpret_cast<float *>(lds);
-    if (quarter == 0) stat[0][wave][col] = m, stat[1][wave][col] = l;
-    __syncthreads();  // the turning tiles are read
+
+    // All steps, the first of which is on its way; the sums of a lane's column are then complete.
+    __device__ __forceinline__ void run() {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) acc[i] = f4_t{};
+        m = kNegInf, l = 0.0f;
+        auto low_bits = [](int n) { return n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1; };
+        for (int s = 0; s < steps; ++s) {
+            uint32_t seen = page_of(s, 0) < 0 ? 0u : low_bits(pos + 1 - base_of(s, 0));
+            seen |= (page_of(s, 1) < 0 ? 0u : low_bits(pos + 1 - base_of(s, 1))) << 16;
+            if (seen == ~0u)
+                step<false>(s, seen);
+            else if (seen != 0)
+                step<true>(s, seen);
+            else
+                ahead(s);
+        }
+        l = sum_quarters(l);
+    }
+};
+
+// Many items: one for each wave, the same kv head of 4 neighbouring rows in a workgroup.
+template <int D, bool E4M3>
+__global__ __launch_bounds__(256, 2) void attn_blocks_many_kernel(BlocksArgs a) {
+    __shared__ __attribute__((aligned(1024))) char lds[4 * 32 * D];
+    const int wave = uniform((int)threadIdx.x >> 6), per_row = a.H * a.blocks;
+    const int t = (int)(blockIdx.x / (uint32_t)per_row) * 4 + wave, hb = (int)(blockIdx.x % (uint32_t)per_row);
+    if (t >= a.Tq) return;
+    Walk<D, E4M3> w(a, lds + wave * 32 * D);
+    w.h = hb / a.blocks;
+    const int first = (hb - w.h * a.blocks) * 16, rows = min(16, a.G - first);
+    w.picks = a.picks + ((int64_t)t * a.H + w.h) * a.count, w.g0 = 0, w.stride = 2;
+    const int pick = w.entry(0);  // on its way while the row is looked for
+    const Row row = find_row(a.cu, a.lens, a.B, a.Tq, a.max_pages << a.shift, t);
+    if (row.b < 0) return;
+    w.pos = row.pos, w.groups = entries(a, row.pos) << (a.shift - 4), w.steps = (w.groups + 1) / 2;
+    w.table = a.table + row.b * a.max_pages;
+    w.look_up(0, pick);
+    w.queries(t, first, rows);
+    if (w.steps > 0) w.fetch(0);
+    w.run();
+    if (w.col >= rows) return;
+    uint16_t *op = a.o + ((int64_t)t * a.Hq + w.h * a.G + first + w.col) * D + 4 * w.quarter;
+    const float inv = w.l == 0.0f ? 0.0f : 1.0f / w.l;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
-        *reinterpret_cast<f4_t *>(join + (wave * R + col) * kPad + 16 * i + 4 * quarter) = acc[i];
-    __syncthreads();
-    float *out = a.part + (int64_t)(item * a.parts + part) * (R * (D + 2));
+        *reinterpret_cast<uint2 *>(op + 16 * i) =
+            make_uint2(pack_bf16(w.acc[i][0] * inv, w.acc[i][1] * inv), pack_bf16(w.acc[i][2] * inv, w.acc[i][3] * inv));
+}
+
+// Few items: the 4 waves of a workgroup, and `parts` workgroups, take an item's steps in
+// turn; they are joined in LDS, and over the parts by the workgroup that finishes last
+// (qw3_attn_dev.h).
+template <int D, bool E4M3>
+__global__ __launch_bounds__(256, 2) void attn_blocks_few_kernel(BlocksArgs a) {
+    constexpr int R = 16, W = 4, kPad = D + 4;
+    constexpr int kTurn = W * 32 * D, kJoin = W * R * kPad * 4;
+    __shared__ __attribute__((aligned(1024))) char lds[kTurn > kJoin ? kTurn : kJoin];
+    __shared__ float stat[2][W][R];
+    __shared__ int arrived;
+    const int tid = threadIdx.x, wave = uniform(tid >> 6), per_row = a.H * a.blocks;
+    if (a.parts > 1 && blockIdx.x == 0) clear_next<256>(a.clear);
+    const int item = (int)(blockIdx.x / (uint32_t)a.parts), part = (int)blockIdx.x - item * a.parts;
+    const int t = (int)((uint32_t)item / (uint32_t)per_row), hb = item - t * per_row;
+    Walk<D, E4M3> w(a, lds + wave * 32 * D);
+    w.h = hb / a.blocks;
+    const int first = (hb - w.h * a.blocks) * R, rows = min(R, a.G - first);
+    w.picks = a.picks + ((int64_t)t * a.H + w.h) * a.count;
+    w.g0 = 2 * (part * W + wave), w.stride = 2 * W * a.parts;
+    const int pick = w.entry(0);  // on its way while the row is looked for
+    w.queries(t, first, rows);
+    const Row row = find_row(a.cu, a.lens, a.B, a.Tq, a.max_pages << a.shift, t);
+    if (row.b < 0) return;  // all parts
+    w.pos = row.pos, w.groups = entries(a, row.pos) << (a.shift - 4);
+    w.steps = w.g0 < w.groups ? (w.groups - w.g0 + w.stride - 1) / w.stride : 0;
+    w.table = a.table + row.b * a.max_pages;
+    if (w.steps > 0) w.look_up(0, pick);
+    if (w.steps > 0) w.fetch(0);
+    w.run();
+
+    uint16_t *op = a.o + ((int64_t)t * a.Hq + w.h * a.G + first) * D;
+    float *join = reinterpret_cast<float *>(lds);
+    float *out = a.part + (int64_t)blockIdx.x * (R * (D + 2));
+    if (w.quarter == 0) stat[0][wave][w.col] = w.m, stat[1][wave][w.col] = w.l;
+    lds_barrier();  // the turning tiles are read
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) *reinterpret_cast<f4_t *>(join + (wave * R + w.col) * kPad + 16 * i + 4 * w.quarter) = w.acc[i];
+    lds_barrier();
     for (int e = tid; e < rows * D / 2; e += 256) {
         const int r = e / (D / 2), c = 2 * (e % (D / 2));
         float mm = kNegInf;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) mm = fmaxf(mm, stat[0][w][r]);
+        for (int x = 0; x < W; ++x) mm = fmaxf(mm, stat[0][x][r]);
         float ll = 0.0f;
         f2_t sum = {};
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float f = stat[0][w][r] == kNegInf ? 0.0f : exp2_fast(stat[0][w][r] - mm);
-            ll += f * stat[1][w][r];
-            sum += f * *reinterpret_cast<const f2_t *>(join + (w * R + r) * kPad + c);
+        for (int x = 0; x < W; ++x) {
+            const float f = stat[0][x][r] == kNegInf ? 0.0f : exp2_fast(stat[0][x][r] - mm);
+            ll += f * stat[1][x][r];
+            sum += f * *reinterpret_cast<const f2_t *>(join + (x * R + r) * kPad + c);
         }
         if (a.parts == 1) {
             const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
@@ -738,7 +858,7 @@ __global__ __launch_bounds__(256, 2) void attn_blocks_kernel(BlocksArgs a) {
     __syncthreads();
     if (uniform(arrived) != a.parts - 1) return;
     const float *parts0 = a.part + (int64_t)item * a.parts * (R * (D + 2));
-    auto slot_of = [&](int g) { return parts0 + (int64_t)g * (R * (D + 2)); };
+    auto slot_of = [&](int g) -> const float * { return parts0 + (int64_t)g * (R * (D + 2)); };
     auto row_out = [&](int r) { return op + r * D; };
     if (rows <= R / 2)
         join_rows<R, D, R / 8>(slot_of, 0, a.parts - 1, rows, row_out);
@@ -753,18 +873,21 @@ qw3_status launch_blocks(BlocksArgs a, hipStream_t stream) {
     qw3_status st = cu_count(&cus);
     if (st != QW3_OK) return st;
     const int64_t items = (int64_t)a.Tq * a.H * a.blocks;
-    // An item of n units of 128 keys in parts of u: u + c n / u, as in qattn_cache, and
-    // no more parts than twice the CUs have room for.
-    const float units = (float)(((int64_t)a.count << a.shift) / 128 + 1);
+    if (items >= 8 * (int64_t)cus) {  // an item for each wave fills the card
+        const int64_t wgs = ceil_div(a.Tq, 4) * a.H * a.blocks;
+        hipLaunchKernelGGL((attn_blocks_many_kernel<D, E4M3>), dim3((unsigned)wgs), dim3(256), 0, stream, a);
+        return check_launch();
+    }
+    // An item of n units of 128 keys in parts of u units takes u + 0.14 n / u, as in
+    // qattn_cache: least at u = sqrt(0.14 n); and no more parts than the CUs have room for,
+    // two workgroups each.  One row of 8 kv heads, 64 pages of 64 tokens, with 1, 4, 8, 16, 32
+    // parts: 49, 19, 13.5, 12.5, 14 us; 48 rows of 8, 64 pages of 16, with 1, 2, 4: 22, 26, 31.
+    const int64_t entries = a.count < a.max_pages ? a.count : a.max_pages;
+    const float units = (float)((entries << a.shift) / 128 + 1);
     const int most = (int)(units / __builtin_sqrtf(0.14f * units));
     const int64_t room = items < 2 * (int64_t)cus ? 2 * (int64_t)cus / items : 1;
     a.parts = (int)(room < most ? room : most);
     if (a.parts < 1 || items > kCounts) a.parts = 1;
-    if (items >= 8 * (int64_t)cus) {  // an item for each wave
-        const int64_t wgs = ceil_div(a.Tq, 4) * a.H * a.blocks;
-        hipLaunchKernelGGL((attn_blocks_kernel<D, E4M3, 1>), dim3((unsigned)wgs), dim3(256), 0, stream, a);
-        return check_launch();
-    }
     if (a.parts > 1) {
         void *ws = nullptr;
         st = workspace(stream, (size_t)(items * a.parts) * 16 * (D + 2) * sizeof(float), &ws);
@@ -773,38 +896,52 @@ qw3_status launch_blocks(BlocksArgs a, hipStream_t stream) {
         st = counters(stream, (int)items, &a.counts, &a.clear);
         if (st != QW3_OK) return st;
     }
-    hipLaunchKernelGGL((attn_blocks_kernel<D, E4M3, 4>), dim3((unsigned)(items * a.parts)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((attn_blocks_few_kernel<D, E4M3>), dim3((unsigned)(items * a.parts)), dim3(256), 0, stream, a);
     return check_launch();
 }
 
-constexpr int64_t kTileKeys = 12288, kRowKeys = 4100;  // words of LDS for the keys of 16 rows, of one
+constexpr int64_t kTileKeys = 32768;              // words of LDS for the keys of 16 rows
 constexpr int64_t kKeyBytes = int64_t(64) << 20;  // of keys in memory at a time
+constexpr int64_t kRowPages = 256;
 
+// One CU reads 30 GB/s of bounds, 512 pages of 128 channels in 4.5 us.  So a row's pages
+// are read by one workgroup only where a table has few; else by as many as there are
+// pages for, through memory, and picked by a second launch.  One row of 8 kv heads, 64 of
+// 256, 512, 1024, 2048 pages: in one workgroup 7.6, 11.5, 19.7, 34.9 us, through memory
+// 10.8, 11.3, 11.7, 13.4; 48 rows, 64 of 64, 512, 1024 pages: 7.2, 17.4, 28.5 and 9.5,
+// 19.8, 32.1; 48 rows of 17 to 16,000 tokens in pages of 16, where the longest are
+// waited for: KKK.
 template <int D>
 qw3_status launch_select(SelectArgs a, hipStream_t stream) {
+    int cus = 0;
+    qw3_status st = cu_count(&cus);
+    if (st != QW3_OK) return st;
     a.pitch = (int)(ceil_div(a.max_pages, 16) * 16 + 4);  // rows of the keys begin in different banks
     const int64_t tiles = a.cu ? a.Tq / 16 + a.B : a.B;
     if (a.cu && a.Tq >= 4 * (int64_t)a.B && 16 * a.pitch <= kTileKeys) {
-        hipLaunchKernelGGL((select_tile_kernel<D>), dim3((unsigned)(tiles * a.H)), dim3(256), 16 * a.pitch * 4, stream, a);
+        hipLaunchKernelGGL((select_tile_kernel<D>), dim3((unsigned)(tiles * a.H)), dim3(1024), 16 * a.pitch * 4, stream, a);
         return check_launch();
     }
-    if (a.pitch <= kRowKeys) {
-        hipLaunchKernelGGL((select_row_kernel<D, 1024>), dim3((unsigned)(a.Tq * a.H)), dim3(1024), a.pitch * 4, stream, a);
+    if (a.max_pages <= kRowPages) {
+        hipLaunchKernelGGL((select_row_kernel<D>), dim3((unsigned)(a.Tq * a.H)), dim3(256), a.pitch * 4, stream, a);
         return check_launch();
     }
     int64_t rows = kKeyBytes / (4 * (int64_t)a.pitch * a.H);
     rows = rows < 16 ? 16 : rows;
     rows = rows < a.Tq ? rows : a.Tq;
     void *ws = nullptr;
-    const qw3_status st = workspace(stream, (size_t)(rows * a.H * a.pitch) * 4, &ws);
+    st = workspace(stream, (size_t)(rows * a.H * a.pitch) * 4, &ws);
     if (st != QW3_OK) return st;
     a.keys = static_cast<uint32_t *>(ws);
-    int64_t some = ceil_div(a.max_pages, 64);  // workgroups of a tile
+    int64_t some = ceil_div(a.max_pages, 256);  // workgroups of a tile
     some = some < 64 ? some : 64;
     for (int64_t t = 0; t < a.Tq; t += rows) {
         a.t0 = (int)t, a.rows = (int)(rows < a.Tq - t ? rows : a.Tq - t);
         hipLaunchKernelGGL((score_kernel<D>), dim3((unsigned)(tiles * a.H), (unsigned)some), dim3(256), 0, stream, a);
-        hipLaunchKernelGGL((pick_kernel<1024>), dim3((unsigned)(a.rows * a.H)), dim3(1024), 0, stream, a);
+        if ((int64_t)a.rows * a.H >= cus)
+            hipLaunchKernelGGL((pick_kernel<256>), dim3((unsigned)(a.rows * a.H)), dim3(256), 0, stream, a);
+        else
+            hipLaunchKernelGGL((pick_kernel<1024>), dim3((unsigned)(a.rows * a.H)), dim3(1024), 0, stream, a);
     }
     return check_launch();
 }

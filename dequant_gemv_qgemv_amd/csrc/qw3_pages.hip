@@ -307,18 +307,19 @@ __global__ __launch_bounds__(256) void copy_kernel(uint8_t *__restrict__ codes, 
     const uint4 *src = reinterpret_cast<const uint4 *>(codes + from * page_bytes);
     uint4 *dst = reinterpret_cast<uint4 *>(codes + to * page_bytes);
     const int64_t at = (int64_t)chunk * (kCopyBytes / 16) + threadIdx.x, end = page_bytes / 16;
-    uint4 w[kCopyLoads];
-#pragma unroll
-    for (int k = 0; k < kCopyLoads; ++k)
-        if (at + 256 * k < end) w[k] = src[at + 256 * k];
+    // the loads past the page's end read its last piece, so that none waits for a branch
+    static_assert(kCopyLoads == 4);
+    const uint4 w0 = src[min(at, end - 1)], w1 = src[min(at + 256, end - 1)], w2 = src[min(at + 512, end - 1)],
+                w3 = src[min(at + 768, end - 1)];
     if (chunk == 0) {
         const float4 *s = reinterpret_cast<const float4 *>(scales + from * page_scales);
         float4 *d = reinterpret_cast<float4 *>(scales + to * page_scales);
         for (int64_t k = threadIdx.x; k < page_scales / 4; k += 256) d[k] = s[k];
     }
-#pragma unroll
-    for (int k = 0; k < kCopyLoads; ++k)
-        if (at + 256 * k < end) dst[at + 256 * k] = w[k];
+    if (at < end) dst[at] = w0;
+    if (at + 256 < end) dst[at + 256] = w1;
+    if (at + 512 < end) dst[at + 512] = w2;
+    if (at + 768 < end) dst[at + 768] = w3;
 }
 
 // ---------------------------------------------------------------- compact --

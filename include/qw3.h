@@ -568,10 +568,9 @@ qw3_status qcache_bounds(const void *codes, const float *scales, int32_t code_ty
  * infinity in a row's queries its u and n are zeros.
  * 1 <= count <= QW3_MAX_PICKS, first >= 0, recent >= 1, first + recent <= count,
  * (Tq + B) H < 2^22, else QW3_ERR_SHAPE.
- * Workspace, by the rules of qgemm_w3g128_smallM: none with at most 752 pages in the
- * table's width for sequences of 4 new tokens and more on average, or with at most
- * 4096; else the scores of at least 16 rows, 4 H (max_pages + 20) bytes each, 64 MiB
- * where that is more.
+ * Workspace, by the rules of qgemm_w3g128_smallM: none with max_pages up to 256, or up
+ * to 2032 where there are 4 new tokens and more for each sequence on average; else the
+ * scores of at least 16 rows, 4 H (max_pages + 20) bytes each, 64 MiB where that is more.
  */
 qw3_status qblock_select(const uint16_t *q, const int8_t *bounds, const float *bound_scales, const int32_t *block_table,
                          const int32_t *lens, const int32_t *cu_q, int32_t *picks, int64_t B, int64_t max_pages, int64_t Tq,
@@ -581,15 +580,16 @@ qw3_status qblock_select(const uint16_t *q, const int8_t *bounds, const float *b
 /*
  * qattn_blocks -- attention of new tokens over the pages picked for them.
  *   q     [Tq, Hq, D] bf16, strided; query head h reads kv head h / (Hq / H)
- *   picks [Tq, H, count] int32: places in the row's block table, in any order; one
- *         outside 0 .. max_pages - 1, or of a page behind the row, counts for nothing; one
- *         named twice counts twice
+ *   picks [Tq, H, count] int32: places in the row's block table, in any order, of which
+ *         as many are read as the row sees pages, `count` at most; one outside 0 ..
+ *         max_pages - 1, or of a page behind the row, counts for nothing; one named twice
+ *         counts twice
  *   out   [Tq, Hq, D] bf16, contiguous, written
  * The formula of qattn_cache over the tokens of the picked pages up to the row's own;
  * a row that sees nothing gets zeros.  fp32 scores and sums, the weights as two
  * bf16 each.
  * Workspace and counters, by the rules of qattn_cache: none with Tq H ceil(Hq / H / 16)
- * at twice the number of CUs or above; else at most 2 x CUs parts of 16 (D + 2) floats.
+ * above the number of CUs; else at most 2 x CUs parts of 16 (D + 2) floats.
  * 1 <= count <= QW3_MAX_PICKS, count * page_size <= 2^30, (Tq + 4) H ceil(Hq / H / 16)
  * < 2^26, else QW3_ERR_SHAPE.
  */

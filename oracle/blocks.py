@@ -90,9 +90,10 @@ def select(q, limits, steps, table, lens, cu, count, size, first, recent):
 
 
 def tokens_of(picks, size, pos, page, pages):
-    """The positions, with repetition, that a row at `pos` sees through its picks; page: its sequence's row of the table."""
+    """The positions, with repetition, that a row at `pos` sees through its picks, as many of them as it sees pages; page: its
+    sequence's row of the table."""
     got = []
-    for p in picks:
+    for p in picks[:0 if pos < 0 else pos // size + 1]:
         if 0 <= p < len(page) and 0 <= page[p] < pages:
             got += [t for t in range(p * size, (p + 1) * size) if t <= pos]
     return np.array(got, int)

@@ -130,6 +130,7 @@ SELECT = [  # page size, heads, kv heads, channels, lengths, new tokens, count, 
     (32, 34, 2, 128, [2000, 60, 0, 999], [5, 60, 0, 70], 9, 1, 2, None), (16, 14, 2, 64, [6000], [50], 40, 1, 1, None),
     (16, 4, 4, 128, [9000, 300], None, 64, 2, 1, 700), (16, 16, 2, 64, [12000, 70], [20, 3], 33, 1, 4, 800),
     (16, 8, 8, 64, [70000, 3000], None, 100, 1, 1, None), (16, 4, 1, 128, [66000, 40], [35, 40], 17, 1, 1, 4500),
+    (16, 8, 2, 64, [30000, 500], [9, 4], 20, 1, 1, 2000), (16, 8, 8, 64, [70000, 3000], None, 100, 1, 1, 8300),
     (16, 8, 1, 64, [500], [480], 2, 1, 1, None), (16, 8, 1, 64, [500], [480], 300, 5, 5, None)]
 
 
