@@ -103,7 +103,7 @@ def qblock_select(q: torch.Tensor, bounds: torch.Tensor, bound_scales: torch.Ten
                          % (count, first, recent))
     shape = (rows, heads, count)
     if out is None:
-        out = torch.empty(shape, dtype=torch.int32, device=q.device)
+        out = lens.new_empty(shape)
     else:
         _ints(out, "out", torch.int32, dev, shape)
     _call(dev, _lib.qblock_select, "qblock_select", q.data_ptr(), bounds.data_ptr(), bound_scales.data_ptr(),

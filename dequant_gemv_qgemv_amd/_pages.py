@@ -75,9 +75,9 @@ def qcache_reserve(refs: torch.Tensor, block_table: torch.Tensor, lens: torch.Te
         _ints(cu, "cu", torch.int32, dev, (batch + 1,))
         if total is None or total < 0:
             raise ValueError("with cu, total must say how many new tokens there are")
-    slots = torch.empty(total, dtype=torch.int64, device=refs.device)
+    slots = lens.new_empty((total,), dtype=torch.int64)
     lens_out = torch.empty_like(lens)
-    copies = torch.empty((batch, 2), dtype=torch.int32, device=refs.device)
+    copies = lens.new_empty((batch, 2))
     _call(dev, _lib.qcache_reserve, "qcache_reserve", refs.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
           cu.data_ptr() if cu is not None else None, slots.data_ptr(), lens_out.data_ptr(), copies.data_ptr(), batch,
           max_pages, total, pages, page_size)
@@ -93,8 +93,8 @@ def qcache_fork(refs: torch.Tensor, block_table: torch.Tensor, lens: torch.Tenso
         raise ValueError("parents must be [sequences], got %s" % (tuple(parents.shape),))
     _ints(parents, "parents", torch.int32, dev, parents.shape)
     count = parents.shape[0]
-    table_out = torch.empty((count, max_pages), dtype=torch.int32, device=refs.device)
-    lens_out = torch.empty(count, dtype=torch.int32, device=refs.device)
+    table_out = torch.empty_like(block_table) if count == batch else lens.new_empty((count, max_pages))
+    lens_out = torch.empty_like(parents)
     _call(dev, _lib.qcache_fork, "qcache_fork", refs.data_ptr(), block_table.data_ptr(), lens.data_ptr(), parents.data_ptr(),
           table_out.data_ptr(), lens_out.data_ptr(), batch, count, max_pages, pages, page_size)
     return table_out, lens_out

@@ -28,14 +28,15 @@ def _angles(positions, rates, axis, style, tokens, index):
     kind = _STYLES.get(style)
     if kind is None:
         raise ValueError('style must be "halves" or "pairs", got %r' % (style,))
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    _ints(positions, "positions", torch.int32, index, (axes, tokens) if positions.dim() == 2 else (tokens,))
-    if rates.dim() != 1:
-        raise ValueError("rates must be [pairs], got %s" % (tuple(rates.shape),))
-    _ints(rates, "rates", torch.float64, index, rates.shape)
+    shape, pairs = positions.shape, rates.shape
+    axes = shape[0] if len(shape) == 2 else 1
+    _ints(positions, "positions", torch.int32, index, (axes, tokens) if len(shape) == 2 else (tokens,))
+    if len(pairs) != 1:
+        raise ValueError("rates must be [pairs], got %s" % (tuple(pairs),))
+    _ints(rates, "rates", torch.float64, index, pairs)
     if axis is not None:
-        _ints(axis, "axis", torch.int32, index, rates.shape)
-    return kind, axes, 2 * rates.shape[0]
+        _ints(axis, "axis", torch.int32, index, pairs)
+    return kind, axes, 2 * pairs[0]
 
 
 def qrope(x: torch.Tensor, positions: torch.Tensor, rates: torch.Tensor, axis: torch.Tensor | None = None,

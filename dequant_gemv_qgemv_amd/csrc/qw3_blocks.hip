@@ -346,7 +346,7 @@ __device__ __forceinline__ void pick(const SelectArgs &a, const uint32_t *keys, 
     int left = a.count - a.first - a.recent;
     const bool none = left <= 0;
     // a few keys are kept, more are read anew in each pass
-    constexpr int kHeld = 4;
+    constexpr int kHeld = T == 64 ? 16 : 4;
     const bool held = hi - lo <= kHeld * T;
     uint32_t kept[kHeld];
 #pragma unroll
@@ -737,10 +737,17 @@ struct Walk {
         }
     }
 
-    __device__ __forceinline__ void ahead(int s) {  // the loads of the step behind s
-        if (s + 1 >= steps) return;
-        if (((s + 1) & 31) == 0) look_up(s + 1, entry(s + 1));
-        fetch(s + 1);
+    __device__ __forceinline__ void ahead(int s) {  // the loads of the step behind s; behind the last the last one's again
+        const int n = min(s + 1, steps - 1);
+        if ((n & 31) == 0) look_up(n, entry(n));
+        fetch(n);
+    }
+
+    // Of a step's 32 keys those that the row sees, as bits.
+    __device__ __forceinline__ uint32_t seen_of(int s) const {
+        auto low_bits = [](int n) { return n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1; };
+        const uint32_t lo = page_of(s, 0) < 0 ? 0u : low_bits(pos + 1 - base_of(s, 0));
+        return lo | (page_of(s, 1) < 0 ? 0u : low_bits(pos + 1 - base_of(s, 1))) << 16;
     }
 
     // All steps, the first of which is on its way; the sums of a lane's column are then complete.
@@ -748,13 +755,14 @@ struct Walk {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) acc[i] = f4_t{};
         m = kNegInf, l = 0.0f;
-        auto low_bits = [](int n) { return n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1; };
         for (int s = 0; s < steps; ++s) {
-            uint32_t seen = page_of(s, 0) < 0 ? 0u : low_bits(pos + 1 - base_of(s, 0));
-            seen |= (page_of(s, 1) < 0 ? 0u : low_bits(pos + 1 - base_of(s, 1))) << 16;
-            if (seen == ~0u)
+            uint32_t seen = seen_of(s);
+            while (seen == ~0u) {  // a loop of its own, whose registers need no copies
                 step<false>(s, seen);
-            else if (seen != 0)
+                seen = ++s < steps ? seen_of(s) : 0u;
+            }
+            if (s >= steps) break;
+            if (seen != 0)
                 step<true>(s, seen);
             else
                 ahead(s);

@@ -333,6 +333,7 @@ struct CompactArgs {
     int64_t max_pages, pages;
     int64_t layer_rows;  // rows of one layer: pages 2 H page_size
     int4 *moves;         // staged: for each new token its place in the table, where it is, where it goes (-1: it stays)
+    int *kept;           // staged: how many of each 4096 tokens stay
     uint4 *stage;        // staged: the rows of `span` tokens from t0 on, of `layers` layers from layer0 on
     float *stage_scales;
     int t0, span, layer0, layers;
@@ -422,37 +423,106 @@ __global__ __launch_bounds__(256) void compact_kernel(CompactArgs a) {
     if (layer == 0 && h == 0 && which == 0 && tid == 0) a.lens_out[b] = dst;
 }
 
-// Staged, for many tokens of few sequences: where each goes (one workgroup for each
-// sequence), then by all of the card the rows of some tokens into the workspace and
+// Staged, for many tokens of few sequences: how many are kept of each 4096, where each
+// goes, and then by all of the card the rows of some tokens into the workspace and
 // from there to their places.
-constexpr int kRankTokens = 16;  // of a thread at a time
+constexpr int kCountShift = 12, kCountTokens = 1 << kCountShift;
 
-__global__ __launch_bounds__(kWide) void compact_rank_kernel(CompactArgs a) {
-    const int b = blockIdx.x;
-    const NewTokens s = new_tokens<kWide>(a, b);
-    const int ctx = s.len - s.n;
-    int dst = max(ctx, 0);
-    for (int i0 = 0; i0 < s.n; i0 += kWide * kRankTokens) {
-        const int i = i0 + (int)threadIdx.x * kRankTokens;
-        uint32_t kept = 0;
-#pragma unroll
-        for (int k = 0; k < kRankTokens; ++k)
-            if (i + k < s.n && ctx + i + k >= 0 && a.keep[s.first + i + k] != 0) kept |= 1u << k;
-        int all;
-        const int at = dst + group_scan<kWide>(__popc(kept), &all);
-#pragma unroll
-        for (int k = 0; k < kRankTokens; ++k) {
-            const int to = at + __popc(kept & ((1u << k) - 1)), from = ctx + i + k;
-            if (i + k < s.n) a.moves[s.first + i + k] = make_int4(b, from, (kept >> k & 1) && to != from ? to : -1, 0);
+// The workgroup's sequence and 4096 of its new tokens: sequence b owns the workgroups
+// from start / 4096 + b on, room for its tokens whatever their number.
+struct Chunk {
+    NewTokens s;
+    int b, at, n;  // b < 0: nothing; tokens s.first + at .. + n - 1
+};
+__device__ __forceinline__ Chunk find_chunk(const CompactArgs &a) {
+    const int lane = threadIdx.x & 63, rank = blockIdx.x;
+    Chunk c = {{0, 0, 0}, -1, 0, 0};
+    int first = rank, floor = 0;
+    if (a.cu) {
+        for (int base = 0; base < a.B; base += 64) {
+            const int start = max(floor, wave_scan_max(base + lane < a.B ? clamp_row(a.cu[min(base + lane, a.B - 1)], a.total) : 0));
+            const unsigned long long in = __ballot(base + lane < a.B && (start >> kCountShift) + base + lane <= rank);
+            if (in == 0) break;
+            const int i = __popcll(in) - 1;
+            c.b = base + i, first = __builtin_amdgcn_readlane(start, i);
+            floor = __builtin_amdgcn_readlane(start, 63);
+            if (in != ~0ull) break;
         }
-        dst += all;
+        if (c.b < 0) return c;
+    } else {
+        c.b = rank;
     }
-    if (threadIdx.x == 0) a.lens_out[b] = dst;
-    // rows of no sequence
-    if (b == 0)
-        for (int t = threadIdx.x; t < s.first; t += kWide) a.moves[t] = make_int4(0, 0, -1, 0);
-    if (b == a.B - 1)
-        for (int t = s.first + s.n + (int)threadIdx.x; t < a.total; t += kWide) a.moves[t] = make_int4(0, 0, -1, 0);
+    c.s.first = first, c.s.n = a.cu ? max(clamp_row(a.cu[c.b + 1], a.total) - first, 0) : 1;
+    c.s.len = (int)max((int64_t)0, min((int64_t)a.lens[c.b], a.max_pages << a.shift));
+    c.at = a.cu ? (rank - (first >> kCountShift) - c.b) << kCountShift : 0;
+    c.n = max(min(kCountTokens, c.s.n - c.at), 0);
+    if (c.at > 0 && c.n == 0) c.b = -1;  // every sequence has a first chunk, of no tokens perhaps
+    return c;
+}
+
+// Whether token i of the chunk, which has some, stays; read whether or not there is a token i, so that a
+// thread's loads are on their way together.
+__device__ __forceinline__ bool stays(const CompactArgs &a, const Chunk &c, int i) {
+    const uint8_t keep = a.keep[c.s.first + c.at + min(i, c.n - 1)];
+    return (keep != 0) & (i < c.n) & (c.s.len - c.s.n + c.at + i >= 0);
+}
+
+__global__ __launch_bounds__(256) void compact_count_kernel(CompactArgs a) {
+    const Chunk c = find_chunk(a);
+    if (c.b < 0) return;
+    int n = 0, all;
+    if (c.n > 0)
+#pragma unroll
+        for (int k = 0; k < kCountTokens / 256; ++k) n += stays(a, c, 256 * k + threadIdx.x) ? 1 : 0;
+    group_scan<256>(n, &all);
+    if (threadIdx.x == 0) a.kept[blockIdx.x] = all;
+}
+
+__global__ __launch_bounds__(256) void compact_rank_kernel(CompactArgs a) {
+    constexpr int kTurns = kCountTokens / 256;
+    __shared__ int waves[kTurns][4];
+    __shared__ int top;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    // rows of no sequence, by all workgroups: before the first start and from the largest on
+    const int4 nowhere = make_int4(0, 0, -1, 0);
+    if (a.cu) {
+        int end = 0;
+        for (int i = tid; i <= a.B; i += 256) end = max(end, clamp_row(a.cu[i], a.total));
+        end = group_scan_max<256>(end);
+        if (tid == 255) top = end;
+        __syncthreads();
+        const int before = clamp_row(a.cu[0], a.total), step = (int)gridDim.x * 256;
+        for (int64_t t = blockIdx.x * 256 + tid; t < before; t += step) a.moves[t] = nowhere;
+        for (int64_t t = (int64_t)top + blockIdx.x * 256 + tid; t < a.total; t += step) a.moves[t] = nowhere;
+    }
+    const Chunk c = find_chunk(a);
+    if (c.b < 0) return;
+    bool kept[kTurns];
+    int before[kTurns];
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) kept[k] = c.n > 0 && stays(a, c, 256 * k + tid);
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        const unsigned long long m = __ballot(kept[k]);
+        before[k] = __popcll(m & ((1ull << lane) - 1));
+        if (lane == 0) waves[k][wave] = __popcll(m);
+    }
+    // kept tokens of the sequence's chunks before this one
+    int sum = 0, base, all;
+    const int chunk0 = (int)blockIdx.x - (c.at >> kCountShift);
+    for (int i = tid; i < c.at >> kCountShift; i += 256) sum += a.kept[chunk0 + i];
+    group_scan<256>(sum, &base);
+    static_assert(kTurns * 4 == 64, "one lane for each wave's turn");
+    const int mine = (&waves[0][0])[lane], upto = wave_scan(mine);
+    all = __builtin_amdgcn_readlane(upto, 63);
+    const int ctx = c.s.len - c.s.n, dst = max(ctx, 0) + base;
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        const int i = 256 * k + tid, from = ctx + c.at + i;
+        const int to = dst + __shfl(upto - mine, 4 * k + wave, 64) + before[k];
+        if (i < c.n) a.moves[c.s.first + c.at + i] = make_int4(c.b, from, kept[k] && to != from ? to : -1, 0);
+    }
+    if (tid == 0 && c.at + c.n >= c.s.n) a.lens_out[c.b] = dst + all;
 }
 
 // A workgroup has 16 tokens and a layer; OUT: from the workspace to their places.
@@ -512,12 +582,15 @@ qw3_status launch_compact(CompactArgs a, int64_t layers, hipStream_t stream) {
     }
     span = span < 16 ? 16 : span;
     void *ws = nullptr;
-    const qw3_status st = workspace(stream, (size_t)(a.total * int64_t(16) + span * some * token), &ws);
+    const int64_t chunks = a.cu ? (a.total >> kCountShift) + a.B : a.B, counts = ceil_div(chunks, 4) * 4;
+    const qw3_status st = workspace(stream, (size_t)(a.total * int64_t(16) + counts * 4 + span * some * token), &ws);
     if (st != QW3_OK) return st;
     a.moves = static_cast<int4 *>(ws);
-    a.stage = reinterpret_cast<uint4 *>(a.moves + a.total);
+    a.kept = reinterpret_cast<int *>(a.moves + a.total);
+    a.stage = reinterpret_cast<uint4 *>(a.kept + counts);
     a.stage_scales = reinterpret_cast<float *>(a.stage + span * some * 2 * a.H * (D / 16));
-    hipLaunchKernelGGL(compact_rank_kernel, dim3(a.B), dim3(kWide), 0, stream, a);
+    hipLaunchKernelGGL(compact_count_kernel, dim3((unsigned)chunks), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(compact_rank_kernel, dim3((unsigned)chunks), dim3(256), 0, stream, a);
     for (int64_t layer = 0; layer < layers; layer += some)
         for (int64_t t = 0; t < a.total; t += span) {
             a.layer0 = (int)layer, a.layers = (int)(some < layers - layer ? some : layers - layer);

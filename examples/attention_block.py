@@ -1,13 +1,15 @@
 """The attention half of a decoder layer, with W3G128 projections and a quantised
-cache: what a server runs for each layer.
+cache whose pages are counted on the GPU: what a server runs for each layer.
 
-  prompt   q/k/v products of all rows -> rotary embedding -> the new keys and
+  prompt   q/k/v products of all rows -> rotary embedding, and the new keys and
            values into the cache -> qattn_prompt -> o product.  A prompt may come
            in chunks: the cached prefix is read back dense for the next one.
   verify   a tree of drafted tokens for each sequence (or one token): q/k/v
-           products -> rotary embedding by depth -> cache -> qattn_cache with the
+           products -> rotary embedding by depth and cache -> qattn_cache with the
            tree's masks -> o product.
   accept   the accepted path's rows move to the end of the context.
+  step     one token for each sequence over the pages that its query selects.
+  fork     sequences that follow others, page by page, as beams and samples do.
 
 Run on a GPU:  python3 examples/attention_block.py
 """
@@ -30,7 +32,7 @@ def random_weight(rows, cols, generator):
 
 
 class AttentionBlock:
-    def __init__(self, hidden=8192, heads=64, kv_heads=8, dim=128, pages=64, page_size=16, codes=torch.int8, seed=0):
+    def __init__(self, hidden=8192, heads=64, kv_heads=8, dim=128, pages=64, page_size=16, codes=torch.int8, seed=0, longest=1024):
         g = torch.Generator(device="cuda")
         g.manual_seed(seed)
         self.heads, self.kv_heads, self.dim, self.page_size = heads, kv_heads, dim, page_size
@@ -38,67 +40,69 @@ class AttentionBlock:
         self.qkv = random_weight((heads + 2 * kv_heads) * dim, hidden, g)
         self.o = random_weight(hidden, heads * dim, g)
         self.codes, self.scales = q3.new_cache(pages, page_size, kv_heads, dim, codes)
-        self.free = list(range(pages))
-        self.tables = []   # the pages of each sequence
-        self.lens = []     # its cached tokens
-        self.rate = 10000.0 ** (-torch.arange(0, dim, 2, device="cuda", dtype=torch.float32) / dim)
+        self.bounds = q3.new_bounds(self.codes)
+        self.refs = torch.zeros(pages, dtype=torch.int32, device="cuda")  # who holds each page
+        self.table = torch.empty((0, longest // page_size), dtype=torch.int32, device="cuda")
+        self.lens = torch.empty(0, dtype=torch.int32, device="cuda")
+        self.counts = []  # the same lengths on the host, which decides them here
+        self.rates = 10000.0 ** (-torch.arange(0, dim, 2, device="cuda", dtype=torch.float64) / dim)
 
     # -------------------------------------------------------- bookkeeping --
     def add(self):
-        self.tables.append([])
-        self.lens.append(0)
-        return len(self.lens) - 1
+        """A new, empty sequence: its number."""
+        self.fork(list(range(len(self.counts))) + [-1])
+        return len(self.counts) - 1
 
-    def reserve(self, seqs, new):
-        """Pages for `new` more tokens of each sequence; the slots of those tokens, in order."""
-        slots = []
+    def fork(self, parents):
+        """Sequence i becomes what parents[i] is now (-1: empty); sequences that nobody follows end."""
+        self.table, self.lens = q3.qcache_fork(self.refs, self.table, self.lens, self.ints(parents), self.page_size)
+        self.counts = [self.counts[p] if p >= 0 else 0 for p in parents]
+
+    def reserve(self, new):
+        """Room for new[b] more tokens of sequence b: their slots, and the sequences' lengths with them."""
+        slots, lens, copies = q3.qcache_reserve(self.refs, self.table, self.lens, self.page_size, cu=self.starts(new), total=sum(new))
+        q3.qcache_copy(self.codes, self.scales, copies)  # pages that were shared until now
+        return slots, lens
+
+    def spread(self, seqs, new):
+        """The number of new tokens of each sequence, 0 for those that are not in seqs (ascending)."""
+        assert list(seqs) == sorted(set(seqs))
+        each = [0] * len(self.counts)
         for b, n in zip(seqs, new):
-            table = self.tables[b]
-            while len(table) * self.page_size < self.lens[b] + n:
-                table.append(self.free.pop())
-            slots += [table[t // self.page_size] * self.page_size + t % self.page_size
-                      for t in range(self.lens[b], self.lens[b] + n)]
-        return torch.tensor(slots, dtype=torch.int64, device="cuda")
-
-    def block_table(self, seqs):
-        most = max(len(self.tables[b]) for b in seqs)
-        return torch.tensor([self.tables[b] + [0] * (most - len(self.tables[b])) for b in seqs], dtype=torch.int32,
-                            device="cuda")
+            each[b] = n
+        return each
 
     @staticmethod
-    def starts(n):
-        return torch.tensor([sum(n[:i]) for i in range(len(n) + 1)], dtype=torch.int32, device="cuda")
+    def ints(x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    @classmethod
+    def starts(cls, n):
+        return cls.ints([sum(n[:i]) for i in range(len(n) + 1)])
 
     # ------------------------------------------------------------ the layer --
-    def project(self, x, positions):
-        """q (bf16, rotated), k (float32, rotated) and v (a float32 view) of rows x [T, hidden]."""
+    def project(self, x, positions, slots, dense=False):
+        """Rotated q (bf16) of rows x [T, hidden], whose keys and values go into the cache; with `dense` those too."""
         y = q3.qgemm_w3g128_smallM(x, *self.qkv).view(x.shape[0], self.heads + 2 * self.kv_heads, self.dim)
-        qk, v = y[:, :self.heads + self.kv_heads], y[:, self.heads + self.kv_heads:]
-        angle = positions.float()[:, None, None] * self.rate
-        cos, sin = angle.cos(), angle.sin()
-        a, b = qk[..., :self.dim // 2], qk[..., self.dim // 2:]
-        qk = torch.cat([a * cos - b * sin, b * cos + a * sin], dim=-1)
-        return qk[:, :self.heads].to(torch.bfloat16), qk[:, self.heads:].contiguous(), v
+        q, k, v = y.split([self.heads, self.kv_heads, self.kv_heads], dim=1)
+        return q3.qrope_write(q, k, v, self.ints(positions), self.rates, slots, self.codes, self.scales, dense=dense)
 
     def output(self, attended):
         return q3.qgemm_w3g128_smallM(attended.view(attended.shape[0], -1), *self.o)
 
     def prompt(self, seqs, new, x):
         """The next new[i] prompt tokens of sequence seqs[i], packed in x [sum(new), hidden]."""
-        at = [self.lens[b] for b in seqs]
-        positions = torch.cat([torch.arange(p, p + n, device="cuda") for p, n in zip(at, new)])
-        q, k, v = self.project(x, positions)
-        q3.qcache_write(k, v, self.reserve(seqs, new), self.codes, self.scales)
-        for b, n in zip(seqs, new):
-            self.lens[b] += n
-        cu_q = self.starts(new)
-        if any(at):  # a later chunk: the prefix comes back from the cache, this chunk with it
-            lens = [self.lens[b] for b in seqs]
-            cu_k = self.starts(lens)
-            kd, vd = q3.qcache_read(self.codes, self.scales, self.block_table(seqs), cu_k, sum(lens))
-        else:
-            cu_k, kd, vd = cu_q, k.to(torch.bfloat16), v.to(torch.bfloat16)
-        return self.output(q3.qattn_prompt(q, kd, vd, cu_q, cu_k))
+        each = self.spread(seqs, new)
+        slots, self.lens = self.reserve(each)
+        q, k, v = self.project(x, [t for n, c in zip(each, self.counts) for t in range(c, c + n)], slots, dense=True)
+        later = any(self.counts[b] for b in seqs)  # not the first chunk
+        self.counts = [c + n for c, n in zip(self.counts, each)]
+        cu_q = cu_k = self.starts(each)
+        q3.qcache_bounds(self.codes, self.scales, self.table, self.lens, *self.bounds, cu_q=cu_q, total=sum(each))
+        if later:  # the prefix comes back from the cache, this chunk with it
+            cu_k = self.starts(self.counts)
+            k, v = q3.qcache_read(self.codes, self.scales, self.table, cu_k, sum(self.counts))
+        return self.output(q3.qattn_prompt(q, k, v, cu_q, cu_k))
 
     def verify(self, seqs, parents, x):
         """Drafted tokens of each sequence, x packed [sum of drafts, hidden]. parents[i][j]: the draft that draft j of
@@ -109,32 +113,39 @@ class AttentionBlock:
             for j, p in enumerate(up):
                 d.append(0 if p < 0 else d[p] + 1)
                 w.append((0 if p < 0 else w[p]) | 1 << j)
-            depth += [self.lens[b] + i for i in d]
+            depth += [self.counts[b] + i for i in d]
             words += [i - (1 << 64) if i >> 63 else i for i in w]
-        new = [len(up) for up in parents]
-        q, k, v = self.project(x, torch.tensor(depth, device="cuda"))
-        q3.qcache_write(k, v, self.reserve(seqs, new), self.codes, self.scales)
-        lens = torch.tensor([self.lens[b] + n for b, n in zip(seqs, new)], dtype=torch.int32, device="cuda")
-        attended = q3.qattn_cache(q, self.codes, self.scales, self.block_table(seqs), lens,
-                                  cu_q=None if all(n == 1 for n in new) else self.starts(new),
+        self.drafts = self.spread(seqs, [len(up) for up in parents])
+        slots, self.ahead = self.reserve(self.drafts)
+        q = self.project(x, depth, slots)
+        attended = q3.qattn_cache(q, self.codes, self.scales, self.table, self.ahead, cu_q=self.starts(self.drafts),
                                   tree=torch.tensor(words, dtype=torch.int64, device="cuda"))
         return self.output(attended)
 
-    def accept(self, b, path):
-        """Keep the drafts on `path` (ascending) of sequence b: their cache rows follow the context."""
-        def place(t):
-            return self.tables[b][t // self.page_size], t % self.page_size
-        raw = self.codes.view(torch.uint8)
-        for i, j in enumerate(path):
-            (p0, s0), (p1, s1) = place(self.lens[b] + j), place(self.lens[b] + i)
-            raw[p1, :, :, s1] = raw[p0, :, :, s0]
-            self.scales[p1, :, :, s1] = self.scales[p0, :, :, s0]
-        self.lens[b] += len(path)
+    def accept(self, paths):
+        """Of the drafts of the last verify() keep those on paths[b] of sequence b: their cache rows follow the context."""
+        keep = [j in paths.get(b, ()) for b, n in enumerate(self.drafts) for j in range(n)]
+        cu = self.starts(self.drafts)
+        self.lens = q3.qcache_compact(self.codes, self.scales, self.table, self.ahead, torch.tensor(keep, device="cuda"), cu_q=cu)
+        self.counts = [c + len(paths.get(b, ())) for b, c in enumerate(self.counts)]
+        kept = [len(paths.get(b, ())) for b in range(len(self.counts))]
+        q3.qcache_bounds(self.codes, self.scales, self.table, self.lens, *self.bounds, cu_q=self.starts(kept), total=sum(kept))
+
+    def step(self, x, count):
+        """One token for every sequence, x [sequences, hidden], which attends to `count` pages for each kv head."""
+        each = [1] * len(self.counts)
+        slots, self.lens = self.reserve(each)
+        q = self.project(x, self.counts, slots)
+        self.counts = [c + 1 for c in self.counts]
+        q3.qcache_bounds(self.codes, self.scales, self.table, self.lens, *self.bounds)
+        picks = q3.qblock_select(q, *self.bounds, self.table, self.lens, count, self.page_size)
+        return self.output(q3.qattn_blocks(q, self.codes, self.scales, self.table, self.lens, picks))
 
 
 def demo(hidden=1024, heads=8, kv_heads=2, dim=128, codes=torch.int8, verbose=True):
-    """Two prompts, the second in two chunks, then a drafted tree for each; the accepted path's outputs against those of
-    the same tokens as a plain prompt. Returns the largest relative difference (the cache holds 8 bits)."""
+    """Two prompts, the second in two chunks, then a drafted tree for each; the accepted path's outputs, and those of the
+    next tokens of both sequences and of a fork of the first, against the same tokens as a plain prompt. Returns the largest
+    relative difference (the cache holds 8 bits)."""
     g = torch.Generator(device="cuda")
     g.manual_seed(1)
     x = torch.randn(2, 80, hidden, device="cuda", generator=g).to(torch.bfloat16)
@@ -148,16 +159,17 @@ def demo(hidden=1024, heads=8, kv_heads=2, dim=128, codes=torch.int8, verbose=Tr
     wrong = torch.randn(1, hidden, device="cuda", generator=g).to(torch.bfloat16)
     drafts = torch.cat([torch.cat([x[i, n:n + 2], wrong, x[i, n + 2:n + 3]]) for i, n in ((0, 50), (1, 37))])
     got = block.verify([a, b], parents, drafts).view(2, 4, -1)[:, [0, 1, 3]]
-    for s in (a, b):
-        block.accept(s, [0, 1, 3])
-    step = block.verify([a, b], [[-1], [-1]], torch.stack([x[0, 53], x[1, 40]]))  # one more token for each
+    block.accept({a: [0, 1, 3], b: [0, 1, 3]})
+    # one more token for each, and for a fork of the first, which goes on with another one
+    block.fork([a, b, a])
+    step = block.step(torch.stack([x[0, 53], x[1, 40], wrong[0]]), count=8)  # as many pages as there are
 
     plain = AttentionBlock(hidden, heads, kv_heads, dim, codes=codes)
-    want = plain.prompt([plain.add(), plain.add()], [54, 41], torch.cat([x[0, :54], x[1, :41]]))
+    want = plain.prompt([plain.add(), plain.add(), plain.add()], [54, 41, 54], torch.cat([x[0, :54], x[1, :41], x[0, :53], wrong]))
     far = 0.0
-    for i, end in ((0, 54), (1, 95)):
-        w = want[end - 4:end]
-        have = torch.cat([got[i], step[i:i + 1]])
+    for i, end in ((0, 54), (1, 95), (2, 149)):
+        w = want[end - 4:end] if i < 2 else want[end - 1:end]
+        have = torch.cat([got[i], step[i:i + 1]]) if i < 2 else step[2:]
         far = max(far, float((have - w).norm() / w.norm()))
     if verbose:
         print("largest relative difference from the unquantised prompt: %.4f" % far)

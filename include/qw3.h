@@ -512,8 +512,8 @@ qw3_status qcache_copy(void *codes, float *scales, const int32_t *copies, int64_
  * whose page is not there is zeros where it goes.  Pages are neither taken nor given
  * back: those behind the new length are used again by qcache_reserve and given up by
  * qcache_fork.  Pages that are written must not be shared.
- * Workspace, by the rules of qgemm_w3g128_smallM: none where Tq <= 512 B; else 16 Tq
- * bytes and the rows on the way, 64 MiB or 16 tokens of one layer if that is more.
+ * Workspace, by the rules of qgemm_w3g128_smallM: none where Tq <= 512 B; else 17 Tq +
+ * 4 B bytes and the rows on the way, 64 MiB or 16 tokens of one layer if that is more.
  * layers B H < 2^23, else QW3_ERR_SHAPE.
  */
 qw3_status qcache_compact(void *codes, float *scales, const int32_t *block_table, const int32_t *lens, const int32_t *cu_q,
@@ -544,6 +544,8 @@ qw3_status qcache_compact(void *codes, float *scales, const int32_t *block_table
  * S = max_d max(|mx_d|, |mn_d|) / 127 (a float32 quotient), and mx_d / S and mn_d / S
  * rounded to the nearest whole number, ties to even, at most 127 in size; zeros where S is zero.  A page
  * whose keys hold an infinity or NaN gets S = NaN and zeros.
+ * Pages that qcache_compact moved tokens into, and pages whose numbers changed, are
+ * up to date after a call whose n reach back to the first of them.
  * The pages of two sequences are different, or hold the same tokens.
  * Tq is the number of rows that cu_q speaks of.
  * (Tq / page_size + 2 B) H < 2^26 (B H < 2^26 without cu_q), else QW3_ERR_SHAPE.
