@@ -60,9 +60,17 @@ struct BoundsArgs {
     int64_t max_pages, pages;
 };
 
+// The larger of two numbers that come as bits from other lanes.  In asm because the
+// compiler would first make quiet NaN of each, which costs as much again; a NaN that
+// is lost here has been seen before.
+__device__ __forceinline__ float max_bits(uint32_t x, uint32_t y) {
+    float r;
+    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(x), "v"(y));
+    return r;
+}
 // The larger of what lanes l and l ^ 8 (l ^ 4) of each 16 hold, in both.
-__device__ __forceinline__ float max_ror8(float x) { return fmaxf(x, dpp_f32<0x128>(x)); }
-__device__ __forceinline__ float max_ror4(float x) { return fmaxf(x, dpp_f32<0x124>(x)); }
+__device__ __forceinline__ float max_ror8(float x) { return max_bits(__float_as_uint(x), __float_as_uint(dpp_f32<0x128>(x))); }
+__device__ __forceinline__ float max_ror4(float x) { return max_bits(__float_as_uint(x), __float_as_uint(dpp_f32<0x124>(x))); }
 
 // A wave has one page and head.  D / 16 lanes take a row, 16 channels each, and the
 // wave 1024 / D rows at a time; what lanes of the same channels hold is joined at the
@@ -112,12 +120,10 @@ __global__ __launch_bounds__(256) void bounds_kernel(BoundsArgs a) {
     const uint8_t *codes = a.codes + row0 * D + piece * 16;
     const float *scales = a.scales + row0;
     float v[32];  // the channels' largest values, then those of the values' opposites
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = kNegInf;
     uint32_t nans = 0;
     float worst = 0.0f;
     constexpr int kAt = 32 / kRows;  // 32 rows on their way together, compared in twos
-    for (int base = 0; base < count; base += 32) {
+    auto rows32 = [&](int base, auto first_c) {
         uint4 w[kAt];
         float s[kAt];
 #pragma unroll
@@ -128,7 +134,8 @@ __global__ __launch_bounds__(256) void bounds_kernel(BoundsArgs a) {
         }
 #pragma unroll
         for (int k = 0; k < kAt; k += 2) {
-            if (base + k * kRows >= count) break;
+            constexpr bool kFirst = decltype(first_c)::value;
+            if (k > 0 && base + k * kRows >= count) break;
             const uint32_t d[2][4] = {{w[k].x, w[k].y, w[k].z, w[k].w}, {w[k + 1].x, w[k + 1].y, w[k + 1].z, w[k + 1].w}};
             worst += s[k] * 0.0f + s[k + 1] * 0.0f;  // stays 0 unless a scale is not finite
 #pragma unroll
@@ -137,7 +144,7 @@ __global__ __launch_bounds__(256) void bounds_kernel(BoundsArgs a) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     if (E4M3) {
-                        nans |= ((d[j][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                        nans |= (d[j][i] & 0x7f7f7f7fu) + 0x01010101u;
                         const f2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8(d[j][i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(d[j][i], true);
                         f[j][0] = lo[0], f[j][1] = lo[1], f[j][2] = hi[0], f[j][3] = hi[1];
                     } else {
@@ -148,37 +155,48 @@ __global__ __launch_bounds__(256) void bounds_kernel(BoundsArgs a) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float x = f[0][e] * s[k], y = f[1][e] * s[k + 1];
-                    v[4 * i + e] = fmaxf(fmaxf(x, y), v[4 * i + e]);
-                    v[16 + 4 * i + e] = fmaxf(fmaxf(-x, -y), v[16 + 4 * i + e]);
+                    v[4 * i + e] = kFirst && k == 0 ? fmaxf(x, y) : fmaxf(fmaxf(x, y), v[4 * i + e]);
+                    v[16 + 4 * i + e] = kFirst && k == 0 ? fmaxf(-x, -y) : fmaxf(fmaxf(-x, -y), v[16 + 4 * i + e]);
                 }
             }
         }
-    }
+    };
+    rows32(0, std::true_type{});
+    for (int base = 32; base < count; base += 32) rows32(base, std::false_type{});
     const bool bad = !(worst == 0.0f);
     // lanes 0..31 keep the maxima, the others those of the opposites; then the even
     // sixteens of lanes the first 8 channels, the odd ones the last
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[16 + i]), false, false);
-        v[i] = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+        v[i] = max_bits(r[0], r[1]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[8 + i]), false, false);
-        v[i] = max_ror8(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+        v[i] = max_ror8(max_bits(r[0], r[1]));
         if (D == 64) v[i] = max_ror4(v[i]);
     }
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
     top = (uint32_t)wave_max((int)top);
-    const bool finite = top < 0x7f800000u && !__any(bad || nans != 0);
+    const bool finite = top < 0x7f800000u && !__any(bad || (nans & 0x80808080u) != 0);
     const float step = finite ? __uint_as_float(top) / 127.0f : __uint_as_float(0x7fc00000u);
+    // quotients as in qw3_quant.h; the sign of those of the opposites goes into the divisor
     float y[8];
+    const float divisor = lane < 32 ? step : -step;
+    if (step > 0x1p-80f && step < 0x1p100f) {
+        const float r = 1.0f / divisor;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float x = lane < 32 ? v[i] : -v[i];
-        y[i] = step > 0.0f ? fminf(fmaxf(x / step, -127.0f), 127.0f) : 0.0f;
+        for (int i = 0; i < 8; ++i) {
+            float q = v[i] * r;
+            q = fmaf(fmaf(-q, divisor, v[i]), r, q);
+            y[i] = fmaf(fmaf(-q, divisor, v[i]), r, q);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = step > 0.0f ? fminf(fmaxf(v[i] / divisor, -127.0f), 127.0f) : 0.0f;
     }
     const uint32_t lo = codes4<false>({y[0], y[1], y[2], y[3]}), hi = codes4<false>({y[4], y[5], y[6], y[7]});
     const int64_t to = (int64_t)page * a.H + h;
