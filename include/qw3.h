@@ -513,8 +513,9 @@ qw3_status qcache_copy(void *codes, float *scales, const int32_t *copies, int64_
  * back: those behind the new length are used again by qcache_reserve and given up by
  * qcache_fork.  Pages that are written must not be shared.
  * Workspace, by the rules of qgemm_w3g128_smallM: none where Tq <= 512 B; else 17 Tq +
- * 4 B bytes and the rows on the way, 64 MiB or 16 tokens of one layer if that is more.
- * layers B H < 2^23, else QW3_ERR_SHAPE.
+ * 4 B bytes, and 8 MiB at most.
+ * layers B H < 2^23 and Tq H < 2^30 (H rounded up to a power of two, above 8 to a
+ * multiple of 8), else QW3_ERR_SHAPE.
  */
 qw3_status qcache_compact(void *codes, float *scales, const int32_t *block_table, const int32_t *lens, const int32_t *cu_q,
                           const uint8_t *keep, int32_t *lens_out, int64_t B, int64_t max_pages, int64_t Tq,

@@ -143,13 +143,13 @@ def test_copy(kind, layers, pages, heads, page, dim):
     same(scales, want_s)
 
 
-# layers, heads, page, dim, lengths, new tokens: up to 512 for each sequence on average in one workgroup for each head, more through the workspace
+# layers, heads, page, dim, lengths, new tokens: up to 512 for each sequence on average in one workgroup for each head, more by all of the card
 COMPACT = [(1, 1, 16, 64, [1], [1]), (2, 3, 16, 128, [40, 16, 0, 7], [13, 16, 0, 7]), (1, 2, 64, 128, [700, 300, 90], [600, 256, 64]),
            (1, 8, 16, 64, [300, 20, 900, 33], [257, 5, 700, 33]), (2, 2, 32, 128, [1500], [1500]), (1, 3, 16, 64, [2000, 5, 0, 700], [1999, 5, 0, 700]),
-           (3, 1, 16, 128, [17000, 300], [16999, 120])]
+           (3, 1, 16, 128, [17000, 300], [16999, 120]), (2, 5, 64, 128, [9000, 40, 5000], [8000, 40, 4999]), (1, 11, 16, 64, [4000], [3990])]
 
 
-@pytest.mark.parametrize("share", [0.0, 0.5, 0.97, 1.0])
+@pytest.mark.parametrize("share", [0.0, 0.04, 0.5, 0.97, 1.0])
 @pytest.mark.parametrize("case", COMPACT, ids=str)
 def test_compact(case, share):
     say("compact", case, share)
@@ -188,7 +188,7 @@ def test_compact_out_of_range():
     lens = np.array([50, 3, 96, -4, 1 << 30, 20], np.int32)
     table = rng.permutation(pages)[:36].reshape(6, width).astype(np.int32)
     for cu in (np.array([0, 9, 30, 12, 60, 61, 70]), np.array([-5, 20, 20, 90, 7, 1 << 30, 3]), None):
-        for extra in (0, 4000):  # the second through the workspace: room for rows that nobody has
+        for extra in (0, 4000):  # the second by all of the card: room for rows that nobody has
             if cu is None and extra:
                 continue
             keep = rng.random(75 + extra if cu is not None else 6) < 0.6
@@ -201,15 +201,16 @@ def test_compact_out_of_range():
             same(scales, want_s)
 
 
-def test_compact_in_several_batches():
-    """More rows than the workspace holds at a time, in tokens and in layers."""
+@pytest.mark.parametrize("share", [0.02, 0.6, 0.999])
+def test_compact_many_heads(share):
+    """Units of several groups of heads, by far more of them than run at a time."""
     rng = np.random.default_rng(10)
-    layers, heads, page, dim, n = 3, 40, 64, 128, 8000  # 10.6 KB a token and layer: 6355 tokens at a time
+    layers, heads, page, dim, n = 3, 40, 64, 128, 8000
     pages = n // page
     codes = torch.randint(0, 256, (layers, pages, 2, heads, page, dim), dtype=torch.uint8, device="cuda")
     scales = torch.randn(layers, pages, 2, heads, page, device="cuda")
     table = rng.permutation(pages)[None].astype(np.int32)
-    keep = rng.random(n) < 0.6
+    keep = rng.random(n) < share
     order = torch.tensor(np.flatnonzero(keep), device="cuda")
     rows = dev(table[0]).long()
     want_c, want_s = codes.clone(), scales.clone()
@@ -219,6 +220,27 @@ def test_compact_in_several_batches():
     got = q().qcache_compact(codes.view(torch.int8), scales, dev(table), dev([n]), dev(keep, torch.bool), cu_q=dev([0, n]))
     assert got.tolist() == [len(order)]
     assert torch.equal(codes, want_c) and torch.equal(scales, want_s)
+
+
+def test_compact_in_several_launches():
+    """More units than a launch has: a cache of 1024 layers, and rows of no sequence behind the two that there are."""
+    rng = np.random.default_rng(19)
+    layers, heads, page, dim, lens, new, rows = 1024, 1, 16, 64, [420, 300], [410, 300], (1 << 20) + 600
+    pages = 50
+    table = rng.permutation(pages)[:48].reshape(2, 24).astype(np.int32)
+    table = np.pad(table, ((0, 0), (0, 4)), constant_values=-1)
+    raw = rng.integers(0, 256, (1, pages, 2, heads, page, dim), dtype=np.uint8)
+    floats = rng.standard_normal((1, pages, 2, heads, page)).astype(np.float32)
+    codes = torch.tensor(raw).cuda().repeat(layers, 1, 1, 1, 1, 1) ^ (torch.arange(layers, device="cuda") % 256).to(torch.uint8).view(-1, 1, 1, 1, 1, 1)
+    scales = torch.tensor(floats).cuda() + torch.arange(layers, device="cuda").view(-1, 1, 1, 1, 1)
+    keep = rng.random(rows) < 0.5
+    cu = np.r_[0, np.cumsum(new)]
+    want_c, want_s = codes.cpu().numpy(), scales.cpu().numpy()
+    want = ref.compact(want_c, want_s, table, lens, keep, cu, page)
+    got = q().qcache_compact(codes.view(torch.int8), scales, dev(table), dev(lens), dev(keep, torch.bool), cu_q=dev(cu))
+    same(got, want)
+    same(codes, want_c)
+    same(scales, want_s)
 
 
 def test_life_of_sequences():

@@ -43,7 +43,7 @@ def test_tables(call, bad):
     (copy, dict(n=-1)), (copy, dict(n=1 << 27)), (copy, dict(layers=-1)), (copy, dict(layers=1025)), (copy, dict(H=0)),
     (copy, dict(D=96)), (copy, dict(size=20)), (copy, dict(n=1 << 24)), (copy, dict(n=1 << 20, layers=1000)),
     (compact, dict(Tq=-1)), (compact, dict(Tq=1 << 27)), (compact, dict(cu=NULL)), (compact, dict(layers=0)),
-    (compact, dict(layers=1025)), (compact, dict(D=32)), (compact, dict(H=1025)), (compact, dict(B=60000, H=300, layers=2))], ids=str)
+    (compact, dict(layers=1025)), (compact, dict(D=32)), (compact, dict(H=1025)), (compact, dict(B=60000, H=300, layers=2)), (compact, dict(Tq=1 << 26, H=16)), (compact, dict(Tq=1 << 26, H=9))], ids=str)
 def test_shapes(call, bad):
     assert call(**bad) == q.QW3_ERR_SHAPE
 
