@@ -590,48 +590,67 @@ struct BlocksArgs {
 // The pages that a row reads: entries of its picks, no more than it sees.
 __device__ __forceinline__ int entries(const BlocksArgs &a, int pos) { return pos < 0 || a.pages == 0 ? 0 : min(a.count, (pos >> a.shift) + 1); }
 
-// An item is a row, a kv head and up to 16 of its queries: 16 columns of the matrix
-// unit's result.  Its keys are the picked pages' in groups of 16, which lie in one
-// page whatever its size; a wave takes two groups at a time, a step.  What a wave
-// has of an item: the steps' pages, the codes and scales on their way, and the sums.
-template <int D, bool E4M3>
+// The bits of a step's keys.
+template <int kKeys>
+struct Bits {
+    typedef uint32_t type;
+};
+template <>
+struct Bits<64> {
+    typedef uint64_t type;
+};
+
+// An item is a row, a kv head and up to 16 of its queries.  Its keys are the picked pages'
+// in groups of 16, which lie in one page whatever its size; a wave takes two or four groups
+// at a time, a step.  What a wave has of an item: the steps' pages, the codes and scales on
+// their way, and the sums.
+// The matrix unit's result has 16 columns.  Up to 16 queries have one each (S = 1); up to
+// 8 have two, up to 4 four, for S subsets of the keys: column c has query c % (16 / S) and
+// the step's groups c / (16 / S).  The product of a group with queries that are zeros in
+// the other columns adds nothing there, so the groups share a result, and a score, an
+// exponential and a weight are made once for each query and key, in all lanes.  The columns
+// of a query have one maximum, and their sums are added at the end.
+template <int D, bool E4M3, int S>
 struct Walk {
-    static constexpr int kPieces = D / 16, kVLoads = D / 32;
+    static constexpr int kPieces = D / 16, kEach = D / 64;         // 16-byte pieces of a row; of a group, for each lane
+    static constexpr int kGroups = S == 4 ? 4 : 2, kSets = S == 1 ? 2 : 1;  // of a step; results, of 4 scores a lane
+    static constexpr int kCols = 16 / S, kAhead = 64 / kGroups;     // columns of queries; steps whose pages are looked up together
+    static constexpr int kTile = 16 * kGroups * D;                  // bytes of the wave's V tile
+    typedef typename Bits<16 * kGroups>::type bits_t;
     const BlocksArgs &a;
     char *turn;  // the wave's V tile in LDS: row r, 16-byte piece c at place c ^ f(r), so that the turning reads spread over the banks
-    int lane, quarter, col;
-    // the item: its kv head, the row's position and number of entries; step s has groups g0 + stride s and the next
+    int lane, quarter, col, own;  // own: the lane's group, where it has one
+    // the item: its kv head, the row's position and number of entries; step s has groups g0 + stride s and the next ones
     int h, pos, groups, g0, stride, steps;
     const int32_t *table, *picks;
-    int ids, bases;  // of 32 steps: lane 2 s + g has of group g of step s the page (-1: none that the row sees) and its first token's position
-    uint4 k[2][D / 64], v[kVLoads];
-    float4 ks[2], vs[2];
-    bf8_t qf[D / 32];
+    int ids, bases;  // of kAhead steps: lane kGroups s + g has of group g of step s the page (-1: none that the row sees) and its first token's position
+    uint4 k[kGroups][kEach], v[kGroups][kEach];
+    float4 ks[kSets], vs[kSets];
+    bf8_t qf[S][D / 32];
     f4_t acc[D / 16];
     float m, l;
 
     __device__ __forceinline__ Walk(const BlocksArgs &args, char *lds) : a(args), turn(lds) {
         lane = threadIdx.x & 63, quarter = lane >> 4, col = lane & 15;
+        own = col / kCols;
         steps = 0;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) k[g][c] = make_uint4(0, 0, 0, 0);
-            ks[g] = vs[g] = make_float4(0, 0, 0, 0);
-        }
+            for (int c = 0; c < kEach; ++c) k[g][c] = v[g][c] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int c = 0; c < kVLoads; ++c) v[c] = make_uint4(0, 0, 0, 0);
+        for (int x = 0; x < kSets; ++x) ks[x] = vs[x] = make_float4(0, 0, 0, 0);
     }
 
     __device__ __forceinline__ static int place(int r) { return D == 128 ? (r >> 1) & 7 : (r >> 2) & 3; }
 
-    // The lane's entry of the 32 steps from s0 on, and what it says once the row is known.
-    __device__ __forceinline__ int entry(int s0) const {
-        const int64_t g = (g0 + (int64_t)(s0 + (lane >> 1)) * stride + (lane & 1)) >> (a.shift - 4);
-        return picks[min(g, (int64_t)a.count - 1)];
+    // The lane's group of the kAhead steps from s0 on, its entry, and what that says once the row is known.
+    __device__ __forceinline__ int64_t group(int s0) const {
+        return g0 + (int64_t)(s0 + lane / kGroups) * stride + lane % kGroups;
     }
+    __device__ __forceinline__ int entry(int s0) const { return picks[min(group(s0) >> (a.shift - 4), (int64_t)a.count - 1)]; }
     __device__ __forceinline__ void look_up(int s0, int pick) {
-        const int64_t g = g0 + (int64_t)(s0 + (lane >> 1)) * stride + (lane & 1);
+        const int64_t g = group(s0);
         ids = -1, bases = 0;
         if (g < groups) {
             const int64_t base = ((int64_t)pick << a.shift) + ((g << 4) & ((1 << a.shift) - 1));
@@ -641,82 +660,113 @@ struct Walk {
             }
         }
     }
-    __device__ __forceinline__ int page_of(int s, int g) const { return __builtin_amdgcn_readlane(ids, 2 * (s & 31) + g); }
-    __device__ __forceinline__ int base_of(int s, int g) const { return __builtin_amdgcn_readlane(bases, 2 * (s & 31) + g); }
+    __device__ __forceinline__ int page_of(int s, int g) const { return __builtin_amdgcn_readlane(ids, kGroups * (s % kAhead) + g); }
+    __device__ __forceinline__ int base_of(int s, int g) const { return __builtin_amdgcn_readlane(bases, kGroups * (s % kAhead) + g); }
 
     __device__ __forceinline__ void fetch(int s) {
         const int64_t page_rows = (int64_t)(2 * a.H) << a.shift, to_v = (int64_t)a.H << a.shift;
+        // a uniform base and a lane's offset
+        uint32_t ko = col * D + quarter * 16, vo = lane * 16, so = 4 * quarter;
+        asm("" : "+v"(ko), "+v"(vo), "+v"(so));
+        int64_t mine = 0;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < kGroups; ++g) {
             const int page = max(page_of(s, g), 0);  // one that does not exist reads page 0: hidden below
             const int64_t at = uniform(page * page_rows + ((int64_t)h << a.shift) + (base_of(s, g) & ((1 << a.shift) - 1)));
             const uint8_t *kp = a.codes + at * D, *vp = kp + to_v * D;
-            const float *sp = a.scales + at;
-            // a uniform base and a lane's offset
-            uint32_t ko = col * D + quarter * 16, vo = lane * 16, so = 4 * quarter;
-            asm("" : "+v"(ko), "+v"(vo), "+v"(so));
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) k[g][c] = *reinterpret_cast<const uint4 *>(kp + ko + 64 * c);
+            for (int c = 0; c < kEach; ++c) k[g][c] = *reinterpret_cast<const uint4 *>(kp + ko + 64 * c);
 #pragma unroll
-            for (int c = 0; c < kVLoads / 2; ++c) v[g * (kVLoads / 2) + c] = *reinterpret_cast<const uint4 *>(vp + vo + 1024 * c);
-            ks[g] = *reinterpret_cast<const float4 *>(sp + so);
-            vs[g] = *reinterpret_cast<const float4 *>(sp + to_v + so);
+            for (int c = 0; c < kEach; ++c) v[g][c] = *reinterpret_cast<const uint4 *>(vp + vo + 1024 * c);
+            if (S == 1) {
+                const float *sp = a.scales + at;
+                ks[g % kSets] = *reinterpret_cast<const float4 *>(sp + so);
+                vs[g % kSets] = *reinterpret_cast<const float4 *>(sp + to_v + so);
+            } else {
+                mine = own == g ? at : mine;
+            }
+        }
+        if (S > 1) {
+            const float *sp = a.scales + mine + so;
+            ks[0] = *reinterpret_cast<const float4 *>(sp);
+            vs[0] = *reinterpret_cast<const float4 *>(sp + to_v);
         }
     }
 
     // the queries t, h G + first .. + rows - 1, as B operands with the channels in the order of K's pieces
     __device__ __forceinline__ void queries(int t, int first, int rows) {
-        const uint16_t *qp = a.q + (int64_t)t * a.q_ts + (int64_t)(h * a.G + first + min(col, rows - 1)) * a.q_hs;
+        const uint16_t *qp = a.q + (int64_t)t * a.q_ts + (int64_t)(h * a.G + first + min(col % kCols, rows - 1)) * a.q_hs;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) qf[i] = *reinterpret_cast<const bf8_t *>(qp + 16 * (quarter + 4 * (i / 2)) + 8 * (i & 1));
+        for (int i = 0; i < D / 32; ++i) {
+            const bf8_t x = *reinterpret_cast<const bf8_t *>(qp + 16 * (quarter + 4 * (i / 2)) + 8 * (i & 1));
+#pragma unroll
+            for (int g = 0; g < S; ++g) qf[g][i] = S == 1 || own == g ? x : bf8_t{};
+        }
+    }
+
+    // The columns of a query: the largest, the sum.
+    __device__ __forceinline__ static float max_columns(float x) {
+        if (S > 1) x = fmaxf(x, dpp_f32<0x128>(x));  // row_ror 8
+        if (S > 2) x = fmaxf(x, dpp_f32<0x124>(x));  // row_ror 4
+        return x;
+    }
+    __device__ __forceinline__ static float sum_columns(float x) {
+        if (S > 1) x += dpp_f32<0x128>(x);
+        if (S > 2) x += dpp_f32<0x124>(x);
+        return x;
     }
 
     // A step; masked: of some group not all 16 keys are seen.  What is hidden is
-    // hidden from all columns, which are queries of one token: its values are taken as zeros.
+    // hidden from all columns, which are queries of one token: its values are taken as
+    // zeros, and so are its keys where other groups share their result.
     template <bool kMasked>
-    __device__ __forceinline__ void step(int s, uint32_t seen) {
+    __device__ __forceinline__ void step(int s, bits_t seen) {
 #pragma unroll
-        for (int c = 0; c < kVLoads; ++c) {
+        for (int c = 0; c < kGroups * kEach; ++c) {
             const int r = lane / kPieces + c * (64 / kPieces);
-            if (E4M3 && kMasked && !((seen >> r) & 1)) v[c] = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(turn + r * D + (((lane % kPieces) ^ place(r)) << 4)) = v[c];
+            uint4 &w = v[c / kEach][c % kEach];
+            if (E4M3 && kMasked && !((seen >> r) & 1)) w = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(turn + r * D + (((lane % kPieces) ^ place(r)) << 4)) = w;
         }
-        float kc[2][4], vc[2][4];
+        float kc[kSets][4], vc[kSets][4];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            kc[g][0] = ks[g].x * a.scale, kc[g][1] = ks[g].y * a.scale, kc[g][2] = ks[g].z * a.scale, kc[g][3] = ks[g].w * a.scale;
-            vc[g][0] = vs[g].x, vc[g][1] = vs[g].y, vc[g][2] = vs[g].z, vc[g][3] = vs[g].w;
+        for (int x = 0; x < kSets; ++x) {
+            kc[x][0] = ks[x].x * a.scale, kc[x][1] = ks[x].y * a.scale, kc[x][2] = ks[x].z * a.scale, kc[x][3] = ks[x].w * a.scale;
+            vc[x][0] = vs[x].x, vc[x][1] = vs[x].y, vc[x][2] = vs[x].z, vc[x][3] = vs[x].w;
             // copies, so that the next step's loads are not waited for at the end of this one
 #pragma unroll
-            for (int r = 0; r < 4; ++r) asm volatile("" : "+v"(vc[g][r]));
+            for (int r = 0; r < 4; ++r) asm volatile("" : "+v"(vc[x][r]));
         }
-        f4_t sc[2];
+        f4_t sc[kSets];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            sc[g] = f4_t{};
+        for (int x = 0; x < kSets; ++x) sc[x] = f4_t{};
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                const uint4 w = k[g][c];
-                sc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8<E4M3>(w.x, w.y), qf[2 * c], sc[g], 0, 0, 0);
-                sc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8<E4M3>(w.z, w.w), qf[2 * c + 1], sc[g], 0, 0, 0);
+        for (int g = 0; g < kGroups; ++g) {
+            f4_t &to = sc[g % kSets];
+            const bool hidden = S > 1 && E4M3 && kMasked && !((seen >> (16 * g + col)) & 1);
+#pragma unroll
+            for (int c = 0; c < kEach; ++c) {
+                const uint4 w = hidden ? make_uint4(0, 0, 0, 0) : k[g][c];
+                to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8<E4M3>(w.x, w.y), qf[g % S][2 * c], to, 0, 0, 0);
+                to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8<E4M3>(w.z, w.w), qf[g % S][2 * c + 1], to, 0, 0, 0);
             }
         }
         ahead(s);
-        bool hid[2][4];
-        const uint32_t vis = seen >> (4 * quarter);
+        bool hid[kSets][4];
+        const uint32_t vis = (uint32_t)(seen >> (S == 1 ? 4 * quarter : 16 * own + 4 * quarter));
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+        for (int x = 0; x < kSets; ++x)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                sc[g][r] *= kc[g][r];
-                hid[g][r] = kMasked && !((vis >> (16 * g + r)) & 1);
-                if (kMasked) sc[g][r] = hid[g][r] ? kNegInf : sc[g][r];
+                sc[x][r] *= kc[x][r];
+                hid[x][r] = kMasked && !((vis >> (16 * x + r)) & 1);
+                if (kMasked) sc[x][r] = hid[x][r] ? kNegInf : sc[x][r];
             }
         float top = sc[0][0];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) top = fmaxf(top, sc[i / 4][i % 4]);
+        for (int i = 1; i < 4 * kSets; ++i) top = fmaxf(top, sc[i / 4][i % 4]);
         if (__any(top > m + kSlack)) {
-            const float m1 = fmaxf(m, max_quarters(top));
+            const float m1 = fmaxf(m, max_columns(max_quarters(top)));
             const float f = m1 == kNegInf ? 1.0f : exp2_fast(m - m1);
             m = m1;
             l *= f;
@@ -725,34 +775,55 @@ struct Walk {
         }
         const float ms = m == kNegInf ? 0.0f : m;
         // a weight is the sum of two bf16: its rounding and the rounding of what that leaves
-        uint32_t p[4], pr[4];
+        uint32_t p[2 * kSets], pr[2 * kSets];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2 * kSets; ++i) {
             float w[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int g = i / 2, r = 2 * (i & 1) + e;
-                const float pe = exp2_fast(sc[g][r] - ms);
+                const int x = i / 2, r = 2 * (i & 1) + e;
+                const float pe = exp2_fast(sc[x][r] - ms);
                 l += pe;
-                w[e] = hid[g][r] ? 0.0f : pe * vc[g][r];  // a hidden key's scale may be anything
+                w[e] = hid[x][r] ? 0.0f : pe * vc[x][r];  // a hidden key's scale may be anything
             }
             p[i] = pack_bf16(w[0], w[1]);
             pr[i] = pack_bf16(w[0] - __uint_as_float(p[i] << 16), w[1] - __uint_as_float(p[i] & 0xffff0000u));
         }
-        const bf8_t pf = __builtin_bit_cast(bf8_t, i4_t{(int)p[0], (int)p[1], (int)p[2], (int)p[3]});
-        const bf8_t pl = __builtin_bit_cast(bf8_t, i4_t{(int)pr[0], (int)pr[1], (int)pr[2], (int)pr[3]});
+        // The products of 32 keys and the weights, zeros in the columns of other groups.  With four
+        // groups half of the columns would be idle in each: they take what the first rounding left of
+        // the weights in the other half.
+        constexpr int kPairs = kGroups / 2, kTerms = S == 4 ? 1 : 2;
+        bf8_t pf[kPairs][kTerms];
+        auto operand = [&](uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+            return __builtin_bit_cast(bf8_t, i4_t{(int)w0, (int)w1, (int)w2, (int)w3});
+        };
+        const bool even = (own & 1) == 0;
+        if constexpr (S == 1) {
+            pf[0][0] = operand(p[0], p[1], p[2], p[3]), pf[0][1] = operand(pr[0], pr[1], pr[2], pr[3]);
+        } else if constexpr (S == 2) {
+            pf[0][0] = operand(even ? p[0] : 0, even ? p[1] : 0, even ? 0 : p[0], even ? 0 : p[1]);
+            pf[0][1] = operand(even ? pr[0] : 0, even ? pr[1] : 0, even ? 0 : pr[0], even ? 0 : pr[1]);
+        } else {
+            const uint32_t r0 = dpp_u32<0x128>(pr[0]), r1 = dpp_u32<0x128>(pr[1]);  // row_ror 8
+            const bool low = own < 2;
+            const uint32_t x0 = low ? p[0] : r0, x1 = low ? p[1] : r1, y0 = low ? r0 : p[0], y1 = low ? r1 : p[1];
+            pf[0][0] = operand(even ? x0 : 0, even ? x1 : 0, even ? 0 : x0, even ? 0 : x1);
+            pf[1][0] = operand(even ? y0 : 0, even ? y1 : 0, even ? 0 : y0, even ? 0 : y1);
+        }
         // V^T: keys 4 quarter + 0..3 and 16 + 4 quarter + 0..3 of 16 channels
         const int vkey = 4 * quarter + ((col >> 1) & 3) + 16 * (col >> 3);
         int xv = place(vkey) << 4;
         asm("" : "+v"(xv));  // 8 addresses made anew in each step, not kept
         const char *from = turn + vkey * D + (col & 1) * 8;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            const i2_t w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS_AS i2_t *)(from + ((i << 4) ^ xv)));
-            const bf8_t vf = decode8<E4M3>((uint32_t)w[0], (uint32_t)w[1]);
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf, acc[i], 0, 0, 0);
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pl, acc[i], 0, 0, 0);
-        }
+        for (int j = 0; j < kPairs; ++j)
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const i2_t w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS_AS i2_t *)(from + 32 * j * D + ((i << 4) ^ xv)));
+                const bf8_t vf = decode8<E4M3>((uint32_t)w[0], (uint32_t)w[1]);
+#pragma unroll
+                for (int x = 0; x < kTerms; ++x) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[j][x], acc[i], 0, 0, 0);
+            }
     }
 
     // The loads of the step behind s; behind the last the last one's again: without a branch
@@ -760,15 +831,18 @@ struct Walk {
     // where 97 were measured: 510 rows of 64 channels, 40 pages of 32 tokens each).
     __device__ __forceinline__ void ahead(int s) {
         const int n = min(s + 1, steps - 1);
-        if (n > s && (n & 31) == 0) look_up(n, entry(n));
+        if (n > s && n % kAhead == 0) look_up(n, entry(n));
         fetch(n);
     }
 
-    // Of a step's 32 keys those that the row sees, as bits.
-    __device__ __forceinline__ uint32_t seen_of(int s) const {
+    // Of a step's keys those that the row sees, as bits.
+    __device__ __forceinline__ bits_t seen_of(int s) const {
         auto low_bits = [](int n) { return n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1; };
-        const uint32_t lo = page_of(s, 0) < 0 ? 0u : low_bits(pos + 1 - base_of(s, 0));
-        return lo | (page_of(s, 1) < 0 ? 0u : low_bits(pos + 1 - base_of(s, 1))) << 16;
+        bits_t seen = 0;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+            seen |= (bits_t)(page_of(s, g) < 0 ? 0u : low_bits(pos + 1 - base_of(s, g))) << (16 * g);
+        return seen;
     }
 
     // All steps, the first of which is on its way; the sums of a lane's column are then complete.
@@ -777,10 +851,10 @@ struct Walk {
         for (int i = 0; i < D / 16; ++i) acc[i] = f4_t{};
         m = kNegInf, l = 0.0f;
         for (int s = 0; s < steps; ++s) {
-            uint32_t seen = seen_of(s);
-            while (seen == ~0u) {  // a loop of its own, whose registers need no copies
+            bits_t seen = seen_of(s);
+            while (seen == ~bits_t{0}) {  // a loop of its own, whose registers need no copies
                 step<false>(s, seen);
-                seen = ++s < steps ? seen_of(s) : 0u;
+                seen = ++s < steps ? seen_of(s) : 0;
             }
             if (s >= steps) break;
             if (seen != 0)
@@ -788,25 +862,30 @@ struct Walk {
             else
                 ahead(s);
         }
-        l = sum_quarters(l);
+        l = sum_columns(sum_quarters(l));
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[i][r] = sum_columns(acc[i][r]);
     }
 };
 
 // Many items: one for each wave, the same kv head of 4 neighbouring rows in a workgroup.
-template <int D, bool E4M3>
+template <int D, bool E4M3, int S>
 __global__ __launch_bounds__(256, 2) void attn_blocks_many_kernel(BlocksArgs a) {
-    __shared__ __attribute__((aligned(1024))) char lds[4 * 32 * D];
+    typedef Walk<D, E4M3, S> W;
+    __shared__ __attribute__((aligned(1024))) char lds[4 * W::kTile];
     const int wave = uniform((int)threadIdx.x >> 6), per_row = a.H * a.blocks;
     const int t = (int)(blockIdx.x / (uint32_t)per_row) * 4 + wave, hb = (int)(blockIdx.x % (uint32_t)per_row);
     if (t >= a.Tq) return;
-    Walk<D, E4M3> w(a, lds + wave * 32 * D);
+    W w(a, lds + wave * W::kTile);
     w.h = hb / a.blocks;
     const int first = (hb - w.h * a.blocks) * 16, rows = min(16, a.G - first);
-    w.picks = a.picks + ((int64_t)t * a.H + w.h) * a.count, w.g0 = 0, w.stride = 2;
+    w.picks = a.picks + ((int64_t)t * a.H + w.h) * a.count, w.g0 = 0, w.stride = W::kGroups;
     const int pick = w.entry(0);  // on its way while the row is looked for
     const Row row = find_row(a.cu, a.lens, a.B, a.Tq, a.max_pages << a.shift, t);
     if (row.b < 0) return;
-    w.pos = row.pos, w.groups = entries(a, row.pos) << (a.shift - 4), w.steps = (w.groups + 1) / 2;
+    w.pos = row.pos, w.groups = entries(a, row.pos) << (a.shift - 4), w.steps = (w.groups + W::kGroups - 1) / W::kGroups;
     w.table = a.table + row.b * a.max_pages;
     w.look_up(0, pick);
     w.queries(t, first, rows);
@@ -824,10 +903,11 @@ __global__ __launch_bounds__(256, 2) void attn_blocks_many_kernel(BlocksArgs a) 
 // Few items: the 4 waves of a workgroup, and `parts` workgroups, take an item's steps in
 // turn; they are joined in LDS, and over the parts by the workgroup that finishes last
 // (qw3_attn_dev.h).
-template <int D, bool E4M3>
+template <int D, bool E4M3, int S>
 __global__ __launch_bounds__(256, 2) void attn_blocks_few_kernel(BlocksArgs a) {
+    typedef Walk<D, E4M3, S> Wave;
     constexpr int R = 16, W = 4, kPad = D + 4;
-    constexpr int kTurn = W * 32 * D, kJoin = W * R * kPad * 4;
+    constexpr int kTurn = W * Wave::kTile, kJoin = W * R * kPad * 4;
     __shared__ __attribute__((aligned(1024))) char lds[kTurn > kJoin ? kTurn : kJoin];
     __shared__ float stat[2][W][R];
     __shared__ int arrived;
@@ -835,11 +915,11 @@ __global__ __launch_bounds__(256, 2) void attn_blocks_few_kernel(BlocksArgs a) {
     if (a.parts > 1 && blockIdx.x == 0) clear_next<256>(a.clear);
     const int item = (int)(blockIdx.x / (uint32_t)a.parts), part = (int)blockIdx.x - item * a.parts;
     const int t = (int)((uint32_t)item / (uint32_t)per_row), hb = item - t * per_row;
-    Walk<D, E4M3> w(a, lds + wave * 32 * D);
+    Wave w(a, lds + wave * Wave::kTile);
     w.h = hb / a.blocks;
     const int first = (hb - w.h * a.blocks) * R, rows = min(R, a.G - first);
     w.picks = a.picks + ((int64_t)t * a.H + w.h) * a.count;
-    w.g0 = 2 * (part * W + wave), w.stride = 2 * W * a.parts;
+    w.g0 = Wave::kGroups * (part * W + wave), w.stride = Wave::kGroups * W * a.parts;
     const int pick = w.entry(0);  // on its way while the row is looked for
     w.queries(t, first, rows);
     const Row row = find_row(a.cu, a.lens, a.B, a.Tq, a.max_pages << a.shift, t);
@@ -896,7 +976,7 @@ __global__ __launch_bounds__(256, 2) void attn_blocks_few_kernel(BlocksArgs a) {
     if (tid == 0) __hip_atomic_store(a.counts + item, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int S>
 qw3_status launch_blocks(BlocksArgs a, hipStream_t stream) {
     int cus = 0;
     qw3_status st = cu_count(&cus);
@@ -904,7 +984,7 @@ qw3_status launch_blocks(BlocksArgs a, hipStream_t stream) {
     const int64_t items = (int64_t)a.Tq * a.H * a.blocks;
     if (items >= 8 * (int64_t)cus) {  // an item for each wave fills the card
         const int64_t wgs = ceil_div(a.Tq, 4) * a.H * a.blocks;
-        hipLaunchKernelGGL((attn_blocks_many_kernel<D, E4M3>), dim3((unsigned)wgs), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((attn_blocks_many_kernel<D, E4M3, S>), dim3((unsigned)wgs), dim3(256), 0, stream, a);
         return check_launch();
     }
     // An item of n units of 128 keys in parts of u units takes u + 0.14 n / u, as in
@@ -925,8 +1005,14 @@ qw3_status launch_blocks(BlocksArgs a, hipStream_t stream) {
         st = counters(stream, (int)items, &a.counts, &a.clear);
         if (st != QW3_OK) return st;
     }
-    hipLaunchKernelGGL((attn_blocks_few_kernel<D, E4M3>), dim3((unsigned)(items * a.parts)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((attn_blocks_few_kernel<D, E4M3, S>), dim3((unsigned)(items * a.parts)), dim3(256), 0, stream, a);
     return check_launch();
+}
+
+template <int D, bool E4M3>
+qw3_status launch_blocks(const BlocksArgs &a, hipStream_t stream) {
+    if (D == 64 && a.G <= 4) return launch_blocks<D, E4M3, D == 64 ? 4 : 2>(a, stream);
+    return a.G <= 8 ? launch_blocks<D, E4M3, 2>(a, stream) : launch_blocks<D, E4M3, 1>(a, stream);
 }
 
 constexpr int64_t kTileKeys = 32768;              // words of LDS for the keys of 16 rows

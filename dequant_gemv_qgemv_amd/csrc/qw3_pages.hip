@@ -554,6 +554,7 @@ __global__ __launch_bounds__(1024) void compact_move_kernel(CompactArgs a) {
     if (tid == 0) drawn = (int)((uint32_t)atomicAdd(a.ticket, 1) - (uint32_t)a.epoch * (uint32_t)a.units);
     __syncthreads();
     const int unit = drawn;
+    if ((uint32_t)unit >= gridDim.x) return;  // calls that overlap, again
     // the unit's tokens: `chunk` of 2^token_shift; its kv heads: `group` of 2^head_shift
     const int chunk = unit / lanes, lane = unit - chunk * lanes;
     const int layer = lane / a.groups, group = lane - layer * a.groups;

@@ -65,7 +65,8 @@ enum {
     QW3_ERR_SHAPE = -2, /* negative size, K % 128 != 0, or K > QW3_MAX_K      */
     QW3_ERR_ALIGN = -3, /* a pointer is not aligned as stated above           */
     QW3_ERR_HIP = -4,   /* the HIP runtime reported an error                  */
-    QW3_ERR_CAPTURE = -5, /* qgemm_w3g128_smallM, qattn_cache or qattn_prompt would have to
+    QW3_ERR_CAPTURE = -5, /* qgemm_w3g128_smallM, qattn_cache, qattn_prompt, qcache_compact,
+                             qblock_select or qattn_blocks would have to
                              allocate while the stream is being captured       */
     QW3_ERR_SCRATCH = -6  /* qgemm_w3g128_smallM_noalloc needs more than
                              QW3_NOALLOC_SCRATCH_BYTES of scratch               */
