@@ -605,11 +605,11 @@ struct Bits<64> {
 // at a time, a step.  What a wave has of an item: the steps' pages, the codes and scales on
 // their way, and the sums.
 // The matrix unit's result has 16 columns.  Up to 16 queries have one each (S = 1); up to
-// 8 have two, up to 4 four, for S subsets of the keys: column c has query c % (16 / S) and
-// the step's groups c / (16 / S).  The product of a group with queries that are zeros in
-// the other columns adds nothing there, so the groups share a result, and a score, an
-// exponential and a weight are made once for each query and key, in all lanes.  The columns
-// of a query have one maximum, and their sums are added at the end.
+// 8 have two, up to 4 four, for S subsets of the keys: column c has query c % (16 / S), and
+// of the results of a step's groups that of group c / (16 / S).  So all lanes have scores,
+// and each exponential and weight is made once.  The columns of a query have one maximum,
+// and their sums are added at the end.  512 rows of 8 kv heads, 40 pages of 32 tokens each,
+// e4m3: 4 queries of 64 channels 51 us, 8 of them 59 (S = 1: 70), of 128 channels 110 (115).
 template <int D, bool E4M3, int S>
 struct Walk {
     static constexpr int kPieces = D / 16, kEach = D / 64;         // 16-byte pieces of a row; of a group, for each lane
@@ -626,7 +626,7 @@ struct Walk {
     int ids, bases;  // of kAhead steps: lane kGroups s + g has of group g of step s the page (-1: none that the row sees) and its first token's position
     uint4 k[kGroups][kEach], v[kGroups][kEach];
     float4 ks[kSets], vs[kSets];
-    bf8_t qf[S][D / 32];
+    bf8_t qf[D / 32];
     f4_t acc[D / 16];
     float m, l;
 
@@ -697,11 +697,7 @@ struct Walk {
     __device__ __forceinline__ void queries(int t, int first, int rows) {
         const uint16_t *qp = a.q + (int64_t)t * a.q_ts + (int64_t)(h * a.G + first + min(col % kCols, rows - 1)) * a.q_hs;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            const bf8_t x = *reinterpret_cast<const bf8_t *>(qp + 16 * (quarter + 4 * (i / 2)) + 8 * (i & 1));
-#pragma unroll
-            for (int g = 0; g < S; ++g) qf[g][i] = S == 1 || own == g ? x : bf8_t{};
-        }
+        for (int i = 0; i < D / 32; ++i) qf[i] = *reinterpret_cast<const bf8_t *>(qp + 16 * (quarter + 4 * (i / 2)) + 8 * (i & 1));
     }
 
     // The columns of a query: the largest, the sum.
@@ -717,8 +713,7 @@ struct Walk {
     }
 
     // A step; masked: of some group not all 16 keys are seen.  What is hidden is
-    // hidden from all columns, which are queries of one token: its values are taken as
-    // zeros, and so are its keys where other groups share their result.
+    // hidden from all columns, which are queries of one token: its values are taken as zeros.
     template <bool kMasked>
     __device__ __forceinline__ void step(int s, bits_t seen) {
 #pragma unroll
@@ -739,17 +734,19 @@ struct Walk {
         }
         f4_t sc[kSets];
 #pragma unroll
-        for (int x = 0; x < kSets; ++x) sc[x] = f4_t{};
-#pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-            f4_t &to = sc[g % kSets];
-            const bool hidden = S > 1 && E4M3 && kMasked && !((seen >> (16 * g + col)) & 1);
+            f4_t x = {};
 #pragma unroll
             for (int c = 0; c < kEach; ++c) {
-                const uint4 w = hidden ? make_uint4(0, 0, 0, 0) : k[g][c];
-                to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8<E4M3>(w.x, w.y), qf[g % S][2 * c], to, 0, 0, 0);
-                to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8<E4M3>(w.z, w.w), qf[g % S][2 * c + 1], to, 0, 0, 0);
+                const uint4 w = k[g][c];
+                x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8<E4M3>(w.x, w.y), qf[2 * c], x, 0, 0, 0);
+                x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8<E4M3>(w.z, w.w), qf[2 * c + 1], x, 0, 0, 0);
             }
+            if (S == 1 || g == 0)
+                sc[g % kSets] = x;
+            else
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sc[0][r] = own == g ? x[r] : sc[0][r];
         }
         ahead(s);
         bool hid[kSets][4];
@@ -871,8 +868,9 @@ struct Walk {
 };
 
 // Many items: one for each wave, the same kv head of 4 neighbouring rows in a workgroup.
+// With 64 channels four waves of a SIMD have the registers (51 us where three took 54).
 template <int D, bool E4M3, int S>
-__global__ __launch_bounds__(256, 2) void attn_blocks_many_kernel(BlocksArgs a) {
+__global__ __launch_bounds__(256, D == 64 ? 4 : 2) void attn_blocks_many_kernel(BlocksArgs a) {
     typedef Walk<D, E4M3, S> W;
     __shared__ __attribute__((aligned(1024))) char lds[4 * W::kTile];
     const int wave = uniform((int)threadIdx.x >> 6), per_row = a.H * a.blocks;
@@ -977,16 +975,28 @@ __global__ __launch_bounds__(256, 2) void attn_blocks_few_kernel(BlocksArgs a) {
 }
 
 template <int D, bool E4M3, int S>
+qw3_status launch_many(const BlocksArgs &a, hipStream_t stream) {
+    const int64_t wgs = ceil_div(a.Tq, 4) * a.H * a.blocks;
+    hipLaunchKernelGGL((attn_blocks_many_kernel<D, E4M3, S>), dim3((unsigned)wgs), dim3(256), 0, stream, a);
+    return check_launch();
+}
+template <int D, bool E4M3, int S>
+qw3_status launch_few(const BlocksArgs &a, int64_t items, hipStream_t stream) {
+    hipLaunchKernelGGL((attn_blocks_few_kernel<D, E4M3, S>), dim3((unsigned)(items * a.parts)), dim3(256), 0, stream, a);
+    return check_launch();
+}
+
+template <int D, bool E4M3>
 qw3_status launch_blocks(BlocksArgs a, hipStream_t stream) {
     int cus = 0;
     qw3_status st = cu_count(&cus);
     if (st != QW3_OK) return st;
     const int64_t items = (int64_t)a.Tq * a.H * a.blocks;
-    if (items >= 8 * (int64_t)cus) {  // an item for each wave fills the card
-        const int64_t wgs = ceil_div(a.Tq, 4) * a.H * a.blocks;
-        hipLaunchKernelGGL((attn_blocks_many_kernel<D, E4M3, S>), dim3((unsigned)wgs), dim3(256), 0, stream, a);
-        return check_launch();
-    }
+    const int subsets = a.G <= 4 ? 4 : a.G <= 8 ? 2 : 1;
+    if (items >= 8 * (int64_t)cus)  // an item for each wave fills the card
+        return subsets == 4   ? launch_many<D, E4M3, 4>(a, stream)
+               : subsets == 2 ? launch_many<D, E4M3, 2>(a, stream)
+                              : launch_many<D, E4M3, 1>(a, stream);
     // An item of n units of 128 keys in parts of u units takes u + 0.14 n / u, as in
     // qattn_cache: least at u = sqrt(0.14 n); and no more parts than the CUs have room for,
     // two workgroups each.  One row of 8 kv heads, 64 pages of 64 tokens, with 1, 4, 8, 16, 32
@@ -1005,14 +1015,11 @@ qw3_status launch_blocks(BlocksArgs a, hipStream_t stream) {
         st = counters(stream, (int)items, &a.counts, &a.clear);
         if (st != QW3_OK) return st;
     }
-    hipLaunchKernelGGL((attn_blocks_few_kernel<D, E4M3, S>), dim3((unsigned)(items * a.parts)), dim3(256), 0, stream, a);
-    return check_launch();
-}
-
-template <int D, bool E4M3>
-qw3_status launch_blocks(const BlocksArgs &a, hipStream_t stream) {
-    if (D == 64 && a.G <= 4) return launch_blocks<D, E4M3, D == 64 ? 4 : 2>(a, stream);
-    return a.G <= 8 ? launch_blocks<D, E4M3, 2>(a, stream) : launch_blocks<D, E4M3, 1>(a, stream);
+    // Workgroups that are all on the card at once wait for memory, and gain nothing from fewer
+    // instructions: 48 rows of 8 heads, 64 pages of 16 tokens of 128 channels, S = 1, 2, 4: 19, 20,
+    // 21 us; 500 rows of 2 heads, 100 pages of 32 tokens of 64 channels: 58, 50, 45.
+    if (items <= 2 * (int64_t)cus || subsets == 1) return launch_few<D, E4M3, 1>(a, items, stream);
+    return subsets == 4 ? launch_few<D, E4M3, 4>(a, items, stream) : launch_few<D, E4M3, 2>(a, items, stream);
 }
 
 constexpr int64_t kTileKeys = 32768;              // words of LDS for the keys of 16 rows

@@ -225,7 +225,12 @@ ATTEND = [  # page size, heads, kv heads, channels, lengths, new tokens, count
     (16, 1, 1, 64, [1], None, 1), (16, 64, 8, 128, [1000], None, 12), (64, 8, 1, 64, [4000, 100, 64, 65], None, 9),
     (16, 34, 2, 128, [300, 90], None, 5), (32, 5, 5, 128, [500, 40], [9, 40], 4), (256, 6, 2, 64, [900, 255], [7, 200], 2),
     (16, 8, 2, 128, [400], [390], 6), (128, 4, 4, 64, [700, 300, 0], [300, 290, 0], 3), (16, 128, 2, 64, [90, 33], [20, 17], 4),
-    (16, 32, 32, 128, [60, 80, 7], [60, 11, 7], 3), (64, 16, 2, 128, [30000], None, 200)]
+    (16, 32, 32, 128, [60, 80, 7], [60, 11, 7], 3), (64, 16, 2, 128, [30000], None, 200),
+    # more than 512 items of up to 4, 8 and 16 queries, and more than 2048
+    (16, 8, 4, 128, [300, 77], [140, 60], 7), (16, 28, 4, 64, [260, 70], [150, 70], 5), (32, 18, 2, 64, [333], [320], 3),
+    (16, 4, 4, 128, [500], [200], 9), (16, 16, 4, 64, [700, 20], [510, 20], 4), (32, 12, 4, 128, [40, 620], [40, 490], 5),
+    (16, 24, 4, 64, [800], [600], 6), (16, 32, 4, 128, [650, 9], [560, 9], 5), (16, 64, 4, 64, [560, 1], [530, 1], 5),
+    (32, 72, 4, 128, [310, 45], [260, 40], 4), (64, 6, 6, 64, [1000], [400], 6)]
 
 
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
