@@ -74,7 +74,9 @@ __device__ __forceinline__ float max_ror4(float x) { return max_bits(__float_as_
 
 // A wave has one page and head.  D / 16 lanes take a row, 16 channels each, and the
 // wave 1024 / D rows at a time; what lanes of the same channels hold is joined at the
-// end, halving in each step the channels that a lane stands for.
+// end, halving in each step the channels that a lane stands for.  30,001 tokens of 8 heads
+// of 128 channels in pages of 32, e4m3: 9.9 us, 33 MB at 3.3 TB/s; vector instructions (a
+// conversion, a product, two comparisons for each code) are issued 64 % of the time.
 template <int D, bool E4M3>
 __global__ __launch_bounds__(256) void bounds_kernel(BoundsArgs a) {
     constexpr int kPieces = D / 16, kRows = 64 / kPieces;
@@ -511,7 +513,8 @@ __device__ __forceinline__ Tile find_tile(const SelectArgs &a, int rank) {
 }
 
 // 16 rows of a sequence and a kv head: the pages' bounds are read once for all of
-// them, and each wave picks for one.
+// them, and each wave picks for one.  510 rows of 8 heads, 40 of up to 938 pages: 17.5 us;
+// vector instructions, of the picking for the most part, are issued half of the time.
 template <int D>
 __global__ __launch_bounds__(1024) void select_tile_kernel(SelectArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint32_t keys[];
@@ -537,7 +540,8 @@ __global__ __launch_bounds__(1024) void select_tile_kernel(SelectArgs a) {
 }
 
 // Scores alone, into memory: 16 rows of a sequence, a kv head and 256 of every
-// 256 gridDim.y pages.
+// 256 gridDim.y pages.  48 rows of up to 16,000 tokens, 8 heads of 128 channels, pages of 16:
+// 10.5 us for 20 MB, the chain of length, page number and bounds; picking from them 4.4.
 template <int D>
 __global__ __launch_bounds__(256) void score_kernel(SelectArgs a) {
     __shared__ __attribute__((aligned(16))) uint8_t w[16 * 2 * D];
@@ -869,6 +873,8 @@ struct Walk {
 
 // Many items: one for each wave, the same kv head of 4 neighbouring rows in a workgroup.
 // With 64 channels four waves of a SIMD have the registers (51 us where three took 54).
+// 510 rows of 4 queries of 8 heads of 64 channels, 40 pages of 32 tokens, e4m3: 55 us; vector
+// instructions take 63 % of the time and the matrix unit 18 %, and they hardly overlap.
 template <int D, bool E4M3, int S>
 __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void attn_blocks_many_kernel(BlocksArgs a) {
     typedef Walk<D, E4M3, S> W;
@@ -900,7 +906,8 @@ __global__ __launch_bounds__(256, D == 64 ? 4 : 2) void attn_blocks_many_kernel(
 
 // Few items: the 4 waves of a workgroup, and `parts` workgroups, take an item's steps in
 // turn; they are joined in LDS, and over the parts by the workgroup that finishes last
-// (qw3_attn_dev.h).
+// (qw3_attn_dev.h).  48 rows of 8 heads, 64 pages of 16 tokens of 128 channels: 20 us for 62
+// MB; a CU reads some 30 bytes a ns, and of 384 items many have to share one.
 template <int D, bool E4M3, int S>
 __global__ __launch_bounds__(256, 2) void attn_blocks_few_kernel(BlocksArgs a) {
     typedef Walk<D, E4M3, S> Wave;
@@ -1026,7 +1033,7 @@ constexpr int64_t kTileKeys = 32768;              // words of LDS for the keys o
 constexpr int64_t kKeyBytes = int64_t(64) << 20;  // of keys in memory at a time
 constexpr int64_t kRowPages = 256;
 
-// One CU reads 30 GB/s of bounds, 512 pages of 128 channels in 4.5 us.  So a row's pages
+// One CU reads some 30 bytes of bounds a ns, 512 pages of 128 channels in 4.5 us.  So a row's pages
 // are read by one workgroup only where a table has few; else by as many as there are
 // pages for, through memory, and picked by a second launch.  One row of 8 kv heads, 64 of
 // 256, 512, 1024, 2048 pages: in one workgroup 7.6, 11.5, 19.7, 34.9 us, through memory

@@ -3,9 +3,10 @@
 // of the library (C ABI in include/qw3.h) shares -- the format, the decode,
 // the activation conversion and the exactness guard -- and the host helpers
 // its translation units share (qw3_gemv.hip: the batch-1 kernels; qw3.hip:
-// the other products, the workspace and their C ABI; qw3_cache.hip and
-// qw3_attn.hip: the key/value cache and attention, which use only the host
-// helpers).
+// the other products, the workspace and their C ABI; qw3_cache.hip,
+// qw3_attn.hip, qw3_rope.hip, qw3_pages.hip and qw3_blocks.hip: the key/value
+// cache, attention, rotary positions, the cache's pages and attention over
+// selected pages, which use the host helpers and some of the exchanges between lanes).
 //
 // Format (GSQ model card "Llama-3.1-70B-Instruct-3Bit-GSQ", "Storage layout"):
 // a row of K weights is a little-endian bitstream of 3K bits packed into 3K/32

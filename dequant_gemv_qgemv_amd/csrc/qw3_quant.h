@@ -16,8 +16,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // The quotients.  A row's 128 divisions by the same s cost more than all else of
-// a kernel that writes it.  With r the correctly rounded 1 / s, one division for the row, each
-// quotient is refined by its exact remainder: q = x r; q += (x - q s) r makes it
+// a kernel that writes it.  With r the correctly rounded 1 / s, one division for
+// the row, each quotient is refined by its exact remainder: q = x r; q += (x - q s) r makes it
 // one of the two floats around x / s; q += (x - q s) r the correctly rounded one
 // (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
 // processor", 1990), where neither r nor a remainder leaves the normal numbers:
