@@ -445,7 +445,8 @@ __device__ __forceinline__ void pick(const SelectArgs &a, const uint32_t *keys, 
             }
         }
         const int taken = min(equals, left), e_taken = min(equals + e_before, left) - taken;
-        if (more || (equal && equals + e_before < left)) out[place + m_before + e_taken] = i;
+        const int to = place + m_before + e_taken;  // below count, but for calls that overlap and share the keys' memory
+        if ((more || (equal && equals + e_before < left)) && to < a.count) out[to] = i;
         place += mores + min(equals + same, left) - taken;
         equals += same;
     };

@@ -541,14 +541,14 @@ __global__ __launch_bounds__(256) void compact_rank_kernel(CompactArgs a) {
 // workgroup draws once it runs; a unit says that it has read before it waits for any
 // other, and waits only for units of lower tickets: those run, and read without
 // waiting.  Should calls overlap that share the workspace, which they must not, a wait
-// ends after kPolls looks all the same.
+// ends after kPolls looks all the same (some 50 ms; a unit reads for a few us).
 // The rows of a token are read by its own unit alone, and other units write to them only
 // after that, so no unit ever reads what another has written: a flag orders a read
 // before a write, passes no data, and needs no cache written back.
 // Half of 50,000 tokens of 8 heads of 128 channels in two layers: 45 us (211 MB, 4.7
 // TB/s), of which the waits are 4; in units of 256 rows 85, since all draw from one place (6
 // ns each); through memory in two steps 105.
-constexpr int kUnitRows = 1024, kPolls = 1 << 20;
+constexpr int kUnitRows = 1024, kPolls = 1 << 16;
 
 template <int D>
 __global__ __launch_bounds__(1024) void compact_move_kernel(CompactArgs a) {
@@ -559,7 +559,7 @@ __global__ __launch_bounds__(1024) void compact_move_kernel(CompactArgs a) {
     if (tid == 0) drawn = (int)((uint32_t)atomicAdd(a.ticket, 1) - (uint32_t)a.epoch * (uint32_t)a.units);
     __syncthreads();
     const int unit = drawn;
-    if ((uint32_t)unit >= gridDim.x) return;  // calls that overlap, again
+    if ((uint32_t)unit >= gridDim.x) return;  // calls that overlap, as below
     // the unit's tokens: `chunk` of 2^token_shift; its kv heads: `group` of 2^head_shift
     const int chunk = unit / lanes, lane = unit - chunk * lanes;
     const int layer = lane / a.groups, group = lane - layer * a.groups;
@@ -567,10 +567,13 @@ __global__ __launch_bounds__(1024) void compact_move_kernel(CompactArgs a) {
     int over = -1;  // the chunk whose row this thread's token is written over
     if (tid < n) {
         const int4 move = a.moves[t0 + tid];
-        const int32_t *table = a.table + move.x * a.max_pages;
-        from[tid] = move.z < 0 ? -1 : row_of(a, table, move.y, 0, 0);
-        to[tid] = move.z < 0 ? -1 : row_of(a, table, move.z, 0, 0);
-        if (move.z >= 0) over = move.w >> a.token_shift;
+        // always so where it moves, but for calls that overlap: those spoil each other's rows, and reach no others
+        const uint32_t room = (uint32_t)(a.max_pages << a.shift);
+        const bool moves = move.z >= 0 && (uint32_t)move.z < room && (uint32_t)move.y < room && (uint32_t)move.x < (uint32_t)a.B;
+        const int32_t *table = a.table + (moves ? move.x * a.max_pages : 0);
+        from[tid] = moves ? row_of(a, table, move.y, 0, 0) : -1;
+        to[tid] = moves ? row_of(a, table, move.z, 0, 0) : -1;
+        if (moves) over = move.w >> a.token_shift;
     }
     __syncthreads();
     uint4 *codes = reinterpret_cast<uint4 *>(a.codes + (a.layer0 + layer) * a.layer_rows * D);
@@ -597,7 +600,7 @@ __global__ __launch_bounds__(1024) void compact_move_kernel(CompactArgs a) {
     for (int p = 0; p < kPasses; ++p) asm volatile("" : "+v"(w[p].x), "+v"(w[p].y), "+v"(w[p].z), "+v"(w[p].w), "+v"(scale[p]));
     __syncthreads();
     if (tid == 0) __hip_atomic_store(a.read + unit, a.epoch + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (over >= 0 && over != chunk) {
+    if (over >= 0 && over < chunk) {
         const int *other = a.read + over * lanes + lane;
         for (int polls = 0; polls < kPolls; ++polls) {
             if (__hip_atomic_load(other, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) > a.epoch) break;
