@@ -39,10 +39,11 @@ def _bind(lib, fail):
 # torch offers it, one comparison for each property that is checked.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(index, fn, where, *args):
-    if index == torch.cuda.current_device():
+    if index == _device():
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -112,8 +113,8 @@ def _scale(sm_scale, dim):
 def _out(out, like, shape):
     """`out` checked, or a new contiguous bf16 tensor of `shape` on like's device."""
     if out is None:
-        if like.dtype is torch.bfloat16 and like.is_contiguous() and like.shape == shape:
-            return torch.empty_like(like)
+        if like.shape == shape:
+            return torch.empty_like(like, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
         return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
     if out.dtype is not torch.bfloat16 or out.shape != shape or out.device != like.device or not out.is_contiguous():
         raise ValueError("out must be contiguous bfloat16 %s on %s" % (tuple(shape), like.device))

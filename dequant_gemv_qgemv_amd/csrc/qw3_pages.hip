@@ -339,7 +339,6 @@ struct CompactArgs {
     int64_t layer_rows;  // rows of one layer: pages 2 H page_size
     // many tokens, in the workspace: ...
     int4 *moves;  // ... for each its sequence, where it is, where it goes (-1: it stays), and the token there now
-    int *kept;    // ... how many of each 4096 stay
     int *ticket;  // ... how many units have been drawn
     int *read;    // ... whether a unit has read its rows, by the number of its launch
     // a launch: `layers` layers from layer0 on, the epoch-th, with `units` in each of those before
@@ -430,12 +429,12 @@ __global__ __launch_bounds__(256) void compact_kernel(CompactArgs a) {
     if (layer == 0 && h == 0 && which == 0 && tid == 0) a.lens_out[b] = dst;
 }
 
-// For many tokens of few sequences, by all of the card: how many are kept of each 4096,
-// where each goes, and then their rows from one place to the other.
-constexpr int kCountShift = 12, kCountTokens = 1 << kCountShift;
+// For many tokens of few sequences, by all of the card: where each goes, and then their
+// rows from one place to the other.
+constexpr int kChunkShift = 11, kChunkTokens = 1 << kChunkShift;
 
-// The workgroup's sequence and 4096 of its new tokens: sequence b owns the workgroups
-// from start / 4096 + b on, room for its tokens whatever their number.
+// The workgroup's sequence and 2048 of its new tokens: sequence b owns the workgroups
+// from start / 2048 + b on, room for its tokens whatever their number.
 struct Chunk {
     NewTokens s;
     int b, at, n;  // b < 0: nothing; tokens s.first + at .. + n - 1
@@ -447,7 +446,7 @@ __device__ __forceinline__ Chunk find_chunk(const CompactArgs &a) {
     if (a.cu) {
         for (int base = 0; base < a.B; base += 64) {
             const int start = max(floor, wave_scan_max(base + lane < a.B ? clamp_row(a.cu[min(base + lane, a.B - 1)], a.total) : 0));
-            const unsigned long long in = __ballot(base + lane < a.B && (start >> kCountShift) + base + lane <= rank);
+            const unsigned long long in = __ballot(base + lane < a.B && (start >> kChunkShift) + base + lane <= rank);
             if (in == 0) break;
             const int i = __popcll(in) - 1;
             c.b = base + i, first = __builtin_amdgcn_readlane(start, i);
@@ -460,8 +459,8 @@ __device__ __forceinline__ Chunk find_chunk(const CompactArgs &a) {
     }
     c.s.first = first, c.s.n = a.cu ? max(clamp_row(a.cu[c.b + 1], a.total) - first, 0) : 1;
     c.s.len = (int)max((int64_t)0, min((int64_t)a.lens[c.b], a.max_pages << a.shift));
-    c.at = a.cu ? (rank - (first >> kCountShift) - c.b) << kCountShift : 0;
-    c.n = max(min(kCountTokens, c.s.n - c.at), 0);
+    c.at = a.cu ? (rank - (first >> kChunkShift) - c.b) << kChunkShift : 0;
+    c.n = max(min(kChunkTokens, c.s.n - c.at), 0);
     if (c.at > 0 && c.n == 0) c.b = -1;  // every sequence has a first chunk, of no tokens perhaps
     return c;
 }
@@ -473,24 +472,39 @@ __device__ __forceinline__ bool stays(const CompactArgs &a, const Chunk &c, int 
     return (keep != 0) & (i < c.n) & (c.s.len - c.s.n + c.at + i >= 0);
 }
 
-__global__ __launch_bounds__(256) void compact_count_kernel(CompactArgs a) {
-    // the ticket and the flags of compact_move_kernel, which lie together, start from zeros
-    for (int i = (int)blockIdx.x * 256 + threadIdx.x; i <= a.units; i += (int)gridDim.x * 256) a.ticket[i] = 0;
-    const Chunk c = find_chunk(a);
-    if (c.b < 0) return;
-    int n = 0, all;
-    if (c.n > 0)
+// How many of n bytes are not zero, those that this thread of 256 takes: 16 at a time.
+__device__ __forceinline__ int count_bytes(const uint8_t *p, int n) {
+    const int head = min(n, (int)(-(uintptr_t)p & 15)), pieces = (n - head) / 16, tail = head + 16 * pieces;
+    int sum = 0;
+    if ((int)threadIdx.x < head) sum += p[threadIdx.x] != 0;
+    if ((int)threadIdx.x < n - tail) sum += p[tail + threadIdx.x] != 0;
+    const uint4 *words = reinterpret_cast<const uint4 *>(p + head);
+    for (int i0 = threadIdx.x; i0 < pieces; i0 += 256 * 8) {
+        uint4 w[8];  // on their way together
 #pragma unroll
-        for (int k = 0; k < kCountTokens / 256; ++k) n += stays(a, c, 256 * k + threadIdx.x) ? 1 : 0;
-    group_scan<256>(n, &all);
-    if (threadIdx.x == 0) a.kept[blockIdx.x] = all;
+        for (int j = 0; j < 8; ++j) w[j] = words[min(i0 + 256 * j, pieces - 1)];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t d[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+            int n16 = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) n16 += __popc((((d[k] & 0x7f7f7f7fu) + 0x7f7f7f7fu) | d[k]) & 0x80808080u);
+            sum += i0 + 256 * j < pieces ? n16 : 0;
+        }
+    }
+    return sum;
 }
 
+// Each workgroup counts the kept tokens before its own anew: with a launch that counts for all
+// the call took 54 us for two contexts of 25,000 tokens in two layers, so 51 (this one 7).  The
+// counting grows with the square of a sequence, for 2^20 tokens to some 3 % of the call.
 __global__ __launch_bounds__(256) void compact_rank_kernel(CompactArgs a) {
-    constexpr int kTurns = kCountTokens / 256;
+    constexpr int kTurns = kChunkTokens / 256;
     __shared__ int waves[kTurns][4];
     __shared__ int top;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    // the ticket and the flags of compact_move_kernel, which lie together, start from zeros
+    for (int i = (int)blockIdx.x * 256 + tid; i <= a.units; i += (int)gridDim.x * 256) a.ticket[i] = 0;
     // rows of no sequence, by all workgroups: before the first start and from the largest on
     const int4 nowhere = make_int4(0, 0, -1, 0);
     if (a.cu) {
@@ -515,15 +529,13 @@ __global__ __launch_bounds__(256) void compact_rank_kernel(CompactArgs a) {
         before[k] = __popcll(m & ((1ull << lane) - 1));
         if (lane == 0) waves[k][wave] = __popcll(m);
     }
-    // kept tokens of the sequence's chunks before this one
-    int sum = 0, base, all;
-    const int chunk0 = (int)blockIdx.x - (c.at >> kCountShift);
-    for (int i = tid; i < c.at >> kCountShift; i += 256) sum += a.kept[chunk0 + i];
-    group_scan<256>(sum, &base);
-    static_assert(kTurns * 4 == 64, "one lane for each wave's turn");
-    const int mine = (&waves[0][0])[lane], upto = wave_scan(mine);
-    all = __builtin_amdgcn_readlane(upto, 63);
-    const int ctx = c.s.len - c.s.n, dst = max(ctx, 0) + base;
+    // kept tokens of the sequence's chunks before this one, from its first that is there on
+    const int ctx = c.s.len - c.s.n, there = min(max(-ctx, 0), c.at);
+    int base;
+    group_scan<256>(count_bytes(a.keep + c.s.first + there, c.at - there), &base);
+    static_assert(kTurns * 4 <= 64, "one lane for each wave's turn");
+    const int mine = lane < kTurns * 4 ? (&waves[0][0])[lane] : 0, upto = wave_scan(mine);
+    const int all = __builtin_amdgcn_readlane(upto, 63), dst = max(ctx, 0) + base;
 #pragma unroll
     for (int k = 0; k < kTurns; ++k) {
         const int i = 256 * k + tid, from = ctx + c.at + i;
@@ -637,15 +649,13 @@ qw3_status launch_compact(CompactArgs a, int64_t layers, hipStream_t stream) {
     some = some < 1 ? 1 : some < layers ? some : layers;
     const int64_t units = chunks * a.groups * some;
     a.units = (int)units;
-    const int64_t counts = a.cu ? (a.total >> kCountShift) + a.B : a.B;
+    const int64_t ranks = a.cu ? (a.total >> kChunkShift) + a.B : a.B;
     void *ws = nullptr;
-    const qw3_status st = workspace(stream, (size_t)(a.total * int64_t(16) + (counts + 1 + units) * int64_t(4)), &ws);
+    const qw3_status st = workspace(stream, (size_t)(a.total * int64_t(16) + (1 + units) * int64_t(4)), &ws);
     if (st != QW3_OK) return st;
     a.moves = static_cast<int4 *>(ws);
-    a.kept = reinterpret_cast<int *>(a.moves + a.total);
-    a.ticket = a.kept + counts, a.read = a.ticket + 1;
-    hipLaunchKernelGGL(compact_count_kernel, dim3((unsigned)counts), dim3(256), 0, stream, a);
-    hipLaunchKernelGGL(compact_rank_kernel, dim3((unsigned)counts), dim3(256), 0, stream, a);
+    a.ticket = reinterpret_cast<int *>(a.moves + a.total), a.read = a.ticket + 1;
+    hipLaunchKernelGGL(compact_rank_kernel, dim3((unsigned)ranks), dim3(256), 0, stream, a);
     for (; a.layer0 < layers; a.layer0 += (int)some, ++a.epoch) {
         a.layers = (int)(some < layers - a.layer0 ? some : layers - a.layer0);
         hipLaunchKernelGGL((compact_move_kernel<D>), dim3((unsigned)(chunks * a.groups * a.layers)), dim3(1024), 0, stream, a);

@@ -513,8 +513,8 @@ qw3_status qcache_copy(void *codes, float *scales, const int32_t *copies, int64_
  * whose page is not there is zeros where it goes.  Pages are neither taken nor given
  * back: those behind the new length are used again by qcache_reserve and given up by
  * qcache_fork.  Pages that are written must not be shared.
- * Workspace, by the rules of qgemm_w3g128_smallM: none where Tq <= 512 B; else 17 Tq +
- * 4 B bytes, and 8 MiB at most.
+ * Workspace, by the rules of qgemm_w3g128_smallM: none where Tq <= 512 B; else 16 Tq
+ * bytes, and up to 9 MiB.
  * layers B H < 2^23 and Tq H < 2^30 (H rounded up to a power of two, above 8 to a
  * multiple of 8), else QW3_ERR_SHAPE.
  */

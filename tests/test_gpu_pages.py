@@ -201,6 +201,42 @@ def test_compact_out_of_range():
             same(scales, want_s)
 
 
+def test_compact_any_bytes_captured_and_replayed():
+    """By all of the card: keep of any values at any address, more tokens than there are; a graph with other contents."""
+    rng = np.random.default_rng(20)
+    page, width, heads, dim, rows = 64, 160, 2, 64, 11001
+    pages = 2 * width
+    table = rng.permutation(pages).reshape(2, width).astype(np.int32)
+    codes, scales = random_layers(rng, "int8", 1, pages, heads, page, dim)
+    pool = torch.zeros(rows + 40, dtype=torch.uint8, device="cuda")
+    lens, cu, t = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda"), dev(table)
+    for skew in (0, 1, 7, 15, 16, 23):
+        keep = pool[skew:skew + rows]
+
+        def call():
+            return q().qcache_compact(codes, scales, t, lens, keep, cu_q=cu)
+
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = call()
+        for have, starts in (([10240, 4000], [0, 8000, 11001]), ([2047, 900], [3, 6001, 10990]), ([9000, 3000], [0, 8193, 11001])):
+            say("compact", skew, have, starts)
+            bytes_ = np.where(rng.random(rows) < 0.5, 0, rng.choice([1, 2, 127, 128, 255], rows)).astype(np.uint8)
+            keep.copy_(torch.tensor(bytes_))
+            lens.copy_(dev(have))
+            cu.copy_(dev(starts))
+            want_c, want_s = codes.view(torch.uint8).cpu().numpy(), scales.cpu().numpy()
+            want = ref.compact(want_c, want_s, table, have, bytes_, np.array(starts), page)
+            graph.replay()
+            same(out, want)
+            same(codes.view(torch.uint8), want_c)
+            same(scales, want_s)
+
+
 @pytest.mark.parametrize("share", [0.02, 0.6, 0.999])
 def test_compact_many_heads(share):
     """Units of several groups of heads, by far more of them than run at a time."""
