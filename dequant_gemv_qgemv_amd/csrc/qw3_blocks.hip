@@ -215,6 +215,7 @@ struct SelectArgs {
     const int32_t *table, *lens, *cu;
     int32_t *picks;
     uint32_t *keys;  // in memory: those of the rows t0 .. t0 + rows - 1, [rows, H, pitch]
+    int *counts, *clear;  // how many workgroups of a row and kv head have finished, and the next call's counters
     int64_t q_ts, q_hs, max_pages, pages;
     int B, Tq, H, G, shift, count, first, recent, pitch, t0, rows;
 };
@@ -277,10 +278,10 @@ __device__ __forceinline__ uint32_t page_at(const SelectArgs &a, const int32_t *
 // Keys of the pages from p on below `pages`, 64 for each step of `stride` pages, by one wave;
 // page: page_at(p).  The matrix unit's rows are 16 pages, its columns the kRows rows' w,
 // which prepare() sees to, once the first pages are on their way.
-// to(row, page): where the keys of 4 pages go, for the first n rows.
-template <int D, int kRows, class Prepare, class To>
+// put(row, page, keys): the keys of 4 pages from one on, for the first n rows.
+template <int D, int kRows, class Prepare, class Put>
 __device__ __forceinline__ void score_pages(const SelectArgs &a, const int32_t *table, int h, int p, int stride, int pages, int n,
-                                            uint32_t page, const uint8_t *w, Prepare prepare, To to) {
+                                            uint32_t page, const uint8_t *w, Prepare prepare, Put put) {
     constexpr int kSteps = 2 * D / 64;
     const int lane = threadIdx.x & 63, col = lane & 15, quarter = lane >> 4;
     uint32_t step;
@@ -327,7 +328,7 @@ __device__ __forceinline__ void score_pages(const SelectArgs &a, const int32_t *
                 key[r] = s == kNoPage ? 0u : key_of((float)sum[r] * __uint_as_float(s));
             }
             if (col < n && at + 16 * j < pages)
-                *reinterpret_cast<uint4 *>(to(col, at + 16 * j + 4 * quarter)) = make_uint4(key[0], key[1], key[2], key[3]);
+                put(col, at + 16 * j + 4 * quarter, make_uint4(key[0], key[1], key[2], key[3]));
         }
         if (p < pages) load();
     }
@@ -348,6 +349,7 @@ template <int T>
 struct PickSpace {
     int bins[T > 64 ? 4 : 1][256];
     uint32_t waves[2][T / 64];
+    int taken[T > 64 ? 64 : 1];
 };
 
 // A row's picks out of `seen` pages, by T threads whose number among them is tid.
@@ -356,8 +358,9 @@ struct PickSpace {
 // a time, below the bits that all keys have in common, in counts of the keys that have the
 // bits found so far; then the pages are gone through in order, and of those with that key
 // the first are taken.
-template <int T>
-__device__ __forceinline__ void pick(const SelectArgs &a, const uint32_t *keys, int seen, int32_t *out, PickSpace<T> &space, int tid) {
+// key_at(i): page i's key; up to kHeld T of them are kept, more are read anew in each pass.
+template <int T, int kHeld, class Key>
+__device__ __forceinline__ void pick(const SelectArgs &a, Key key_at, int seen, int32_t *out, PickSpace<T> &space, int tid) {
     if (seen <= a.count) {
         for (int i = tid; i < a.count; i += T) out[i] = i < seen ? i : -1;
         return;
@@ -365,19 +368,18 @@ __device__ __forceinline__ void pick(const SelectArgs &a, const uint32_t *keys, 
     const int lane = tid & 63, wave = tid >> 6, lo = a.first, hi = seen - a.recent;
     int left = a.count - a.first - a.recent;
     const bool none = left <= 0;
-    // a few keys are kept, more are read anew in each pass
-    constexpr int kHeld = T == 64 ? 16 : 4;
+    constexpr int kWaves = T / 64;
     const bool held = hi - lo <= kHeld * T;
     uint32_t kept[kHeld];
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j) kept[j] = keys[min(lo + tid + T * j, hi - 1)];
+    for (int j = 0; j < kHeld; ++j) kept[j] = key_at(min(lo + tid + T * j, hi - 1));
     auto each = [&](auto f) {
         if (held) {
 #pragma unroll
             for (int j = 0; j < kHeld; ++j)
                 if (lo + tid + T * j < hi) f(kept[j]);
         } else {
-            for (int i = lo + tid; i < hi; i += T) f(keys[i]);
+            for (int i = lo + tid; i < hi; i += T) f(key_at(i));
         }
     };
     uint32_t prefix = 0, mask = 0;
@@ -423,9 +425,36 @@ __device__ __forceinline__ void pick(const SelectArgs &a, const uint32_t *keys, 
             if (count == left) break;  // all keys with these bits are taken
         }
     }
+    for (int i = tid; i < a.first; i += T) out[i] = i;
+    for (int i = tid; i < a.recent; i += T) out[a.count - a.recent + i] = hi + i;
+    if (none) return;
+    if constexpr (T > 64) {
+        if (held) {  // by what each wave takes of each T pages, in their order one below the other
+            static_assert(kHeld * kWaves <= 64, "one lane for each");
+            int before[kHeld];  // in the wave: those with a larger key << 16 | those with the bits
+#pragma unroll
+            for (int j = 0; j < kHeld; ++j) {
+                const uint32_t key = kept[j] & mask;
+                const bool there = lo + tid + T * j < hi;
+                const unsigned long long m = __ballot(there && key > prefix), e = __ballot(there && key == prefix), below = (1ull << lane) - 1;
+                before[j] = __popcll(m & below) << 16 | __popcll(e & below);
+                if (lane == 0) space.taken[kWaves * j + wave] = __popcll(m) << 16 | __popcll(e);
+            }
+            __syncthreads();
+            const int mine = lane < kHeld * kWaves ? space.taken[lane] : 0, start = wave_scan(mine) - mine;
+#pragma unroll
+            for (int j = 0; j < kHeld; ++j) {
+                const uint32_t key = kept[j] & mask;
+                const int i = lo + tid + T * j, upto = before[j] + __builtin_amdgcn_readlane(start, uniform(kWaves * j + wave));
+                const int equals = upto & 0xffff, to = a.first + (upto >> 16) + min(equals, left);
+                // below count, but for calls that overlap and share the keys' memory
+                if (i < hi && (key > prefix || (key == prefix && equals < left)) && to < a.count) out[to] = i;
+            }
+            return;
+        }
+    }
     // place: of the next pick; equals: how many with the bits have been passed
     int place = a.first, equals = 0;
-    for (int i = tid; i < a.first; i += T) out[i] = i;
     auto take = [&](int i, uint32_t key) {  // T pages in order, of which the thread has page i
         key &= mask;
         const bool more = i < hi && key > prefix, equal = i < hi && key == prefix;
@@ -453,17 +482,16 @@ __device__ __forceinline__ void pick(const SelectArgs &a, const uint32_t *keys, 
     if (held) {
 #pragma unroll
         for (int j = 0; j < kHeld; ++j)
-            if (lo + T * j < hi && !none) take(lo + tid + T * j, kept[j]);
+            if (lo + T * j < hi) take(lo + tid + T * j, kept[j]);
     } else {
-        for (int i0 = lo; i0 < hi && !none; i0 += T) take(i0 + tid, keys[min(i0 + tid, hi - 1)]);
+        for (int i0 = lo; i0 < hi; i0 += T) take(i0 + tid, key_at(min(i0 + tid, hi - 1)));
     }
-    for (int i = tid; i < a.recent; i += T) out[a.count - a.recent + i] = hi + i;
 }
 
 // Pages that a row at a position sees.
 __device__ __forceinline__ int pages_seen(const SelectArgs &a, int pos) { return pos < 0 ? 0 : (pos >> a.shift) + 1; }
 
-// One row and kv head: scores and picks in one workgroup, the keys in LDS.
+// One row and kv head of up to kRowPages pages: scores and picks in one workgroup, the keys in LDS.
 template <int D>
 __global__ __launch_bounds__(256) void select_row_kernel(SelectArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint32_t keys[];
@@ -481,10 +509,10 @@ __global__ __launch_bounds__(256) void select_row_kernel(SelectArgs a) {
             if (wave == 3) query_codes<D>(a, t, h, w);  // the wave with the fewest pages
             __syncthreads();
         };
-        score_pages<D, 1>(a, table, h, 64 * wave, 256, seen, 1, page, w, prepare, [&](int, int p) { return keys + p; });
+        score_pages<D, 1>(a, table, h, 64 * wave, 256, seen, 1, page, w, prepare, [&](int, int p, uint4 k) { *reinterpret_cast<uint4 *>(keys + p) = k; });
         __syncthreads();
     }
-    pick<256>(a, keys, seen, a.picks + ((int64_t)t * a.H + h) * a.count, space, threadIdx.x);
+    pick<256, 1>(a, [&](int i) { return keys[i]; }, seen, a.picks + ((int64_t)t * a.H + h) * a.count, space, threadIdx.x);
 }
 
 // The rank-th tile of 16 rows: sequence b owns the ranks from start / 16 + b on (room
@@ -532,11 +560,12 @@ __global__ __launch_bounds__(1024) void select_tile_kernel(SelectArgs a) {
             if (wave < tile.n) query_codes<D>(a, tile.first + wave, h, w + wave * 2 * D);
             __syncthreads();
         };
-        score_pages<D, 16>(a, table, h, 64 * wave, 1024, most, tile.n, page_at(a, table, 64 * wave), w, prepare, [&](int r, int p) { return keys + r * a.pitch + p; });
+        score_pages<D, 16>(a, table, h, 64 * wave, 1024, most, tile.n, page_at(a, table, 64 * wave), w, prepare,
+                           [&](int r, int p, uint4 k) { *reinterpret_cast<uint4 *>(keys + r * a.pitch + p) = k; });
         __syncthreads();
     }
     if (wave < tile.n)
-        pick<64>(a, keys + wave * a.pitch, pages_seen(a, tile.pos + wave),
+        pick<64, 16>(a, [&](int i) { return keys[wave * a.pitch + i]; }, pages_seen(a, tile.pos + wave),
                  a.picks + ((int64_t)(tile.first + wave) * a.H + h) * a.count, space[wave], lane);
 }
 
@@ -563,8 +592,9 @@ __global__ __launch_bounds__(256) void score_kernel(SelectArgs a) {
         for (int r = 3 - wave; r < tile.n; r += 4) query_codes<D>(a, tile.first + r, h, w + r * 2 * D);
         __syncthreads();
     };
-    score_pages<D, 16>(a, table, h, p, 256 * (int)gridDim.y, most, tile.n, page, w, prepare,
-                       [&](int r, int k) { return a.keys + ((int64_t)(tile.first - a.t0 + r) * a.H + h) * a.pitch + k; });
+    score_pages<D, 16>(a, table, h, p, 256 * (int)gridDim.y, most, tile.n, page, w, prepare, [&](int r, int p, uint4 k) {
+        *reinterpret_cast<uint4 *>(a.keys + ((int64_t)(tile.first - a.t0 + r) * a.H + h) * a.pitch + p) = k;
+    });
 }
 
 template <int T>
@@ -573,8 +603,46 @@ __global__ __launch_bounds__(T) void pick_kernel(SelectArgs a) {
     const int r = (int)(blockIdx.x / (uint32_t)a.H), h = (int)blockIdx.x - r * a.H, t = a.t0 + r;
     const Row row = find_row(a.cu, a.lens, a.B, a.Tq, a.max_pages << a.shift, t);
     if (row.b < 0) return;
-    pick<T>(a, a.keys + ((int64_t)r * a.H + h) * a.pitch, pages_seen(a, row.pos), a.picks + ((int64_t)t * a.H + h) * a.count,
-            space, threadIdx.x);
+    const uint32_t *keys = a.keys + ((int64_t)r * a.H + h) * a.pitch;
+    pick<T, 4>(a, [&](int i) { return keys[i]; }, pages_seen(a, row.pos), a.picks + ((int64_t)t * a.H + h) * a.count, space, threadIdx.x);
+}
+
+// Both in one launch, for one new token each: 256 of every 256 gridDim.y pages of a row and kv
+// head; the workgroup that finishes last picks, from keys that it reads past its own caches.
+template <int D, int kHeld>
+__global__ __launch_bounds__(256, 4) void select_parts_kernel(SelectArgs a) {
+    __shared__ __attribute__((aligned(16))) uint8_t w[2 * D];
+    __shared__ PickSpace<256> space;
+    __shared__ int arrived;
+    if (blockIdx.x == 0 && blockIdx.y == 0) clear_next<256>(a.clear);
+    const int t = (int)(blockIdx.x / (uint32_t)a.H), h = (int)blockIdx.x - t * a.H, wave = uniform((int)threadIdx.x >> 6);
+    const int p = 256 * (int)blockIdx.y + 64 * wave;
+    const int32_t *table = a.table + t * a.max_pages;
+    const uint32_t page = page_at(a, table, p);  // beside the length
+    const int seen = pages_seen(a, (int)max((int64_t)0, min((int64_t)a.lens[t], a.max_pages << a.shift)) - 1);
+    const int parts = seen <= a.count ? 1 : min((int)gridDim.y, (seen + 255) / 256);
+    if ((int)blockIdx.y >= parts) return;
+    uint32_t *keys = a.keys + (int64_t)blockIdx.x * a.pitch;
+    if (seen > a.count) {
+        auto prepare = [&]() {
+            if (wave == 3) query_codes<D>(a, t, h, w);  // the wave with the fewest pages
+            __syncthreads();
+        };
+        score_pages<D, 1>(a, table, h, p, 256 * (int)gridDim.y, seen, 1, page, w, prepare, [&](int, int i, uint4 k) {
+            store_agent(reinterpret_cast<float *>(keys + i), __uint_as_float(k.x), __uint_as_float(k.y));
+            store_agent(reinterpret_cast<float *>(keys + i + 2), __uint_as_float(k.z), __uint_as_float(k.w));
+        });
+        wait_vm0();
+        __syncthreads();
+        if (parts > 1) {
+            if (threadIdx.x == 0) arrived = __hip_atomic_fetch_add(a.counts + blockIdx.x, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __syncthreads();
+            if (uniform(arrived) != parts - 1) return;
+        }
+    }
+    pick<256, kHeld>(a, [&](int i) { return __hip_atomic_load(keys + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }, seen,
+              a.picks + (int64_t)blockIdx.x * a.count, space, threadIdx.x);
+    if (parts > 1 && threadIdx.x == 0) __hip_atomic_store(a.counts + blockIdx.x, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // -------------------------------------------------------------- attention --
@@ -1032,15 +1100,17 @@ qw3_status launch_blocks(BlocksArgs a, hipStream_t stream) {
 
 constexpr int64_t kTileKeys = 32768;              // words of LDS for the keys of 16 rows
 constexpr int64_t kKeyBytes = int64_t(64) << 20;  // of keys in memory at a time
-constexpr int64_t kRowPages = 256;
+constexpr int64_t kRowPages = 256, kPartPages = 2048;
 
-// One CU reads some 30 bytes of bounds a ns, 512 pages of 128 channels in 4.5 us.  So a row's pages
-// are read by one workgroup only where a table has few; else by as many as there are
-// pages for, through memory, and picked by a second launch.  One row of 8 kv heads, 64 of
-// 256, 512, 1024, 2048 pages: in one workgroup 7.6, 11.5, 19.7, 34.9 us, through memory
-// 10.8, 11.3, 11.7, 13.4; 48 rows, 64 of 64, 512, 1024 pages: 7.2, 17.4, 28.5 and 9.5,
-// 19.8, 32.1; 48 rows of 17 to 16,000 tokens in pages of 16, where the longest are
-// waited for: 19.9 and 15.8.
+// One CU reads some 30 bytes of bounds a ns, 512 pages of 128 channels in 4.5 us.  So a row's
+// pages are read by one workgroup only where a table has few; else by as many as there are
+// pages for, through memory, of which the last picks, or a second launch where more workgroups
+// than are counted, more keys than 256 threads keep, or several rows of a sequence want it.
+// One row of 8 kv heads, 64 of 250, 512, 1024, 2048, 4096 pages: in one workgroup 7.8, 11.5, 19.7,
+// 34.9 us (up to 2048), picked by the last 9.9, 9.9, 10.2, 12.2, 16.4, by a second launch 12.1, 12.2,
+// 11.9, 12.7, 13.6; 48 rows, 250, 512, 1024, 2048 pages: 10.0, 17.4 and 28.5 (1024), by the last 12.4, 17.8,
+// 29.3, 51.3, by a second launch 14.1, 21.1, 31.1, 56.5; 48 rows of 17 to 16,000 tokens in pages of 16, where
+// the longest are waited for: 19.9, 15.4 and 15.8.
 template <int D>
 qw3_status launch_select(SelectArgs a, hipStream_t stream) {
     int cus = 0;
@@ -1065,6 +1135,13 @@ qw3_status launch_select(SelectArgs a, hipStream_t stream) {
     a.keys = static_cast<uint32_t *>(ws);
     int64_t some = ceil_div(a.max_pages, 256);  // workgroups of a tile
     some = some < 64 ? some : 64;
+    if (!a.cu && a.max_pages <= kPartPages && a.Tq * (int64_t)a.H <= kCounts) {
+        st = counters(stream, a.Tq * a.H, &a.counts, &a.clear);
+        if (st != QW3_OK) return st;
+        const auto kernel = a.max_pages <= 1024 ? select_parts_kernel<D, 4> : select_parts_kernel<D, 8>;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(a.Tq * a.H), (unsigned)some), dim3(256), 0, stream, a);
+        return check_launch();
+    }
     for (int64_t t = 0; t < a.Tq; t += rows) {
         a.t0 = (int)t, a.rows = (int)(rows < a.Tq - t ? rows : a.Tq - t);
         hipLaunchKernelGGL((score_kernel<D>), dim3((unsigned)(tiles * a.H), (unsigned)some), dim3(256), 0, stream, a);

@@ -574,7 +574,8 @@ qw3_status qcache_bounds(const void *codes, const float *scales, int32_t code_ty
  * (Tq + B) H < 2^22, else QW3_ERR_SHAPE.
  * Workspace, by the rules of qgemm_w3g128_smallM: none with max_pages up to 256, or up
  * to 2032 where there are 4 new tokens and more for each sequence on average; else the
- * scores of at least 16 rows, 4 H (max_pages + 20) bytes each, 64 MiB where that is more.
+ * scores of at least 16 rows, 4 H (max_pages + 20) bytes each, 64 MiB where that is more;
+ * and without cu_q, up to 2048 pages and Tq H <= 1024, the counters of qattn_cache.
  */
 qw3_status qblock_select(const uint16_t *q, const int8_t *bounds, const float *bound_scales, const int32_t *block_table,
                          const int32_t *lens, const int32_t *cu_q, int32_t *picks, int64_t B, int64_t max_pages, int64_t Tq,

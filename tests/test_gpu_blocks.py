@@ -131,7 +131,11 @@ SELECT = [  # page size, heads, kv heads, channels, lengths, new tokens, count, 
     (16, 4, 4, 128, [9000, 300], None, 64, 2, 1, 700), (16, 16, 2, 64, [12000, 70], [20, 3], 33, 1, 4, 800),
     (16, 8, 8, 64, [70000, 3000], None, 100, 1, 1, None), (16, 4, 1, 128, [66000, 40], [35, 40], 17, 1, 1, 4500),
     (16, 8, 2, 64, [30000, 500], [9, 4], 20, 1, 1, 2000), (16, 8, 8, 64, [70000, 3000], None, 100, 1, 1, 8300),
-    (16, 8, 1, 64, [500], [480], 2, 1, 1, None), (16, 8, 1, 64, [500], [480], 300, 5, 5, None)]
+    (16, 8, 1, 64, [500], [480], 2, 1, 1, None), (16, 8, 1, 64, [500], [480], 300, 5, 5, None),
+    # one new token each, tables of 257 to 4096 pages and more, more rows than are counted
+    (16, 8, 2, 128, [4112, 4097, 4096, 17, 0, 65536], None, 11, 1, 1, 4096), (32, 8, 8, 64, [8256, 130000, 40000], None, 300, 7, 9, 4096),
+    (16, 4, 4, 128, [4100] * 30 + [900, 5000], None, 2, 1, 1, 320), (16, 20, 10, 64, [5000, 20, 4200] * 40, None, 5, 0, 1, 330),
+    (16, 2, 1, 128, [65600, 300], None, 30, 1, 1, 4110), (64, 8, 1, 64, [262000], None, 4000, 1, 1, 4094)]
 
 
 @pytest.mark.parametrize("coarse", [False, True])
@@ -161,6 +165,50 @@ def test_select(coarse, case):
                             cu_q=None if cu is None else dev(cu), first=first, recent=recent)
     assert got.shape == (total, heads, count) and got.dtype is torch.int32
     assert np.array_equal(got.cpu().numpy(), want)
+
+
+def test_a_captured_step_over_long_tables():
+    """Selection and attention, both split over workgroups and joined by the last, captured, and replayed with other lengths and
+    queries, eager calls on the same stream between."""
+    rng = np.random.default_rng(21)
+    size, hq, heads, dim, batch, width, count = 16, 8, 2, 64, 5, 1200, 24
+    pages = batch * width
+    table = dev(rng.permutation(pages).reshape(batch, width))
+    codes = torch.tensor(rng.integers(0, 256, (pages, 2, heads, size, dim), dtype=np.uint8)).cuda().view(torch.int8)
+    scales = torch.tensor(rng.uniform(0.005, 0.02, (pages, 2, heads, size)), dtype=torch.float32).cuda()
+    limits, steps = q().new_bounds(codes)
+    lens = dev([width * size] * batch)
+    cu = np.arange(batch + 1) * width * size
+    q().qcache_bounds(codes, scales, table, lens, limits, steps, cu_q=dev(cu), total=int(cu[-1]))
+    x = rows(rng, batch, hq, dim)
+
+    def call():
+        picks = q().qblock_select(x, limits, steps, table, lens, count, size)
+        return picks, q().qattn_blocks(x, codes, scales, table, lens, picks)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        first = call()
+        second = call()
+    for turn in range(6):
+        say("replay", turn)
+        have = rng.integers(1, width * size, batch) if turn % 2 else np.array([4096, 4112, 0, 19200, 300])
+        lens.copy_(dev(have))
+        x.copy_(rows(rng, batch, hq, dim))
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            graph.replay()
+            eager = call()
+            graph.replay()
+        torch.cuda.synchronize()
+        want = blocks.select(f64(x), limits.cpu().numpy(), steps.cpu().numpy(), table.cpu().numpy(), have, None, count, size, 1, 1)
+        for picks, out in (first, second, eager):
+            assert np.array_equal(picks.cpu().numpy(), want)
+            assert torch.equal(out, eager[1])
 
 
 def test_select_in_several_batches():
