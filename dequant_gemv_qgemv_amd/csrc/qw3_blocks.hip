@@ -1104,13 +1104,13 @@ constexpr int64_t kRowPages = 256, kPartPages = 2048;
 
 // One CU reads some 30 bytes of bounds a ns, 512 pages of 128 channels in 4.5 us.  So a row's
 // pages are read by one workgroup only where a table has few; else by as many as there are
-// pages for, through memory, of which the last picks, or a second launch where more workgroups
-// than are counted, more keys than 256 threads keep, or several rows of a sequence want it.
-// One row of 8 kv heads, 64 of 250, 512, 1024, 2048, 4096 pages: in one workgroup 7.8, 11.5, 19.7,
-// 34.9 us (up to 2048), picked by the last 9.9, 9.9, 10.2, 12.2, 16.4, by a second launch 12.1, 12.2,
-// 11.9, 12.7, 13.6; 48 rows, 250, 512, 1024, 2048 pages: 10.0, 17.4 and 28.5 (1024), by the last 12.4, 17.8,
-// 29.3, 51.3, by a second launch 14.1, 21.1, 31.1, 56.5; 48 rows of 17 to 16,000 tokens in pages of 16, where
-// the longest are waited for: 19.9, 15.4 and 15.8.
+// pages for, through memory, of which the last picks; or a second launch, where there are more
+// workgroups than counters, more keys than 256 threads keep, or several rows of a sequence.
+// 64 pages for one row of 8 kv heads, tables of 250, 512, 1024, 2048, 4096: by one workgroup 7.8,
+// 11.5, 19.7, 34.9 us, by the last 9.9 (260), 9.9, 10.2, 12.2, 16.4, by a second launch 12.1, 12.2,
+// 11.9, 12.7, 13.6.  48 rows, 250, 512, 1024, 2048: by one 10.0, 17.4, 28.5, by the last 12.4, 17.8,
+// 29.3, 51.3, by a second launch 14.1, 21.1, 31.1, 56.5; 17 to 16,000 tokens each in pages of 16, where
+// the longest are waited for: 19.9, 15.4, 15.8.
 template <int D>
 qw3_status launch_select(SelectArgs a, hipStream_t stream) {
     int cus = 0;
