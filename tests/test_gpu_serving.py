@@ -1,5 +1,6 @@
 """The cache's calls together, as a server uses them: a decode step captured once
 and replayed, with beams that part, against the same steps done one by one."""
+import ctypes
 import math
 import sys
 
@@ -136,3 +137,43 @@ def test_sequences_that_get_no_room_write_nothing():
     assert int((scales != 0).sum()) == 20 * 2 * kv
     out = q().qattn_cache(x.to(torch.bfloat16), codes, scales, table, after, cu_q=cu)
     assert (out[20:] == 0).all() and (out[:20] != 0).any(dim=2).all()
+
+
+def test_a_capture_that_would_allocate_is_refused():
+    """On a stream that has not run the calls at their size a capture is refused, and nothing is enqueued; after one call it is taken."""
+    m = q()
+    with open("/proc/self/maps") as maps:  # the runtime that is loaded, and no other copy
+        hip = ctypes.CDLL(next(line.split()[-1] for line in maps if "libamdhip64" in line))
+    size, heads, dim, width = 16, 2, 64, 1500
+    codes, scales = m.new_cache(2 * width, size, heads, dim)
+    bounds = m.new_bounds(codes)
+    table = torch.arange(2 * width, dtype=torch.int32, device="cuda").view(2, width)
+    lens = torch.full((2,), width * size, dtype=torch.int32, device="cuda")
+    x = torch.randn(2, 4, dim, device="cuda").to(torch.bfloat16)
+    picks = torch.arange(40, dtype=torch.int32, device="cuda").expand(2, heads, 40).contiguous()
+    keep = torch.ones(2 * width * size, dtype=torch.bool, device="cuda")
+    cu = torch.tensor([0, width * size, 2 * width * size], dtype=torch.int32, device="cuda")
+    calls = [lambda: m.qblock_select(x, *bounds, table, lens, 40, size), lambda: m.qattn_blocks(x, codes, scales, table, lens, picks),
+             lambda: m.qcache_compact(codes, scales, table, lens, keep, cu_q=cu)]
+    for call in calls:
+        call()  # the kernels are loaded; on another stream than below
+        torch.cuda.synchronize()
+        handle = ctypes.c_void_p()  # torch's own streams are used again and again; this one is nobody else's
+        assert hip.hipStreamCreate(ctypes.byref(handle)) == 0
+        side, graph = torch.cuda.ExternalStream(handle.value), torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side):
+            with torch.cuda.graph(graph, stream=side):
+                still = lens + 0
+                with pytest.raises(m.Qw3Error) as refused:
+                    call()
+            assert refused.value.status == m.QW3_ERR_CAPTURE
+            graph.replay()
+            assert torch.equal(still, lens)
+            want = call()
+            side.synchronize()
+            again = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(again, stream=side):
+                got = call()
+            again.replay()
+            side.synchronize()
+            assert torch.equal(got, want)
