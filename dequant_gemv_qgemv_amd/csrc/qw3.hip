@@ -1395,7 +1395,8 @@ __global__ __launch_bounds__(256) void fill_zero_kernel(float *__restrict__ y, i
 // process ends, because work queued earlier -- or a graph captured earlier --
 // may still use it: nothing is ever freed or synchronized.  A call that would
 // allocate while its stream is being captured returns QW3_ERR_CAPTURE.
-// Calls on one stream run in order and share its buffer; other streams get
+// Calls on one stream run in order and share its buffer, which a call keeps
+// to itself from here to its last launch (Scratch); other streams get
 // their own.  Streams are told apart by handle (the HIP runtime the library
 // runs under offers no stream id), so a stream created at the address of a
 // destroyed one inherits its buffer: the header asks callers to let a
@@ -1404,8 +1405,9 @@ __global__ __launch_bounds__(256) void fill_zero_kernel(float *__restrict__ y, i
 struct Workspace {
     int dev;
     hipStream_t stream;
-    void *ptr;
+    void *ptr;  // null: none yet
     size_t bytes;
+    std::mutex *turn;  // of the calls that use it; never freed
 };
 std::mutex g_ws_mutex;
 std::vector<Workspace> g_ws;
@@ -1422,34 +1424,41 @@ bool qw3_shared::stream_capturing(hipStream_t stream) {
     return cs != hipStreamCaptureStatusNone;
 }
 
-qw3_status qw3_shared::workspace(hipStream_t stream, size_t bytes, void **out) {
+qw3_status qw3_shared::workspace(hipStream_t stream, size_t bytes, Scratch *out) {
     int dev = 0;
     hipError_t err = hipGetDevice(&dev);
     if (err != hipSuccess) return hip_fail(err);
-    std::lock_guard<std::mutex> lock(g_ws_mutex);
-    Workspace *w = nullptr;
-    for (auto &e : g_ws)
-        if (e.dev == dev && e.stream == stream) w = &e;
-    if (w && w->bytes >= bytes) {
-        *out = w->ptr;
-        return QW3_OK;
+    std::unique_lock<std::mutex> lock(g_ws_mutex);
+    auto find = [&]() -> Workspace * {
+        for (auto &e : g_ws)
+            if (e.dev == dev && e.stream == stream) return &e;
+        return nullptr;
+    };
+    Workspace *w = find();
+    if (!w) {
+        std::mutex *turn = qw3_host::room_for_one(g_ws) ? new (std::nothrow) std::mutex : nullptr;
+        if (!turn) return hip_fail(hipErrorOutOfMemory);
+        g_ws.push_back(Workspace{dev, stream, nullptr, 0, turn});
+        w = &g_ws.back();
     }
-    if (stream_capturing(stream)) return QW3_ERR_CAPTURE;
-    size_t grow = (bytes + (size_t(1) << 20) - 1) & ~((size_t(1) << 20) - 1);
-    if (w && grow < 2 * w->bytes) grow = 2 * w->bytes;
-    if (w ? !qw3_host::room_for_one(g_ws_retired) : !qw3_host::room_for_one(g_ws))
-        return hip_fail(hipErrorOutOfMemory);
-    void *p = nullptr;
-    err = hipMalloc(&p, grow);
-    if (err != hipSuccess) return hip_fail(err);
-    if (w) {
-        g_ws_retired.push_back(w->ptr);
+    std::mutex *turn = w->turn;
+    lock.unlock();  // other streams' calls do not wait for this one's
+    out->turn = std::unique_lock<std::mutex>(*turn);
+    lock.lock();
+    w = find();
+    if (!w->ptr || w->bytes < bytes) {
+        if (stream_capturing(stream)) return QW3_ERR_CAPTURE;
+        size_t grow = (bytes + (size_t(1) << 20) - 1) & ~((size_t(1) << 20) - 1);
+        if (grow < 2 * w->bytes) grow = 2 * w->bytes;
+        if (!qw3_host::room_for_one(g_ws_retired)) return hip_fail(hipErrorOutOfMemory);
+        void *p = nullptr;
+        err = hipMalloc(&p, grow);
+        if (err != hipSuccess) return hip_fail(err);
+        if (w->ptr) g_ws_retired.push_back(w->ptr);
         w->ptr = p;
         w->bytes = grow;
-    } else {
-        g_ws.push_back(Workspace{dev, stream, p, grow});
     }
-    *out = p;
+    out->ptr = w->ptr;
     return QW3_OK;
 }
 
@@ -1460,26 +1469,28 @@ namespace {
 // process.  On the host its name is only a stand-in; the device address is
 // looked up once per device with hipGetSymbolAddress (with that device
 // current) and used everywhere instead.  Calls on one device share the array,
-// so calls that overlap on one device race; every byte a call reads from it
-// is written earlier by the same call, so nothing needs clearing.
+// one at a time from here to its last launch, so calls that overlap on one device
+// race on the card alone; every byte a call reads from it is written earlier by the
+// same call, so nothing needs clearing.
 constexpr size_t kScratchBytes = size_t(QW3_NOALLOC_SCRATCH_BYTES);
 __device__ __align__(256) unsigned char scratch[kScratchBytes];
 void *g_scratch_ptr[64];
+std::mutex g_scratch_turn[64];
 
-qw3_status static_scratch(size_t bytes, void **out) {
+qw3_status static_scratch(size_t bytes, Scratch *out) {
     if (bytes > kScratchBytes) return QW3_ERR_SCRATCH;
     int dev = 0;
     hipError_t err = hipGetDevice(&dev);
     if (err != hipSuccess) return hip_fail(err);
     if (dev < 0 || dev >= 64) return hip_fail(hipErrorInvalidDevice);
-    std::lock_guard<std::mutex> lock(g_dev_mutex);
+    out->turn = std::unique_lock<std::mutex>(g_scratch_turn[dev]);
     if (g_scratch_ptr[dev] == nullptr) {
         void *p = nullptr;
         err = hipGetSymbolAddress(&p, HIP_SYMBOL(scratch));
         if (err != hipSuccess) return hip_fail(err);
         g_scratch_ptr[dev] = p;
     }
-    *out = g_scratch_ptr[dev];
+    out->ptr = g_scratch_ptr[dev];
     return QW3_OK;
 }
 
@@ -1487,7 +1498,7 @@ qw3_status static_scratch(size_t bytes, void **out) {
 struct ScratchSrc {
     hipStream_t stream;
     bool fixed;  // the static array instead of the per-stream workspace
-    qw3_status get(size_t bytes, void **out) const {
+    qw3_status get(size_t bytes, Scratch *out) const {
         return fixed ? static_scratch(bytes, out) : workspace(stream, bytes, out);
     }
 };
@@ -1547,11 +1558,11 @@ qw3_status launch_gemm_pf(const uint16_t *x, const uint32_t *packed, const uint1
     size_t at[4];
     tile_x_layout(Mp, K, cv, at);
     const size_t part_at = cv.take(C > 1 ? (size_t)C * (size_t)M * (size_t)N * sizeof(float) : 0);
-    void *base = nullptr;
+    Scratch base;
     st = src.get(cv.off, &base);
     if (st != QW3_OK) return st;
-    const TileX tx = tile_x_at(base, at);
-    float *part = reinterpret_cast<float *>(static_cast<char *>(base) + part_at);
+    const TileX tx = tile_x_at(base.ptr, at);
+    float *part = reinterpret_cast<float *>(static_cast<char *>(base.ptr) + part_at);
     hipLaunchKernelGGL(prep_tile_x_kernel, dim3((unsigned)Mp), dim3(256), 0, src.stream, x, tx.xq, tx.xe, tx.xd,
                        tx.dtot, (int)M, K);
     st = check_launch();
@@ -1596,10 +1607,10 @@ qw3_status launch_gemm_mt(const uint16_t *x, const uint32_t *packed, const uint1
     qw3_status st = cu_count(&cus);
     if (st == QW3_OK) st = blocks_per_cu(kern, 64 * WAVES, lds, &per_cu);
     if (st != QW3_OK) return st;
-    void *base = nullptr;
+    Scratch base;
     st = src.get(cv.off, &base);
     if (st != QW3_OK) return st;
-    char *b = static_cast<char *>(base);
+    char *b = static_cast<char *>(base.ptr);
     uint4 *xq = reinterpret_cast<uint4 *>(b + xq_at);
     int16_t *xe = reinterpret_cast<int16_t *>(b + xe_at);
     float *xd = reinterpret_cast<float *>(b + xd_at);
@@ -1648,13 +1659,12 @@ qw3_status launch_gemm_m4(const uint16_t *x, const uint32_t *packed, const uint1
     if (st == QW3_OK)
         st = blocks_per_cu(reinterpret_cast<const void *>(&qgemm_m4_kernel<WAVES, TOK>), 64 * WAVES, lds, &per_cu);
     if (st != QW3_OK) return st;
-    float *part = nullptr;
+    Scratch base;
     if (part_bytes > 0) {
-        void *base = nullptr;
         st = src.get(part_bytes, &base);
         if (st != QW3_OK) return st;
-        part = static_cast<float *>(base);
     }
+    float *part = static_cast<float *>(base.ptr);
     const int64_t tiles = ceil_div(N, 16);
     int64_t tb = (int64_t)cus * per_cu / C;
     if (tb < 1) tb = 1;
@@ -1727,10 +1737,10 @@ qw3_status launch_gemm_small(const uint16_t *x, const uint32_t *packed, const ui
     const size_t xq_at = cv.take((size_t)mchunk * (size_t)K * 2);
     const size_t xe_at = cv.take((size_t)G * mchunk * sizeof(int16_t));
     const size_t xd_at = cv.take((size_t)G * mchunk * sizeof(float));
-    void *base = nullptr;
+    Scratch base;
     qw3_status st = src.get(cv.off, &base);
     if (st != QW3_OK) return st;
-    char *b = static_cast<char *>(base);
+    char *b = static_cast<char *>(base.ptr);
     uint4 *xq = reinterpret_cast<uint4 *>(b + xq_at);
     int16_t *xe = reinterpret_cast<int16_t *>(b + xe_at);
     float *xd = reinterpret_cast<float *>(b + xd_at);

@@ -1524,10 +1524,10 @@ qw3_status launch_cache(CacheArgs a, hipStream_t stream) {
     qw3_status st = cu_count(&cus);
     if (st != QW3_OK) return st;
     a.groups = cus * (R == 256 ? 1 : 2);
-    void *ws = nullptr;
+    Scratch ws;
     st = workspace(stream, (size_t)a.groups * 2 * R * (D + 2) * sizeof(float), &ws);
     if (st != QW3_OK) return st;
-    a.part = static_cast<float *>(ws);
+    a.part = static_cast<float *>(ws.ptr);
     st = counters(stream, a.groups, &a.counts, &a.clear);
     if (st != QW3_OK) return st;
     if constexpr (R <= 32)
@@ -1662,11 +1662,11 @@ qw3_status qattn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v,
     const hipStream_t stream = (hipStream_t)hip_stream;
     // in slices while the tiles leave half of the CUs' places empty
     a.slices = few && Tk > (kSliceLeast - 1) * kKeys ? (int)std::max<int64_t>(2 * cus / (tiles * Hq), 1) : 1;
+    Scratch ws;
     if (a.slices > 1) {
-        void *ws = nullptr;
         st = workspace(stream, (size_t)(tiles * Hq * a.slices) * 64 * (D + 2) * sizeof(float), &ws);
         if (st != QW3_OK) return st;
-        a.part = static_cast<float *>(ws);
+        a.part = static_cast<float *>(ws.ptr);
         st = counters(stream, (int)(tiles * Hq), &a.counts, &a.clear);
         if (st != QW3_OK) return st;
     }

@@ -1083,11 +1083,11 @@ qw3_status launch_blocks(BlocksArgs a, hipStream_t stream) {
     const int64_t room = items < 2 * (int64_t)cus ? 2 * (int64_t)cus / items : 1;
     a.parts = (int)(room < most ? room : most);
     if (a.parts < 1 || items > kCounts) a.parts = 1;
+    Scratch ws;
     if (a.parts > 1) {
-        void *ws = nullptr;
         st = workspace(stream, (size_t)(items * a.parts) * 16 * (D + 2) * sizeof(float), &ws);
         if (st != QW3_OK) return st;
-        a.part = static_cast<float *>(ws);
+        a.part = static_cast<float *>(ws.ptr);
         st = counters(stream, (int)items, &a.counts, &a.clear);
         if (st != QW3_OK) return st;
     }
@@ -1129,10 +1129,10 @@ qw3_status launch_select(SelectArgs a, hipStream_t stream) {
     int64_t rows = kKeyBytes / (4 * (int64_t)a.pitch * a.H);
     rows = rows < 16 ? 16 : rows;
     rows = rows < a.Tq ? rows : a.Tq;
-    void *ws = nullptr;
+    Scratch ws;
     st = workspace(stream, (size_t)(rows * a.H * a.pitch) * 4, &ws);
     if (st != QW3_OK) return st;
-    a.keys = static_cast<uint32_t *>(ws);
+    a.keys = static_cast<uint32_t *>(ws.ptr);
     int64_t some = ceil_div(a.max_pages, 256);  // workgroups of a tile
     some = some < 64 ? some : 64;
     if (!a.cu && a.max_pages <= kPartPages && a.Tq * (int64_t)a.H <= kCounts) {

@@ -57,6 +57,7 @@
 #include <string.h>
 
 #include <mutex>
+#include <new>
 #include <type_traits>
 
 #include "qw3.h"
@@ -610,8 +611,15 @@ inline qw3_status blocks_per_cu(const void *kernel, int wgs, size_t lds, int *ou
     return QW3_OK;
 }
 
+// Scratch that a call has to itself: host threads that call on one stream take turns,
+// so that no launch of another call stands between those of one that pass data in the
+// scratch to each other.  Kept up to the call's last launch.
+struct Scratch {
+    void *ptr = nullptr;
+    std::unique_lock<std::mutex> turn;
+};
 // Scratch of `stream` on the current device, at least `bytes` (qw3.hip).
-qw3_status workspace(hipStream_t stream, size_t bytes, void **out);
+qw3_status workspace(hipStream_t stream, size_t bytes, Scratch *out);
 // Counters of `stream` on the current device for one call, zero when it runs, and
 // those of the next, which the call clears (qw3_attn.hip).
 qw3_status counters(hipStream_t stream, int n, int **use, int **clear);

@@ -650,10 +650,10 @@ qw3_status launch_compact(CompactArgs a, int64_t layers, hipStream_t stream) {
     const int64_t units = chunks * a.groups * some;
     a.units = (int)units;
     const int64_t ranks = a.cu ? (a.total >> kChunkShift) + a.B : a.B;
-    void *ws = nullptr;
+    Scratch ws;
     const qw3_status st = workspace(stream, (size_t)(a.total * int64_t(16) + (1 + units) * int64_t(4)), &ws);
     if (st != QW3_OK) return st;
-    a.moves = static_cast<int4 *>(ws);
+    a.moves = static_cast<int4 *>(ws.ptr);
     a.ticket = reinterpret_cast<int *>(a.moves + a.total), a.read = a.ticket + 1;
     hipLaunchKernelGGL(compact_rank_kernel, dim3((unsigned)ranks), dim3(256), 0, stream, a);
     for (; a.layer0 < layers; a.layer0 += (int)some, ++a.epoch) {

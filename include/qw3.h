@@ -170,7 +170,8 @@ qw3_status qgemv_w3g128_multi(const uint16_t *x, int32_t count, const int32_t *c
  *     superseded one is never freed or reused while the process runs, so work
  *     queued earlier and graphs captured earlier stay valid.  Buffers are held
  *     until the process ends.  The library never synchronizes a stream.
- *   - Calls on one stream run in order and share its buffer; calls on
+ *   - Calls on one stream run in order and share its buffer; host threads may
+ *     call on one stream at once, each call's launches follow each other.  Calls on
  *     different streams use different buffers and may overlap.  Streams are
  *     told apart by handle: before destroying a stream that has calls of this
  *     library queued, wait for them (hipStreamSynchronize), since a stream
@@ -236,7 +237,7 @@ qw3_status qgemm_w3g128_batch_invariant(const uint16_t *x, const int32_t *packed
  *                     tokens against an 8192 x 28672 matrix).
  *   All calls on one device share the array: calls that overlap in time on
  *   one device (different streams, or graph replays) race and must be
- *   ordered by the caller.
+ *   ordered by the caller.  On one stream they never overlap, whatever threads call.
  */
 qw3_status qgemm_w3g128_smallM_noalloc(const uint16_t *x, const int32_t *packed,
                                        const uint16_t *scales, float *y, int64_t M, int64_t N,
