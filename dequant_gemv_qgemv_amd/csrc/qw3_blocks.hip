@@ -345,8 +345,9 @@ __device__ __forceinline__ void group_sync() {
 }
 
 // What T threads need to pick: a histogram of 256 for each byte, and what waves exchange.
+// bins are cleared and summed 16 bytes at a time, in each PickSpace of an array.
 template <int T>
-struct PickSpace {
+struct alignas(16) PickSpace {
     int bins[T > 64 ? 4 : 1][256];
     uint32_t waves[2][T / 64];
     int taken[T > 64 ? 64 : 1];
