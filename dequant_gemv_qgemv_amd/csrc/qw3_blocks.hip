@@ -236,7 +236,8 @@ __device__ __forceinline__ void query_codes(const SelectArgs &a, int row, int h,
     const int lane = threadIdx.x & 63;
     double u[kPer] = {}, l[kPer] = {};
     const uint16_t *q = a.q + (int64_t)row * a.q_ts + (int64_t)h * a.G * a.q_hs + kPer * lane;
-    // in 64 bits: exact for all that bf16 adds up to, so the order does not matter
+    // in 64 bits and in the queries' order, which is part of the definition: what lies more than
+    // 53 bits below another is rounded away
 #pragma unroll 8
     for (int g = 0; g < a.G; ++g) {
         const uint32_t d = kPer == 2 ? *reinterpret_cast<const uint32_t *>(q + g * a.q_hs) : (uint32_t)q[g * a.q_hs] << 16;
@@ -249,13 +250,19 @@ __device__ __forceinline__ void query_codes(const SelectArgs &a, int row, int h,
         }
     }
     float x[2][kPer];
-    uint32_t top = 0;
+    auto round_all = [&](double times) {  // the largest, as bits
+        uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        x[0][i] = (float)u[i], x[1][i] = (float)l[i];
-        top = max(top, max(__float_as_uint(x[0][i]) & 0x7fffffffu, __float_as_uint(x[1][i]) & 0x7fffffffu));
-    }
-    top = (uint32_t)wave_max((int)top);
+        for (int i = 0; i < kPer; ++i) {
+            x[0][i] = (float)(u[i] * times), x[1][i] = (float)(l[i] * times);
+            top = max(top, max(__float_as_uint(x[0][i]) & 0x7fffffffu, __float_as_uint(x[1][i]) & 0x7fffffffu));
+        }
+        return (uint32_t)wave_max((int)top);
+    };
+    uint32_t top = round_all(1.0);
+    // finite queries may add up to more than fp32 holds; the scale of u and n is nobody's
+    static_assert(QW3_MAX_HEADS <= 1 << 15, "2^128 each");
+    if (top >= 0x7f800000u) top = round_all(0x1p-16);
     const float s = top < 0x7f800000u ? __uint_as_float(top) / 127.0f : 0.0f;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {

@@ -566,8 +566,9 @@ qw3_status qcache_bounds(const void *codes, const float *scales, int32_t code_ty
  * A row that sees at most `count` pages gets all of them.  Otherwise the first `first`
  * and the last `recent` (its own among them), and of the others the
  * count - first - recent with the highest scores, of equal ones the lower place:
- *   u_d = sum of max(q_d, 0), n_d = sum of min(q_d, 0) over the kv head's queries (exact,
- *   then float32), both as int8 under one scale, max / 127, rounded as the bounds are;
+ *   u_d = sum of max(q_d, 0), n_d = sum of min(q_d, 0) over the kv head's queries (added
+ *   in 64 bits in their order, then rounded to float32; where one is too large for that, all
+ *   times 2^-16), both as int8 under one scale, max / 127, rounded as the bounds are;
  *   score = float(sum_d u_d mx_d + n_d mn_d) * S   in float32: a whole number, one rounding.
  * NaN is the highest score; a page that is not there comes last.  With NaN or an
  * infinity in a row's queries its u and n are zeros.

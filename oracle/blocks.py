@@ -60,6 +60,18 @@ def bounds(codes, scales, kind, table, lens, cu, total, size, out, out_scales):
                 out[page, h], out_scales[page, h] = codes_of(ends)
 
 
+def sums_of(mine):
+    """A kv head's queries [queries, D] float64: the sums of their positive and negative values [2, D], in 64 bits and in
+    their order, as float32 numbers; where one passes those, all times 2^-16."""
+    sums = np.zeros((2, mine.shape[1]))
+    for x in mine:
+        sums[0] += np.maximum(x, 0)
+        sums[1] += np.minimum(x, 0)
+    with np.errstate(over="ignore"):
+        single = sums.astype(np.float32)
+    return (sums * 2.0 ** -16).astype(np.float32) if np.isfinite(sums).all() and not np.isfinite(single).all() else single
+
+
 def select(q, limits, steps, table, lens, cu, count, size, first, recent):
     """picks [rows, H, count]; q [rows, Hq, D] in float64, limits int8 [pages, H, 2, D], steps float32 [pages, H]. Rows of
     no sequence: -9."""
@@ -74,7 +86,7 @@ def select(q, limits, steps, table, lens, cu, count, size, first, recent):
                 picks[t, h, :seen] = np.arange(seen)
                 continue
             mine = q[t, h * (hq // heads):(h + 1) * (hq // heads)]
-            w = codes_of(np.stack([np.maximum(mine, 0).sum(0), np.minimum(mine, 0).sum(0)]))[0].astype(np.int64)
+            w = codes_of(sums_of(mine))[0].astype(np.int64)
             page = table[b, :seen]
             there = (page >= 0) & (page < pages)
             at = np.where(there, page, 0)

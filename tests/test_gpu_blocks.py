@@ -167,6 +167,35 @@ def test_select(coarse, case):
     assert np.array_equal(got.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new,width", [(None, 100), (None, 900), (None, 3000), ([20, 3], 100), ([20, 3], 3000)], ids=str)
+def test_select_by_queries_whose_sums_pass_float32(dim, new, width):
+    """Finite queries rank the pages, however large: 3.3e38 and more together, beside rows of ordinary ones, of
+    infinities and of numbers far apart."""
+    rng = np.random.default_rng(dim + width)
+    size, hq, heads, lens, count = 16, 16, 2, [1590, 1400], 9
+    table, pages = tables(rng, lens, size, width=width)
+    limits = rng.integers(-127, 128, (pages, heads, 2, dim)).astype(np.int8)
+    steps = rng.uniform(0.01, 0.05, (pages, heads)).astype(np.float32)
+    cu = None if new is None else np.r_[0, np.cumsum(new)]
+    total = 2 if new is None else int(cu[-1])
+    x = rows(rng, total, hq, dim)
+    x[0] = (x[0] * 1e38).clamp(-3.3e38, 3.3e38)  # some sums pass, of most channels
+    x[-1, :, 1] = 3.3e38                         # of one channel; the others count for nothing beside it ...
+    x[-1, :, 2:9] = -1e38                        # ... but for these
+    assert torch.isfinite(x).all()
+    if total > 2:
+        x[1] *= 1e38
+        x[1, 3, 5] = float("inf")
+        x[2] *= torch.tensor(np.exp2(rng.integers(-100, 100, (hq, 1))), device="cuda")
+        x[3] *= 1e-38
+    want = blocks.select(f64(x), limits, steps, table, lens, cu, count, size, 1, 1)
+    assert (want[0, 0, 1:-1] != np.arange(1, count - 1)).any()
+    got = q().qblock_select(x, torch.tensor(limits).cuda(), torch.tensor(steps).cuda(), dev(table), dev(lens), count, size,
+                            cu_q=None if cu is None else dev(cu))
+    assert np.array_equal(got.cpu().numpy(), want)
+
+
 def test_a_captured_step_over_long_tables():
     """Selection and attention, both split over workgroups and joined by the last, captured, and replayed with other lengths and
     queries, eager calls on the same stream between."""
