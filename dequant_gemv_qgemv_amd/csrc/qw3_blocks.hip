@@ -214,10 +214,11 @@ struct SelectArgs {
     const float *steps;
     const int32_t *table, *lens, *cu;
     int32_t *picks;
-    uint32_t *keys;  // in memory: those of the rows t0 .. t0 + rows - 1, [rows, H, pitch]
+    uint32_t *keys;  // in memory: those of the launch's rows, [rows, H, pitch]
     int *counts, *clear;  // how many workgroups of a row and kv head have finished, and the next call's counters
     int64_t q_ts, q_hs, max_pages, pages;
-    int B, Tq, H, G, shift, count, first, recent, pitch, t0, rows;
+    int B, Tq, H, G, shift, count, first, recent, pitch;
+    int t0, rows;  // the rows of a launch: from t0 on
 };
 
 // A score as a number that orders like it; NaN above all, 0 for a page that is not there.
@@ -523,30 +524,38 @@ __global__ __launch_bounds__(256) void select_row_kernel(SelectArgs a) {
     pick<256, 1>(a, [&](int i) { return keys[i]; }, seen, a.picks + ((int64_t)t * a.H + h) * a.count, space, threadIdx.x);
 }
 
-// The rank-th tile of 16 rows: sequence b owns the ranks from start / 16 + b on (room
-// for its rows whatever their number).  n: the tile's rows, 0 if there are none.
+// The rank-th tile of 16 rows of those of the launch: a sequence that has some, the first
+// of them t0 + s, owns the ranks from s / 16 + the number of such sequences before it on
+// (room for its rows whatever their number).  n: the tile's rows, 0 if there are none.
 struct Tile {
     int b, first, n, pos;  // its first row and that row's position
 };
+inline int64_t tiles_of(int64_t rows, int64_t B) { return rows / 16 + (B < rows ? B : rows); }
 __device__ __forceinline__ Tile find_tile(const SelectArgs &a, int rank) {
     const int lane = threadIdx.x & 63;
     const int64_t room = a.max_pages << a.shift;
     auto length = [&](int b) { return (int)max((int64_t)0, min((int64_t)a.lens[b], room)); };
-    if (a.cu == nullptr) return Tile{rank, rank, 1, length(rank) - 1};
-    int b = -1, first = 0, floor = 0;
+    if (a.cu == nullptr) return Tile{a.t0 + rank, a.t0 + rank, 1, length(a.t0 + rank) - 1};
+    int b = -1, first = 0, end = 0, until = 0, at = 0, floor = 0, before = 0;
     for (int base = 0; base < a.B; base += 64) {
-        const int start = max(floor, wave_scan_max(base + lane < a.B ? clamp_row(a.cu[min(base + lane, a.B - 1)], a.Tq) : 0));
-        const unsigned long long in = __ballot(base + lane < a.B && start / 16 + base + lane <= rank);
-        if (in == 0) break;
-        const int i = __popcll(in) - 1;
-        b = base + i, first = __builtin_amdgcn_readlane(start, i);
-        floor = __builtin_amdgcn_readlane(start, 63);
-        if (in != ~0ull) break;
+        const int mine = min(base + lane, a.B - 1), to = clamp_row(a.cu[mine + 1], a.Tq);
+        const int start = max(floor, wave_scan_max(base + lane < a.B ? clamp_row(a.cu[mine], a.Tq) : 0));
+        const int s = clamp_row(start - a.t0, a.rows), e = clamp_row(to - a.t0, a.rows);
+        const unsigned long long some = __ballot(base + lane < a.B && e > s);
+        const int own = s / 16 + before + __popcll(some & ((1ull << lane) - 1));
+        const unsigned long long in = some & __ballot(own <= rank);
+        if (in != 0) {  // their ranks rise, so these are the first that have rows
+            const int i = 63 - __builtin_clzll(in);
+            b = base + i, first = __builtin_amdgcn_readlane(s, i), end = __builtin_amdgcn_readlane(e, i);
+            until = __builtin_amdgcn_readlane(to, i), at = __builtin_amdgcn_readlane(own, i);
+        }
+        before += __popcll(some), floor = __builtin_amdgcn_readlane(start, 63);
+        if (in != some || floor - a.t0 >= a.rows) break;
     }
-    b = uniform(b), first = uniform(first);
+    b = uniform(b);
     if (b < 0) return Tile{0, 0, 0, 0};
-    const int n = clamp_row(a.cu[b + 1], a.Tq) - first, skip = 16 * (rank - first / 16 - b);
-    return Tile{b, first + skip, max(min(16, n - skip), 0), length(b) - n + skip};
+    first = uniform(first) + 16 * (rank - uniform(at));
+    return Tile{b, a.t0 + first, max(min(16, uniform(end) - first), 0), length(b) - uniform(until) + a.t0 + first};
 }
 
 // 16 rows of a sequence and a kv head: the pages' bounds are read once for all of
@@ -586,11 +595,8 @@ __global__ __launch_bounds__(256) void score_kernel(SelectArgs a) {
     const int rank = (int)(blockIdx.x / (uint32_t)a.H), h = (int)blockIdx.x - rank * a.H;
     const int wave = uniform((int)threadIdx.x >> 6);
     const int p = 256 * (int)blockIdx.y + 64 * wave;
-    uint32_t page = a.cu ? kNoPage : page_at(a, a.table + rank * a.max_pages, p);  // beside the length
-    Tile tile = find_tile(a, rank);
-    // of the tile's rows those of this launch
-    const int skip = max(a.t0 - tile.first, 0);
-    tile.n = min(tile.n, a.t0 + a.rows - tile.first) - skip, tile.first += skip, tile.pos += skip;
+    uint32_t page = a.cu ? kNoPage : page_at(a, a.table + (a.t0 + rank) * a.max_pages, p);  // beside the length
+    const Tile tile = find_tile(a, rank);
     if (tile.n <= 0) return;
     const int most = pages_seen(a, tile.pos + tile.n - 1);
     if (most <= a.count || 256 * (int)blockIdx.y >= most) return;
@@ -1125,9 +1131,9 @@ qw3_status launch_select(SelectArgs a, hipStream_t stream) {
     qw3_status st = cu_count(&cus);
     if (st != QW3_OK) return st;
     a.pitch = (int)(ceil_div(a.max_pages, 16) * 16 + 4);  // rows of the keys begin in different banks
-    const int64_t tiles = a.cu ? a.Tq / 16 + a.B : a.B;
     if (a.cu && a.Tq >= 4 * (int64_t)a.B && 16 * a.pitch <= kTileKeys) {
-        hipLaunchKernelGGL((select_tile_kernel<D>), dim3((unsigned)(tiles * a.H)), dim3(1024), 16 * a.pitch * 4, stream, a);
+        a.rows = a.Tq;
+        hipLaunchKernelGGL((select_tile_kernel<D>), dim3((unsigned)(tiles_of(a.Tq, a.B) * a.H)), dim3(1024), 16 * a.pitch * 4, stream, a);
         return check_launch();
     }
     if (a.max_pages <= kRowPages) {
@@ -1152,6 +1158,9 @@ qw3_status launch_select(SelectArgs a, hipStream_t stream) {
     }
     for (int64_t t = 0; t < a.Tq; t += rows) {
         a.t0 = (int)t, a.rows = (int)(rows < a.Tq - t ? rows : a.Tq - t);
+        // tiles of these rows alone, so that the work grows with the rows whatever the batches: a chunk of
+        // 30,000 rows over 8192 pages, 8 heads, is 118 batches
+        const int64_t tiles = a.cu ? tiles_of(a.rows, a.B) : a.rows;
         hipLaunchKernelGGL((score_kernel<D>), dim3((unsigned)(tiles * a.H), (unsigned)some), dim3(256), 0, stream, a);
         if ((int64_t)a.rows * a.H >= cus)
             hipLaunchKernelGGL((pick_kernel<256>), dim3((unsigned)(a.rows * a.H)), dim3(256), 0, stream, a);

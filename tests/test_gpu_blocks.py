@@ -258,6 +258,28 @@ def test_select_in_several_batches():
     assert np.array_equal(got[sample], want)
 
 
+@pytest.mark.parametrize("falls", [False, True])
+def test_select_of_many_sequences_in_batches_of_16_rows(falls):
+    """Sequences of no row and of up to 40, several to a batch and several batches to one; rows of nobody before, between
+    (starts that fall) and behind."""
+    rng = np.random.default_rng(31 + falls)
+    size, heads, dim, count, width = 16, 32, 64, 4, 66000  # the scores of 16 rows are more than is kept at a time
+    new = [0, 3, 1, 16, 17, 0, 0, 5, 40, 2, 1, 1, 31, 0] + [1] * 70 + [0] * 70 + [9]
+    lens = [n + int(rng.integers(0, 200)) for n in new]
+    cu = 5 + np.r_[0, np.cumsum(new)]
+    if falls:
+        cu[20], cu[33], cu[90] = 0, cu[40], -7
+    total = int(cu.max()) + 6
+    table, pages = tables(rng, lens, size, width=width)
+    limits = rng.integers(-127, 128, (pages, heads, 2, dim)).astype(np.int8)
+    steps = rng.uniform(0.01, 0.05, (pages, heads)).astype(np.float32)
+    x = rows(rng, total, heads, dim)
+    want = blocks.select(f64(x), limits, steps, table, lens, cu, count, size, 1, 1)
+    out = torch.full((total, heads, count), -9, dtype=torch.int32, device="cuda")
+    q().qblock_select(x, torch.tensor(limits).cuda(), torch.tensor(steps).cuda(), dev(table), dev(lens), count, size, cu_q=dev(cu), out=out)
+    assert np.array_equal(out.cpu().numpy(), want)
+
+
 def test_select_out_of_range_and_nobodys_rows():
     rng = np.random.default_rng(9)
     lens = [40, -6, 1 << 30, 96, 10]

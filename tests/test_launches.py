@@ -88,6 +88,17 @@ int main(int argc, char **argv) {
         return (fixed ? qgemm_w3g128_smallM_noalloc_ : qgemm_w3g128_smallM_)(at<uint16_t>(0), at<int32_t>(1), at<uint16_t>(2),
                                                                             at<float>(3), M, 1024, 8192, s);
     };
+    if (!strcmp(argv[2], "select")  && argc > 6) {  // new tokens, sequences, table width, kv heads: the workgroups of each launch
+        const int64_t Tq = atoll(argv[3]), B = atoll(argv[4]), width = atoll(argv[5]), H = atoll(argv[6]);
+        const int status = qblock_select_(at<uint16_t>(0), at<int8_t>(1), at<float>(2), at<int32_t>(3), at<int32_t>(4),
+                                          Tq == B ? nullptr : at<int32_t>(5), at<int32_t>(6), B, width, Tq, H, H, 128, 60000, 16,
+                                          20, 1, 1, 128 * H, 128, at<void>(20));
+        if (status) { fprintf(stderr, "status %d\n", status); return 3; }
+        for (const Launch &x : launches) printf("%llu ", (unsigned long long)x.groups);
+        printf("\n");
+        fflush(stdout);
+        _Exit(0);
+    }
     // two threads, the second of which calls once the first is between two of its launches
     pause_first = true;
     int first = 0, second = 0;
@@ -142,3 +153,15 @@ def test_calls_of_two_threads_in_the_static_array_do_not_mix(program, first, sec
 @pytest.mark.parametrize("first,second", [("compact", "select"), ("select", "attention"), ("gemm16", "gemm16")])
 def test_calls_on_two_streams_do_not_wait_for_each_other(program, first, second):
     assert program(first, second, 1)[:2] == ["1", "2"]
+
+
+@pytest.mark.parametrize("rows,batch,width,heads", [(30000, 1, 8192, 8), (30000, 7500, 8192, 8), (30000, 30000, 8192, 8),
+                                                    (60000, 3, 60000, 16), (5000, 5000, 300, 1), (90, 1, 1 << 20, 64)])
+def test_the_work_of_a_selection_grows_with_its_rows(program, rows, batch, width, heads):
+    """However many batches the scores are made in: tiles of 16 rows, one more for each sequence that a batch has rows of,
+    each with up to 64 workgroups for its pages; and one workgroup for each row to pick."""
+    groups = [int(x) for x in program("select", rows, batch, width, heads)]
+    batches = max(len(groups) // 2, 1)
+    some = min(-(-width // 256), 64)
+    tiles = rows // 16 + min(batch * batches, rows) + batches
+    assert sum(groups) <= heads * (some * tiles + rows)
