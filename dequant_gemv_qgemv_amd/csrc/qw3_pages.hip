@@ -430,7 +430,8 @@ __global__ __launch_bounds__(256) void compact_kernel(CompactArgs a) {
 }
 
 // For many tokens of few sequences, by all of the card: where each goes, and then their
-// rows from one place to the other.
+// rows from one place to the other.  There are always starts: one token for each sequence
+// is never more than compact_kernel takes.
 constexpr int kChunkShift = 11, kChunkTokens = 1 << kChunkShift;
 
 // The workgroup's sequence and 2048 of its new tokens: sequence b owns the workgroups
@@ -442,24 +443,20 @@ struct Chunk {
 __device__ __forceinline__ Chunk find_chunk(const CompactArgs &a) {
     const int lane = threadIdx.x & 63, rank = blockIdx.x;
     Chunk c = {{0, 0, 0}, -1, 0, 0};
-    int first = rank, floor = 0;
-    if (a.cu) {
-        for (int base = 0; base < a.B; base += 64) {
-            const int start = max(floor, wave_scan_max(base + lane < a.B ? clamp_row(a.cu[min(base + lane, a.B - 1)], a.total) : 0));
-            const unsigned long long in = __ballot(base + lane < a.B && (start >> kChunkShift) + base + lane <= rank);
-            if (in == 0) break;
-            const int i = __popcll(in) - 1;
-            c.b = base + i, first = __builtin_amdgcn_readlane(start, i);
-            floor = __builtin_amdgcn_readlane(start, 63);
-            if (in != ~0ull) break;
-        }
-        if (c.b < 0) return c;
-    } else {
-        c.b = rank;
+    int first = 0, floor = 0;
+    for (int base = 0; base < a.B; base += 64) {
+        const int start = max(floor, wave_scan_max(base + lane < a.B ? clamp_row(a.cu[min(base + lane, a.B - 1)], a.total) : 0));
+        const unsigned long long in = __ballot(base + lane < a.B && (start >> kChunkShift) + base + lane <= rank);
+        if (in == 0) break;
+        const int i = __popcll(in) - 1;
+        c.b = base + i, first = __builtin_amdgcn_readlane(start, i);
+        floor = __builtin_amdgcn_readlane(start, 63);
+        if (in != ~0ull) break;
     }
-    c.s.first = first, c.s.n = a.cu ? max(clamp_row(a.cu[c.b + 1], a.total) - first, 0) : 1;
+    if (c.b < 0) return c;
+    c.s.first = first, c.s.n = max(clamp_row(a.cu[c.b + 1], a.total) - first, 0);
     c.s.len = (int)max((int64_t)0, min((int64_t)a.lens[c.b], a.max_pages << a.shift));
-    c.at = a.cu ? (rank - (first >> kChunkShift) - c.b) << kChunkShift : 0;
+    c.at = (rank - (first >> kChunkShift) - c.b) << kChunkShift;
     c.n = max(min(kChunkTokens, c.s.n - c.at), 0);
     if (c.at > 0 && c.n == 0) c.b = -1;  // every sequence has a first chunk, of no tokens perhaps
     return c;
@@ -507,16 +504,14 @@ __global__ __launch_bounds__(256) void compact_rank_kernel(CompactArgs a) {
     for (int i = (int)blockIdx.x * 256 + tid; i <= a.units; i += (int)gridDim.x * 256) a.ticket[i] = 0;
     // rows of no sequence, by all workgroups: before the first start and from the largest on
     const int4 nowhere = make_int4(0, 0, -1, 0);
-    if (a.cu) {
-        int end = 0;
-        for (int i = tid; i <= a.B; i += 256) end = max(end, clamp_row(a.cu[i], a.total));
-        end = group_scan_max<256>(end);
-        if (tid == 255) top = end;
-        __syncthreads();
-        const int before = clamp_row(a.cu[0], a.total), step = (int)gridDim.x * 256;
-        for (int64_t t = blockIdx.x * 256 + tid; t < before; t += step) a.moves[t] = nowhere;
-        for (int64_t t = (int64_t)top + blockIdx.x * 256 + tid; t < a.total; t += step) a.moves[t] = nowhere;
-    }
+    int end = 0;
+    for (int i = tid; i <= a.B; i += 256) end = max(end, clamp_row(a.cu[i], a.total));
+    end = group_scan_max<256>(end);
+    if (tid == 255) top = end;
+    __syncthreads();
+    const int first = clamp_row(a.cu[0], a.total), step = (int)gridDim.x * 256;
+    for (int64_t t = blockIdx.x * 256 + tid; t < first; t += step) a.moves[t] = nowhere;
+    for (int64_t t = (int64_t)top + blockIdx.x * 256 + tid; t < a.total; t += step) a.moves[t] = nowhere;
     const Chunk c = find_chunk(a);
     if (c.b < 0) return;
     bool kept[kTurns];
@@ -649,7 +644,7 @@ qw3_status launch_compact(CompactArgs a, int64_t layers, hipStream_t stream) {
     some = some < 1 ? 1 : some < layers ? some : layers;
     const int64_t units = chunks * a.groups * some;
     a.units = (int)units;
-    const int64_t ranks = a.cu ? (a.total >> kChunkShift) + a.B : a.B;
+    const int64_t ranks = (a.total >> kChunkShift) + a.B;
     Scratch ws;
     const qw3_status st = workspace(stream, (size_t)(a.total * int64_t(16) + (1 + units) * int64_t(4)), &ws);
     if (st != QW3_OK) return st;
