@@ -10,6 +10,7 @@
 
 using namespace qw3_shared;
 using qw3_units::clamp_row;
+using qw3_units::wait_until;
 
 namespace {
 
@@ -548,7 +549,8 @@ __global__ __launch_bounds__(256) void compact_rank_kernel(CompactArgs a) {
 // workgroup draws once it runs; a unit says that it has read before it waits for any
 // other, and waits only for units of lower tickets: those run, and read without
 // waiting.  Should calls overlap that share the workspace, which they must not, a wait
-// ends after kPolls looks all the same (some 50 ms; a unit reads for a few us).
+// ends after kPolls looks all the same (some 50 ms; a unit reads for a few us), and the
+// sequence, whose rows are then lost, has the length -1.
 // The rows of a token are read by its own unit alone, and other units write to them only
 // after that, so no unit ever reads what another has written: a flag orders a read
 // before a write, passes no data, and needs no cache written back.
@@ -571,7 +573,7 @@ __global__ __launch_bounds__(1024) void compact_move_kernel(CompactArgs a) {
     const int chunk = unit / lanes, lane = unit - chunk * lanes;
     const int layer = lane / a.groups, group = lane - layer * a.groups;
     const int t0 = chunk << a.token_shift, n = min(1 << a.token_shift, a.total - t0);
-    int over = -1;  // the chunk whose row this thread's token is written over
+    int over = -1, sequence = 0;  // the chunk whose row this thread's token is written over
     if (tid < n) {
         const int4 move = a.moves[t0 + tid];
         // always so where it moves, but for calls that overlap: those spoil each other's rows, and reach no others
@@ -580,7 +582,7 @@ __global__ __launch_bounds__(1024) void compact_move_kernel(CompactArgs a) {
         const int32_t *table = a.table + (moves ? move.x * a.max_pages : 0);
         from[tid] = moves ? row_of(a, table, move.y, 0, 0) : -1;
         to[tid] = moves ? row_of(a, table, move.z, 0, 0) : -1;
-        if (moves) over = move.w >> a.token_shift;
+        if (moves) over = move.w >> a.token_shift, sequence = move.x;
     }
     __syncthreads();
     uint4 *codes = reinterpret_cast<uint4 *>(a.codes + (a.layer0 + layer) * a.layer_rows * D);
@@ -609,10 +611,8 @@ __global__ __launch_bounds__(1024) void compact_move_kernel(CompactArgs a) {
     if (tid == 0) __hip_atomic_store(a.read + unit, a.epoch + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (over >= 0 && over < chunk) {
         const int *other = a.read + over * lanes + lane;
-        for (int polls = 0; polls < kPolls; ++polls) {
-            if (__hip_atomic_load(other, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) > a.epoch) break;
-            __builtin_amdgcn_s_sleep(1);
-        }
+        auto seen = [&]() { return __hip_atomic_load(other, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) > a.epoch; };
+        if (!wait_until(seen, []() { __builtin_amdgcn_s_sleep(1); }, kPolls)) a.lens_out[sequence] = -1;
     }
     __syncthreads();
 #pragma unroll

@@ -1,7 +1,7 @@
 // How the attention calls count their work: which rows a sequence has, what an
-// item is worth in units, which run of units a workgroup takes.  Constexpr
-// functions alone, without HIP, so that a test runs this very accounting on the
-// CPU over starts and lengths that no kernel should meet unprepared.
+// item is worth in units, which run of units a workgroup takes; and a wait that
+// ends.  Constexpr functions alone, without HIP, so that a test runs these very
+// ones on the CPU over what no kernel should meet unprepared.
 #pragma once
 
 #include <stdint.h>
@@ -91,5 +91,16 @@ struct Banks {
         return BankChoice{use, captured, fresh};
     }
 };
+
+// A wait that ends: looks until seen(), `polls` times at most, with pause() after each look
+// in vain.  Whether it was seen.
+template <class Seen, class Pause>
+constexpr bool wait_until(Seen seen, Pause pause, int polls) {
+    for (int i = 0; i < polls; ++i) {
+        if (seen()) return true;
+        pause();
+    }
+    return false;
+}
 
 }  // namespace qw3_units

@@ -513,7 +513,9 @@ qw3_status qcache_copy(void *codes, float *scales, const int32_t *copies, int64_
  * and behind.  Tokens at negative places are not there and are dropped; a kept one
  * whose page is not there is zeros where it goes.  Pages are neither taken nor given
  * back: those behind the new length are used again by qcache_reserve and given up by
- * qcache_fork.  Pages that are written must not be shared.
+ * qcache_fork.  Pages that are written must not be shared.  A new length of -1 says that
+ * rows of the sequence are lost, to a call that overlapped with this one in the same
+ * workspace, which none may.
  * Workspace, by the rules of qgemm_w3g128_smallM: none where Tq <= 512 B; else 16 Tq
  * bytes, and up to 9 MiB.
  * layers B H < 2^23 and Tq H < 2^30 (H rounded up to a power of two, above 8 to a
