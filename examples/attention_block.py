@@ -62,6 +62,11 @@ class AttentionBlock:
         """Room for new[b] more tokens of sequence b: their slots, and the sequences' lengths with them."""
         slots, lens, copies = q3.qcache_reserve(self.refs, self.table, self.lens, self.page_size, cu=self.starts(new), total=sum(new))
         q3.qcache_copy(self.codes, self.scales, copies)  # pages that were shared until now
+        # The host decides lengths here and has to know. A server lets the sequences whose lens did not grow wait; the
+        # others keep the pages that they got and find them at the next call.
+        if slots.numel() and int(slots.min()) < 0:
+            raise RuntimeError("no room for the new tokens: %d pages, contexts of up to %d tokens"
+                               % (self.refs.numel(), self.table.shape[1] * self.page_size))
         return slots, lens
 
     def spread(self, seqs, new):
@@ -115,8 +120,9 @@ class AttentionBlock:
                 w.append((0 if p < 0 else w[p]) | 1 << j)
             depth += [self.counts[b] + i for i in d]
             words += [i - (1 << 64) if i >> 63 else i for i in w]
-        self.drafts = self.spread(seqs, [len(up) for up in parents])
-        slots, self.ahead = self.reserve(self.drafts)
+        each = self.spread(seqs, [len(up) for up in parents])
+        slots, self.ahead = self.reserve(each)
+        self.drafts = each
         q = self.project(x, depth, slots)
         attended = q3.qattn_cache(q, self.codes, self.scales, self.table, self.ahead, cu_q=self.starts(self.drafts),
                                   tree=torch.tensor(words, dtype=torch.int64, device="cuda"))
