@@ -70,12 +70,23 @@ class AttentionBlock:
         return slots, lens
 
     def spread(self, seqs, new):
-        """The number of new tokens of each sequence, 0 for those that are not in seqs (ascending)."""
-        assert list(seqs) == sorted(set(seqs))
+        """The number of new tokens of each sequence, 0 for those that are not in seqs."""
+        if len(set(seqs)) != len(seqs):
+            raise ValueError("a sequence is named twice: %s" % (seqs,))
         each = [0] * len(self.counts)
         for b, n in zip(seqs, new):
             each[b] = n
         return each
+
+    @staticmethod
+    def by_number(call, seqs, new, x):
+        """call(places in seqs, rows), whose rows are packed by their sequences' numbers, for rows x packed as seqs are."""
+        order = sorted(range(len(seqs)), key=lambda i: seqs[i])
+        if order == list(range(len(seqs))):
+            return call(order, x)
+        part = x.split(list(new))
+        out = call(order, torch.cat([part[i] for i in order])).split([new[i] for i in order])
+        return torch.cat([out[order.index(i)] for i in range(len(seqs))])
 
     @staticmethod
     def ints(x):
@@ -97,6 +108,9 @@ class AttentionBlock:
 
     def prompt(self, seqs, new, x):
         """The next new[i] prompt tokens of sequence seqs[i], packed in x [sum(new), hidden]."""
+        return self.by_number(lambda order, rows: self.prompt_rows([seqs[i] for i in order], [new[i] for i in order], rows), seqs, new, x)
+
+    def prompt_rows(self, seqs, new, x):
         each = self.spread(seqs, new)
         slots, self.lens = self.reserve(each)
         q, k, v = self.project(x, [t for n, c in zip(each, self.counts) for t in range(c, c + n)], slots, dense=True)
@@ -112,6 +126,10 @@ class AttentionBlock:
     def verify(self, seqs, parents, x):
         """Drafted tokens of each sequence, x packed [sum of drafts, hidden]. parents[i][j]: the draft that draft j of
         seqs[i] follows, -1 for the last cached token. The drafts lie behind the context until accept()."""
+        return self.by_number(lambda order, rows: self.verify_rows([seqs[i] for i in order], [parents[i] for i in order], rows), seqs,
+                              [len(up) for up in parents], x)
+
+    def verify_rows(self, seqs, parents, x):
         depth, words = [], []
         for b, up in zip(seqs, parents):
             d, w = [], []

@@ -47,3 +47,28 @@ def test_a_context_longer_than_a_table_is_an_error():
     b = block(pages=40, longest=64)
     with pytest.raises(RuntimeError, match="room"):
         b.prompt([b.add()], [65], tokens(65))
+
+
+def test_sequences_in_any_order():
+    """Prompts, chunks and drafts packed in the caller's order, whatever numbers their sequences have."""
+    x = tokens(150)
+    parents = [[-1, 0, 0], [-1], [-1, 0, 1, 1]]
+    straight, turned = block(), block()
+    for b in (straight, turned):
+        for _ in range(3):
+            b.add()
+    for new, at in (([30, 20, 40], 0), ([1, 7, 16], 90)):  # then a second chunk
+        part = x[at:at + sum(new)].split(new)
+        want = straight.prompt([0, 1, 2], new, torch.cat(part)).split(new)
+        got = turned.prompt([2, 0, 1], [new[i] for i in (2, 0, 1)], torch.cat([part[i] for i in (2, 0, 1)])).split([new[i] for i in (2, 0, 1)])
+        assert all(torch.equal(got[j], want[i]) for j, i in enumerate((2, 0, 1)))
+    n = [3, 1, 4]
+    part = x[114:122].split(n)
+    want = straight.verify([0, 1, 2], parents, torch.cat(part)).split(n)
+    got = turned.verify([1, 2, 0], [parents[i] for i in (1, 2, 0)], torch.cat([part[i] for i in (1, 2, 0)])).split([1, 4, 3])
+    assert all(torch.equal(got[j], want[i]) for j, i in enumerate((1, 2, 0)))
+    for b in (straight, turned):
+        b.accept({0: [0, 2], 2: [0, 1, 3]})
+    assert torch.equal(straight.step(x[122:125], 3), turned.step(x[122:125], 3))
+    with pytest.raises(ValueError):
+        turned.prompt([1, 1], [2, 2], x[:4])
