@@ -60,17 +60,20 @@ struct BoundsArgs {
     int64_t max_pages, pages;
 };
 
-// The larger of two numbers that come as bits from other lanes.  In asm because the
-// compiler would first make quiet NaN of each, which costs as much again; a NaN that
-// is lost here has been seen before.
-__device__ __forceinline__ float max_bits(uint32_t x, uint32_t y) {
-    float r;
-    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(x), "v"(y));
-    return r;
-}
-// The larger of what lanes l and l ^ 8 (l ^ 4) of each 16 hold, in both.
-__device__ __forceinline__ float max_ror8(float x) { return max_bits(__float_as_uint(x), __float_as_uint(dpp_f32<0x128>(x))); }
-__device__ __forceinline__ float max_ror4(float x) { return max_bits(__float_as_uint(x), __float_as_uint(dpp_f32<0x124>(x))); }
+// The larger of two numbers that come as bits from other lanes: the middle one of them and
+// +inf, since of a maximum the compiler would first make quiet NaN of each, which costs as
+// much again; a NaN that is lost here has been seen before.  Not in asm: what an exchange
+// between lanes reads has to be two instructions old, which the compiler sees to for its own.
+struct Larger {
+    float inf = __builtin_huge_valf();
+    __device__ __forceinline__ Larger() { asm("" : "+s"(inf)); }  // a constant would make it a maximum again
+    __device__ __forceinline__ float operator()(uint32_t x, uint32_t y) const {
+        return __builtin_amdgcn_fmed3f(__uint_as_float(x), __uint_as_float(y), inf);
+    }
+    // of what lanes l and l ^ 8 (l ^ 4) of each 16 hold, in both
+    __device__ __forceinline__ float ror8(float x) const { return (*this)(__float_as_uint(x), __float_as_uint(dpp_f32<0x128>(x))); }
+    __device__ __forceinline__ float ror4(float x) const { return (*this)(__float_as_uint(x), __float_as_uint(dpp_f32<0x124>(x))); }
+};
 
 // A wave has one page and head.  D / 16 lanes take a row, 16 channels each, and the
 // wave 1024 / D rows at a time; what lanes of the same channels hold is joined at the
@@ -166,18 +169,19 @@ __global__ __launch_bounds__(256) void bounds_kernel(BoundsArgs a) {
     rows32(0, std::true_type{});
     for (int base = 32; base < count; base += 32) rows32(base, std::false_type{});
     const bool bad = !(worst == 0.0f);
+    const Larger larger;
     // lanes 0..31 keep the maxima, the others those of the opposites; then the even
     // sixteens of lanes the first 8 channels, the odd ones the last
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[16 + i]), false, false);
-        v[i] = max_bits(r[0], r[1]);
+        v[i] = larger(r[0], r[1]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[8 + i]), false, false);
-        v[i] = max_ror8(max_bits(r[0], r[1]));
-        if (D == 64) v[i] = max_ror4(v[i]);
+        v[i] = larger.ror8(larger(r[0], r[1]));
+        if (D == 64) v[i] = larger.ror4(v[i]);
     }
     uint32_t top = 0;
 #pragma unroll
