@@ -573,7 +573,7 @@ __global__ __launch_bounds__(1024) void compact_move_kernel(CompactArgs a) {
     const int chunk = unit / lanes, lane = unit - chunk * lanes;
     const int layer = lane / a.groups, group = lane - layer * a.groups;
     const int t0 = chunk << a.token_shift, n = min(1 << a.token_shift, a.total - t0);
-    int over = -1, sequence = 0;  // the chunk whose row this thread's token is written over
+    int over = -1;  // the chunk whose row this thread's token is written over
     if (tid < n) {
         const int4 move = a.moves[t0 + tid];
         // always so where it moves, but for calls that overlap: those spoil each other's rows, and reach no others
@@ -582,7 +582,7 @@ __global__ __launch_bounds__(1024) void compact_move_kernel(CompactArgs a) {
         const int32_t *table = a.table + (moves ? move.x * a.max_pages : 0);
         from[tid] = moves ? row_of(a, table, move.y, 0, 0) : -1;
         to[tid] = moves ? row_of(a, table, move.z, 0, 0) : -1;
-        if (moves) over = move.w >> a.token_shift, sequence = move.x;
+        if (moves) over = move.w >> a.token_shift;
     }
     __syncthreads();
     uint4 *codes = reinterpret_cast<uint4 *>(a.codes + (a.layer0 + layer) * a.layer_rows * D);
@@ -612,7 +612,10 @@ __global__ __launch_bounds__(1024) void compact_move_kernel(CompactArgs a) {
     if (over >= 0 && over < chunk) {
         const int *other = a.read + over * lanes + lane;
         auto seen = [&]() { return __hip_atomic_load(other, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) > a.epoch; };
-        if (!wait_until(seen, []() { __builtin_amdgcn_s_sleep(1); }, kPolls)) a.lens_out[sequence] = -1;
+        if (!wait_until(seen, []() { __builtin_amdgcn_s_sleep(1); }, kPolls)) {
+            const int b = a.moves[t0 + tid].x;  // anew, as a register for it would leave a CU room for one workgroup, not two
+            if ((uint32_t)b < (uint32_t)a.B) a.lens_out[b] = -1;
+        }
     }
     __syncthreads();
 #pragma unroll
