@@ -73,17 +73,6 @@ __device__ __forceinline__ void clear_next(int *counts) {
         store_agent(reinterpret_cast<float *>(counts) + 2 * (i + threadIdx.x), 0.0f, 0.0f);
 }
 
-// Inclusive maximum over the wave's lanes up to one's own, of values >= 0.
-__device__ __forceinline__ int wave_scan_max(int x) {
-    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false));  // row_shr 1, 2, 4, 8
-    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false));
-    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false));
-    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false));
-    x = max(x, __builtin_amdgcn_update_dpp(0, x, kDppRowBcast15, 0xA, 0xF, false));
-    x = max(x, __builtin_amdgcn_update_dpp(0, x, kDppRowBcast31, 0xC, 0xF, false));
-    return x;
-}
-
 __device__ __forceinline__ int wave_sum(int x) {  // over all 64 lanes, in every lane
     x += (int)dpp_u32<0xB1>((uint32_t)x);   // quad_perm [1, 0, 3, 2]
     x += (int)dpp_u32<0x4E>((uint32_t)x);   // quad_perm [2, 3, 0, 1]
@@ -93,16 +82,6 @@ __device__ __forceinline__ int wave_sum(int x) {  // over all 64 lanes, in every
     x = (int)(r[0] + r[1]);
     r = __builtin_amdgcn_permlane32_swap((uint32_t)x, (uint32_t)x, false, false);
     return (int)(r[0] + r[1]);
-}
-
-__device__ __forceinline__ int wave_scan(int x) {  // inclusive prefix sum over the wave
-    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
-    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
-    x += __builtin_amdgcn_update_dpp(0, x, kDppRowBcast15, 0xA, 0xF, false);
-    x += __builtin_amdgcn_update_dpp(0, x, kDppRowBcast31, 0xC, 0xF, false);
-    return x;
 }
 
 __device__ __forceinline__ int wave_max(int x) {  // over all 64 lanes, in every lane

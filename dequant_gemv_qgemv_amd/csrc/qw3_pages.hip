@@ -14,25 +14,6 @@ using qw3_units::wait_until;
 
 namespace {
 
-__device__ __forceinline__ int wave_scan(int x) {  // inclusive prefix sum over the wave
-    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
-    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
-    x += __builtin_amdgcn_update_dpp(0, x, kDppRowBcast15, 0xA, 0xF, false);
-    x += __builtin_amdgcn_update_dpp(0, x, kDppRowBcast31, 0xC, 0xF, false);
-    return x;
-}
-__device__ __forceinline__ int wave_scan_max(int x) {  // inclusive maximum, of values >= 0
-    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false));
-    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false));
-    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false));
-    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false));
-    x = max(x, __builtin_amdgcn_update_dpp(0, x, kDppRowBcast15, 0xA, 0xF, false));
-    x = max(x, __builtin_amdgcn_update_dpp(0, x, kDppRowBcast31, 0xC, 0xF, false));
-    return x;
-}
-
 // Exclusive prefix sum over the workgroup's kThreads threads; *total: of all.
 template <int kThreads>
 __device__ __forceinline__ int group_scan(int x, int *total) {

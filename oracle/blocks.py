@@ -6,18 +6,7 @@ so they are computed in those; attention is in 64 bits (oracle/attention.py)."""
 import numpy as np
 
 from oracle import attention as ref
-
-
-def starts_of(cu, batch, total):
-    """First row and number of rows of each sequence: a start below an earlier one counts as that one."""
-    if cu is None:
-        return [(b, 1) for b in range(batch)]
-    got, floor = [], 0
-    for b in range(batch):
-        first = max(min(max(int(cu[b]), 0), total), floor)
-        got.append((first, max(min(max(int(cu[b + 1]), 0), total) - first, 0)))
-        floor = first
-    return got
+from oracle.pages import starts_of
 
 
 def rows_of(lens, cu, total, room):
