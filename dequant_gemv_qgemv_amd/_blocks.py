@@ -90,7 +90,8 @@ def qblock_select(q: torch.Tensor, bounds: torch.Tensor, bound_scales: torch.Ten
     to: int32 [Tq, H, count] places in their sequence's block table, ascending, -1 behind the last.
 
     All where a row sees at most count; else its first ones, its recent ones
-    (its own is the last) and those with the highest scores by the bounds."""
+    (its own is the last) and those with the highest scores by the bounds.
+    page_size is the cache's, which this call does not see and cannot check."""
     dev = q.get_device()
     qts, qhs = _rows(q, "q", _BF16, dev)
     pages, heads, dim = _bounds(bounds, bound_scales, dev)

@@ -3,7 +3,8 @@ marshalling only, like the package's other calls.
 
 Who holds a page is counted in a tensor that the caller allocates with the cache
 and keeps: refs [pages] int32, zeros at first.  A block table starts as -1 in
-every entry, lengths as 0.  A cache of several layers is codes [layers, pages, 2,
+every entry, lengths as 0.  page_size is the cache's, which qcache_reserve and
+qcache_fork do not see and cannot check.  A cache of several layers is codes [layers, pages, 2,
 H, page_size, D] and scales [layers, pages, 2, H, page_size]; codes[i] and
 scales[i] are what the calls of one layer take.
 """

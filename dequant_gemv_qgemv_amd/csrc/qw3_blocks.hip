@@ -78,8 +78,11 @@ struct Larger {
 // A wave has one page and head.  D / 16 lanes take a row, 16 channels each, and the
 // wave 1024 / D rows at a time; what lanes of the same channels hold is joined at the
 // end, halving in each step the channels that a lane stands for.  30,001 tokens of 8 heads
-// of 128 channels in pages of 32, e4m3: 9.9 us, 33 MB at 3.3 TB/s; vector instructions (a
-// conversion, a product, two comparisons for each code) are issued 64 % of the time.
+// of 128 channels in pages of 32, e4m3: 9.9 us (11 on an input that the caches do not hold), 33
+// MB at 3.3 TB/s; vector instructions are issued 64 % of the time.  A page's 32 rows take a wave
+// some 480 of them, 7.5 for each of a lane's 64 codes: conversions, products and maxima are 160, the
+// NaN test of e4m3 codes 40, the joins across lanes 130, quotients and codes 75, finding the
+// sequence 40, addresses the rest.
 template <int D, bool E4M3>
 __global__ __launch_bounds__(256) void bounds_kernel(BoundsArgs a) {
     constexpr int kPieces = D / 16, kRows = 64 / kPieces;
@@ -959,7 +962,8 @@ struct Walk {
 };
 
 // Many items: one for each wave, the same kv head of 4 neighbouring rows in a workgroup.
-// With 64 channels four waves of a SIMD have the registers (51 us where three took 54).
+// With 64 channels four waves of a SIMD share the registers (51 us where three took 54), of
+// which up to three are spilled with 4 queries in e4m3 and with more than 8.
 // 510 rows of 4 queries of 8 heads of 64 channels, 40 pages of 32 tokens, e4m3: 55 us; vector
 // instructions take 63 % of the time and the matrix unit 18 %, and they hardly overlap.
 template <int D, bool E4M3, int S>
@@ -1129,6 +1133,9 @@ constexpr int64_t kRowPages = 256, kPartPages = 2048;
 // 11.9, 12.7, 13.6.  48 rows, 250, 512, 1024, 2048: by one 10.0, 17.4, 28.5, by the last 12.4, 17.8,
 // 29.3, 51.3, by a second launch 14.1, 21.1, 31.1, 56.5; 17 to 16,000 tokens each in pages of 16, where
 // the longest are waited for: 19.9, 15.4, 15.8.
+// The host knows the table's width alone.  Where it is more than the rows see: 24 pages for one row
+// over 1000 tokens in pages of 16, tables of 63 to 250 pages 6.5 us, 257 to 1024 8.1, 2048 8.8, 2049 to
+// 8192 9.5; 16 such rows 6.6, 8.3 (512), 9.2 (2048), 10.7 (8192).
 template <int D>
 qw3_status launch_select(SelectArgs a, hipStream_t stream) {
     int cus = 0;

@@ -34,7 +34,7 @@
  *   - Alignment: `codes`, `packed`, `x` and `w_out` must be 16-byte aligned,
  *     `scales` 2-byte and `y` 4-byte aligned, else QW3_ERR_ALIGN.
  *   - Each call is deterministic: the same inputs give bit-identical outputs
- *     on every run (all reductions run in a fixed order, no atomics).
+ *     on every run (all reductions run in a fixed order; atomics only count).
  *   - Inputs must be finite; NaN or Inf in x or scales give unspecified y.
  *     The products also assume every |s| * |x| below 2^100 and every
  *     sum_k |x_k w_k| below 2^120 (far inside fp32), so that no partial sum
@@ -436,6 +436,8 @@ qw3_status qrope_write(const void *q, const void *k, const void *v, int32_t src_
  * 0 .. pages - 1 names no page (-1 is what these calls write).  A page with a
  * count of more than one is shared: nothing may be written into it, and
  * qcache_reserve sees to that.
+ *   - page_size is the cache's.  qcache_reserve, qcache_fork and qblock_select do not see
+ *     the cache and cannot check it: another one gives wrong slots, tables and picks.
  *   - max_pages * page_size <= 2^30, B * max_pages < 2^32, else QW3_ERR_SHAPE.
  *   - Lengths are clipped to 0 .. max_pages * page_size; starts (cu) as above.
  *   - Alignment: 16 bytes for refs, codes and scales, 8 for slots and copies, 4
@@ -464,6 +466,10 @@ qw3_status qrope_write(const void *q, const void *k, const void *v, int32_t src_
  * holds tokens of the sequence (lens is not a multiple of page_size, first entry), the
  * pair goes into copies, and qcache_copy has to run, for every layer, before the new
  * tokens are written and before the next qcache_reserve.
+ * Whether a page is shared is judged by refs as they are before the call: where all n
+ * holders of a page take new tokens in it in one call, all n need a page and the old one goes
+ * free, so n - 1 free pages leave the last of them without room in this call, though not
+ * in the next.
  * No room: a sequence that would pass max_pages * page_size tokens needs nothing and
  * gets nothing.  Where free pages run out, the first sequence whose needs are not all
  * met and every later one that needs a page get nothing and stay as they are; later ones that
@@ -517,7 +523,8 @@ qw3_status qcache_copy(void *codes, float *scales, const int32_t *copies, int64_
  * rows of the sequence are lost, to a call that overlapped with this one in the same
  * workspace, which none may.
  * Workspace, by the rules of qgemm_w3g128_smallM: none where Tq <= 512 B; else 16 Tq
- * bytes, and up to 9 MiB.
+ * bytes, and up to 9 MiB.  Without workspace a sequence's tokens are moved by one workgroup
+ * for each head and layer, however many of the 512 B are its own.
  * layers B H < 2^23 and Tq H < 2^30 (H rounded up to a power of two, above 8 to a
  * multiple of 8), else QW3_ERR_SHAPE.
  */
@@ -549,8 +556,8 @@ qw3_status qcache_compact(void *codes, float *scales, const int32_t *block_table
  * S = max_d max(|mx_d|, |mn_d|) / 127 (a float32 quotient), and mx_d / S and mn_d / S
  * rounded to the nearest whole number, ties to even, at most 127 in size; zeros where S is zero.  A page
  * whose keys hold an infinity or NaN gets S = NaN and zeros.
- * Pages that qcache_compact moved tokens into, and pages whose numbers changed, are
- * up to date after a call whose n reach back to the first of them.
+ * Pages that qcache_compact moved tokens into or dropped tokens from, and pages whose
+ * numbers changed, are up to date after a call whose n reach back to the first of them.
  * The pages of two sequences are different, or hold the same tokens.
  * Tq is the number of rows that cu_q speaks of.
  * (Tq / page_size + 2 B) H < 2^26 (B H < 2^26 without cu_q), else QW3_ERR_SHAPE.
@@ -573,7 +580,7 @@ qw3_status qcache_bounds(const void *codes, const float *scales, int32_t code_ty
  *   times 2^-16), both as int8 under one scale, max / 127, rounded as the bounds are;
  *   score = float(sum_d u_d mx_d + n_d mn_d) * S   in float32: a whole number, one rounding.
  * NaN is the highest score; a page that is not there comes last.  With NaN or an
- * infinity in a row's queries its u and n are zeros.
+ * infinity in a row's queries of the kv head u and n are zeros.
  * 1 <= count <= QW3_MAX_PICKS, first >= 0, recent >= 1, first + recent <= count,
  * (Tq + B) H < 2^22, else QW3_ERR_SHAPE.
  * Workspace, by the rules of qgemm_w3g128_smallM: none with max_pages up to 256, or up

@@ -399,3 +399,23 @@ def test_refusals():
         with pytest.raises(q().Qw3Error) as e:
             bad()
         assert e.value.status == q().QW3_ERR_SHAPE
+
+
+def test_all_holders_of_a_page_take_tokens_in_one_call():
+    """Three that share a partly filled page need three pages; with two the last has room in the next call, in the page itself."""
+    size, pages = 16, 5
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    table, lens = dev([[-1] * 3]), dev([0])
+    _, lens, _ = q().qcache_reserve(refs, table, lens, size, cu=dev([0, 40]), total=40)
+    table, lens = q().qcache_fork(refs, table, lens, dev([0, 0, 0]), size)
+    assert refs.tolist() == [3, 3, 3, 0, 0]
+    slots, lens, copies = q().qcache_reserve(refs, table, lens, size)
+    assert slots.tolist() == [3 * 16 + 8, 4 * 16 + 8, -1] and lens.tolist() == [41, 41, 40]
+    assert copies.tolist() == [[2, 3], [2, 4], [-1, -1]] and refs.tolist() == [3, 3, 1, 1, 1]
+    slots, lens, copies = q().qcache_reserve(refs, table, lens, size)
+    assert slots.tolist() == [3 * 16 + 9, 4 * 16 + 9, 2 * 16 + 8] and lens.tolist() == [42, 42, 41]
+    assert (copies == -1).all() and table.tolist() == [[0, 1, 3], [0, 1, 4], [0, 1, 2]]
+    # with a page for each the old one goes free
+    refs = dev([3, 3, 3, 0, 0, 0])
+    slots, _, copies = q().qcache_reserve(refs, dev([[0, 1, 2]] * 3), dev([40] * 3), size)
+    assert refs.tolist() == [3, 3, 0, 1, 1, 1] and copies.tolist() == [[2, 3], [2, 4], [2, 5]] and (slots % 16 == 8).all()
